@@ -20,7 +20,9 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libampfp8.so")
 SOURCES = ["api.cu", "unscale_check.cu", "adamw_master.cu", "adamw_noalloc.cu", "emit_bf16.cu",
            "fp8_quant.cu",
-           "fp8_rowwise.cu", "fp8_groupwise.cu", "update_scale.cu"]
+           "fp8_rowwise.cu", "fp8_groupwise.cu", "update_scale.cu",
+           "ops_api.cu", "fp4_mx.cu", "fp4_product.cu", "layer_norm_fwd.cu", "layer_norm_bwd.cu",
+           "act_mx8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # --fmad=false: no multiply-add is fused behind the code's back; the kernels
 # spell out the rounding of every operation.  IEEE division and square root
@@ -46,7 +48,7 @@ def _stale(target: str, deps) -> bool:
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers.append(os.path.join(INCLUDE, "ampfp8.h"))
+    headers += [os.path.join(INCLUDE, f) for f in ("ampfp8.h", "ampops.h")]
     cc = nvcc()
     procs, objs = [], []
     for src in SOURCES:

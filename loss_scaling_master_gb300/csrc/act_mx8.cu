@@ -1,0 +1,345 @@
+// act_mx8.cu - activations whose inputs are kept as 8-bit checkpoints (e4m3,
+// blocks of 32 with a power-of-two scale: mx.cuh), their gradients from those
+// checkpoints, and the checkpoint on its own.
+//
+//   forward   y = f(x) [* u];  x [, u] -> codes and scales in the same pass
+//   backward  xh, uh = the checkpoint's values;
+//             dx = dy f'(xh) [* uh], du = dy f(xh)
+//   f(x) = x Phi(x), x sigma(2 z(x)) with z = sqrt(2/pi) (x + 0.044715 x^3)
+//          (= x/2 (1 + tanh z)), or x sigma(x)
+//
+// Every element is read and written once, so memory bounds the kernels as long
+// as the arithmetic stays under the issue rate.  A thread takes 8 elements
+// (one 16-byte access of a 16-bit tensor), 4 threads a block, whose maximum
+// takes two shuffles.  Rows that are not whole groups of 8 elements, or not
+// 16-byte aligned, take one element a lane and one block a warp instead.
+#include <algorithm>
+
+#include "ampops.h"
+#include "internal.h"
+#include "mx.cuh"
+#include "pdl.cuh"
+
+namespace amp {
+namespace {
+
+enum Mode : int { kSave = 3 };  // after the three amp_act values: no activation
+
+struct ActFwd {
+    const void *x, *u;
+    void *y;
+    uint8_t *q, *s, *qu, *su;
+    int64_t rows, cols, kb;  // kb: blocks a row
+    int64_t blocks;          // rows * kb
+};
+struct ActBwd {
+    const void *dy;
+    const uint8_t *q, *s, *qu, *su;
+    void *dx, *du;
+    int64_t rows, cols, kb, blocks;
+};
+
+// 1 / (1 + exp(-t)) as 1 / (1 + e) or e / (1 + e), e = exp(-|t|): the
+// denominator stays in [1, 2], so neither overflow nor the flush to zero of a
+// large one's reciprocal cuts the tail off (it keeps its relative precision
+// down to the subnormals).
+__device__ __forceinline__ float sigmoid(float t) {
+    const float e = __expf(-fabsf(t));
+    return __fdividef(t >= 0.0f ? 1.0f : e, 1.0f + e);
+}
+
+// The magnitude past which sigma(2z) and Phi are 0 or 1 to the last bit, so
+// cubes and squares of larger x need not be formed (they would overflow and
+// meet a zero factor).  NaN stays.
+__device__ __forceinline__ float act_clamp(float x) { return fabsf(x) > 30.0f ? copysignf(30.0f, x) : x; }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float x) {
+    if constexpr (ACT == AMP_ACT_SILU) return x * sigmoid(x);
+    if constexpr (ACT == AMP_ACT_GELU)
+        return x * __fmaf_rn(0.5f, erff(x * 0.70710678118654752f), 0.5f);
+    const float c = act_clamp(x);
+    // 2 sqrt(2/pi) = 1.5957691216, times 0.044715 = 0.0713548163
+    return x * sigmoid(c * __fmaf_rn(c * c, 0.07135481627159954f, 1.5957691216057308f));
+}
+// f(x) and f'(x)
+template <int ACT>
+__device__ __forceinline__ void act_both(float x, float &f, float &d) {
+    if constexpr (ACT == AMP_ACT_SILU) {
+        const float s = sigmoid(x);
+        f = x * s;
+        d = s * __fmaf_rn(x, 1.0f - s, 1.0f);
+    } else if constexpr (ACT == AMP_ACT_GELU) {
+        const float p = __fmaf_rn(0.5f, erff(x * 0.70710678118654752f), 0.5f);
+        const float c = act_clamp(x);
+        f = x * p;
+        d = __fmaf_rn(c * 0.3989422804014327f, __expf(-0.5f * c * c), p);
+    } else {
+        const float c = act_clamp(x), c2 = c * c;
+        const float s = sigmoid(c * __fmaf_rn(c2, 0.07135481627159954f, 1.5957691216057308f));
+        f = x * s;
+        d = __fmaf_rn(c * s * (1.0f - s), __fmaf_rn(c2, 3.0f * 0.07135481627159954f, 1.5957691216057308f), s);
+    }
+}
+
+// fp32 bits of max |y| over the 8 elements and the 4 lanes of the block
+__device__ __forceinline__ uint32_t block_max8(const float (&y)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float f) {
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float a, b;
+        mul2_rn(y[2 * j], y[2 * j + 1], f, f, a, b);
+        h[j] = f32x2_to_fp8x2_raw<kE4M3>(a, b);
+    }
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+__device__ __forceinline__ void values8(uint2 q, float s, float (&y)[8]) {
+    e4m3x4_to_f32x4(q.x, y);
+    e4m3x4_to_f32x4(q.y, y + 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(y[j], s);
+}
+
+template <int XT>
+__device__ __forceinline__ void ldv(const void *p, int64_t k, float (&y)[8]) {
+    constexpr int esz = XT == kF32 ? 4 : 2;
+    uint4 u[kWords8<XT>];
+#pragma unroll
+    for (int j = 0; j < kWords8<XT>; ++j) u[j] = ld16(static_cast<const char *>(p) + k * esz + 16 * j);
+    raw8_to_f32<XT>(u, y);
+}
+template <int XT>
+__device__ __forceinline__ void stv(void *p, int64_t k, const float (&y)[8]) {
+    constexpr int esz = XT == kF32 ? 4 : 2;
+    uint4 u[kWords8<XT>];
+    f32_to_raw8<XT>(y, u);
+#pragma unroll
+    for (int j = 0; j < kWords8<XT>; ++j) st16(static_cast<char *>(p) + k * esz + 16 * j, u[j]);
+}
+
+// 8 elements a thread; rows are whole groups of 8 and every address aligned.
+template <int XT, int ACT, bool GATED, bool KEEP>
+__global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t n = P.blocks * 4;
+    // the 4 threads of a block run together: the count of blocks is not a
+    // multiple of 8, so every thread of a warp walks the loop and guards
+    for (int64_t t0 = int64_t(blockIdx.x) * kThreads; t0 < n; t0 += int64_t(gridDim.x) * kThreads) {
+        const int64_t t = t0 + threadIdx.x;
+        const int64_t b = t >> 2;
+        const int64_t r = b / P.kb;
+        const int64_t col = (b - r * P.kb) * kMxBlock + 8 * (t & 3);
+        const bool in = t < n && col < P.cols;
+        const int64_t k = r * P.cols + col;
+        float x[8], u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = u[j] = 0.0f;
+        if (in) {
+            ldv<XT>(P.x, k, x);
+            if (GATED) ldv<XT>(P.u, k, u);
+        }
+        if (KEEP) {
+            const uint32_t e = mx_scale_code<MxE4M3>(block_max8(x));
+            if (in) *reinterpret_cast<uint2 *>(P.q + k) = codes8(x, mx_unscale(e));
+            if (t < n && (t & 3) == 0) P.s[b] = uint8_t(e);
+            if (GATED) {
+                const uint32_t eu = mx_scale_code<MxE4M3>(block_max8(u));
+                if (in) *reinterpret_cast<uint2 *>(P.qu + k) = codes8(u, mx_unscale(eu));
+                if (t < n && (t & 3) == 0) P.su[b] = uint8_t(eu);
+            }
+        }
+        if (ACT != kSave && in) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = act_value<ACT>(x[j]);
+                if (GATED) x[j] *= u[j];
+            }
+            stv<XT>(P.y, k, x);
+        }
+    }
+}
+
+// One block a warp, one element a lane: any size, any address.
+template <int XT, int ACT, bool GATED, bool KEEP>
+__global__ void __launch_bounds__(kThreads) act_fwd_elem(ActFwd P) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t step = int64_t(gridDim.x) * (kThreads / 32);
+    for (int64_t b = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); b < P.blocks; b += step) {
+        const int64_t r = b / P.kb;
+        const int64_t col = (b - r * P.kb) * kMxBlock + lane;
+        const bool in = col < P.cols;
+        const int64_t k = r * P.cols + col;
+        const float x = in ? load_elem<XT>(P.x, k) : 0.0f;
+        const float u = GATED && in ? load_elem<XT>(P.u, k) : 0.0f;
+        if (KEEP) {
+            const uint32_t e = mx_scale_code<MxE4M3>(warp_max_u32(__float_as_uint(x) & 0x7FFFFFFFu));
+            if (in) P.q[k] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(x * mx_unscale(e), 0.0f));
+            if (lane == 0) P.s[b] = uint8_t(e);
+            if (GATED) {
+                const uint32_t eu = mx_scale_code<MxE4M3>(warp_max_u32(__float_as_uint(u) & 0x7FFFFFFFu));
+                if (in) P.qu[k] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(u * mx_unscale(eu), 0.0f));
+                if (lane == 0) P.su[b] = uint8_t(eu);
+            }
+        }
+        if (ACT != kSave && in) {
+            float y = act_value<ACT>(x);
+            if (GATED) y *= u;
+            store_elem<XT>(P.y, k, y);
+        }
+    }
+}
+
+template <int XT, int ACT, bool GATED>
+__global__ void __launch_bounds__(kThreads) act_bwd_vec(ActBwd P) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t n = P.blocks * 4;
+    for (int64_t t = int64_t(blockIdx.x) * kThreads + threadIdx.x; t < n;
+         t += int64_t(gridDim.x) * kThreads) {
+        const int64_t b = t >> 2;
+        const int64_t r = b / P.kb;
+        const int64_t col = (b - r * P.kb) * kMxBlock + 8 * (t & 3);
+        if (col >= P.cols) continue;
+        const int64_t k = r * P.cols + col;
+        float x[8], u[8], g[8], o[8];
+        values8(*reinterpret_cast<const uint2 *>(P.q + k), mx_scale(P.s[b]), x);
+        if (GATED) values8(*reinterpret_cast<const uint2 *>(P.qu + k), mx_scale(P.su[b]), u);
+        if (ACT != kSave) ldv<XT>(P.dy, k, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (ACT == kSave) {
+                g[j] = x[j];
+            } else {
+                float f, d;
+                act_both<ACT>(x[j], f, d);
+                o[j] = g[j] * f;
+                g[j] = (GATED ? g[j] * u[j] : g[j]) * d;
+            }
+        }
+        stv<XT>(P.dx, k, g);
+        if (GATED) stv<XT>(P.du, k, o);
+    }
+}
+
+template <int XT, int ACT, bool GATED>
+__global__ void __launch_bounds__(kThreads) act_bwd_elem(ActBwd P) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t step = int64_t(gridDim.x) * (kThreads / 32);
+    for (int64_t b = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); b < P.blocks; b += step) {
+        const int64_t r = b / P.kb;
+        const int64_t col = (b - r * P.kb) * kMxBlock + lane;
+        if (col >= P.cols) continue;
+        const int64_t k = r * P.cols + col;
+        float v[4];
+        e4m3x4_to_f32x4(P.q[k], v);
+        const float x = __fmul_rn(v[0], mx_scale(P.s[b]));
+        if constexpr (ACT == kSave) {
+            store_elem<XT>(P.dx, k, x);
+        } else {
+            float g = load_elem<XT>(P.dy, k), f, d;
+            act_both<ACT>(x, f, d);
+            if (GATED) {
+                e4m3x4_to_f32x4(P.qu[k], v);
+                store_elem<XT>(P.du, k, g * f);
+                g *= __fmul_rn(v[0], mx_scale(P.su[b]));
+            }
+            store_elem<XT>(P.dx, k, g * d);
+        }
+    }
+}
+
+bool ptr_ok(const void *p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) == 0; }
+
+unsigned grid_of(int64_t threads, int device) {
+    const int64_t want = (threads + kThreads - 1) / kThreads;
+    return unsigned(std::min<int64_t>(want, int64_t(sm_count(device)) * 64));
+}
+
+template <int XT, int ACT, bool GATED>
+cudaError_t fwd(const ActFwd &P, bool keep, bool vec, int dev, cudaStream_t s) {
+    const dim3 block(kThreads), gv(grid_of(P.blocks * 4, dev)), ge(grid_of(P.blocks * 32, dev));
+    if constexpr (ACT == kSave)
+        return vec ? launch_pdl(act_fwd_vec<XT, ACT, GATED, true>, gv, block, 0, s, P)
+                   : launch_pdl(act_fwd_elem<XT, ACT, GATED, true>, ge, block, 0, s, P);
+    else if (keep)
+        return vec ? launch_pdl(act_fwd_vec<XT, ACT, GATED, true>, gv, block, 0, s, P)
+                   : launch_pdl(act_fwd_elem<XT, ACT, GATED, true>, ge, block, 0, s, P);
+    else
+        return vec ? launch_pdl(act_fwd_vec<XT, ACT, GATED, false>, gv, block, 0, s, P)
+                   : launch_pdl(act_fwd_elem<XT, ACT, GATED, false>, ge, block, 0, s, P);
+}
+template <int XT, int ACT, bool GATED>
+cudaError_t bwd(const ActBwd &P, bool vec, int dev, cudaStream_t s) {
+    const dim3 block(kThreads);
+    return vec ? launch_pdl(act_bwd_vec<XT, ACT, GATED>, dim3(grid_of(P.blocks * 4, dev)), block, 0, s, P)
+               : launch_pdl(act_bwd_elem<XT, ACT, GATED>, dim3(grid_of(P.blocks * 32, dev)), block, 0, s, P);
+}
+
+template <int XT>
+cudaError_t fwd_x(const ActFwd &P, int act, bool keep, bool vec, int dev, cudaStream_t s) {
+    if (act == kSave) return fwd<XT, kSave, false>(P, keep, vec, dev, s);
+    if (P.u) {
+        if (act == AMP_ACT_GELU) return fwd<XT, AMP_ACT_GELU, true>(P, keep, vec, dev, s);
+        if (act == AMP_ACT_GELU_TANH) return fwd<XT, AMP_ACT_GELU_TANH, true>(P, keep, vec, dev, s);
+        return fwd<XT, AMP_ACT_SILU, true>(P, keep, vec, dev, s);
+    }
+    if (act == AMP_ACT_GELU) return fwd<XT, AMP_ACT_GELU, false>(P, keep, vec, dev, s);
+    if (act == AMP_ACT_GELU_TANH) return fwd<XT, AMP_ACT_GELU_TANH, false>(P, keep, vec, dev, s);
+    return fwd<XT, AMP_ACT_SILU, false>(P, keep, vec, dev, s);
+}
+template <int XT>
+cudaError_t bwd_x(const ActBwd &P, int act, bool vec, int dev, cudaStream_t s) {
+    if (act == kSave) return bwd<XT, kSave, false>(P, vec, dev, s);
+    if (P.qu) {
+        if (act == AMP_ACT_GELU) return bwd<XT, AMP_ACT_GELU, true>(P, vec, dev, s);
+        if (act == AMP_ACT_GELU_TANH) return bwd<XT, AMP_ACT_GELU_TANH, true>(P, vec, dev, s);
+        return bwd<XT, AMP_ACT_SILU, true>(P, vec, dev, s);
+    }
+    if (act == AMP_ACT_GELU) return bwd<XT, AMP_ACT_GELU, false>(P, vec, dev, s);
+    if (act == AMP_ACT_GELU_TANH) return bwd<XT, AMP_ACT_GELU_TANH, false>(P, vec, dev, s);
+    return bwd<XT, AMP_ACT_SILU, false>(P, vec, dev, s);
+}
+
+}  // namespace
+
+cudaError_t launch_act_fwd(int act, const void *x, const void *u, int elem, int64_t rows, int64_t cols,
+                           void *y, uint8_t *q, uint8_t *sc, uint8_t *qu, uint8_t *su, int device,
+                           cudaStream_t s) {
+    ActFwd P{x, u, y, q, sc, qu, su, rows, cols, (cols + kMxBlock - 1) / kMxBlock, 0};
+    P.blocks = rows * P.kb;
+    const bool vec = cols % 8 == 0 && ptr_ok(x, 15) && ptr_ok(u, 15) && ptr_ok(y, 15) && ptr_ok(q, 7) && ptr_ok(qu, 7);
+    const int a = act < 0 ? int(kSave) : act;
+    cudaError_t e = elem == kF32   ? fwd_x<kF32>(P, a, q != nullptr, vec, device, s)
+                    : elem == kF16 ? fwd_x<kF16>(P, a, q != nullptr, vec, device, s)
+                                   : fwd_x<kBF16>(P, a, q != nullptr, vec, device, s);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_act_bwd(int act, const void *dy, int elem, int64_t rows, int64_t cols,
+                           const uint8_t *q, const uint8_t *sc, const uint8_t *qu, const uint8_t *su,
+                           void *dx, void *du, int device, cudaStream_t s) {
+    ActBwd P{dy, q, sc, qu, su, dx, du, rows, cols, (cols + kMxBlock - 1) / kMxBlock, 0};
+    P.blocks = rows * P.kb;
+    const bool vec = cols % 8 == 0 && ptr_ok(dy, 15) && ptr_ok(dx, 15) && ptr_ok(du, 15) && ptr_ok(q, 7) && ptr_ok(qu, 7);
+    const int a = act < 0 ? int(kSave) : act;
+    cudaError_t e = elem == kF32   ? bwd_x<kF32>(P, a, vec, device, s)
+                    : elem == kF16 ? bwd_x<kF16>(P, a, vec, device, s)
+                                   : bwd_x<kBF16>(P, a, vec, device, s);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace amp

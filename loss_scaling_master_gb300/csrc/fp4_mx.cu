@@ -1,0 +1,337 @@
+// fp4_mx.cu - microscaled 4-bit quantisation (both orientations in one pass)
+// and its inverse.
+//
+// Mathematics: mx.cuh.  One CTA takes a 128x128 tile of x, which holds whole
+// blocks of both orientations and exactly one 512-byte scale tile of each, so
+// x is read once: 2 bytes (16-bit x) in and 17/32 byte out per element and
+// orientation.
+//
+// A warp takes 32 rows x 64 columns, a lane 8 rows x 8 columns of it (16-byte
+// loads), all in registers.  The 4 lanes side by side hold a row block, the 4
+// lanes below one another a column block.  Their maxima are exchanged by a
+// transposing reduction (each step halves the number of words a lane still
+// carries), after which every lane holds the finished maxima of two rows and
+// two columns, forms their scale bytes and hands them round with 4 shuffles.
+// The lane's 8 consecutive rows make the transposed copy's nibbles without an
+// exchange; only the 16-byte pieces of that copy go through shared memory, so
+// that a column's 64 bytes leave together.
+#include <algorithm>
+
+#include "internal.h"
+#include "mx.cuh"
+#include "pdl.cuh"
+
+namespace amp {
+namespace {
+
+struct Fp4Quant {
+    const void *x;
+    int64_t rows, cols;
+    uint8_t *out, *scales, *out_t, *scales_t;
+    const int32_t *skip;
+    int64_t tiles_c;  // tiles along the columns
+    int vec;          // 16-byte access to every row of x
+};
+
+// Words w[0..N) over the 4 lanes of two lane bits -> the maxima of words
+// i * N / 4 .. for the lane with index i in the group.  `Op` is an associative
+// maximum; hi and lo are the lane masks of the group's two index bits.
+template <int N, class Op>
+__device__ __forceinline__ void transposing_max4(uint32_t (&w)[N], uint32_t (&r)[N / 4], int hi,
+                                                 int lo, int lane, Op op) {
+    const bool bh = lane & hi, bl = lane & lo;
+    uint32_t h[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const uint32_t mine = bh ? w[N / 2 + i] : w[i], other = bh ? w[i] : w[N / 2 + i];
+        h[i] = op(mine, __shfl_xor_sync(0xFFFFFFFFu, other, hi));
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        const uint32_t mine = bl ? h[N / 4 + i] : h[i], other = bl ? h[i] : h[N / 4 + i];
+        r[i] = op(mine, __shfl_xor_sync(0xFFFFFFFFu, other, lo));
+    }
+}
+
+template <int XT, bool T>
+__global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : 4) fp4_quant_kernel(Fp4Quant P) {
+    __shared__ __align__(16) uint32_t s_t[T ? 128 * 16 : 4];  // transposed codes, 64 B a column
+    __shared__ __align__(16) uint8_t s_rs[512];
+    __shared__ __align__(16) uint8_t s_cs[T ? 512 : 16];
+    constexpr int W = kWords8<XT>;
+    pdl_wait();
+    pdl_trigger();
+    if (P.skip && *P.skip != 0) return;
+    const int64_t tr = int64_t(blockIdx.x) / P.tiles_c, tc = int64_t(blockIdx.x) % P.tiles_c;
+    const int64_t r0 = tr * kTile, c0 = tc * kTile;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cl = lane & 7, rl = lane >> 3;
+    const int lr = 32 * (warp >> 1) + 8 * rl;  // first of the lane's 8 rows in the tile
+    const int lc = 64 * (warp & 1) + 8 * cl;   // first of its 8 columns
+    const int64_t row = r0 + lr, col = c0 + lc;
+    constexpr int esz = XT == kF32 ? 4 : 2;
+
+    uint4 raw[8][W];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int u = 0; u < W; ++u) raw[i][u] = make_uint4(0, 0, 0, 0);
+    if (P.vec) {
+        if (col < P.cols) {  // a row's length is a multiple of 8 here
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (row + i < P.rows) {
+                    const char *p = static_cast<const char *>(P.x) + ((row + i) * P.cols + col) * esz;
+#pragma unroll
+                    for (int u = 0; u < W; ++u) raw[i][u] = ld16(p + 16 * u);
+                }
+        }
+    } else {
+        const int n = int(min(int64_t(8), P.cols - col));
+        if (n > 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (row + i < P.rows) load_raw8_tail<XT>(P.x, (row + i) * P.cols + col, n, raw[i]);
+        }
+    }
+
+    // rmax[k]: fp32 bits of the maximum of row 2 (cl % 4) + k's block; cmax[k]:
+    // of column 2 rl + k's
+    uint32_t rmax[2], cmax[2] = {0, 0};
+    if constexpr (XT == kF32) {
+        uint32_t rw[8], cw[8];
+        auto op = [](uint32_t a, uint32_t b) { return max(a, b); };
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rw[i] = cw[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
+                                   raw[i][W - 1].x, raw[i][W - 1].y, raw[i][W - 1].z, raw[i][W - 1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t a = w[j] & 0x7FFFFFFFu;
+                rw[i] = max(rw[i], a);
+                if (T) cw[j] = max(cw[j], a);
+            }
+        }
+        transposing_max4<8>(rw, rmax, 2, 1, lane, op);
+        if (T) transposing_max4<8>(cw, cmax, 16, 8, lane, op);
+    } else {
+        // 16-bit magnitudes order like their values (NaN above inf): maxima on
+        // packed pairs
+        uint32_t m[8], rw[4], cw[4] = {0, 0, 0, 0}, r1[1], c1[1] = {0};
+        auto op = [](uint32_t a, uint32_t b) { return max_u16x2(a, b); };
+        auto widen = [](uint32_t h) { return __float_as_uint(lowp_to_f32<XT>(h & 0xFFFFu)) & 0x7FFFFFFFu; };
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w[4] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w};
+            m[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a = w[j] & 0x7FFF7FFFu;
+                m[i] = max_u16x2(m[i], a);
+                if (T) cw[j] = max_u16x2(cw[j], a);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            rw[i] = max_u16x2(__byte_perm(m[2 * i], m[2 * i + 1], 0x5410),
+                              __byte_perm(m[2 * i], m[2 * i + 1], 0x7632));
+        transposing_max4<4>(rw, r1, 2, 1, lane, op);
+        rmax[0] = widen(r1[0]);
+        rmax[1] = widen(r1[0] >> 16);
+        if (T) {
+            transposing_max4<4>(cw, c1, 16, 8, lane, op);
+            cmax[0] = widen(c1[0]);
+            cmax[1] = widen(c1[0] >> 16);
+        }
+    }
+
+    // ---- rows: scale bytes, codes
+    const uint32_t e0 = mx_scale_code<MxE2M1>(rmax[0]), e1 = mx_scale_code<MxE2M1>(rmax[1]);
+    {
+        // byte (r % 32) * 16 + r / 32 * 4 + block, rows lr + 2 (cl % 4) + {0, 1}
+        uint8_t *s = s_rs + (8 * rl + 2 * (cl & 3)) * 16 + (warp >> 1) * 4 + 2 * (warp & 1) + (cl >> 2);
+        s[0] = uint8_t(e0);
+        s[16] = uint8_t(e1);
+    }
+    const int64_t rowb = (P.cols + kMxBlock - 1) / kMxBlock * 16;  // bytes a packed row
+    const bool colin = col / 2 < rowb;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t e = __shfl_sync(0xFFFFFFFFu, e0 | (e1 << 16), (lane & ~3) + k);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = 2 * k + h;
+            const float f = mx_unscale(h ? e >> 16 : e & 0xFFFFu);
+            float y[8];
+            raw8_to_f32<XT>(raw[i], y);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) mul2_rn(y[j], y[j + 1], f, f, y[j], y[j + 1]);
+            const uint32_t w = f32x8_to_e2m1x8(y);
+            if (colin && row + i < P.rows)
+                *reinterpret_cast<uint32_t *>(P.out + (row + i) * rowb + col / 2) = w;
+        }
+    }
+
+    // ---- columns
+    if constexpr (T) {
+        const uint32_t d0 = mx_scale_code<MxE2M1>(cmax[0]), d1 = mx_scale_code<MxE2M1>(cmax[1]);
+        {
+            const int c = lc + 2 * rl;  // c and c + 1 are in the same group of 32 columns
+            uint8_t *s = s_cs + (c % 32) * 16 + (c / 32) * 4 + (warp >> 1);
+            s[0] = uint8_t(d0);
+            s[16] = uint8_t(d1);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t e = __shfl_sync(0xFFFFFFFFu, d0 | (d1 << 16), cl + 8 * k);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = 2 * k + h;
+                const float f = mx_unscale(h ? e >> 16 : e & 0xFFFFu);
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (XT == kF32) {
+                        const uint4 q = raw[i][j / 4];
+                        y[i] = __uint_as_float(j % 4 == 0 ? q.x : j % 4 == 1 ? q.y : j % 4 == 2 ? q.z : q.w);
+                    } else {
+                        const uint4 q = raw[i][0];
+                        const uint32_t w = j / 2 == 0 ? q.x : j / 2 == 1 ? q.y : j / 2 == 2 ? q.z : q.w;
+                        if constexpr (XT == kBF16)
+                            y[i] = __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
+                        else
+                            y[i] = f16_bits_to_f32(j & 1 ? w >> 16 : w & 0xFFFFu);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) mul2_rn(y[i], y[i + 1], f, f, y[i], y[i + 1]);
+                // column lc + j, row group lr / 8, 16-byte pieces permuted by cl
+                s_t[(lc + j) * 16 + ((lr / 8) ^ ((cl & 3) << 2))] = f32x8_to_e2m1x8(y);
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int64_t tile = tr * P.tiles_c + tc;
+        st16(P.scales + tile * 512 + 16 * threadIdx.x, reinterpret_cast<const uint4 *>(s_rs)[threadIdx.x]);
+    }
+    if constexpr (T) {
+        const int64_t tiles_r = (P.rows + kTile - 1) / kTile;
+        if (threadIdx.x >= 32 && threadIdx.x < 64) {
+            const int64_t tile = tc * tiles_r + tr;
+            st16(P.scales_t + tile * 512 + 16 * (threadIdx.x - 32),
+                 reinterpret_cast<const uint4 *>(s_cs)[threadIdx.x - 32]);
+        }
+        const int64_t rowb_t = (P.rows + kMxBlock - 1) / kMxBlock * 16;
+        const int q = threadIdx.x & 3;
+        const int64_t at = r0 / 2 + 16 * q;  // byte in the transposed row
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = (threadIdx.x >> 2) + 64 * k;
+            if (c0 + c < P.cols && at < rowb_t)
+                st16(P.out_t + (c0 + c) * rowb_t + at,
+                     *reinterpret_cast<const uint4 *>(&s_t[c * 16 + ((q ^ ((c >> 3) & 3)) << 2)]));
+        }
+    }
+}
+
+// ---- values of the codes -------------------------------------------------
+struct Fp4Dequant {
+    const uint8_t *q, *scales;
+    int64_t rows, cols, words;  // words: 8-element words a packed row
+    int64_t total;              // rows * words
+    void *out;
+    int vec;
+};
+
+// One packed word (8 elements) a thread.
+template <int XT>
+__global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(Fp4Dequant P) {
+    pdl_wait();
+    pdl_trigger();
+    for (int64_t t = int64_t(blockIdx.x) * kThreads + threadIdx.x; t < P.total;
+         t += int64_t(gridDim.x) * kThreads) {
+        const int64_t r = t / P.words;
+        const int64_t w = t - r * P.words;
+        const int64_t col = 8 * w;
+        const int n = int(min(int64_t(8), P.cols - col));
+        if (n <= 0) continue;
+        const int64_t b = w >> 2;
+        const int64_t tile = (r >> 7) * ((P.cols + kTile - 1) / kTile) + (b >> 2);
+        const uint32_t e = P.scales[tile * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3)];
+        const uint32_t codes = reinterpret_cast<const uint32_t *>(P.q)[t];
+        const float s = mx_scale(e);
+        float y[8];
+        e2m1x8_to_f32x8(codes, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(y[j], s);
+        const int64_t k = r * P.cols + col;
+        if (P.vec && n == 8) {
+            uint4 u[kWords8<XT>];
+            f32_to_raw8<XT>(y, u);
+#pragma unroll
+            for (int j = 0; j < kWords8<XT>; ++j)
+                st16(static_cast<char *>(P.out) + k * (XT == kF32 ? 4 : 2) + 16 * j, u[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) store_elem<XT>(P.out, k + j, y[j]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_quant(const void *x, int xelem, int64_t rows, int64_t cols, uint8_t *out,
+                             uint8_t *scales, uint8_t *out_t, uint8_t *scales_t,
+                             const int32_t *skip_if, cudaStream_t s) {
+    Fp4Quant P;
+    P.x = x;
+    P.rows = rows;
+    P.cols = cols;
+    P.out = out;
+    P.scales = scales;
+    P.out_t = out_t;
+    P.scales_t = scales_t;
+    P.skip = skip_if;
+    P.tiles_c = (cols + kTile - 1) / kTile;
+    const int esz = xelem == kF32 ? 4 : 2;
+    // whole groups of 8 elements: every group of 8 columns lies inside the row
+    P.vec = (cols % 8 == 0 && (cols * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0) ? 1 : 0;
+    const int64_t tiles = ((rows + kTile - 1) / kTile) * P.tiles_c;
+    const dim3 grid((unsigned)tiles), block(kThreads);
+    cudaError_t e;
+#define FP4_Q(XT)                                                                   \
+    e = out_t ? launch_pdl(fp4_quant_kernel<XT, true>, grid, block, 0, s, P)        \
+              : launch_pdl(fp4_quant_kernel<XT, false>, grid, block, 0, s, P)
+    if (xelem == kF32) FP4_Q(kF32);
+    else if (xelem == kF16) FP4_Q(kF16);
+    else FP4_Q(kBF16);
+#undef FP4_Q
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_fp4_dequant(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t cols,
+                               void *out, int oelem, int device, cudaStream_t s) {
+    Fp4Dequant P;
+    P.q = q;
+    P.scales = scales;
+    P.rows = rows;
+    P.cols = cols;
+    P.words = (cols + kMxBlock - 1) / kMxBlock * 4;
+    P.total = rows * P.words;
+    P.out = out;
+    const int esz = oelem == kF32 ? 4 : 2;
+    P.vec = ((cols * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) ? 1 : 0;
+    const int64_t want = (P.total + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)std::min<int64_t>(want, int64_t(sm_count(device)) * 64)), block(kThreads);
+    cudaError_t e;
+    if (oelem == kF32) e = launch_pdl(fp4_dequant_kernel<kF32>, grid, block, 0, s, P);
+    else if (oelem == kF16) e = launch_pdl(fp4_dequant_kernel<kF16>, grid, block, 0, s, P);
+    else e = launch_pdl(fp4_dequant_kernel<kBF16>, grid, block, 0, s, P);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace amp

@@ -146,4 +146,35 @@ cudaError_t launch_fp8_quant_list(const ListView &x, int64_t n_tiles, bool any_e
                                   const int32_t *sr_step = nullptr, uint64_t sr_seed = 0,
                                   bool use_slots = false);
 
+// ---- the operators of ampops.h (pointers that may be NULL are the optional
+// arguments of the entry points; sizes are checked there) ----
+cudaError_t launch_fp4_quant(const void *x, int xelem, int64_t rows, int64_t cols, uint8_t *out,
+                             uint8_t *scales, uint8_t *out_t, uint8_t *scales_t,
+                             const int32_t *skip_if, cudaStream_t s);
+cudaError_t launch_fp4_dequant(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t cols,
+                               void *out, int oelem, int device, cudaStream_t s);
+cudaError_t launch_fp4_product(const void *a, const uint8_t *sa, const void *b, const uint8_t *sb,
+                               int64_t m, int64_t n, int64_t k, void *out, int oelem, int device,
+                               cudaStream_t s);
+// Reads and clears the product's sticky error word (waits for the stream).
+cudaError_t fp4_error_take(int32_t *v, cudaStream_t s);
+
+cudaError_t launch_norm_fwd(const void *x, int xelem, int64_t rows, int64_t cols, const void *w,
+                            const void *b, int welem, float eps, void *y, float *mean, float *rstd,
+                            uint8_t *q, uint8_t *sc, cudaStream_t s);
+// Rows of the backward's partial sums (2 * cols floats each).
+int64_t norm_parts(int64_t rows, int64_t cols, int device);
+cudaError_t launch_norm_bwd(const void *dy, const void *x, int elem, const uint8_t *q,
+                            const uint8_t *sc, int64_t rows, int64_t cols, const void *w, int welem,
+                            const float *mean, const float *rstd, void *dx, void *dw, void *db,
+                            float *part, int device, cudaStream_t s);
+
+// act: an amp_act, or -1 for the checkpoint alone (y / dy unused).
+cudaError_t launch_act_fwd(int act, const void *x, const void *u, int elem, int64_t rows,
+                           int64_t cols, void *y, uint8_t *q, uint8_t *sc, uint8_t *qu, uint8_t *su,
+                           int device, cudaStream_t s);
+cudaError_t launch_act_bwd(int act, const void *dy, int elem, int64_t rows, int64_t cols,
+                           const uint8_t *q, const uint8_t *sc, const uint8_t *qu, const uint8_t *su,
+                           void *dx, void *du, int device, cudaStream_t s);
+
 }  // namespace amp

@@ -1,0 +1,117 @@
+// tcgen05.cuh - the fifth-generation tensor-core instructions that the 4-bit
+// product uses (PTX ISA, "TensorCore 5th generation"): tensor memory, the
+// descriptors of shared-memory operands, block-scaled products and the copies
+// of scales; and the tensor-map loads that feed them.
+#pragma once
+
+#include <cuda.h>
+
+#include "bulk_copy.cuh"
+
+namespace amp {
+
+// ---- tensor memory (512 columns x 128 lanes x 32 bits an SM) -------------
+template <int COLS>
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot) {  // one whole warp
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)),
+                 "n"(COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+template <int COLS>
+__device__ __forceinline__ void tmem_free(uint32_t base) {  // the warp that allocated
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(COLS) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 lanes x 16 columns of fp32: the calling warp's quarter of the lanes
+// (address bits 16 and up), lane l's columns in its v[].  The wait is part of
+// the statement, so nothing uses v[] before it.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr)
+        : "memory");
+}
+
+// ---- descriptors -----------------------------------------------------------
+// Shared-memory operand: address and strides in units of 16 bytes, bit 46 the
+// version, bits 61-63 the swizzle (0 none, 2 128 bytes).
+// Rows of 128 bytes (256 4-bit elements) as a 128-byte-swizzled tensor-map
+// load lays them out: groups of 8 rows, 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+    return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// A 512-byte scale tile: 32 rows of 16 bytes, groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+}
+// Instruction: e2m1 x e2m1 (bits 7, 10), N / 8 (17), E8M0 scales (23), M / 128
+// (27); which half of the four scale bytes a step of 64 uses (4, 29).
+__host__ __device__ constexpr uint32_t mxf4_instr(int m, int n) {
+    return (1u << 7) | (1u << 10) | (uint32_t(n / 8) << 17) | (1u << 23) | (uint32_t(m / 128) << 27);
+}
+__host__ __device__ constexpr uint32_t mxf4_half(int h) { return (uint32_t(2 * h) << 4) | (uint32_t(2 * h) << 29); }
+
+// D (+)= A B^T over 64 elements of the reduction, 2 scales a row of each.
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, uint32_t sa,
+                                         uint32_t sb, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(instr), "r"(sa), "r"(sb), "r"(uint32_t(add))
+        : "memory");
+}
+// A scale tile into 4 columns, repeated over the four quarters of the lanes.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// One arrival on the barrier when everything this thread issued has finished.
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_addr(bar))
+                 : "memory");
+}
+
+// ---- tensor-map loads ------------------------------------------------------
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *m, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_addr(dst)),
+        "l"(m), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *b) {
+    asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_addr(b)) : "memory");
+}
+
+// ---- clusters ----------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the float at this shared-memory address of CTA `rank` of the cluster
+__device__ __forceinline__ float cluster_ld(uint32_t saddr, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v)
+                 : "r"(saddr), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+}  // namespace amp
