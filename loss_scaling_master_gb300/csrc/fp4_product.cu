@@ -9,15 +9,21 @@
 // instruction (N = 16, 32, 64) instead of leaving lanes empty.
 //
 // Pipeline.  One warp's thread loads (tensor-map loads of 128 bytes = 256
-// elements a row, plain bulk copies of the scale tiles, whose layout is already
-// the one the copy to tensor memory takes), one issues the scale copies and the
-// products, four warps read finished accumulators and store.  Stages are handed
-// over with mbarriers.  CTAs stay and walk tiles.
+// elements a row; the scales come in the order that the copy to tensor memory
+// takes), one issues the scale copies and the products, the other warps read
+// finished accumulators and store.  Stages are handed over with mbarriers.
+// CTAs stay and walk tiles.
 //
-// Few tiles.  Where the tiles of C do not fill the GPU, the reduction axis is
-// cut over the CTAs of a cluster; each leaves its fp32 partial tile in shared
-// memory and the cluster's CTAs add them, rank by rank, from there (so the
-// order of the sum is fixed and nothing goes through global memory).
+// Many tiles: pairs of CTAs (cta_group::2) share 256 x 256 tiles.  Each loads
+// half of both operands and the products read the other half from the
+// neighbour, so a product of 256 x 256 x 64 costs each SM 8 KB of shared-memory
+// reads and 8 KB of fills instead of 12 and 12 for a tile of its own.
+//
+// Few tiles: one CTA a tile, and where the tiles do not fill the GPU the
+// reduction axis is cut over the CTAs of a cluster; each leaves its fp32
+// partial tile in shared memory and the cluster's CTAs add them, rank by rank,
+// from there (so the order of the sum is fixed and nothing goes through global
+// memory).
 //
 // Every wait gives up after a second of GPU time: the thread sets the error
 // word, the others see the CTA's flag, copies in flight are waited for, tensor
@@ -36,51 +42,294 @@ namespace {
 
 __device__ int32_t g_fp4_error;
 
-constexpr int kLanes = 128;        // rows of B a tile
-constexpr int kStageBytes = 128;   // bytes of a row a stage: 256 elements
-constexpr int kProductThreads = 256;
+constexpr int kLanes = 128;       // rows of B a CTA
+constexpr int kStageBytes = 128;  // bytes of a row a stage: 256 elements
 
 struct Fp4Product {
     const uint8_t *sa, *sb;  // scale tiles of A and B
     void *out;
     int64_t m, n;
-    int ot;             // ElemType of out
-    int kt;             // scale tiles (128 elements) along the reduction
-    int k64;            // products of 64 along the reduction
+    int ot;      // ElemType of out
+    int packed;  // 16-bit out with even rows and 4-byte alignment: two elements a store
+    int kt;      // scale tiles (128 elements) along the reduction
+    int k64;     // products of 64 along the reduction
     int tiles_m, tiles_n;
 };
 
-template <int BN>
-struct Shape {
-    static constexpr int tok_tiles = BN > 128 ? BN / 128 : 1;  // scale tiles along the tokens
-    static constexpr int w_bytes = kLanes * kStageBytes;
-    static constexpr int t_bytes = BN * kStageBytes;
-    static constexpr int t_room = (t_bytes + 1023) / 1024 * 1024;
-    static constexpr int stage = w_bytes + t_room + 1024 + 1024 * tok_tiles;
-    static constexpr int stages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-    static constexpr int acc_bufs = BN == 256 ? 1 : 2;
-    static constexpr int sf_cols = 8 + 8 * tok_tiles;  // columns of a stage's scales
-    static constexpr int sf_base = BN * acc_bufs < 32 ? 32 : BN * acc_bufs;
-    static constexpr int tmem_cols = sf_base + stages * sf_cols > 256 ? 512 : 256;
-    static_assert(sf_base + stages * sf_cols <= 512, "tensor memory");
-    static constexpr int smem = stages * stage + 1024;  // and the alignment to 1024
-};
-
-template <int OT>
-__device__ __forceinline__ void store_chunk(const Fp4Product &P, int64_t m0, int64_t nn, int cols,
-                                            const float *v) {
-    if (nn >= P.n) return;
-#pragma unroll
-    for (int c = 0; c < 16; ++c)
-        if (c < cols) store_elem<OT>(P.out, (m0 + c) * P.n + nn, v[c]);
+// tile -> (token tile, output tile): `side` output tiles side by side, so the
+// CTAs that run together share operands in L2
+__device__ __forceinline__ void tile_at(const Fp4Product &P, int side, int tile, int &tm, int &tn) {
+    const int per = side * P.tiles_m, g = tile / per, in = tile - g * per;
+    const int w = min(side, P.tiles_n - side * g);
+    tm = in / w;
+    tn = side * g + in % w;
 }
 
+// The 16-bit results of one lane (column nn of C) for CNT tokens from m0, of
+// which `rows` are in C; p[i]: tokens 2 i and 2 i + 1.  Packed: neighbouring
+// lanes swap halves, so each stores two neighbouring elements of one row.
+template <int CNT>
+__device__ __forceinline__ void store16(const Fp4Product &P, int64_t m0, int rows, int64_t nn,
+                                        const uint32_t (&p)[CNT / 2]) {
+    uint16_t *out = static_cast<uint16_t *>(P.out);
+    if (P.packed) {
+        const int odd = threadIdx.x & 1;
+        char *at = reinterpret_cast<char *>(out + (m0 + odd) * P.n + (nn - odd));
+        const int64_t step = 4 * P.n;
+#pragma unroll
+        for (int i = 0; i < CNT / 2; ++i) {
+            const uint32_t r = __shfl_xor_sync(0xFFFFFFFFu, p[i], 1);
+            const uint32_t v = odd ? __byte_perm(r, p[i], 0x7632) : __byte_perm(p[i], r, 0x5410);
+            if (nn < P.n && 2 * i + odd < rows) *reinterpret_cast<uint32_t *>(at) = v;
+            at += step;
+        }
+    } else if (nn < P.n) {
+        uint16_t *at = out + m0 * P.n + nn;
+#pragma unroll
+        for (int i = 0; i < CNT / 2; ++i) {
+            if (2 * i < rows) *at = uint16_t(p[i]);
+            at += P.n;
+            if (2 * i + 1 < rows) *at = uint16_t(p[i] >> 16);
+            at += P.n;
+        }
+    }
+}
+template <int CNT>
+__device__ __forceinline__ void store32(const Fp4Product &P, int64_t m0, int rows, int64_t nn,
+                                        const uint32_t (&v)[CNT]) {
+    if (nn >= P.n) return;
+    float *at = static_cast<float *>(P.out) + m0 * P.n + nn;
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) {
+        if (i < rows) *at = __uint_as_float(v[i]);
+        at += P.n;
+    }
+}
+template <int OT, int CNT>
+__device__ __forceinline__ void pack16(const uint32_t (&v)[CNT], uint32_t *p) {
+#pragma unroll
+    for (int i = 0; i < CNT / 2; ++i)
+        p[i] = f32x2_to_16x2<OT>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+}
+
+// ------------------------------------------------------------------ a pair of CTAs a tile
+constexpr int kPairThreads = 384;  // load, issue, allocate, (idle), 8 store warps
+struct Pair {
+    static constexpr int w_bytes = kLanes * kStageBytes;  // this CTA's half of the tile's rows of B
+    static constexpr int t_bytes = 128 * kStageBytes;     // and of its rows of A
+    static constexpr int loads = w_bytes + t_bytes + 1024 + 2048;
+    static constexpr int stage = loads;
+    static constexpr int stages = 6;
+    static constexpr int sf_base = 256, sf_cols = 8 + 16;  // columns of a stage's scales
+    static constexpr int smem = stages * stage + 1024;
+    static_assert(sf_base + stages * sf_cols <= 512, "tensor memory");
+};
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+    fp4_product_pair_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
+                            const __grid_constant__ CUtensorMap map_st,
+                            const __grid_constant__ CUtensorMap map_sw, Fp4Product P) {
+    using S = Pair;
+    constexpr int NS = S::stages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[NS], empty[NS], acc_full, acc_empty, drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_fail;
+    uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], 1);   // the first CTA's: its arrival, and the bytes of both
+            mbar_init(&empty[i], 1);  // both: the products' commit
+        }
+        mbar_init(&acc_full, 1);
+        mbar_init(&acc_empty, 16);  // the first CTA's: the 8 store warps of both
+        mbar_init(&drain, 1);
+        s_fail = 0;
+        mbar_fence_init();
+        tma_prefetch_map(&map_t);
+        tma_prefetch_map(&map_w);
+        tma_prefetch_map(&map_st);
+        tma_prefetch_map(&map_sw);
+    }
+    if (warp == 2) tmem_alloc<2, 512>(&s_tmem);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the barriers exist in both CTAs
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    pdl_wait();
+    pdl_trigger();
+
+    const int tiles = P.tiles_m * P.tiles_n;
+    const int first = int(blockIdx.x >> 1), stride = int(gridDim.x >> 1);
+    const int ks_all = (P.kt + 1) / 2;
+    auto give_up = [&]() {
+        s_fail = 1;
+        g_fp4_error = 1;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int st = 0, issued = 0;
+            uint32_t ph = 0;
+            for (int tile = first; tile < tiles && !s_fail; tile += stride) {
+                int tm, tn;
+                tile_at(P, 8, tile, tm, tn);
+                for (int ks = 0; ks < ks_all && !s_fail; ++ks) {
+                    if (!cluster_mbar_wait(&empty[st], ph ^ 1)) {
+                        give_up();
+                        break;
+                    }
+                    uint8_t *b = smem + st * S::stage;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * S::loads);
+                    const uint32_t bar = cluster_addr(&full[st], 0);
+                    const int x = ks * kStageBytes;
+                    tma_load_2d_pair(b, &map_w, x, tn * 256 + int(rank) * 128, bar);
+                    tma_load_2d_pair(b + S::w_bytes, &map_t, x, tm * 256 + int(rank) * 128, bar);
+                    uint8_t *sf = b + S::w_bytes + S::t_bytes;
+                    tma_load_2d_pair(sf, &map_sw, ks * 256, tn * 2 + int(rank), bar);
+                    tma_load_2d_pair(sf + 1024, &map_st, ks * 256, tm * 2, bar);
+                    ++issued;
+                    if (++st == NS) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (s_fail && rank == 0) {  // wait for the copies still in flight
+                for (int i = 0; i < min(issued, NS); ++i) {
+                    st = st == 0 ? NS - 1 : st - 1;
+                    if (st == NS - 1) ph ^= 1;
+                    cluster_mbar_wait(&full[st], ph);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int st = 0;
+            uint32_t ph = 0, aph = 0;
+            constexpr uint32_t instr = mxf4_instr(256, 256);
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok && !s_fail; tile += stride) {
+                ok = cluster_mbar_wait(&acc_empty, aph ^ 1);
+                tc_fence_after();
+                for (int ks = 0; ks < ks_all && ok; ++ks) {
+                    ok = cluster_mbar_wait(&full[st], ph);
+                    if (!ok || s_fail) break;
+                    tc_fence_after();
+                    const uint32_t b = smem_addr(smem + st * S::stage);
+                    const uint32_t sf = b + S::w_bytes + S::t_bytes;
+                    const uint32_t tw = tmem + S::sf_base + st * S::sf_cols, tt = tw + 8;
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        copy_scales<2>(tw + 4 * a, scale_desc(sf + 512 * a));
+                        copy_scales<2>(tt + 8 * a, scale_desc(sf + 1024 + 512 * a));
+                        copy_scales<2>(tt + 8 * a + 4, scale_desc(sf + 2048 + 512 * a));
+                    }
+                    const uint64_t dw = operand_desc(b), dt = operand_desc(b + S::w_bytes);
+                    const int nj = min(4, P.k64 - 4 * ks);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < nj)
+                            mma_mxf4<2>(tmem, dw + 2 * j, dt + 2 * j, instr | mxf4_half(j & 1), tw + 4 * (j / 2),
+                                        tt + 8 * (j / 2), ks > 0 || j > 0);
+                    tc_commit_pair(&empty[st]);
+                    if (++st == NS) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+                tc_commit_pair(&acc_full);
+                aph ^= 1;
+            }
+            if (!ok) give_up();
+            if (s_fail) {  // wait for the products still in flight
+                tc_commit_pair(&drain);
+                cluster_mbar_wait(&drain, 0);
+            }
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t acc = tmem + 128 * half + (uint32_t(32 * quarter) << 16);
+        const uint32_t done = cluster_addr(&acc_empty, 0);
+        uint32_t aph = 0;
+        for (int tile = first; tile < tiles; tile += stride) {
+            int tm, tn;
+            tile_at(P, 8, tile, tm, tn);
+            const bool ok = cluster_mbar_wait(&acc_full, aph);
+            if (!__all_sync(0xFFFFFFFFu, ok && !s_fail)) {
+                if (!ok) give_up();
+                break;
+            }
+            aph ^= 1;
+            tc_fence_after();
+            const int64_t nn = int64_t(tn) * 256 + rank * 128 + 32 * quarter + lane;
+            const int64_t m0 = int64_t(tm) * 256 + 128 * half;
+            const int rows = int(max(int64_t(0), min(int64_t(128), P.m - m0)));
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) cluster_arrive(done);
+            };
+            if (P.ot == kF32) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld<32>(acc + c, v);
+                    if (c == 96) release();
+                    store32<32>(P, m0 + c, rows - c, nn, v);
+                }
+            } else {
+                // into registers, so the accumulators are free for the next
+                // tile's products while this one is stored
+                uint32_t p[64];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[64];
+                    tmem_ld<64>(acc + 64 * h, v);
+                    if (P.ot == kF16) pack16<kF16>(v, p + 32 * h);
+                    else pack16<kBF16>(v, p + 32 * h);
+                }
+                release();
+                store16<128>(P, m0, rows, nn, p);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // nobody leaves while the other's barriers or memory are in use
+    tc_fence_after();
+    if (warp == 2) tmem_free<2, 512>(tmem);
+}
+
+// ------------------------------------------------------------------ one CTA a tile
+constexpr int kSoloThreads = 256;  // load, issue, allocate, (idle), 4 store warps
+
+template <int BN>
+struct Solo {
+    static constexpr int w_bytes = kLanes * kStageBytes;
+    static constexpr int t_bytes = BN * kStageBytes;
+    static constexpr int stage = w_bytes + t_bytes + 2048;  // and 1 KB of scales of each operand
+    static constexpr int stages = BN == 128 ? 6 : BN == 64 ? 4 : 5;
+    static constexpr int ctas = BN == 128 ? 1 : 2;  // CTAs an SM holds
+    static constexpr int sf_base = 2 * BN;          // two accumulators
+    static constexpr int sf_cols = 16;
+    static constexpr int tmem_cols = BN == 128 ? 512 : 256;
+    static_assert(sf_base + stages * sf_cols <= tmem_cols, "tensor memory");
+    static constexpr int smem = stages * stage + 1024;  // and the alignment to 1024
+    static_assert(BN * kLanes * 4 <= stages * stage, "the partial tile");
+};
+
 template <int BN, bool SPLIT>
-__global__ void __launch_bounds__(kProductThreads, 1)
+__global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
     fp4_product_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
                        Fp4Product P) {
-    using S = Shape<BN>;
-    constexpr int NS = S::stages, NA = S::acc_bufs;
+    using S = Solo<BN>;
+    constexpr int NS = S::stages, NA = 2;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], acc_full[NA], acc_empty[NA], drain;
     __shared__ uint32_t s_tmem;
@@ -103,7 +352,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tma_prefetch_map(&map_t);
         tma_prefetch_map(&map_w);
     }
-    if (warp == 2) tmem_alloc<S::tmem_cols>(&s_tmem);
+    if (warp == 2) tmem_alloc<1, S::tmem_cols>(&s_tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -120,14 +369,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const int first = SPLIT ? int(blockIdx.x / parts) : int(blockIdx.x);
     const int ks_all = (P.kt + 1) / 2;
     const int ks0 = int(int64_t(ks_all) * rank / parts), ks1 = int(int64_t(ks_all) * (rank + 1) / parts);
-    // tile -> (token tile, output tile): 16 output tiles side by side, so the
-    // CTAs that run together share operands in L2
-    auto where = [&](int tile, int &tm, int &tn) {
-        const int per = 16 * P.tiles_m, g = tile / per, in = tile - g * per;
-        const int w = min(16, P.tiles_n - 16 * g);
-        tm = in / w;
-        tn = 16 * g + in % w;
-    };
     auto give_up = [&]() {
         s_fail = 1;
         g_fp4_error = 1;
@@ -135,35 +376,29 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            int st = 0;
+            int st = 0, issued = 0;
             uint32_t ph = 0;
-            int issued = 0;
             for (int tile = first; tile < tiles && !s_fail; tile += stride) {
                 int tm, tn;
-                where(tile, tm, tn);
-                for (int ks = ks0; ks < ks1; ++ks) {
+                tile_at(P, 16, tile, tm, tn);
+                for (int ks = ks0; ks < ks1 && !s_fail; ++ks) {
                     if (!mbar_wait(&empty[st], ph ^ 1)) {
                         give_up();
                         break;
                     }
                     uint8_t *b = smem + st * S::stage;
-                    const int na = min(2, P.kt - 2 * ks);
-                    const int tt = BN > 128 ? min(S::tok_tiles, int((P.m + 127) / 128) - tm * S::tok_tiles) : 1;
-                    mbar_arrive_expect_tx(&full[st], S::w_bytes + S::t_bytes + uint32_t(na) * 512u * uint32_t(1 + tt));
+                    const int sfb = min(2, P.kt - 2 * ks) * 512;
+                    mbar_arrive_expect_tx(&full[st], S::w_bytes + S::t_bytes + 2 * sfb);
                     tma_load_2d(b, &map_w, ks * kStageBytes, tn * kLanes, &full[st]);
                     tma_load_2d(b + S::w_bytes, &map_t, ks * kStageBytes, tm * BN, &full[st]);
-                    uint8_t *sf = b + S::w_bytes + S::t_room;
-                    bulk_g2s(sf, P.sb + (int64_t(tn) * P.kt + 2 * ks) * 512, na * 512, &full[st]);
-                    for (int h = 0; h < tt; ++h)
-                        bulk_g2s(sf + 1024 + 1024 * h,
-                                 P.sa + ((int64_t(tm) * S::tok_tiles + h) * P.kt + 2 * ks) * 512, na * 512,
-                                 &full[st]);
+                    uint8_t *sf = b + S::w_bytes + S::t_bytes;
+                    bulk_g2s(sf, P.sb + (int64_t(tn) * P.kt + 2 * ks) * 512, sfb, &full[st]);
+                    bulk_g2s(sf + 1024, P.sa + (int64_t(tm) * P.kt + 2 * ks) * 512, sfb, &full[st]);
                     ++issued;
                     if (++st == NS) {
                         st = 0;
                         ph ^= 1;
                     }
-                    if (s_fail) break;
                 }
             }
             if (s_fail) {  // wait for the copies still in flight
@@ -189,22 +424,20 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     if (!ok || s_fail) break;
                     tc_fence_after();
                     const uint32_t b = smem_addr(smem + st * S::stage);
-                    const uint32_t sf = b + S::w_bytes + S::t_room;
+                    const uint32_t sf = b + S::w_bytes + S::t_bytes;
                     const uint32_t tw = tmem + S::sf_base + st * S::sf_cols, tt = tw + 8;
                     const int na = min(2, P.kt - 2 * ks);
                     for (int a = 0; a < na; ++a) {
-                        copy_scales(tw + 4 * a, scale_desc(sf + 512 * a));
-#pragma unroll
-                        for (int h = 0; h < S::tok_tiles; ++h)
-                            copy_scales(tt + 4 * (a * S::tok_tiles + h), scale_desc(sf + 1024 + 1024 * h + 512 * a));
+                        copy_scales<1>(tw + 4 * a, scale_desc(sf + 512 * a));
+                        copy_scales<1>(tt + 4 * a, scale_desc(sf + 1024 + 512 * a));
                     }
                     const uint64_t dw = operand_desc(b), dt = operand_desc(b + S::w_bytes);
                     const int nj = min(4, P.k64 - 4 * ks);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (j < nj)
-                            mma_mxf4(acc, dw + 2 * j, dt + 2 * j, instr | mxf4_half(j & 1), tw + 4 * (j / 2),
-                                     tt + 4 * (j / 2) * S::tok_tiles, ks > ks0 || j > 0);
+                            mma_mxf4<1>(acc, dw + 2 * j, dt + 2 * j, instr | mxf4_half(j & 1), tw + 4 * (j / 2),
+                                        tt + 4 * (j / 2), ks > ks0 || j > 0);
                     tc_commit(&empty[st]);
                     if (++st == NS) {
                         st = 0;
@@ -225,12 +458,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
     } else if (warp >= 4) {
         const int quarter = warp & 3;
+        constexpr int CH = BN < 32 ? BN : 32;  // columns at a time
         int ab = 0;
         uint32_t aph = 0;
         for (int tile = first; tile < tiles; tile += stride) {
             int tm, tn;
-            where(tile, tm, tn);
-            bool ok = mbar_wait(&acc_full[ab], aph);
+            tile_at(P, 16, tile, tm, tn);
+            const bool ok = mbar_wait(&acc_full[ab], aph);
             if (!__all_sync(0xFFFFFFFFu, ok && !s_fail)) {
                 if (!ok) give_up();
                 break;
@@ -238,27 +472,25 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             tc_fence_after();
             const uint32_t acc = tmem + ab * BN + (uint32_t(32 * quarter) << 16);
             const int64_t nn = int64_t(tn) * kLanes + 32 * quarter + lane, m0 = int64_t(tm) * BN;
-            const int cols = int(min(int64_t(BN), P.m - m0));
+            const int rows = int(min(int64_t(BN), P.m - m0));
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 16) {
-                if (c >= cols) break;
-                uint32_t v[16];
-                tmem_ld16(acc + c, v);
-                float f[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+            for (int c = 0; c < rows; c += CH) {
+                uint32_t v[CH];
+                tmem_ld<CH>(acc + c, v);
                 if (SPLIT) {
                     // partial tile [column][lane] over the stages' buffers: every
                     // product of this CTA has finished reading them
                     float *part = reinterpret_cast<float *>(smem);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) part[(c + i) * kLanes + 32 * quarter + lane] = f[i];
+                    for (int i = 0; i < CH; ++i)
+                        part[(c + i) * kLanes + 32 * quarter + lane] = __uint_as_float(v[i]);
                 } else if (P.ot == kF32) {
-                    store_chunk<kF32>(P, m0 + c, nn, cols - c, f);
-                } else if (P.ot == kF16) {
-                    store_chunk<kF16>(P, m0 + c, nn, cols - c, f);
+                    store32<CH>(P, m0 + c, rows - c, nn, v);
                 } else {
-                    store_chunk<kBF16>(P, m0 + c, nn, cols - c, f);
+                    uint32_t p[CH / 2];
+                    if (P.ot == kF16) pack16<kF16>(v, p);
+                    else pack16<kBF16>(v, p);
+                    store16<CH>(P, m0 + c, rows - c, nn, p);
                 }
             }
             tc_fence_before();
@@ -274,7 +506,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         __syncwarp();
         cluster_sync();  // every CTA's partial tile is written
         int tm, tn;
-        where(first, tm, tn);
+        tile_at(P, 16, first, tm, tn);
         const int64_t m0 = int64_t(tm) * BN;
         const int cols = int(min(int64_t(BN), P.m - m0));
         const uint32_t part = smem_addr(smem);
@@ -293,10 +525,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
         cluster_sync();  // nobody leaves while its shared memory is read
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 2) tmem_free<S::tmem_cols>(tmem);
+    if (warp == 2) tmem_free<1, S::tmem_cols>(tmem);
 }
 
 // C = 0 for an empty reduction.
@@ -321,50 +554,85 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// Packed rows [rows, row_bytes], boxes of box_rows x 128 bytes, swizzled over
-// 128 bytes; what lies outside reads as zero.
-cudaError_t make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t row_bytes, int box_rows) {
+// [rows, row_elems] of es-byte elements, boxes of box_rows x box_elems; what
+// lies outside reads as zero.
+cudaError_t make_map(CUtensorMap *m, CUtensorMapDataType type, int es, const void *base, int64_t rows,
+                     int64_t row_elems, int box_elems, int box_rows, CUtensorMapSwizzle swizzle) {
     const auto enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {cuuint64_t(row_bytes), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(row_bytes)};
-    const cuuint32_t box[2] = {kStageBytes, cuuint32_t(box_rows)}, es[2] = {1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t dims[2] = {cuuint64_t(row_elems), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(row_elems * es)};
+    const cuuint32_t box[2] = {cuuint32_t(box_elems), cuuint32_t(box_rows)}, one[2] = {1, 1};
+    const CUresult r = enc(m, type, 2, const_cast<void *>(base), dims, strides, box, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+// Packed rows, 128 bytes wide boxes, swizzled over 128 bytes.
+cudaError_t rows_map(CUtensorMap *m, const void *base, int64_t rows, int64_t row_bytes, int box_rows) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, row_bytes, kStageBytes, box_rows,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Scale tiles: a row of kt tiles of 128 words; boxes of two tiles.
+cudaError_t scales_map(CUtensorMap *m, const void *base, int64_t tile_rows, int kt, int box_rows) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, base, tile_rows, int64_t(kt) * 128, 256, box_rows,
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
+}
 
-template <int BN>
-cudaError_t go(Fp4Product P, const void *a, const void *b, int64_t row_bytes, int device, cudaStream_t s) {
-    using S = Shape<BN>;
-    CUtensorMap mt, mw;
-    cudaError_t e = make_map(&mt, a, P.m, row_bytes, BN);
-    if (e == cudaSuccess) e = make_map(&mw, b, P.n, row_bytes, kLanes);
-    if (e != cudaSuccess) return e;
-    P.tiles_m = int((P.m + BN - 1) / BN);
-    P.tiles_n = int((P.n + kLanes - 1) / kLanes);
-    const int64_t tiles = int64_t(P.tiles_m) * P.tiles_n;
-    const int sms = sm_count(device), ks = (P.kt + 1) / 2;
-    int parts = 1;
-    while (parts < 8 && tiles * parts * 2 <= sms && parts * 2 <= ks) parts *= 2;
-    auto *kernel = parts > 1 ? &fp4_product_kernel<BN, true> : &fp4_product_kernel<BN, false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
+cudaError_t launch(const void *kernel, unsigned grid, int threads, int smem, int cluster, cudaStream_t s,
+                   void **args) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(parts > 1 ? tiles * parts : std::min<int64_t>(tiles, sms)));
-    cfg.blockDim = dim3(kProductThreads);
-    cfg.dynamicSmemBytes = S::smem;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = unsigned(parts);
+    at[1].val.clusterDim.x = unsigned(cluster);
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = parts > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, mt, mw, P);
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+cudaError_t go_pair(Fp4Product P, const void *a, const void *b, int64_t row_bytes, int device, cudaStream_t s) {
+    CUtensorMap mt, mw, mst, msw;
+    cudaError_t e = rows_map(&mt, a, P.m, row_bytes, 128);
+    if (e == cudaSuccess) e = rows_map(&mw, b, P.n, row_bytes, 128);
+    if (e == cudaSuccess) e = scales_map(&mst, P.sa, (P.m + 127) / 128, P.kt, 2);
+    if (e == cudaSuccess) e = scales_map(&msw, P.sb, (P.n + 127) / 128, P.kt, 1);
+    if (e != cudaSuccess) return e;
+    P.tiles_m = int((P.m + 255) / 256);
+    P.tiles_n = int((P.n + 255) / 256);
+    const int64_t tiles = int64_t(P.tiles_m) * P.tiles_n;
+    void *args[] = {&mt, &mw, &mst, &msw, &P};
+    return launch(reinterpret_cast<const void *>(&fp4_product_pair_kernel),
+                  unsigned(2 * std::min<int64_t>(tiles, sm_count(device) / 2)), kPairThreads, Pair::smem, 2, s, args);
+}
+
+template <int BN>
+cudaError_t go(Fp4Product P, const void *a, const void *b, int64_t row_bytes, int device, cudaStream_t s) {
+    using S = Solo<BN>;
+    CUtensorMap mt, mw;
+    cudaError_t e = rows_map(&mt, a, P.m, row_bytes, BN);
+    if (e == cudaSuccess) e = rows_map(&mw, b, P.n, row_bytes, kLanes);
+    if (e != cudaSuccess) return e;
+    P.tiles_m = int((P.m + BN - 1) / BN);
+    P.tiles_n = int((P.n + kLanes - 1) / kLanes);
+    const int64_t tiles = int64_t(P.tiles_m) * P.tiles_n, room = int64_t(sm_count(device)) * S::ctas;
+    const int ks = (P.kt + 1) / 2;
+    int parts = 1;
+    while (parts < 8 && tiles * parts * 2 <= room && parts * 2 <= ks) parts *= 2;
+    void *args[] = {&mt, &mw, &P};
+    if (parts > 1)
+        return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, true>), unsigned(tiles * parts),
+                      kSoloThreads, S::smem, parts, s, args);
+    return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, false>),
+                  unsigned(std::min<int64_t>(tiles, room)), kSoloThreads, S::smem, 1, s, args);
 }
 
 }  // namespace
@@ -386,14 +654,16 @@ cudaError_t launch_fp4_product(const void *a, const uint8_t *sa, const void *b, 
     P.m = m;
     P.n = n;
     P.ot = oelem;
+    P.packed = n % 2 == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
     P.kt = int((k + 127) / 128);
     P.k64 = int((k + 63) / 64);
     const int64_t row_bytes = (k + kMxBlock - 1) / kMxBlock * 16;
+    const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
     if (m <= 16) e = go<16>(P, a, b, row_bytes, device, s);
     else if (m <= 32) e = go<32>(P, a, b, row_bytes, device, s);
     else if (m <= 64) e = go<64>(P, a, b, row_bytes, device, s);
-    else if (m <= 128 || ((m + 255) / 256) * ((n + 127) / 128) < sm_count(device)) e = go<128>(P, a, b, row_bytes, device, s);
-    else e = go<256>(P, a, b, row_bytes, device, s);
+    else if (m <= 128 || pair_tiles * 2 < sm_count(device)) e = go<128>(P, a, b, row_bytes, device, s);
+    else e = go_pair(P, a, b, row_bytes, device, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
