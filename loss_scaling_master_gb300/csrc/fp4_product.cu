@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_fail;
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
 
     if (threadIdx.x == 0) {
@@ -172,17 +172,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int st = 0, issued = 0;
-            uint32_t ph = 0;
-            for (int tile = first; tile < tiles && !s_fail; tile += stride) {
-                int tm, tn;
-                tile_at(P, 8, tile, tm, tn);
-                for (int ks = 0; ks < ks_all && !s_fail; ++ks) {
-                    if (!cluster_mbar_wait(&empty[st], ph ^ 1)) {
-                        give_up();
-                        break;
-                    }
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += stride) {
+            int tm, tn;
+            tile_at(P, 8, tile, tm, tn);
+            for (int ks = 0; ks < ks_all; ++ks) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ph ^ 1));
+                if (!ok) break;
+                if (elect_one()) {
                     uint8_t *b = smem + st * S::stage;
                     if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * S::loads);
                     const uint32_t bar = cluster_addr(&full[st], 0);
@@ -192,63 +191,70 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     uint8_t *sf = b + S::w_bytes + S::t_bytes;
                     tma_load_2d_pair(sf, &map_sw, ks * 256, tn * 2 + int(rank), bar);
                     tma_load_2d_pair(sf + 1024, &map_st, ks * 256, tm * 2, bar);
-                    ++issued;
-                    if (++st == NS) {
-                        st = 0;
-                        ph ^= 1;
-                    }
                 }
-            }
-            if (s_fail && rank == 0) {  // wait for the copies still in flight
-                for (int i = 0; i < min(issued, NS); ++i) {
-                    st = st == 0 ? NS - 1 : st - 1;
-                    if (st == NS - 1) ph ^= 1;
-                    cluster_mbar_wait(&full[st], ph);
+                __syncwarp();
+                ++issued;
+                if (++st == NS) {
+                    st = 0;
+                    ph ^= 1;
                 }
             }
         }
+        if (!ok) give_up();
+        if (!ok && rank == 0) {  // wait for the copies still in flight
+            for (int i = 0; i < min(issued, NS); ++i) {
+                st = st == 0 ? NS - 1 : st - 1;
+                if (st == NS - 1) ph ^= 1;
+                mbar_wait(&full[st], ph);
+            }
+        }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int st = 0;
             uint32_t ph = 0, aph = 0;
             constexpr uint32_t instr = mxf4_instr(256, 256);
             bool ok = true;
-            for (int tile = first; tile < tiles && ok && !s_fail; tile += stride) {
-                ok = cluster_mbar_wait(&acc_empty, aph ^ 1);
+            for (int tile = first; tile < tiles && ok; tile += stride) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_empty, aph ^ 1));
                 tc_fence_after();
                 for (int ks = 0; ks < ks_all && ok; ++ks) {
-                    ok = cluster_mbar_wait(&full[st], ph);
-                    if (!ok || s_fail) break;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st], ph));
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t b = smem_addr(smem + st * S::stage);
+                    const uint32_t b = smem_addr(smem) + st * S::stage;
                     const uint32_t sf = b + S::w_bytes + S::t_bytes;
                     const uint32_t tw = tmem + S::sf_base + st * S::sf_cols, tt = tw + 8;
-#pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        copy_scales<2>(tw + 4 * a, scale_desc(sf + 512 * a));
-                        copy_scales<2>(tt + 8 * a, scale_desc(sf + 1024 + 512 * a));
-                        copy_scales<2>(tt + 8 * a + 4, scale_desc(sf + 2048 + 512 * a));
-                    }
-                    const uint64_t dw = operand_desc(b), dt = operand_desc(b + S::w_bytes);
+                    const uint64_t ds = scale_desc(sf), dw = operand_desc(b), dt = operand_desc(b + S::w_bytes);
                     const int nj = min(4, P.k64 - 4 * ks);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (j < nj)
-                            mma_mxf4<2>(tmem, dw + 2 * j, dt + 2 * j, instr | mxf4_half(j & 1), tw + 4 * (j / 2),
-                                        tt + 8 * (j / 2), ks > 0 || j > 0);
-                    tc_commit_pair(&empty[st]);
+                        for (int a = 0; a < 2; ++a) {
+                            copy_scales<2>(tw + 4 * a, ds + 32 * a);  // 512 bytes on
+                            copy_scales<2>(tt + 8 * a, ds + 64 + 32 * a);
+                            copy_scales<2>(tt + 8 * a + 4, ds + 128 + 32 * a);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < nj)
+                                mma_mxf4<2>(tmem, dw + 2 * j, dt + 2 * j, instr | mxf4_half(j & 1), tw + 4 * (j / 2),
+                                            tt + 8 * (j / 2), ks > 0 || j > 0);
+                        tc_commit_pair(&empty[st]);
+                    }
+                    __syncwarp();
                     if (++st == NS) {
                         st = 0;
                         ph ^= 1;
                     }
                 }
-                tc_commit_pair(&acc_full);
+                if (elect_one()) tc_commit_pair(&acc_full);
+                __syncwarp();
                 aph ^= 1;
             }
-            if (!ok) give_up();
-            if (s_fail) {  // wait for the products still in flight
-                tc_commit_pair(&drain);
-                cluster_mbar_wait(&drain, 0);
+            if (!ok) {  // wait for the products still in flight
+                give_up();
+                if (elect_one()) tc_commit_pair(&drain);
+                __syncwarp();
+                mbar_wait(&drain, 0);
             }
         }
     } else if (warp >= 4) {
@@ -259,7 +265,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int tile = first; tile < tiles; tile += stride) {
             int tm, tn;
             tile_at(P, 8, tile, tm, tn);
-            const bool ok = cluster_mbar_wait(&acc_full, aph);
+            const bool ok = mbar_wait(&acc_full, aph);
             if (!__all_sync(0xFFFFFFFFu, ok && !s_fail)) {
                 if (!ok) give_up();
                 break;
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_fail;
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -375,17 +381,16 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int st = 0, issued = 0;
-            uint32_t ph = 0;
-            for (int tile = first; tile < tiles && !s_fail; tile += stride) {
-                int tm, tn;
-                tile_at(P, 16, tile, tm, tn);
-                for (int ks = ks0; ks < ks1 && !s_fail; ++ks) {
-                    if (!mbar_wait(&empty[st], ph ^ 1)) {
-                        give_up();
-                        break;
-                    }
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += stride) {
+            int tm, tn;
+            tile_at(P, 16, tile, tm, tn);
+            for (int ks = ks0; ks < ks1; ++ks) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ph ^ 1));
+                if (!ok) break;
+                if (elect_one()) {
                     uint8_t *b = smem + st * S::stage;
                     const int sfb = min(2, P.kt - 2 * ks) * 512;
                     mbar_arrive_expect_tx(&full[st], S::w_bytes + S::t_bytes + 2 * sfb);
@@ -394,67 +399,73 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
                     uint8_t *sf = b + S::w_bytes + S::t_bytes;
                     bulk_g2s(sf, P.sb + (int64_t(tn) * P.kt + 2 * ks) * 512, sfb, &full[st]);
                     bulk_g2s(sf + 1024, P.sa + (int64_t(tm) * P.kt + 2 * ks) * 512, sfb, &full[st]);
-                    ++issued;
-                    if (++st == NS) {
-                        st = 0;
-                        ph ^= 1;
-                    }
                 }
-            }
-            if (s_fail) {  // wait for the copies still in flight
-                for (int i = 0; i < min(issued, NS); ++i) {
-                    st = st == 0 ? NS - 1 : st - 1;
-                    if (st == NS - 1) ph ^= 1;
-                    mbar_wait(&full[st], ph);
+                __syncwarp();
+                ++issued;
+                if (++st == NS) {
+                    st = 0;
+                    ph ^= 1;
                 }
             }
         }
+        if (!ok) {  // wait for the copies still in flight
+            give_up();
+            for (int i = 0; i < min(issued, NS); ++i) {
+                st = st == 0 ? NS - 1 : st - 1;
+                if (st == NS - 1) ph ^= 1;
+                mbar_wait(&full[st], ph);
+            }
+        }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int st = 0, ab = 0;
-            uint32_t ph = 0, aph = 0;
-            constexpr uint32_t instr = mxf4_instr(kLanes, BN);
-            bool ok = true;
-            for (int tile = first; tile < tiles && ok && !s_fail; tile += stride) {
-                ok = mbar_wait(&acc_empty[ab], aph ^ 1);
+        int st = 0, ab = 0;
+        uint32_t ph = 0, aph = 0;
+        constexpr uint32_t instr = mxf4_instr(kLanes, BN);
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += stride) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_empty[ab], aph ^ 1));
+            tc_fence_after();
+            const uint32_t acc = tmem + ab * BN;
+            for (int ks = ks0; ks < ks1 && ok; ++ks) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st], ph));
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + ab * BN;
-                for (int ks = ks0; ks < ks1 && ok; ++ks) {
-                    ok = mbar_wait(&full[st], ph);
-                    if (!ok || s_fail) break;
-                    tc_fence_after();
-                    const uint32_t b = smem_addr(smem + st * S::stage);
-                    const uint32_t sf = b + S::w_bytes + S::t_bytes;
-                    const uint32_t tw = tmem + S::sf_base + st * S::sf_cols, tt = tw + 8;
-                    const int na = min(2, P.kt - 2 * ks);
-                    for (int a = 0; a < na; ++a) {
-                        copy_scales<1>(tw + 4 * a, scale_desc(sf + 512 * a));
-                        copy_scales<1>(tt + 4 * a, scale_desc(sf + 1024 + 512 * a));
-                    }
-                    const uint64_t dw = operand_desc(b), dt = operand_desc(b + S::w_bytes);
-                    const int nj = min(4, P.k64 - 4 * ks);
+                const uint32_t b = smem_addr(smem) + st * S::stage;
+                const uint32_t tw = tmem + S::sf_base + st * S::sf_cols, tt = tw + 8;
+                const uint64_t ds = scale_desc(b + S::w_bytes + S::t_bytes);
+                const uint64_t dw = operand_desc(b), dt = operand_desc(b + S::w_bytes);
+                const int nj = min(4, P.k64 - 4 * ks);
+                if (elect_one()) {
+#pragma unroll
+                    for (int a = 0; a < 2; ++a)
+                        if (2 * a < nj) {
+                            copy_scales<1>(tw + 4 * a, ds + 32 * a);  // 512 bytes on
+                            copy_scales<1>(tt + 4 * a, ds + 64 + 32 * a);
+                        }
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (j < nj)
                             mma_mxf4<1>(acc, dw + 2 * j, dt + 2 * j, instr | mxf4_half(j & 1), tw + 4 * (j / 2),
                                         tt + 4 * (j / 2), ks > ks0 || j > 0);
                     tc_commit(&empty[st]);
-                    if (++st == NS) {
-                        st = 0;
-                        ph ^= 1;
-                    }
                 }
-                tc_commit(&acc_full[ab]);
-                if (++ab == NA) {
-                    ab = 0;
-                    aph ^= 1;
+                __syncwarp();
+                if (++st == NS) {
+                    st = 0;
+                    ph ^= 1;
                 }
             }
-            if (!ok) give_up();
-            if (s_fail) {  // wait for the products still in flight
-                tc_commit(&drain);
-                mbar_wait(&drain, 0);
+            if (elect_one()) tc_commit(&acc_full[ab]);
+            __syncwarp();
+            if (++ab == NA) {
+                ab = 0;
+                aph ^= 1;
             }
+        }
+        if (!ok) {  // wait for the products still in flight
+            give_up();
+            if (elect_one()) tc_commit(&drain);
+            __syncwarp();
+            mbar_wait(&drain, 0);
         }
     } else if (warp >= 4) {
         const int quarter = warp & 3;

@@ -10,6 +10,19 @@
 
 namespace amp {
 
+// One lane of the calling warp (which has to be converged), the same each time.
+// A role's warp walks its loops as a whole and only the instructions that one
+// thread issues stand behind this: their operands are then known to be uniform.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, e;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---- tensor memory (512 columns x 128 lanes x 32 bits an SM) -------------
 // CTAS = 2: a pair of CTAs of one cluster works as one; both allocate and free,
 // one thread of the first issues the products and scale copies for both.
@@ -194,28 +207,12 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     return a;
 }
+// One arrival on a barrier of any CTA of the cluster.  It orders no memory
+// between the CTAs (a release at cluster scope waits for every store of the
+// thread); what the waiting thread goes on to overwrite is tensor memory, which
+// the tcgen05 fences on both sides order.
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// mbar_wait (bulk_copy.cuh) for arrivals from the other CTAs of the cluster
-__device__ __forceinline__ bool cluster_mbar_wait(uint64_t *b, uint32_t parity) {
-    auto once = [&]() {
-        uint32_t ok;
-        asm volatile(
-            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; "
-            "selp.u32 %0, 1, 0, p; }"
-            : "=r"(ok)
-            : "r"(smem_addr(b)), "r"(parity)
-            : "memory");
-        return ok != 0;
-    };
-    if (once()) return true;
-    const unsigned long long t0 = global_ns();
-    for (;;) {
-        for (int i = 0; i < 64; ++i)
-            if (once()) return true;
-        if (global_ns() - t0 > kWaitLimitNs) return false;
-    }
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // the float at this shared-memory address of CTA `rank` of the cluster
 __device__ __forceinline__ float cluster_ld(uint32_t saddr, uint32_t rank) {
