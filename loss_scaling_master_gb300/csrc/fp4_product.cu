@@ -113,7 +113,7 @@ __device__ __forceinline__ void pack16(const uint32_t (&v)[CNT], uint32_t *p) {
 }
 
 // ------------------------------------------------------------------ a pair of CTAs a tile
-constexpr int kPairThreads = 384;  // load, issue, allocate, (idle), 8 store warps
+constexpr int kPairThreads = 640;  // load, issue, allocate, (idle), 16 store warps
 struct Pair {
     static constexpr int w_bytes = kLanes * kStageBytes;  // this CTA's half of the tile's rows of B
     static constexpr int t_bytes = 128 * kStageBytes;     // and of its rows of A
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(&empty[i], 1);  // both: the products' commit
         }
         mbar_init(&acc_full, 1);
-        mbar_init(&acc_empty, 16);  // the first CTA's: the 8 store warps of both
+        mbar_init(&acc_empty, 32);  // the first CTA's: the 16 store warps of both
         mbar_init(&drain, 1);
         s_fail = 0;
         mbar_fence_init();
@@ -258,49 +258,38 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
         }
     } else if (warp >= 4) {
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t acc = tmem + 128 * half + (uint32_t(32 * quarter) << 16);
+        // a quarter of the lanes and 64 of the 256 columns a warp: into
+        // registers at once, so the accumulators are free for the next tile's
+        // products while this one is rounded and stored
+        const int quarter = warp & 3, c0 = 64 * ((warp - 4) >> 2);
+        const uint32_t acc = tmem + c0 + (uint32_t(32 * quarter) << 16);
         const uint32_t done = cluster_addr(&acc_empty, 0);
         uint32_t aph = 0;
         for (int tile = first; tile < tiles; tile += stride) {
             int tm, tn;
             tile_at(P, 8, tile, tm, tn);
-            const bool ok = mbar_wait(&acc_full, aph);
-            if (!__all_sync(0xFFFFFFFFu, ok && !s_fail)) {
-                if (!ok) give_up();
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full, aph));
+            if (!ok) {
+                give_up();
                 break;
             }
             aph ^= 1;
             tc_fence_after();
+            uint32_t v[64];
+            tmem_ld<64>(acc, v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) cluster_arrive(done);
             const int64_t nn = int64_t(tn) * 256 + rank * 128 + 32 * quarter + lane;
-            const int64_t m0 = int64_t(tm) * 256 + 128 * half;
-            const int rows = int(max(int64_t(0), min(int64_t(128), P.m - m0)));
-            auto release = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) cluster_arrive(done);
-            };
+            const int64_t m0 = int64_t(tm) * 256 + c0;
+            const int rows = int(max(int64_t(0), min(int64_t(64), P.m - m0)));
             if (P.ot == kF32) {
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld<32>(acc + c, v);
-                    if (c == 96) release();
-                    store32<32>(P, m0 + c, rows - c, nn, v);
-                }
+                store32<64>(P, m0, rows, nn, v);
             } else {
-                // into registers, so the accumulators are free for the next
-                // tile's products while this one is stored
-                uint32_t p[64];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[64];
-                    tmem_ld<64>(acc + 64 * h, v);
-                    if (P.ot == kF16) pack16<kF16>(v, p + 32 * h);
-                    else pack16<kBF16>(v, p + 32 * h);
-                }
-                release();
-                store16<128>(P, m0, rows, nn, p);
+                uint32_t p[32];
+                if (P.ot == kF16) pack16<kF16>(v, p);
+                else pack16<kBF16>(v, p);
+                store16<64>(P, m0, rows, nn, p);
             }
         }
     }

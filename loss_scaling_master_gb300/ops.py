@@ -16,7 +16,7 @@ import ctypes
 import torch
 
 from . import _lib as A
-from ._lib import DT, P, _F32, _I32, _TORCH_DT, _buf, _check, _stream
+from ._lib import P, _buf, _check
 
 # every symbol include/ampops.h declares
 EXPORTS = ("fp4_mx_bytes", "fp4_mx_scale_bytes", "fp4_quant_mx", "fp4_dequant_mx",
@@ -54,27 +54,59 @@ def _load():
     return L
 
 
+# What follows runs once or more per argument of every call, next to 2.5 us for
+# the call and launch themselves: the accepted case is tested in as few steps as
+# there are conditions, and a refused tensor goes to _buf for its message.
+_ELEM = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}
+_F32, _I32, _U8, _E4M3 = torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+
+
 def _mat(t, what: str):
     """(rows, cols) of a matrix; a 1-D tensor is one row, leading dimensions are rows."""
-    if t.dim() == 0:
+    shape = t.shape
+    if len(shape) == 2:
+        return shape
+    if len(shape) == 0:
         raise ValueError(f"{what}: needs at least one dimension")
-    cols = t.shape[-1]
-    rows = 1
-    for s in t.shape[:-1]:
-        rows *= s
-    return rows, cols
+    return shape[:-1].numel(), shape[-1]
 
 
 def _code(t, what: str) -> int:
-    name = _TORCH_DT.get(t.dtype)
-    if name not in ("f32", "f16", "bf16"):
+    code = _ELEM.get(t.dtype)
+    if code is None:
         raise ValueError(f"{what}: dtype {t.dtype}; f32, f16 or bf16 is needed")
-    return DT[name]
+    return code
+
+
+def _ptr(t, what: str, numel: int, dtype=None):
+    """Address of a contiguous GPU tensor of the dtype with at least numel elements (None: none)."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.is_contiguous()) or (dtype is not None and t.dtype is not dtype) \
+            or t.numel() < numel:
+        _buf(t, what, dtype, numel)
+    return t.data_ptr()
+
+
+def _bytes(t, what: str, nbytes: int):
+    """Address of a contiguous GPU tensor of one-byte elements, at least nbytes of them."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.is_contiguous()) or t.element_size() != 1 or t.numel() < nbytes:
+        _buf(t, what, numel=nbytes, itemsize=1)
+    return t.data_ptr()
+
+
+def _stream(stream):
+    """Handle of the stream: the current one of the current device for None."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _fp4_sizes(rows: int, cols: int):
     """Bytes of the packed elements and of the scales of a [rows, cols] matrix."""
-    return rows * (-(-cols // 32)) * 16, (-(-rows // 128)) * (-(-cols // 128)) * 512
+    return rows * ((cols + 31) >> 5) * 16, ((rows + 127) >> 7) * ((cols + 127) >> 7) * 512
 
 
 def fp4_mx_buffers(rows: int, cols: int, device="cuda"):
@@ -97,39 +129,38 @@ def fp4_quant_mx(x, q, scales, qt=None, scales_t=None, skip_if=None, stream=None
     rows, cols = _mat(x, "x")
     nq, ns = _fp4_sizes(rows, cols)
     nqt, nst = _fp4_sizes(cols, rows) if qt is not None else (0, 0)
-    _check("fp4_quant_mx",
-           _load().fp4_quant_mx(_buf(x, "x", numel=0), _code(x, "x"), rows, cols,
-                                _buf(q, "q", itemsize=1, numel=nq),
-                                _buf(scales, "scales", itemsize=1, numel=ns),
-                                _buf(qt, "qt", itemsize=1, numel=nqt),
-                                _buf(scales_t, "scales_t", itemsize=1, numel=nst),
-                                _buf(skip_if, "skip_if", _I32), _stream(stream)))
+    st = (_ready or _load()).fp4_quant_mx(
+        _ptr(x, "x", 0), _code(x, "x"), rows, cols, _bytes(q, "q", nq),
+        _bytes(scales, "scales", ns), _bytes(qt, "qt", nqt), _bytes(scales_t, "scales_t", nst),
+        _ptr(skip_if, "skip_if", 1, _I32), _stream(stream))
+    if st:
+        _check("fp4_quant_mx", st)
 
 
 def fp4_dequant_mx(q, scales, out, stream=None):
     """out [rows, cols] = the values of the packed matrix of that shape."""
     rows, cols = _mat(out, "out")
     nq, ns = _fp4_sizes(rows, cols)
-    _check("fp4_dequant_mx",
-           _load().fp4_dequant_mx(_buf(q, "q", itemsize=1, numel=nq),
-                                  _buf(scales, "scales", itemsize=1, numel=ns), rows, cols,
-                                  _buf(out, "out", numel=0), _code(out, "out"), _stream(stream)))
+    st = (_ready or _load()).fp4_dequant_mx(
+        _bytes(q, "q", nq), _bytes(scales, "scales", ns), rows, cols, _ptr(out, "out", 0),
+        _code(out, "out"), _stream(stream))
+    if st:
+        _check("fp4_dequant_mx", st)
 
 
 def fp4_product_mx(a, a_scales, b, b_scales, k: int, out, stream=None):
     """out [m, n] = A [m, k] times B [n, k] transposed, both packed in 4 bits."""
     m, n = _mat(out, "out")
-    k = int(k)
     if k < 0:
         raise ValueError(f"k = {k}")
     na, nas = _fp4_sizes(m, k)
     nb, nbs = _fp4_sizes(n, k)
-    _check("fp4_product_mx",
-           _load().fp4_product_mx(_buf(a, "a", itemsize=1, numel=na),
-                                  _buf(a_scales, "a_scales", itemsize=1, numel=nas),
-                                  _buf(b, "b", itemsize=1, numel=nb),
-                                  _buf(b_scales, "b_scales", itemsize=1, numel=nbs), m, n, k,
-                                  _buf(out, "out", numel=0), _code(out, "out"), _stream(stream)))
+    st = (_ready or _load()).fp4_product_mx(
+        _bytes(a, "a", na), _bytes(a_scales, "a_scales", nas), _bytes(b, "b", nb),
+        _bytes(b_scales, "b_scales", nbs), m, n, k, _ptr(out, "out", 0), _code(out, "out"),
+        _stream(stream))
+    if st:
+        _check("fp4_product_mx", st)
 
 
 def fp4_mx_check(stream=None):
@@ -138,41 +169,49 @@ def fp4_mx_check(stream=None):
 
 
 def _pair(saved, what: str, rows: int, cols: int):
-    """Pointers of an 8-bit checkpoint (q, scales), or (None, None)."""
+    """Addresses of an 8-bit checkpoint (q, scales), or (None, None)."""
     if saved is None:
         return None, None
     q, s = saved
-    return (_buf(q, what, torch.float8_e4m3fn, rows * cols),
-            _buf(s, what + " scales", torch.uint8, rows * -(-cols // 32)))
+    return _ptr(q, what, rows * cols, _E4M3), _ptr(s, what, rows * ((cols + 31) >> 5), _U8)
 
 
 def _same(t, what: str, like):
-    """Pointer of a tensor with the type and size of another."""
-    return _buf(t, what, like.dtype, like.numel()) if t is not None else None
+    """Address of a tensor with the type and size of another."""
+    return None if t is None else _ptr(t, what, like.numel(), like.dtype)
 
 
-def _params(w, others, cols: int):
-    """The parameters' element type: of the first that is given (f32 if none is)."""
-    given = [t for t in (w, *others) if t is not None]
-    if any(t.dtype != given[0].dtype for t in given[1:]):
-        raise ValueError("weight, bias and their gradients need one dtype")
-    if any(t.numel() != cols for t in given):
-        raise ValueError(f"weight, bias and their gradients need {cols} elements")
-    return _code(given[0], "weight") if given else DT["f32"]
+def _params(cols: int, *given):
+    """The element type of the parameters and their gradients (f32 if none is given)."""
+    dtype = None
+    for t in given:
+        if t is None:
+            continue
+        if dtype is None:
+            dtype = t.dtype
+        elif t.dtype is not dtype:
+            raise ValueError("weight, bias and their gradients need one dtype")
+        if t.numel() != cols:
+            raise ValueError(f"weight, bias and their gradients need {cols} elements")
+    if dtype is None:
+        return 1
+    if dtype not in _ELEM:
+        raise ValueError(f"weight: dtype {dtype}; f32, f16 or bf16 is needed")
+    return _ELEM[dtype]
 
 
 def amp_layer_norm_forward(x, weight, bias, eps: float, y, mean=None, rstd=None, saved=None,
                            stream=None):
     """Layer norm over the last dimension; saved: (q, scales) to keep x in 8 bits."""
     rows, cols = _mat(x, "x")
-    wc = _params(weight, (bias,), cols)
+    wc = _params(cols, weight, bias)
     q, s = _pair(saved, "saved", rows, cols)
-    _check("amp_layer_norm_forward",
-           _load().amp_layer_norm_forward(_buf(x, "x", numel=0), _code(x, "x"), rows, cols,
-                                          _buf(weight, "weight"), _buf(bias, "bias"), wc,
-                                          float(eps), _same(y, "y", x),
-                                          _buf(mean, "mean", _F32, rows),
-                                          _buf(rstd, "rstd", _F32, rows), q, s, _stream(stream)))
+    st = (_ready or _load()).amp_layer_norm_forward(
+        _ptr(x, "x", 0), _code(x, "x"), rows, cols, _ptr(weight, "weight", cols),
+        _ptr(bias, "bias", cols), wc, eps, _same(y, "y", x), _ptr(mean, "mean", rows, _F32),
+        _ptr(rstd, "rstd", rows, _F32), q, s, _stream(stream))
+    if st:
+        _check("amp_layer_norm_forward", st)
 
 
 def amp_layer_norm_workspace(x):
@@ -191,24 +230,23 @@ def amp_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, db
     rows, cols = _mat(dy, "dy")
     if (x is None) == (saved is None):
         raise ValueError("either x or saved")
-    wc = _params(weight, (dweight, dbias), cols)
+    wc = _params(cols, weight, dweight, dbias)
     q, s = _pair(saved, "saved", rows, cols)
-    _check("amp_layer_norm_backward",
-           _load().amp_layer_norm_backward(_buf(dy, "dy", numel=0), _same(x, "x", dy),
-                                           _code(dy, "dy"), q, s, rows, cols,
-                                           _buf(weight, "weight"), wc,
-                                           _buf(mean, "mean", _F32, rows),
-                                           _buf(rstd, "rstd", _F32, rows), _same(dx, "dx", dy),
-                                           _buf(dweight, "dweight"), _buf(dbias, "dbias"),
-                                           _buf(workspace, "workspace"),
-                                           workspace.numel() * workspace.element_size()
-                                           if workspace is not None else 0, _stream(stream)))
+    work = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = (_ready or _load()).amp_layer_norm_backward(
+        _ptr(dy, "dy", 0), _same(x, "x", dy), _code(dy, "dy"), q, s, rows, cols,
+        _ptr(weight, "weight", cols), wc, _ptr(mean, "mean", rows, _F32),
+        _ptr(rstd, "rstd", rows, _F32), _same(dx, "dx", dy), _ptr(dweight, "dweight", cols),
+        _ptr(dbias, "dbias", cols), _ptr(workspace, "workspace", 0), work, _stream(stream))
+    if st:
+        _check("amp_layer_norm_backward", st)
 
 
 def _act(kind: str) -> int:
-    if kind not in ACTS:
+    act = ACTS.get(kind)
+    if act is None:
         raise ValueError(f"activation {kind!r}; one of {sorted(ACTS)}")
-    return ACTS[kind]
+    return act
 
 
 def amp_act_forward_mx8(x, kind: str, y, saved=None, up=None, saved_up=None, stream=None):
@@ -216,10 +254,11 @@ def amp_act_forward_mx8(x, kind: str, y, saved=None, up=None, saved_up=None, str
     rows, cols = _mat(x, "x")
     q, s = _pair(saved, "saved", rows, cols)
     qu, su = _pair(saved_up, "saved_up", rows, cols)
-    _check("amp_act_forward_mx8",
-           _load().amp_act_forward_mx8(_act(kind), _buf(x, "x", numel=0), _same(up, "up", x),
-                                       _code(x, "x"), rows, cols, _same(y, "y", x), q, s, qu, su,
-                                       _stream(stream)))
+    st = (_ready or _load()).amp_act_forward_mx8(
+        _act(kind), _ptr(x, "x", 0), _same(up, "up", x), _code(x, "x"), rows, cols,
+        _same(y, "y", x), q, s, qu, su, _stream(stream))
+    if st:
+        _check("amp_act_forward_mx8", st)
 
 
 def amp_act_backward_mx8(dy, kind: str, saved, dx, saved_up=None, dup=None, stream=None):
@@ -227,23 +266,27 @@ def amp_act_backward_mx8(dy, kind: str, saved, dx, saved_up=None, dup=None, stre
     rows, cols = _mat(dy, "dy")
     q, s = _pair(saved, "saved", rows, cols)
     qu, su = _pair(saved_up, "saved_up", rows, cols)
-    _check("amp_act_backward_mx8",
-           _load().amp_act_backward_mx8(_act(kind), _buf(dy, "dy", numel=0), _code(dy, "dy"), rows,
-                                        cols, q, s, qu, su, _same(dx, "dx", dy),
-                                        _same(dup, "dup", dy), _stream(stream)))
+    st = (_ready or _load()).amp_act_backward_mx8(
+        _act(kind), _ptr(dy, "dy", 0), _code(dy, "dy"), rows, cols, q, s, qu, su,
+        _same(dx, "dx", dy), _same(dup, "dup", dy), _stream(stream))
+    if st:
+        _check("amp_act_backward_mx8", st)
 
 
 def amp_ckpt8_save(x, q, scales, stream=None):
     """The 8-bit checkpoint of x."""
     rows, cols = _mat(x, "x")
-    _check("amp_ckpt8_save",
-           _load().amp_ckpt8_save(_buf(x, "x", numel=0), _code(x, "x"), rows, cols,
-                                  *_pair((q, scales), "q", rows, cols), _stream(stream)))
+    st = (_ready or _load()).amp_ckpt8_save(_ptr(x, "x", 0), _code(x, "x"), rows, cols,
+                                            *_pair((q, scales), "q", rows, cols), _stream(stream))
+    if st:
+        _check("amp_ckpt8_save", st)
 
 
 def amp_ckpt8_restore(q, scales, out, stream=None):
     """out = the values of an 8-bit checkpoint."""
     rows, cols = _mat(out, "out")
-    _check("amp_ckpt8_restore",
-           _load().amp_ckpt8_restore(*_pair((q, scales), "q", rows, cols), rows, cols,
-                                     _buf(out, "out", numel=0), _code(out, "out"), _stream(stream)))
+    st = (_ready or _load()).amp_ckpt8_restore(*_pair((q, scales), "q", rows, cols), rows, cols,
+                                               _ptr(out, "out", 0), _code(out, "out"),
+                                               _stream(stream))
+    if st:
+        _check("amp_ckpt8_restore", st)
