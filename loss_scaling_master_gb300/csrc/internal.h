@@ -161,7 +161,7 @@ cudaError_t fp4_error_take(int32_t *v, cudaStream_t s);
 
 cudaError_t launch_norm_fwd(const void *x, int xelem, int64_t rows, int64_t cols, const void *w,
                             const void *b, int welem, float eps, void *y, float *mean, float *rstd,
-                            uint8_t *q, uint8_t *sc, cudaStream_t s);
+                            uint8_t *q, uint8_t *sc, int device, cudaStream_t s);
 // Rows of the backward's partial sums (2 * cols floats each).
 int64_t norm_parts(int64_t rows, int64_t cols, int device);
 cudaError_t launch_norm_bwd(const void *dy, const void *x, int elem, const uint8_t *q,

@@ -1,11 +1,19 @@
 // layer_norm.cuh - what the forward and the backward layer norm share: how a
-// row is spread over threads, its loads and its sums.
+// row is spread over threads, loads and stores, packed fp32 arithmetic, sums.
 //
-// A row of up to 16384 elements is held in registers by TPR threads, thread t
-// taking the groups of 8 elements t, t + TPR, ..., NV of them (row_shape
-// picks the smallest such pair).  Four neighbouring threads hold one block of
-// the 8-bit checkpoint.  Longer rows are walked in pieces (the *_long
-// kernels).
+// A row of up to 16384 elements is held in registers by TPR threads, NV groups
+// of 8 elements each (AMP_NORM_SHAPE picks the pair).  Where rows are whole,
+// 16-byte aligned groups of 8 (VEC), thread t takes the groups t, t + TPR, ...,
+// one 16-byte access each of a 16-bit tensor, and 4 neighbouring threads hold
+// one block of the 8-bit checkpoint.  Otherwise a thread takes single elements
+// TPR apart, so that a warp's accesses stay side by side whatever the row
+// length; a warp then holds one block at a time.  Longer rows are walked in
+// pieces (the *_long kernels).
+//
+// The arithmetic runs two elements an instruction (fp32x2), each rounded as a
+// scalar one: what bounds these kernels besides memory is instruction issue
+// (34 instructions an element in scalar form with per-element guards took 84 us
+// for the forward pass of 16384 x 4096 bf16 with a checkpoint, 50 us of memory).
 #pragma once
 
 #include "internal.h"
@@ -21,54 +29,124 @@ inline bool norm_vec(const void *p, int64_t cols, int esz) {
     return cols % 8 == 0 && (cols * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 }
 
-// The group of 8 elements from k, of which n (<= 0: none) are in the row.
-template <int XT>
-__device__ __forceinline__ void ld_group(const void *x, int64_t k, int n, bool vec,
-                                         uint4 (&u)[kWords8<XT>]) {
+// ---- two fp32 at a time, in one 64-bit register --------------------------------
+// (kept as such from the loads to the stores: as a pair of floats each operand
+// would be moved into an aligned pair of registers first)
+using f2 = uint64_t;
+__device__ __forceinline__ f2 make_f2(float a, float b) {
+    f2 c;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(a), "f"(b));
+    return c;
+}
+__device__ __forceinline__ float2 split(f2 a) {
+    float2 c;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(c.x), "=f"(c.y) : "l"(a));
+    return c;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 c;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(a), "l"(b));
+    return c;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 c;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(a), "l"(b));
+    return c;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f2 both(float v) { return make_f2(v, v); }
+__device__ __forceinline__ float sum2(f2 a) {
+    const float2 s = split(a);
+    return s.x + s.y;
+}
+
+// ---- a thread's 8 elements: group v of thread t ------------------------------
+// Element j's column, and how many of the 8 are in the row (VEC: all or none).
+template <bool VEC, int TPR>
+__device__ __forceinline__ int norm_col(int v, int t, int j) {
+    return VEC ? 8 * (v * TPR + t) + j : (8 * v + j) * TPR + t;
+}
+template <bool VEC, int TPR>
+__device__ __forceinline__ int norm_count(int v, int t, int cols) {
+    if (VEC) return 8 * (v * TPR + t) < cols ? 8 : 0;
+    const int left = cols - 8 * v * TPR - t;  // of elements TPR apart
+    return left <= 0 ? 0 : min(8, (left + TPR - 1) / TPR);
+}
+
+// Raw words of the 8 elements from element k of the tensor, n of them in the
+// row; the rest are zeros.
+template <int XT, bool VEC, int TPR>
+__device__ __forceinline__ void ld8(const void *x, int64_t k, int n, uint4 (&u)[kWords8<XT>]) {
     constexpr int esz = XT == kF32 ? 4 : 2;
-    if (vec) {
+    if constexpr (VEC) {
 #pragma unroll
-        for (int j = 0; j < kWords8<XT>; ++j)
-            u[j] = n > 0 ? ld16(static_cast<const char *>(x) + k * esz + 16 * j) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kWords8<XT>; ++i)
+            u[i] = n > 0 ? ld16(static_cast<const char *>(x) + k * esz + 16 * i) : make_uint4(0, 0, 0, 0);
     } else {
-        load_raw8_tail<XT>(x, k, n, u);
+        uint32_t w[4 * kWords8<XT>];
+#pragma unroll
+        for (int i = 0; i < 4 * kWords8<XT>; ++i) {
+            if constexpr (XT == kF32) {
+                w[i] = i < n ? static_cast<const uint32_t *>(x)[k + i * TPR] : 0u;
+            } else {
+                const uint16_t *p = static_cast<const uint16_t *>(x) + k;
+                const uint32_t a = 2 * i < n ? p[2 * i * TPR] : 0u, b = 2 * i + 1 < n ? p[(2 * i + 1) * TPR] : 0u;
+                w[i] = a | (b << 16);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kWords8<XT>; ++i) u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
 }
 template <int XT>
-__device__ __forceinline__ void st_group(void *x, int64_t k, int n, bool vec, const float (&y)[8]) {
-    constexpr int esz = XT == kF32 ? 4 : 2;
-    if (n <= 0) return;
-    if (vec) {
-        uint4 u[kWords8<XT>];
-        f32_to_raw8<XT>(y, u);
+__device__ __forceinline__ void to_f32(const uint4 (&u)[kWords8<XT>], f2 (&y)[4]) {
+    float f[8];
+    raw8_to_f32<XT>(u, f);
 #pragma unroll
-        for (int j = 0; j < kWords8<XT>; ++j) st16(static_cast<char *>(x) + k * esz + 16 * j, u[j]);
+    for (int i = 0; i < 4; ++i) y[i] = make_f2(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ void split8(const f2 (&y)[4], float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 s = split(y[i]);
+        f[2 * i] = s.x;
+        f[2 * i + 1] = s.y;
+    }
+}
+template <int XT, bool VEC, int TPR>
+__device__ __forceinline__ void st8(void *x, int64_t k, int n, const f2 (&y)[4]) {
+    constexpr int esz = XT == kF32 ? 4 : 2;
+    float f[8];
+    split8(y, f);
+    if constexpr (VEC) {
+        if (n <= 0) return;
+        uint4 u[kWords8<XT>];
+        f32_to_raw8<XT>(f, u);
+#pragma unroll
+        for (int i = 0; i < kWords8<XT>; ++i) st16(static_cast<char *>(x) + k * esz + 16 * i, u[i]);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < n) store_elem<XT>(x, k + j, y[j]);
+            if (j < n) store_elem<XT>(x, k + j * TPR, f[j]);
     }
 }
 
-// A parameter vector of its own type (wt: an ElemType); `fill` where it is NULL.
-__device__ __forceinline__ void ld_param(const void *w, int wt, int64_t c, int n, bool vec, float fill,
-                                         float (&y)[8]) {
-    if (w == nullptr || n <= 0) {
+// A parameter vector (wt: its ElemType); `fill` where it is NULL.
+__device__ __forceinline__ float ld_param(const void *w, int wt, int64_t c, float fill) {
+    if (w == nullptr) return fill;
+    return wt == kF32 ? load_elem<kF32>(w, c) : wt == kF16 ? load_elem<kF16>(w, c) : load_elem<kBF16>(w, c);
+}
+template <bool VEC, int TPR>
+__device__ __forceinline__ void ld_params(const void *w, int wt, int v, int t, int n, float fill, f2 (&y)[4]) {
+    float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = fill;
-    } else if (wt == kF32) {
-        uint4 u[2];
-        ld_group<kF32>(w, c, n, vec, u);
-        raw8_to_f32<kF32>(u, y);
-    } else if (wt == kF16) {
-        uint4 u[1];
-        ld_group<kF16>(w, c, n, vec, u);
-        raw8_to_f32<kF16>(u, y);
-    } else {
-        uint4 u[1];
-        ld_group<kBF16>(w, c, n, vec, u);
-        raw8_to_f32<kBF16>(u, y);
-    }
+    for (int j = 0; j < 8; ++j) f[j] = j < n ? ld_param(w, wt, norm_col<VEC, TPR>(v, t, j), fill) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = make_f2(f[2 * i], f[2 * i + 1]);
 }
 __device__ __forceinline__ void st_param(void *w, int wt, int64_t c, float v) {
     if (wt == kF32) store_elem<kF32>(w, c, v);
@@ -83,9 +161,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // The sums of N values over the TPR threads of a row, given to all of them.
-// Every thread of the CTA calls it (it synchronises); s: CTA scratch of at
-// least N * 32 floats, a different one for calls that follow one another
-// without a barrier between.
+// Every thread of the CTA calls it (it synchronises); s: CTA scratch of N * 32
+// floats, another one for the next call.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float *s) {
 #pragma unroll
@@ -109,19 +186,19 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float *s) {
 }
 
 __host__ __device__ constexpr int norm_cta(int tpr) { return tpr > 256 ? tpr : 256; }
+__host__ __device__ constexpr int norm_rpc(int tpr) { return norm_cta(tpr) / tpr; }  // rows a CTA holds
 
 }  // namespace amp
 
-// Calls F<TPR, NV>(...) for the row length: the rule is the smallest number of
-// threads that holds the row in two groups each (one for the shortest), four
-// for the longest rows, whose CTA could not be larger.
-#define AMP_NORM_SHAPE(cols, F)          \
-    do {                                 \
-        if ((cols) <= 256) { F(32, 1); } \
-        else if ((cols) <= 512) { F(32, 2); } \
-        else if ((cols) <= 1024) { F(64, 2); } \
+// Runs F(TPR, NV) for the row length.  A warp a row up to 1024 elements (no
+// barrier), then the smallest CTA that holds the row in two groups a thread,
+// four for the longest rows, whose CTA could not be larger.
+#define AMP_NORM_SHAPE(cols, F)                 \
+    do {                                        \
+        if ((cols) <= 256) { F(32, 1); }        \
+        else if ((cols) <= 1024) { F(32, 4); }  \
         else if ((cols) <= 2048) { F(128, 2); } \
         else if ((cols) <= 4096) { F(256, 2); } \
         else if ((cols) <= 8192) { F(512, 2); } \
-        else { F(512, 4); }              \
+        else { F(512, 4); }                     \
     } while (0)

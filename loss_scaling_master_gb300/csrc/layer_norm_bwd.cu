@@ -26,75 +26,92 @@ struct NormBwd {
     float *part;  // [grid][2][cols]: dw then db
     int64_t rows, cols;
     float inv_d;
-    int wt, dyvec, xvec, wvec, dxvec, qvec;
+    int wt;
 };
 
-// x of one group: raw words, or 8 codes and the block's scale byte.
+// A thread's 8 elements of dy and of x, or of x's codes with their scale bytes
+// (VEC: 8 codes in x, y and one byte in z; else two codes and bytes a word).
 template <int XT, bool CK>
 struct Group {
     uint4 dy[kWords8<XT>];
-    uint4 x[CK ? 1 : kWords8<XT>];  // CK: codes in x, y; scale byte in z
+    uint4 x[CK ? 1 : kWords8<XT>];
 };
 
-template <int XT, bool CK>
-__device__ __forceinline__ void load_pair(const NormBwd &P, int64_t r, int64_t c, int n, Group<XT, CK> &g) {
+template <int XT, bool CK, bool VEC, int TPR>
+__device__ __forceinline__ void load_pair(const NormBwd &P, int64_t r, int v, int t, int n, Group<XT, CK> &g) {
+    const int c = norm_col<VEC, TPR>(v, t, 0);
     const int64_t k = r * P.cols + c;
-    ld_group<XT>(P.dy, k, n, P.dyvec, g.dy);
-    if constexpr (CK) {
-        uint2 u = make_uint2(0, 0);
-        uint32_t e = 0;
-        if (n > 0) {
-            if (P.qvec) {
-                u = *reinterpret_cast<const uint2 *>(P.q + k);
-            } else {
-                uint32_t w[2] = {0, 0};
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n) w[j / 4] |= uint32_t(P.q[k + j]) << (8 * (j & 3));
-                u = make_uint2(w[0], w[1]);
-            }
-            e = P.s[r * ((P.cols + 31) / 32) + c / 32];
-        }
-        g.x[0] = make_uint4(u.x, u.y, e, 0);
+    ld8<XT, VEC, TPR>(P.dy, k, n, g.dy);
+    if constexpr (!CK) {
+        ld8<XT, VEC, TPR>(P.x, k, n, g.x);
     } else {
-        ld_group<XT>(P.x, k, n, P.xvec, g.x);
+        const int64_t kb = (P.cols + kMxBlock - 1) / kMxBlock;
+        const uint8_t *s = P.s + r * kb;
+        if constexpr (VEC) {
+            uint2 u = make_uint2(0, 0);
+            uint32_t e = 0;
+            if (n > 0) {
+                u = *reinterpret_cast<const uint2 *>(P.q + k);
+                e = s[c / 32];
+            }
+            g.x[0] = make_uint4(u.x, u.y, e, 0);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = 0;
+                if (2 * i < n) w[i] = P.q[k + 2 * i * TPR] | uint32_t(s[(c + 2 * i * TPR) / 32]) << 16;
+                if (2 * i + 1 < n)
+                    w[i] |= uint32_t(P.q[k + (2 * i + 1) * TPR]) << 8 | uint32_t(s[(c + (2 * i + 1) * TPR) / 32]) << 24;
+            }
+            g.x[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
-template <int XT, bool CK>
-__device__ __forceinline__ void unpack_pair(const Group<XT, CK> &g, float (&dy)[8], float (&x)[8]) {
-    raw8_to_f32<XT>(g.dy, dy);
-    if constexpr (CK) {
-        const float s = mx_scale(g.x[0].z);
-        e4m3x4_to_f32x4(g.x[0].x, x);
-        e4m3x4_to_f32x4(g.x[0].y, x + 4);
+template <int XT, bool CK, bool VEC>
+__device__ __forceinline__ void unpack_pair(const Group<XT, CK> &g, f2 (&dy)[4], f2 (&x)[4]) {
+    to_f32<XT>(g.dy, dy);
+    if constexpr (!CK) {
+        to_f32<XT>(g.x, x);
+    } else if constexpr (VEC) {
+        float f[8];
+        e4m3x4_to_f32x4(g.x[0].x, f);
+        e4m3x4_to_f32x4(g.x[0].y, f + 4);
+        const f2 s = both(mx_scale(g.x[0].z));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], s);
+        for (int i = 0; i < 4; ++i) x[i] = mul2(make_f2(f[2 * i], f[2 * i + 1]), s);
     } else {
-        raw8_to_f32<XT>(g.x, x);
+        const uint32_t w[4] = {g.x[0].x, g.x[0].y, g.x[0].z, g.x[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[4];
+            e4m3x4_to_f32x4(w[i] & 0xFFFFu, f);
+            x[i] = mul2(make_f2(f[0], f[1]), make_f2(mx_scale((w[i] >> 16) & 0xFFu), mx_scale(w[i] >> 24)));
+        }
     }
 }
 
-template <int XT, bool CK, int TPR, int NV>
-__global__ void __launch_bounds__(norm_cta(TPR)) norm_bwd_kernel(NormBwd P) {
-    constexpr int RPC = norm_cta(TPR) / TPR;
+template <int XT, bool CK, bool VEC, int TPR, int NV>
+__global__ void __launch_bounds__(norm_cta(TPR), norm_cta(TPR) == 256 && NV <= 2 ? 2 : 1) norm_bwd_kernel(NormBwd P) {
+    constexpr int RPC = norm_rpc(TPR);
+    constexpr bool HOLD = TPR < 512 || NV < 4;  // weights in registers
     __shared__ float scratch[2][2 * 32];
-    extern __shared__ float s_join[];  // RPC > 1: 2 * cols floats
+    extern __shared__ float s_join[];  // RPC > 1: RPC * cols floats
     pdl_wait();
     pdl_trigger();
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    float aw[NV][8], ab[NV][8];
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) aw[v][j] = ab[v][j] = 0.0f;
+    f2 aw[NV][4], ab[NV][4], w[HOLD ? NV : 1][4];
     const int64_t step = int64_t(gridDim.x) * RPC;
-    Group<XT, CK> nxt[NV];
     int64_t r = int64_t(blockIdx.x) * RPC + sub;
     int len[NV];
+    Group<XT, CK> nxt[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        len[v] = int(P.cols) - 8 * (v * TPR + t);
-        load_pair<XT, CK>(P, r, 8 * (v * TPR + t), r < P.rows ? len[v] : 0, nxt[v]);
+        len[v] = norm_count<VEC, TPR>(v, t, int(P.cols));
+        load_pair<XT, CK, VEC, TPR>(P, r, v, t, r < P.rows ? len[v] : 0, nxt[v]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) aw[v][i] = ab[v][i] = both(0.0f);
+        if (HOLD) ld_params<VEC, TPR>(P.w, P.wt, v, t, len[v], 1.0f, w[HOLD ? v : 0]);
     }
     float nmean = r < P.rows ? P.mean[r] : 0.0f, nrstd = r < P.rows ? P.rstd[r] : 0.0f;
     int buf = 0;
@@ -102,125 +119,130 @@ __global__ void __launch_bounds__(norm_cta(TPR)) norm_bwd_kernel(NormBwd P) {
     for (int64_t base = int64_t(blockIdx.x) * RPC; base < P.rows; base += step, r += step, buf ^= 1) {
         const bool in = r < P.rows;
         const float mean = nmean, rstd = nrstd;
-        float g[NV][8], xh[NV][8], sums[2] = {0.0f, 0.0f};
+        const f2 off = both(-mean), rs = both(rstd);
+        f2 g[NV][4], xh[NV][4], s0 = both(0.0f), s1 = both(0.0f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            float w[8];
-            ld_param(P.w, P.wt, 8 * (v * TPR + t), len[v], P.wvec, 1.0f, w);
-            unpack_pair<XT, CK>(nxt[v], g[v], xh[v]);
+            if (!HOLD) ld_params<VEC, TPR>(P.w, P.wt, v, t, len[v], 1.0f, w[0]);
+            unpack_pair<XT, CK, VEC>(nxt[v], g[v], xh[v]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                xh[v][j] = in && j < len[v] ? (xh[v][j] - mean) * rstd : 0.0f;
-                const float dy = g[v][j];
-                aw[v][j] = __fmaf_rn(dy, xh[v][j], aw[v][j]);
-                ab[v][j] += dy;
-                g[v][j] = dy * w[j];
-                sums[0] += g[v][j];
-                sums[1] = __fmaf_rn(g[v][j], xh[v][j], sums[1]);
+            for (int i = 0; i < 4; ++i) {
+                xh[v][i] = mul2(add2(xh[v][i], off), rs);
+                // behind the row's end and the last row: dy and w are 0 there
+                if constexpr (VEC) {
+                    if (!(in && len[v] > 0)) xh[v][i] = 0;
+                } else {
+                    const float2 p = split(xh[v][i]);
+                    xh[v][i] = make_f2(in && 2 * i < len[v] ? p.x : 0.0f, in && 2 * i + 1 < len[v] ? p.y : 0.0f);
+                }
+                aw[v][i] = fma2(g[v][i], xh[v][i], aw[v][i]);
+                ab[v][i] = add2(ab[v][i], g[v][i]);
+                g[v][i] = mul2(g[v][i], w[HOLD ? v : 0][i]);
+                s0 = add2(s0, g[v][i]);
+                s1 = fma2(g[v][i], xh[v][i], s1);
             }
         }
         const int64_t rn = r + step;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            load_pair<XT, CK>(P, rn, 8 * (v * TPR + t), rn < P.rows ? len[v] : 0, nxt[v]);
+        for (int v = 0; v < NV; ++v) load_pair<XT, CK, VEC, TPR>(P, rn, v, t, rn < P.rows ? len[v] : 0, nxt[v]);
         if (rn < P.rows) {
             nmean = P.mean[rn];
             nrstd = P.rstd[rn];
         }
+        float sums[2] = {sum2(s0), sum2(s1)};
         row_sums<TPR>(sums, scratch[buf]);
         if (P.dx && in) {
-            const float c0 = sums[0] * P.inv_d, c1 = sums[1] * P.inv_d;
+            const f2 c0 = both(-sums[0] * P.inv_d), c1 = both(-sums[1] * P.inv_d);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                float o[8];
+                f2 o[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = rstd * (g[v][j] - __fmaf_rn(xh[v][j], c1, c0));
-                st_group<XT>(P.dx, r * P.cols + 8 * (v * TPR + t), len[v], P.dxvec, o);
+                for (int i = 0; i < 4; ++i) o[i] = mul2(rs, add2(g[v][i], fma2(xh[v][i], c1, c0)));
+                st8<XT, VEC, TPR>(P.dx, r * P.cols + norm_col<VEC, TPR>(v, t, 0), len[v], o);
             }
         }
     }
     if (!P.part) return;
     float *out = P.part + int64_t(blockIdx.x) * 2 * P.cols;
+    const int d = int(P.cols);
     if constexpr (RPC > 1) {
-        // the row groups add in turn
-        const int d = int(P.cols);
-        for (int i = 0; i < RPC; ++i) {
-            if (sub == i) {
+        // every row group leaves its sums, then a thread adds a column's
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (j >= len[v]) continue;
-                        const int c = 8 * (v * TPR + t) + j;
-                        s_join[c] = (i ? s_join[c] : 0.0f) + aw[v][j];
-                        s_join[d + c] = (i ? s_join[d + c] : 0.0f) + ab[v][j];
-                    }
-            }
+        for (int k = 0; k < 2; ++k) {
             __syncthreads();
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (j >= len[v]) continue;
+                    const float2 p = split(k ? ab[v][j / 2] : aw[v][j / 2]);
+                    s_join[sub * d + norm_col<VEC, TPR>(v, t, j)] = j & 1 ? p.y : p.x;
+                }
+            __syncthreads();
+            for (int c = threadIdx.x; c < d; c += norm_cta(TPR)) {
+                float a = 0.0f;
+#pragma unroll
+                for (int i = 0; i < RPC; ++i) a += s_join[i * d + c];
+                out[k * d + c] = a;
+            }
         }
-        for (int c = threadIdx.x; c < 2 * d; c += norm_cta(TPR)) out[c] = s_join[c];
     } else {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 if (j >= len[v]) continue;
-                const int c = 8 * (v * TPR + t) + j;
-                out[c] = aw[v][j];
-                out[P.cols + c] = ab[v][j];
+                const int c = norm_col<VEC, TPR>(v, t, j);
+                const float2 a = split(aw[v][j / 2]), b = split(ab[v][j / 2]);
+                out[c] = j & 1 ? a.y : a.x;
+                out[d + c] = j & 1 ? b.y : b.x;
             }
     }
 }
 
-// Rows past kNormRegCols.  dx: one CTA a row, walked twice.
+// Rows past kNormRegCols, an element a thread and step.
+template <int XT, bool CK>
+__device__ __forceinline__ float long_x(const NormBwd &P, int64_t r, int64_t c) {
+    if constexpr (CK) {
+        float v[4];
+        e4m3x4_to_f32x4(P.q[r * P.cols + c], v);
+        return __fmul_rn(v[0], mx_scale(P.s[r * ((P.cols + kMxBlock - 1) / kMxBlock) + c / kMxBlock]));
+    } else {
+        return load_elem<XT>(P.x, r * P.cols + c);
+    }
+}
+// dx: one CTA a row, walked twice.
 template <int XT, bool CK>
 __global__ void __launch_bounds__(512) norm_bwd_long_dx(NormBwd P) {
     __shared__ float scratch[2 * 32];
     pdl_wait();
     pdl_trigger();
     const int64_t r = blockIdx.x;
-    const int64_t steps = (P.cols + 8 * 512 - 1) / (8 * 512);
     const float mean = P.mean[r], rstd = P.rstd[r];
-    float sums[2] = {0.0f, 0.0f}, g[8], xh[8];
-    auto get = [&](int64_t i, int64_t &c) {
-        c = 8 * (i * 512 + threadIdx.x);
-        const int n = int(min(int64_t(8), P.cols - c));
-        Group<XT, CK> p;
-        load_pair<XT, CK>(P, r, c, n, p);
-        float w[8];
-        ld_param(P.w, P.wt, c, n, P.wvec, 1.0f, w);
-        unpack_pair<XT, CK>(p, g, xh);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            xh[j] = j < n ? (xh[j] - mean) * rstd : 0.0f;
-            g[j] *= w[j];
-        }
-        return n;
-    };
-    int64_t c;
-    for (int64_t i = 0; i < steps; ++i) {
-        get(i, c);
+    float sums[2] = {0.0f, 0.0f};
+    for (int64_t c0 = 0; c0 < P.cols; c0 += 4096) {
         float a = 0.0f, b = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            a += g[j];
-            b = __fmaf_rn(g[j], xh[j], b);
+            const int64_t c = c0 + 512 * j + threadIdx.x;
+            if (c < P.cols) {
+                const float g = load_elem<XT>(P.dy, r * P.cols + c) * ld_param(P.w, P.wt, c, 1.0f);
+                a += g;
+                b = __fmaf_rn(g, (long_x<XT, CK>(P, r, c) - mean) * rstd, b);
+            }
         }
         sums[0] += a;
         sums[1] += b;
     }
     row_sums<512>(sums, scratch);
     const float c0 = sums[0] * P.inv_d, c1 = sums[1] * P.inv_d;
-    for (int64_t i = 0; i < steps; ++i) {
-        const int n = get(i, c);
-        float o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = rstd * (g[j] - __fmaf_rn(xh[j], c1, c0));
-        st_group<XT>(P.dx, r * P.cols + c, n, P.dxvec, o);
+    for (int64_t c = threadIdx.x; c < P.cols; c += 512) {
+        const float g = load_elem<XT>(P.dy, r * P.cols + c) * ld_param(P.w, P.wt, c, 1.0f);
+        const float xh = (long_x<XT, CK>(P, r, c) - mean) * rstd;
+        store_elem<XT>(P.dx, r * P.cols + c, rstd * (g - __fmaf_rn(xh, c1, c0)));
     }
 }
-// The parameter sums of long rows: thread = one column, blockIdx.y = a share
-// of the rows.
+// The parameter sums: thread = one column, blockIdx.y = a share of the rows.
 template <int XT, bool CK>
 __global__ void __launch_bounds__(kThreads) norm_bwd_long_params(NormBwd P) {
     pdl_wait();
@@ -230,15 +252,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_long_params(NormBwd P) {
     float a = 0.0f, b = 0.0f;
     for (int64_t r = blockIdx.y; r < P.rows; r += gridDim.y) {
         const float dy = load_elem<XT>(P.dy, r * P.cols + c);
-        float x;
-        if constexpr (CK) {
-            float v[4];
-            e4m3x4_to_f32x4(P.q[r * P.cols + c], v);
-            x = __fmul_rn(v[0], mx_scale(P.s[r * ((P.cols + 31) / 32) + c / 32]));
-        } else {
-            x = load_elem<XT>(P.x, r * P.cols + c);
-        }
-        a = __fmaf_rn(dy, (x - P.mean[r]) * P.rstd[r], a);
+        a = __fmaf_rn(dy, (long_x<XT, CK>(P, r, c) - P.mean[r]) * P.rstd[r], a);
         b += dy;
     }
     float *out = P.part + int64_t(blockIdx.y) * 2 * P.cols;
@@ -246,70 +260,71 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_long_params(NormBwd P) {
     out[P.cols + c] = b;
 }
 
-// Adds the partial rows.  A CTA takes 32 columns; warp w the rows w, w + 8, ...
+// Adds the partial rows.  A CTA takes 32 of the 2 cols columns, warp w the rows
+// w, w + 32, ...: the loads of a warp are independent, so a column costs a few
+// load latencies.
+constexpr int kJoinThreads = 1024;
 struct NormJoin {
     const float *part;
     int64_t parts, cols;
     void *dw, *db;
     int wt;
 };
-__global__ void __launch_bounds__(kThreads) norm_join_kernel(NormJoin P) {
-    __shared__ float s[2][kThreads / 32][32];
+__global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormJoin P) {
+    __shared__ float s[kJoinThreads / 32][33];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = int64_t(blockIdx.x) * 32 + lane;
-    float a = 0.0f, b = 0.0f;
-    if (c < P.cols) {
-#pragma unroll 4
-        for (int64_t p = warp; p < P.parts; p += kThreads / 32) {
-            a += P.part[p * 2 * P.cols + c];
-            b += P.part[p * 2 * P.cols + P.cols + c];
-        }
+    float a = 0.0f;
+    if (c < 2 * P.cols) {
+#pragma unroll 8
+        for (int64_t p = warp; p < P.parts; p += kJoinThreads / 32) a += P.part[p * 2 * P.cols + c];
     }
-    s[0][warp][lane] = a;
-    s[1][warp][lane] = b;
+    s[warp][lane] = a;
     __syncthreads();
-    if (warp < 2 && c < P.cols) {
+    if (warp == 0 && c < 2 * P.cols) {
         float t = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) t += s[warp][w][lane];
-        void *out = warp ? P.db : P.dw;
-        if (out) st_param(out, P.wt, c, t);
+        for (int w = 0; w < kJoinThreads / 32; ++w) t += s[w][lane];
+        void *out = c < P.cols ? P.dw : P.db;
+        if (out) st_param(out, P.wt, c < P.cols ? c : c - P.cols, t);
     }
 }
 
-template <int XT, bool CK>
-cudaError_t go(NormBwd &P, int64_t parts, cudaStream_t s) {
-    if (P.cols > kNormRegCols) {
-        // the parameters first: dx may overwrite dy
-        if (P.part) {
-            cudaError_t e = launch_pdl(norm_bwd_long_params<XT, CK>,
-                                       dim3((unsigned)((P.cols + kThreads - 1) / kThreads), (unsigned)parts),
-                                       dim3(kThreads), 0, s, P);
-            if (e != cudaSuccess) return e;
-        }
-        if (!P.dx || P.rows == 0) return cudaSuccess;
-        return launch_pdl(norm_bwd_long_dx<XT, CK>, dim3((unsigned)P.rows), dim3(512), 0, s, P);
-    }
-#define F(TPR, NV)                                                                              \
-    return launch_pdl(norm_bwd_kernel<XT, CK, TPR, NV>, dim3((unsigned)parts), dim3(norm_cta(TPR)), \
-                      norm_cta(TPR) > TPR ? size_t(P.cols) * 8 : 0, s, P)
+template <int XT, bool CK, bool VEC>
+cudaError_t go(const NormBwd &P, int64_t parts, cudaStream_t s) {
+#define F(TPR, NV)                                                                                           \
+    return launch_pdl(norm_bwd_kernel<XT, CK, VEC, TPR, NV>, dim3((unsigned)parts), dim3(norm_cta(TPR)),     \
+                      norm_rpc(TPR) > 1 ? size_t(P.cols) * 4 * norm_rpc(TPR) : 0, s, P)
     AMP_NORM_SHAPE(P.cols, F);
 #undef F
+}
+template <int XT, bool CK>
+cudaError_t go_x(const NormBwd &P, bool vec, int64_t parts, cudaStream_t s) {
+    if (P.cols <= kNormRegCols) return vec ? go<XT, CK, true>(P, parts, s) : go<XT, CK, false>(P, parts, s);
+    // the parameters first: dx may overwrite dy
+    if (P.part) {
+        const cudaError_t e = launch_pdl(norm_bwd_long_params<XT, CK>,
+                                         dim3((unsigned)((P.cols + kThreads - 1) / kThreads), (unsigned)parts),
+                                         dim3(kThreads), 0, s, P);
+        if (e != cudaSuccess) return e;
+    }
+    if (!P.dx || P.rows == 0) return cudaSuccess;
+    return launch_pdl(norm_bwd_long_dx<XT, CK>, dim3((unsigned)P.rows), dim3(512), 0, s, P);
 }
 
 }  // namespace
 
 // Rows of partial sums: as many CTAs as the device holds at once (2 of 256
-// threads an SM, 1 of 512), at most one for each group of rows.
+// threads an SM, 1 of 512 or with four groups a thread), at most one for each
+// group of rows.
 int64_t norm_parts(int64_t rows, int64_t cols, int device) {
     const int64_t sms = sm_count(device);
     if (cols > kNormRegCols) return std::max<int64_t>(1, std::min<int64_t>(rows, 32));
-#define F(TPR, NV)                                                    \
-    return std::max<int64_t>(                                         \
-        1, std::min<int64_t>((rows + norm_cta(TPR) / TPR - 1) / (norm_cta(TPR) / TPR), \
-                             norm_cta(TPR) > 256 ? sms : 2 * sms))
+#define F(TPR, NV)                                                                     \
+    return std::max<int64_t>(1, std::min<int64_t>((rows + norm_rpc(TPR) - 1) / norm_rpc(TPR), \
+                                                  norm_cta(TPR) == 256 && NV <= 2 ? 2 * sms : sms))
     AMP_NORM_SHAPE(cols, F);
 #undef F
 }
@@ -318,27 +333,24 @@ cudaError_t launch_norm_bwd(const void *dy, const void *x, int elem, const uint8
                             int64_t rows, int64_t cols, const void *w, int welem, const float *mean,
                             const float *rstd, void *dx, void *dw, void *db, float *part, int device,
                             cudaStream_t s) {
-    NormBwd P{dy, x, w, q, sc, mean, rstd, dx, dw || db ? part : nullptr, rows, cols,
-              float(1.0 / double(cols)), welem, 0, 0, 0, 0, 0};
-    const int esz = elem == kF32 ? 4 : 2, wsz = welem == kF32 ? 4 : 2;
-    P.dyvec = norm_vec(dy, cols, esz);
-    P.xvec = norm_vec(x, cols, esz);
-    P.wvec = norm_vec(w, cols, wsz);
-    P.dxvec = norm_vec(dx, cols, esz);
-    P.qvec = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(q) & 7) == 0;
+    const NormBwd P{dy, x, w, q, sc, mean, rstd, dx, dw || db ? part : nullptr, rows, cols,
+                    float(1.0 / double(cols)), welem};
+    const int esz = elem == kF32 ? 4 : 2;
+    const bool vec = norm_vec(dy, cols, esz) && norm_vec(x, cols, esz) && norm_vec(dx, cols, esz) &&
+                     (reinterpret_cast<uintptr_t>(q) & 7) == 0;
     const int64_t parts = norm_parts(rows, cols, device);
     cudaError_t e = cudaSuccess;
     if (q)
-        e = elem == kF32   ? go<kF32, true>(P, parts, s)
-            : elem == kF16 ? go<kF16, true>(P, parts, s)
-                           : go<kBF16, true>(P, parts, s);
+        e = elem == kF32   ? go_x<kF32, true>(P, vec, parts, s)
+            : elem == kF16 ? go_x<kF16, true>(P, vec, parts, s)
+                           : go_x<kBF16, true>(P, vec, parts, s);
     else
-        e = elem == kF32   ? go<kF32, false>(P, parts, s)
-            : elem == kF16 ? go<kF16, false>(P, parts, s)
-                           : go<kBF16, false>(P, parts, s);
+        e = elem == kF32   ? go_x<kF32, false>(P, vec, parts, s)
+            : elem == kF16 ? go_x<kF16, false>(P, vec, parts, s)
+                           : go_x<kBF16, false>(P, vec, parts, s);
     if (e == cudaSuccess && P.part) {
         const NormJoin J{part, parts, cols, dw, db, welem};
-        e = launch_pdl(norm_join_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(kThreads), 0, s, J);
+        e = launch_pdl(norm_join_kernel, dim3((unsigned)((2 * cols + 31) / 32)), dim3(kJoinThreads), 0, s, J);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }

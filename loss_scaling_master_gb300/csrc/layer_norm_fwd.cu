@@ -5,7 +5,9 @@
 //
 // The row sits in registers (layer_norm.cuh), so x is read once although the
 // variance is taken about the finished mean (no cancellation for rows far from
-// zero): read + write of the row is all the traffic, and memory bounds it.
+// zero): read + write of the row is all the traffic.  CTAs stay and walk rows;
+// a thread's parameters are loaded once, and the next row's loads are issued
+// before the present row is worked on.
 #include <algorithm>
 
 #include "layer_norm.cuh"
@@ -20,165 +22,225 @@ struct NormFwd {
     uint8_t *q, *s;
     int64_t rows, cols;
     float eps, inv_d;
-    int wt, xvec, yvec, wvec, bvec, qvec;
+    int wt;
 };
 
-// The checkpoint of one group of 8 (n of them in the row); the 4 lanes of a
-// block call it together.  c: the group's first column.
-__device__ __forceinline__ void keep_group(const NormFwd &P, int64_t r, int64_t c, int n, const float (&x)[8]) {
-    uint32_t m = 0;
+// CTAs an SM holds (and the register bound that lets it).  16384 x 4096 bf16
+// with a checkpoint: 2 CTAs 64 us, 3 59 us, 4 (spills) 68 us.
+template <int XT, bool VEC>
+__host__ __device__ constexpr int fwd_ctas(int tpr, int nv) {
+    return norm_cta(tpr) > 256 || (nv == 4) ? 1 : nv == 1 ? 4 : VEC && XT != kF32 ? 3 : 2;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The checkpoint of a thread's 8 elements of row r; the warp calls it together.
+template <int XT, bool VEC, int TPR>
+__device__ __forceinline__ void keep8(const NormFwd &P, int64_t r, int v, int t, int n,
+                                      const uint4 (&raw)[kWords8<XT>], const f2 (&x)[4]) {
+    const int64_t kb = (P.cols + kMxBlock - 1) / kMxBlock;
+    float f[8];
+    split8(x, f);
+    if constexpr (VEC) {
+        uint32_t m;
+        if constexpr (XT == kF32) {
+            m = max(max(max(abs_bits(f[0]), abs_bits(f[1])), max(abs_bits(f[2]), abs_bits(f[3]))),
+                    max(max(abs_bits(f[4]), abs_bits(f[5])), max(abs_bits(f[6]), abs_bits(f[7]))));
+        } else {  // 16-bit magnitudes order like their values: maxima on packed pairs
+            const uint32_t k = 0x7FFF7FFFu;
+            const uint32_t p = max_u16x2(max_u16x2(raw[0].x & k, raw[0].y & k), max_u16x2(raw[0].z & k, raw[0].w & k));
+            m = abs_bits(lowp_to_f32<XT>(max(p & 0xFFFFu, p >> 16)));
+        }
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        if (n <= 0) return;
+        const uint32_t e = mx_scale_code<MxE4M3>(m);
+        const f2 u = both(mx_unscale(e));
+        uint32_t h[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    if (n <= 0) return;
-    const uint32_t e = mx_scale_code<MxE4M3>(m);
-    const float f = mx_unscale(e);
-    uint32_t h[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        h[j] = f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(x[2 * j], f), __fmul_rn(x[2 * j + 1], f));
-    uint8_t *q = P.q + r * P.cols + c;
-    if (P.qvec) {
-        *reinterpret_cast<uint2 *>(q) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        for (int i = 0; i < 4; ++i) {
+            const float2 z = split(mul2(x[i], u));
+            h[i] = f32x2_to_fp8x2_raw<kE4M3>(z.x, z.y);
+        }
+        const int c = norm_col<true, TPR>(v, t, 0);
+        *reinterpret_cast<uint2 *>(P.q + r * P.cols + c) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        if ((c & 31) == 0) P.s[r * kb + c / 32] = uint8_t(e);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) q[j] = uint8_t(h[j / 2] >> (8 * (j & 1)));
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t e = mx_scale_code<MxE4M3>(warp_max_u32(abs_bits(f[j])));
+            if (j >= n) continue;
+            const int c = norm_col<false, TPR>(v, t, j);
+            P.q[r * P.cols + c] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(f[j], mx_unscale(e)), 0.0f));
+            if ((c & 31) == 0) P.s[r * kb + c / 32] = uint8_t(e);
+        }
     }
-    if ((c & 31) == 0) P.s[r * ((P.cols + 31) / 32) + c / 32] = uint8_t(e);
 }
 
-template <int XT, int TPR, int NV>
-__global__ void __launch_bounds__(norm_cta(TPR)) norm_fwd_kernel(NormFwd P) {
-    __shared__ float s1[32], s2[32];
+template <int XT, bool VEC, int TPR, int NV>
+__global__ void __launch_bounds__(norm_cta(TPR), (fwd_ctas<XT, VEC>(TPR, NV)))
+    norm_fwd_kernel(NormFwd P) {
+    __shared__ float scratch[2][2][32];
     pdl_wait();
     pdl_trigger();
-    constexpr int RPC = norm_cta(TPR) / TPR;
+    constexpr int RPC = norm_rpc(TPR);
     const int t = threadIdx.x % TPR;
-    const int64_t r = int64_t(blockIdx.x) * RPC + threadIdx.x / TPR;
-    const bool in = r < P.rows;
-    uint4 raw[NV][kWords8<XT>];
+    const int64_t step = int64_t(gridDim.x) * RPC;
+    int64_t r = int64_t(blockIdx.x) * RPC + threadIdx.x / TPR;
     int n[NV];
+    f2 w[NV][4], b[NV][4];
+    uint4 nxt[NV][kWords8<XT>];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int c = 8 * (v * TPR + t);
-        n[v] = in ? int(P.cols) - c : 0;
-        ld_group<XT>(P.x, r * P.cols + c, n[v], P.xvec, raw[v]);
+        n[v] = norm_count<VEC, TPR>(v, t, int(P.cols));
+        ld8<XT, VEC, TPR>(P.x, r * P.cols + norm_col<VEC, TPR>(v, t, 0), r < P.rows ? n[v] : 0, nxt[v]);
     }
-    float x[NV][8], a[1] = {0.0f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        raw8_to_f32<XT>(raw[v], x[v]);
-        a[0] += ((x[v][0] + x[v][1]) + (x[v][2] + x[v][3])) + ((x[v][4] + x[v][5]) + (x[v][6] + x[v][7]));
+        ld_params<VEC, TPR>(P.w, P.wt, v, t, n[v], 1.0f, w[v]);
+        ld_params<VEC, TPR>(P.b, P.wt, v, t, n[v], 0.0f, b[v]);
     }
-    row_sums<TPR>(a, s1);
-    const float mean = a[0] * P.inv_d;
-    float b[1] = {0.0f};
+    int buf = 0;
+    // every thread of the CTA walks the same number of steps
+    for (int64_t base = int64_t(blockIdx.x) * RPC; base < P.rows; base += step, r += step, buf ^= 1) {
+        const bool in = r < P.rows;
+        uint4 raw[NV][kWords8<XT>];
+        f2 x[NV][4];
+        float a[1];
+        f2 s2 = both(0.0f);
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float d = j < n[v] ? x[v][j] - mean : 0.0f;
-            b[0] = __fmaf_rn(d, d, b[0]);
+            for (int i = 0; i < kWords8<XT>; ++i) raw[v][i] = nxt[v][i];
+            to_f32<XT>(raw[v], x[v]);
+            s2 = add2(s2, add2(add2(x[v][0], x[v][1]), add2(x[v][2], x[v][3])));
         }
-    row_sums<TPR>(b, s2);
-    const float rstd = 1.0f / sqrtf(__fmaf_rn(b[0], P.inv_d, P.eps));
-    if (in && t == 0) {
-        if (P.mean) P.mean[r] = mean;
-        if (P.rstd) P.rstd[r] = rstd;
-    }
+        const int64_t rn = r + step;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int c = 8 * (v * TPR + t);
-        if (P.q) keep_group(P, r, c, n[v], x[v]);
-        float w[8], o[8];
-        ld_param(P.w, P.wt, c, n[v], P.wvec, 1.0f, w);
-        ld_param(P.b, P.wt, c, n[v], P.bvec, 0.0f, o);
+        for (int v = 0; v < NV; ++v)
+            ld8<XT, VEC, TPR>(P.x, rn * P.cols + norm_col<VEC, TPR>(v, t, 0), rn < P.rows ? n[v] : 0, nxt[v]);
+        a[0] = sum2(s2);
+        row_sums<TPR>(a, scratch[buf][0]);
+        const float mean = a[0] * P.inv_d;
+        if (P.q) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn((x[v][j] - mean) * rstd, w[j], o[j]);
-        st_group<XT>(P.y, r * P.cols + c, n[v], P.yvec, o);
+            for (int v = 0; v < NV; ++v) keep8<XT, VEC, TPR>(P, r, v, t, in ? n[v] : 0, raw[v], x[v]);
+        }
+        s2 = both(0.0f);
+        const f2 off = both(-mean);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            f2 q = both(0.0f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[v][i] = add2(x[v][i], off);
+                if (!VEC) {  // elements behind the row's end
+                    const float2 p = split(x[v][i]);
+                    x[v][i] = make_f2(2 * i < n[v] ? p.x : 0.0f, 2 * i + 1 < n[v] ? p.y : 0.0f);
+                }
+                q = fma2(x[v][i], x[v][i], q);
+            }
+            if (!VEC || n[v] > 0) s2 = add2(s2, q);
+        }
+        a[0] = sum2(s2);
+        row_sums<TPR>(a, scratch[buf][1]);
+        const float rstd = 1.0f / sqrtf(__fmaf_rn(a[0], P.inv_d, P.eps));
+        if (in && t == 0) {
+            if (P.mean) P.mean[r] = mean;
+            if (P.rstd) P.rstd[r] = rstd;
+        }
+        const f2 rs = both(rstd);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            f2 o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = fma2(mul2(x[v][i], rs), w[v][i], b[v][i]);
+            st8<XT, VEC, TPR>(P.y, r * P.cols + norm_col<VEC, TPR>(v, t, 0), in ? n[v] : 0, o);
+        }
     }
 }
 
-// Rows past kNormRegCols: one CTA a row, walked three times (the second and
-// third reads come from L2).
+// Rows past kNormRegCols: one CTA a row, walked three times, an element a
+// thread and step (the second and third reads come from L2).
 template <int XT>
 __global__ void __launch_bounds__(512) norm_fwd_long(NormFwd P) {
     __shared__ float s1[32], s2[32];
     pdl_wait();
     pdl_trigger();
-    const int64_t r = blockIdx.x;
-    const int64_t steps = (P.cols + 8 * 512 - 1) / (8 * 512);
-    float a[1] = {0.0f}, b[1] = {0.0f}, x[8];
-    auto get = [&](int64_t i, int64_t &c) {
-        uint4 raw[kWords8<XT>];
-        c = 8 * (i * 512 + threadIdx.x);
-        const int n = int(min(int64_t(8), P.cols - c));
-        ld_group<XT>(P.x, r * P.cols + c, n, P.xvec, raw);
-        raw8_to_f32<XT>(raw, x);
-        return n;
-    };
-    int64_t c;
-    for (int64_t i = 0; i < steps; ++i) {
-        get(i, c);
-        a[0] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    const int64_t r = blockIdx.x, row = r * P.cols, kb = (P.cols + kMxBlock - 1) / kMxBlock;
+    float a[1] = {0.0f};
+    for (int64_t c0 = 0; c0 < P.cols; c0 += 4096) {
+        float part = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t c = c0 + 512 * j + threadIdx.x;
+            part += c < P.cols ? load_elem<XT>(P.x, row + c) : 0.0f;
+        }
+        a[0] += part;
     }
     row_sums<512>(a, s1);
     const float mean = a[0] * P.inv_d;
-    for (int64_t i = 0; i < steps; ++i) {
-        const int n = get(i, c);
-        float q = 0.0f;
+    a[0] = 0.0f;
+    for (int64_t c0 = 0; c0 < P.cols; c0 += 4096) {
+        float part = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float d = j < n ? x[j] - mean : 0.0f;
-            q = __fmaf_rn(d, d, q);
+            const int64_t c = c0 + 512 * j + threadIdx.x;
+            const float d = c < P.cols ? load_elem<XT>(P.x, row + c) - mean : 0.0f;
+            part = __fmaf_rn(d, d, part);
         }
-        b[0] += q;
+        a[0] += part;
     }
-    row_sums<512>(b, s2);
-    const float rstd = 1.0f / sqrtf(__fmaf_rn(b[0], P.inv_d, P.eps));
+    row_sums<512>(a, s2);
+    const float rstd = 1.0f / sqrtf(__fmaf_rn(a[0], P.inv_d, P.eps));
     if (threadIdx.x == 0) {
         if (P.mean) P.mean[r] = mean;
         if (P.rstd) P.rstd[r] = rstd;
     }
-    for (int64_t i = 0; i < steps; ++i) {
-        const int n = get(i, c);
-        if (P.q) keep_group(P, r, c, n, x);
-        float w[8], o[8];
-        ld_param(P.w, P.wt, c, n, P.wvec, 1.0f, w);
-        ld_param(P.b, P.wt, c, n, P.bvec, 0.0f, o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn((x[j] - mean) * rstd, w[j], o[j]);
-        st_group<XT>(P.y, r * P.cols + c, n, P.yvec, o);
+    for (int64_t c0 = 0; c0 < P.cols; c0 += 512) {
+        const int64_t c = c0 + threadIdx.x;
+        const bool in = c < P.cols;
+        const float x = in ? load_elem<XT>(P.x, row + c) : 0.0f;
+        if (P.q) {
+            const uint32_t e = mx_scale_code<MxE4M3>(warp_max_u32(abs_bits(x)));
+            if (in) P.q[row + c] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(x, mx_unscale(e)), 0.0f));
+            if (in && (c & 31) == 0) P.s[r * kb + c / 32] = uint8_t(e);
+        }
+        if (in)
+            store_elem<XT>(P.y, row + c,
+                           __fmaf_rn((x - mean) * rstd, ld_param(P.w, P.wt, c, 1.0f), ld_param(P.b, P.wt, c, 0.0f)));
     }
 }
 
-template <int XT>
-cudaError_t go(const NormFwd &P, cudaStream_t s) {
-    if (P.cols > kNormRegCols)
-        return launch_pdl(norm_fwd_long<XT>, dim3((unsigned)P.rows), dim3(512), 0, s, P);
-#define F(TPR, NV)                                                                                  \
-    return launch_pdl(norm_fwd_kernel<XT, TPR, NV>,                                                 \
-                      dim3((unsigned)((P.rows + norm_cta(TPR) / TPR - 1) / (norm_cta(TPR) / TPR))), \
+template <int XT, bool VEC>
+cudaError_t go(const NormFwd &P, int device, cudaStream_t s) {
+    const int64_t sms = sm_count(device);
+#define F(TPR, NV)                                                                                       \
+    return launch_pdl(norm_fwd_kernel<XT, VEC, TPR, NV>,                                                 \
+                      dim3((unsigned)std::min<int64_t>((P.rows + norm_rpc(TPR) - 1) / norm_rpc(TPR),     \
+                                                       sms * (fwd_ctas<XT, VEC>(TPR, NV)))), \
                       dim3(norm_cta(TPR)), 0, s, P)
     AMP_NORM_SHAPE(P.cols, F);
 #undef F
+}
+template <int XT>
+cudaError_t go_x(const NormFwd &P, bool vec, int device, cudaStream_t s) {
+    if (P.cols > kNormRegCols)
+        return launch_pdl(norm_fwd_long<XT>, dim3((unsigned)P.rows), dim3(512), 0, s, P);
+    return vec ? go<XT, true>(P, device, s) : go<XT, false>(P, device, s);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_fwd(const void *x, int xelem, int64_t rows, int64_t cols, const void *w,
                             const void *b, int welem, float eps, void *y, float *mean, float *rstd,
-                            uint8_t *q, uint8_t *sc, cudaStream_t s) {
-    NormFwd P{x, w, b, y, mean, rstd, q, sc, rows, cols, eps, float(1.0 / double(cols)), welem, 0, 0, 0, 0, 0};
-    const int esz = xelem == kF32 ? 4 : 2, wsz = welem == kF32 ? 4 : 2;
-    P.xvec = norm_vec(x, cols, esz);
-    P.yvec = norm_vec(y, cols, esz);
-    P.wvec = norm_vec(w, cols, wsz);
-    P.bvec = norm_vec(b, cols, wsz);
-    P.qvec = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(q) & 7) == 0;
-    cudaError_t e = xelem == kF32 ? go<kF32>(P, s) : xelem == kF16 ? go<kF16>(P, s) : go<kBF16>(P, s);
+                            uint8_t *q, uint8_t *sc, int device, cudaStream_t s) {
+    const NormFwd P{x, w, b, y, mean, rstd, q, sc, rows, cols, eps, float(1.0 / double(cols)), welem};
+    const int esz = xelem == kF32 ? 4 : 2;
+    const bool vec = norm_vec(x, cols, esz) && norm_vec(y, cols, esz) && (reinterpret_cast<uintptr_t>(q) & 7) == 0;
+    const cudaError_t e = xelem == kF32   ? go_x<kF32>(P, vec, device, s)
+                          : xelem == kF16 ? go_x<kF16>(P, vec, device, s)
+                                          : go_x<kBF16>(P, vec, device, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -140,8 +140,11 @@ amp_status amp_layer_norm_forward(const void *x, amp_dtype x_dtype, int64_t rows
         return fail(AMP_EINVAL, "%s: ckpt and ckpt_scales go together", fn);
     if (rows * cols == 0) return AMP_OK;
     if (!x || !y) return fail(AMP_EINVAL, kNull, fn);
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return finish(e, fn);
     return finish(amp::launch_norm_fwd(x, xc, rows, cols, weight, bias, wc, float(eps), y, mean, rstd, u8(ckpt),
-                                       u8(ckpt_scales), cu(stream)),
+                                       u8(ckpt_scales), dev, cu(stream)),
                   fn);
 }
 
