@@ -68,25 +68,29 @@ __device__ __forceinline__ void load_pair(const NormBwd &P, int64_t r, int v, in
         }
     }
 }
+// dy and x - mean (a code times its power of two is exact, so one fused
+// multiply-add rounds as the subtraction does).
 template <int XT, bool CK, bool VEC>
-__device__ __forceinline__ void unpack_pair(const Group<XT, CK> &g, f2 (&dy)[4], f2 (&x)[4]) {
+__device__ __forceinline__ void unpack_pair(const Group<XT, CK> &g, f2 off, f2 (&dy)[4], f2 (&x)[4]) {
     to_f32<XT>(g.dy, dy);
     if constexpr (!CK) {
         to_f32<XT>(g.x, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = add2(x[i], off);
     } else if constexpr (VEC) {
         float f[8];
         e4m3x4_to_f32x4(g.x[0].x, f);
         e4m3x4_to_f32x4(g.x[0].y, f + 4);
         const f2 s = both(mx_scale(g.x[0].z));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = mul2(make_f2(f[2 * i], f[2 * i + 1]), s);
+        for (int i = 0; i < 4; ++i) x[i] = fma2(make_f2(f[2 * i], f[2 * i + 1]), s, off);
     } else {
         const uint32_t w[4] = {g.x[0].x, g.x[0].y, g.x[0].z, g.x[0].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float f[4];
             e4m3x4_to_f32x4(w[i] & 0xFFFFu, f);
-            x[i] = mul2(make_f2(f[0], f[1]), make_f2(mx_scale((w[i] >> 16) & 0xFFu), mx_scale(w[i] >> 24)));
+            x[i] = fma2(make_f2(f[0], f[1]), make_f2(mx_scale((w[i] >> 16) & 0xFFu), mx_scale(w[i] >> 24)), off);
         }
     }
 }
@@ -118,23 +122,20 @@ __global__ void __launch_bounds__(norm_cta(TPR), norm_cta(TPR) == 256 && NV <= 2
     // every thread of the CTA walks the same number of steps
     for (int64_t base = int64_t(blockIdx.x) * RPC; base < P.rows; base += step, r += step, buf ^= 1) {
         const bool in = r < P.rows;
-        const float mean = nmean, rstd = nrstd;
+        const float mean = in ? nmean : 0.0f, rstd = in ? nrstd : 0.0f;
         const f2 off = both(-mean), rs = both(rstd);
         f2 g[NV][4], xh[NV][4], s0 = both(0.0f), s1 = both(0.0f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             if (!HOLD) ld_params<VEC, TPR>(P.w, P.wt, v, t, len[v], 1.0f, w[0]);
-            unpack_pair<XT, CK, VEC>(nxt[v], g[v], xh[v]);
+            if (len[v] == 0) continue;
+            // elements behind the row's end have dy = w = 0 and a finite xh
+            // (with the row's own mean and rstd), a row behind the last one
+            // has zeros throughout: neither changes a sum
+            unpack_pair<XT, CK, VEC>(nxt[v], off, g[v], xh[v]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                xh[v][i] = mul2(add2(xh[v][i], off), rs);
-                // behind the row's end and the last row: dy and w are 0 there
-                if constexpr (VEC) {
-                    if (!(in && len[v] > 0)) xh[v][i] = 0;
-                } else {
-                    const float2 p = split(xh[v][i]);
-                    xh[v][i] = make_f2(in && 2 * i < len[v] ? p.x : 0.0f, in && 2 * i + 1 < len[v] ? p.y : 0.0f);
-                }
+                xh[v][i] = mul2(xh[v][i], rs);
                 aw[v][i] = fma2(g[v][i], xh[v][i], aw[v][i]);
                 ab[v][i] = add2(ab[v][i], g[v][i]);
                 g[v][i] = mul2(g[v][i], w[HOLD ? v : 0][i]);
@@ -152,12 +153,13 @@ __global__ void __launch_bounds__(norm_cta(TPR), norm_cta(TPR) == 256 && NV <= 2
         float sums[2] = {sum2(s0), sum2(s1)};
         row_sums<TPR>(sums, scratch[buf]);
         if (P.dx && in) {
-            const f2 c0 = both(-sums[0] * P.inv_d), c1 = both(-sums[1] * P.inv_d);
+            const f2 c0 = both(-sums[0] * P.inv_d * rstd), c1 = both(-sums[1] * P.inv_d * rstd);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
+                if (len[v] == 0) continue;
                 f2 o[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = mul2(rs, add2(g[v][i], fma2(xh[v][i], c1, c0)));
+                for (int i = 0; i < 4; ++i) o[i] = fma2(g[v][i], rs, fma2(xh[v][i], c1, c0));
                 st8<XT, VEC, TPR>(P.dx, r * P.cols + norm_col<VEC, TPR>(v, t, 0), len[v], o);
             }
         }

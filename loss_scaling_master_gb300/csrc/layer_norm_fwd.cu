@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(norm_cta(TPR), (fwd_ctas<XT, VEC>(TPR, NV)))
         const f2 off = both(-mean);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
+            if (VEC && n[v] == 0) continue;
             f2 q = both(0.0f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -140,11 +141,11 @@ __global__ void __launch_bounds__(norm_cta(TPR), (fwd_ctas<XT, VEC>(TPR, NV)))
                 }
                 q = fma2(x[v][i], x[v][i], q);
             }
-            if (!VEC || n[v] > 0) s2 = add2(s2, q);
+            s2 = add2(s2, q);
         }
         a[0] = sum2(s2);
         row_sums<TPR>(a, scratch[buf][1]);
-        const float rstd = 1.0f / sqrtf(__fmaf_rn(a[0], P.inv_d, P.eps));
+        const float rstd = rsqrtf(__fmaf_rn(a[0], P.inv_d, P.eps));
         if (in && t == 0) {
             if (P.mean) P.mean[r] = mean;
             if (P.rstd) P.rstd[r] = rstd;
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(norm_cta(TPR), (fwd_ctas<XT, VEC>(TPR, NV)))
         const f2 rs = both(rstd);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
+            if (n[v] == 0) continue;
             f2 o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = fma2(mul2(x[v][i], rs), w[v][i], b[v][i]);
