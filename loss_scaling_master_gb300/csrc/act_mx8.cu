@@ -20,6 +20,9 @@
 #include "mx.cuh"
 #include "pdl.cuh"
 
+#ifndef VGRID
+#define VGRID 64
+#endif
 namespace amp {
 namespace {
 
@@ -29,14 +32,15 @@ struct ActFwd {
     const void *x, *u;
     void *y;
     uint8_t *q, *s, *qu, *su;
-    int64_t rows, cols, kb;  // kb: blocks a row
-    int64_t blocks;          // rows * kb
+    int64_t rows, cols;
+    int kb;  // blocks a row
 };
 struct ActBwd {
     const void *dy;
     const uint8_t *q, *s, *qu, *su;
     void *dx, *du;
-    int64_t rows, cols, kb, blocks;
+    int64_t rows, cols;
+    int kb;
 };
 
 // 1 / (1 + exp(-t)) as 1 / (1 + e) or e / (1 + e), e = exp(-|t|): the
@@ -131,16 +135,15 @@ template <int XT, int ACT, bool GATED, bool KEEP>
 __global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P) {
     pdl_wait();
     pdl_trigger();
-    const int64_t n = P.blocks * 4;
-    // the 4 threads of a block run together: the count of blocks is not a
-    // multiple of 8, so every thread of a warp walks the loop and guards
-    for (int64_t t0 = int64_t(blockIdx.x) * kThreads; t0 < n; t0 += int64_t(gridDim.x) * kThreads) {
-        const int64_t t = t0 + threadIdx.x;
-        const int64_t b = t >> 2;
-        const int64_t r = b / P.kb;
-        const int64_t col = (b - r * P.kb) * kMxBlock + 8 * (t & 3);
-        const bool in = t < n && col < P.cols;
-        const int64_t k = r * P.cols + col;
+    // the 4 threads of a block run together, so every thread of a warp walks
+    // until the warp's first row is past the end, and guards
+    RowWalk at((int64_t(blockIdx.x) * kThreads + threadIdx.x) / 4, int64_t(gridDim.x) * (kThreads / 4), P.kb);
+    for (; __any_sync(0xFFFFFFFFu, at.row < P.rows); at.next()) {
+        const bool row = at.row < P.rows;
+        const int64_t b = at.row * P.kb + at.at;
+        const int col = at.at * kMxBlock + 8 * (threadIdx.x & 3);
+        const bool in = row && col < P.cols;
+        const int64_t k = at.row * P.cols + col;
         float x[8], u[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = u[j] = 0.0f;
@@ -151,11 +154,11 @@ __global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P) {
         if (KEEP) {
             const uint32_t e = mx_scale_code<MxE4M3>(block_max8(x));
             if (in) *reinterpret_cast<uint2 *>(P.q + k) = codes8(x, mx_unscale(e));
-            if (t < n && (t & 3) == 0) P.s[b] = uint8_t(e);
+            if (row && (threadIdx.x & 3) == 0) P.s[b] = uint8_t(e);
             if (GATED) {
                 const uint32_t eu = mx_scale_code<MxE4M3>(block_max8(u));
                 if (in) *reinterpret_cast<uint2 *>(P.qu + k) = codes8(u, mx_unscale(eu));
-                if (t < n && (t & 3) == 0) P.su[b] = uint8_t(eu);
+                if (row && (threadIdx.x & 3) == 0) P.su[b] = uint8_t(eu);
             }
         }
         if (ACT != kSave && in) {
@@ -169,34 +172,47 @@ __global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P) {
     }
 }
 
-// One block a warp, one element a lane: any size, any address.
+// One block a warp and step, one element a lane: any size, any address.  Four
+// steps' loads are issued before the first is worked on.
+constexpr int kElemSteps = 4;
+
 template <int XT, int ACT, bool GATED, bool KEEP>
 __global__ void __launch_bounds__(kThreads) act_fwd_elem(ActFwd P) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const int64_t step = int64_t(gridDim.x) * (kThreads / 32);
-    for (int64_t b = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); b < P.blocks; b += step) {
-        const int64_t r = b / P.kb;
-        const int64_t col = (b - r * P.kb) * kMxBlock + lane;
-        const bool in = col < P.cols;
-        const int64_t k = r * P.cols + col;
-        const float x = in ? load_elem<XT>(P.x, k) : 0.0f;
-        const float u = GATED && in ? load_elem<XT>(P.u, k) : 0.0f;
-        if (KEEP) {
-            const uint32_t e = mx_scale_code<MxE4M3>(warp_max_u32(__float_as_uint(x) & 0x7FFFFFFFu));
-            if (in) P.q[k] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(x * mx_unscale(e), 0.0f));
-            if (lane == 0) P.s[b] = uint8_t(e);
-            if (GATED) {
-                const uint32_t eu = mx_scale_code<MxE4M3>(warp_max_u32(__float_as_uint(u) & 0x7FFFFFFFu));
-                if (in) P.qu[k] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(u * mx_unscale(eu), 0.0f));
-                if (lane == 0) P.su[b] = uint8_t(eu);
-            }
+    RowWalk at(int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), int64_t(gridDim.x) * (kThreads / 32), P.kb);
+    while (at.row < P.rows) {
+        float x[kElemSteps], u[kElemSteps];
+        int64_t k[kElemSteps], b[kElemSteps];  // element (-1: none), block (-1: none)
+#pragma unroll
+        for (int i = 0; i < kElemSteps; ++i) {
+            const int col = at.at * kMxBlock + lane;
+            b[i] = at.row < P.rows ? at.row * P.kb + at.at : -1;
+            k[i] = b[i] >= 0 && col < P.cols ? at.row * P.cols + col : -1;
+            x[i] = k[i] >= 0 ? load_elem<XT>(P.x, k[i]) : 0.0f;
+            u[i] = GATED && k[i] >= 0 ? load_elem<XT>(P.u, k[i]) : 0.0f;
+            at.next();
         }
-        if (ACT != kSave && in) {
-            float y = act_value<ACT>(x);
-            if (GATED) y *= u;
-            store_elem<XT>(P.y, k, y);
+#pragma unroll
+        for (int i = 0; i < kElemSteps; ++i) {
+            if (b[i] < 0) break;
+            if (KEEP) {
+                const uint32_t e = mx_scale_code<MxE4M3>(warp_max_u32(__float_as_uint(x[i]) & 0x7FFFFFFFu));
+                if (k[i] >= 0) P.q[k[i]] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(x[i], mx_unscale(e)), 0.0f));
+                if (lane == 0) P.s[b[i]] = uint8_t(e);
+                if (GATED) {
+                    const uint32_t eu = mx_scale_code<MxE4M3>(warp_max_u32(__float_as_uint(u[i]) & 0x7FFFFFFFu));
+                    if (k[i] >= 0)
+                        P.qu[k[i]] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(u[i], mx_unscale(eu)), 0.0f));
+                    if (lane == 0) P.su[b[i]] = uint8_t(eu);
+                }
+            }
+            if (ACT != kSave && k[i] >= 0) {
+                float y = act_value<ACT>(x[i]);
+                if (GATED) y *= u[i];
+                store_elem<XT>(P.y, k[i], y);
+            }
         }
     }
 }
@@ -205,14 +221,12 @@ template <int XT, int ACT, bool GATED>
 __global__ void __launch_bounds__(kThreads) act_bwd_vec(ActBwd P) {
     pdl_wait();
     pdl_trigger();
-    const int64_t n = P.blocks * 4;
-    for (int64_t t = int64_t(blockIdx.x) * kThreads + threadIdx.x; t < n;
-         t += int64_t(gridDim.x) * kThreads) {
-        const int64_t b = t >> 2;
-        const int64_t r = b / P.kb;
-        const int64_t col = (b - r * P.kb) * kMxBlock + 8 * (t & 3);
+    RowWalk at((int64_t(blockIdx.x) * kThreads + threadIdx.x) / 4, int64_t(gridDim.x) * (kThreads / 4), P.kb);
+    for (; at.row < P.rows; at.next()) {
+        const int64_t b = at.row * P.kb + at.at;
+        const int col = at.at * kMxBlock + 8 * (threadIdx.x & 3);
         if (col >= P.cols) continue;
-        const int64_t k = r * P.cols + col;
+        const int64_t k = at.row * P.cols + col;
         float x[8], u[8], g[8], o[8];
         values8(*reinterpret_cast<const uint2 *>(P.q + k), mx_scale(P.s[b]), x);
         if (GATED) values8(*reinterpret_cast<const uint2 *>(P.qu + k), mx_scale(P.su[b]), u);
@@ -238,40 +252,59 @@ __global__ void __launch_bounds__(kThreads) act_bwd_elem(ActBwd P) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const int64_t step = int64_t(gridDim.x) * (kThreads / 32);
-    for (int64_t b = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); b < P.blocks; b += step) {
-        const int64_t r = b / P.kb;
-        const int64_t col = (b - r * P.kb) * kMxBlock + lane;
-        if (col >= P.cols) continue;
-        const int64_t k = r * P.cols + col;
-        float v[4];
-        e4m3x4_to_f32x4(P.q[k], v);
-        const float x = __fmul_rn(v[0], mx_scale(P.s[b]));
-        if constexpr (ACT == kSave) {
-            store_elem<XT>(P.dx, k, x);
-        } else {
-            float g = load_elem<XT>(P.dy, k), f, d;
-            act_both<ACT>(x, f, d);
-            if (GATED) {
-                e4m3x4_to_f32x4(P.qu[k], v);
-                store_elem<XT>(P.du, k, g * f);
-                g *= __fmul_rn(v[0], mx_scale(P.su[b]));
+    RowWalk at(int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), int64_t(gridDim.x) * (kThreads / 32), P.kb);
+    while (at.row < P.rows) {
+        uint32_t q[kElemSteps], qu[kElemSteps];  // code, and the scale byte above it
+        float g[kElemSteps];
+        int64_t k[kElemSteps];
+#pragma unroll
+        for (int i = 0; i < kElemSteps; ++i) {
+            const int col = at.at * kMxBlock + lane;
+            const int64_t b = at.row * P.kb + at.at;
+            k[i] = at.row < P.rows && col < P.cols ? at.row * P.cols + col : -1;
+            q[i] = qu[i] = 0;
+            g[i] = 0.0f;
+            if (k[i] >= 0) {
+                q[i] = P.q[k[i]] | uint32_t(P.s[b]) << 8;
+                if (GATED) qu[i] = P.qu[k[i]] | uint32_t(P.su[b]) << 8;
+                if (ACT != kSave) g[i] = load_elem<XT>(P.dy, k[i]);
             }
-            store_elem<XT>(P.dx, k, g * d);
+            at.next();
+        }
+#pragma unroll
+        for (int i = 0; i < kElemSteps; ++i) {
+            if (k[i] < 0) continue;
+            float v[4];
+            e4m3x4_to_f32x4(q[i] & 0xFFu, v);
+            const float x = __fmul_rn(v[0], mx_scale(q[i] >> 8));
+            if constexpr (ACT == kSave) {
+                store_elem<XT>(P.dx, k[i], x);
+            } else {
+                float f, d;
+                act_both<ACT>(x, f, d);
+                float y = g[i];
+                if (GATED) {
+                    e4m3x4_to_f32x4(qu[i] & 0xFFu, v);
+                    store_elem<XT>(P.du, k[i], y * f);
+                    y *= __fmul_rn(v[0], mx_scale(qu[i] >> 8));
+                }
+                store_elem<XT>(P.dx, k[i], y * d);
+            }
         }
     }
 }
 
 bool ptr_ok(const void *p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) == 0; }
 
-unsigned grid_of(int64_t threads, int device) {
+// CTAs for that many threads' work, at most `most` an SM.
+unsigned grid_of(int64_t threads, int most, int device) {
     const int64_t want = (threads + kThreads - 1) / kThreads;
-    return unsigned(std::min<int64_t>(want, int64_t(sm_count(device)) * 64));
+    return unsigned(std::min<int64_t>(want, int64_t(sm_count(device)) * most));
 }
 
 template <int XT, int ACT, bool GATED>
 cudaError_t fwd(const ActFwd &P, bool keep, bool vec, int dev, cudaStream_t s) {
-    const dim3 block(kThreads), gv(grid_of(P.blocks * 4, dev)), ge(grid_of(P.blocks * 32, dev));
+    const dim3 block(kThreads), gv(grid_of(P.rows * P.kb * 4, VGRID, dev)), ge(grid_of(P.rows * P.kb * (32 / kElemSteps), 8, dev));
     if constexpr (ACT == kSave)
         return vec ? launch_pdl(act_fwd_vec<XT, ACT, GATED, true>, gv, block, 0, s, P)
                    : launch_pdl(act_fwd_elem<XT, ACT, GATED, true>, ge, block, 0, s, P);
@@ -285,8 +318,8 @@ cudaError_t fwd(const ActFwd &P, bool keep, bool vec, int dev, cudaStream_t s) {
 template <int XT, int ACT, bool GATED>
 cudaError_t bwd(const ActBwd &P, bool vec, int dev, cudaStream_t s) {
     const dim3 block(kThreads);
-    return vec ? launch_pdl(act_bwd_vec<XT, ACT, GATED>, dim3(grid_of(P.blocks * 4, dev)), block, 0, s, P)
-               : launch_pdl(act_bwd_elem<XT, ACT, GATED>, dim3(grid_of(P.blocks * 32, dev)), block, 0, s, P);
+    return vec ? launch_pdl(act_bwd_vec<XT, ACT, GATED>, dim3(grid_of(P.rows * P.kb * 4, VGRID, dev)), block, 0, s, P)
+               : launch_pdl(act_bwd_elem<XT, ACT, GATED>, dim3(grid_of(P.rows * P.kb * (32 / kElemSteps), 8, dev)), block, 0, s, P);
 }
 
 template <int XT>
@@ -319,8 +352,7 @@ cudaError_t bwd_x(const ActBwd &P, int act, bool vec, int dev, cudaStream_t s) {
 cudaError_t launch_act_fwd(int act, const void *x, const void *u, int elem, int64_t rows, int64_t cols,
                            void *y, uint8_t *q, uint8_t *sc, uint8_t *qu, uint8_t *su, int device,
                            cudaStream_t s) {
-    ActFwd P{x, u, y, q, sc, qu, su, rows, cols, (cols + kMxBlock - 1) / kMxBlock, 0};
-    P.blocks = rows * P.kb;
+    const ActFwd P{x, u, y, q, sc, qu, su, rows, cols, int((cols + kMxBlock - 1) / kMxBlock)};
     const bool vec = cols % 8 == 0 && ptr_ok(x, 15) && ptr_ok(u, 15) && ptr_ok(y, 15) && ptr_ok(q, 7) && ptr_ok(qu, 7);
     const int a = act < 0 ? int(kSave) : act;
     cudaError_t e = elem == kF32   ? fwd_x<kF32>(P, a, q != nullptr, vec, device, s)
@@ -332,8 +364,7 @@ cudaError_t launch_act_fwd(int act, const void *x, const void *u, int elem, int6
 cudaError_t launch_act_bwd(int act, const void *dy, int elem, int64_t rows, int64_t cols,
                            const uint8_t *q, const uint8_t *sc, const uint8_t *qu, const uint8_t *su,
                            void *dx, void *du, int device, cudaStream_t s) {
-    ActBwd P{dy, q, sc, qu, su, dx, du, rows, cols, (cols + kMxBlock - 1) / kMxBlock, 0};
-    P.blocks = rows * P.kb;
+    const ActBwd P{dy, q, sc, qu, su, dx, du, rows, cols, int((cols + kMxBlock - 1) / kMxBlock)};
     const bool vec = cols % 8 == 0 && ptr_ok(dy, 15) && ptr_ok(dx, 15) && ptr_ok(du, 15) && ptr_ok(q, 7) && ptr_ok(qu, 7);
     const int a = act < 0 ? int(kSave) : act;
     cudaError_t e = elem == kF32   ? bwd_x<kF32>(P, a, vec, device, s)

@@ -21,6 +21,9 @@
 #include "mx.cuh"
 #include "pdl.cuh"
 
+#ifndef QMB
+#define QMB 3
+#endif
 namespace amp {
 namespace {
 
@@ -54,7 +57,7 @@ __device__ __forceinline__ void transposing_max4(uint32_t (&w)[N], uint32_t (&r)
 }
 
 template <int XT, bool T>
-__global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : 4) fp4_quant_kernel(Fp4Quant P) {
+__global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : T ? QMB : 4) fp4_quant_kernel(Fp4Quant P) {
     __shared__ __align__(16) uint32_t s_t[T ? 128 * 16 : 4];  // transposed codes, 64 B a column
     __shared__ __align__(16) uint8_t s_rs[512];
     __shared__ __align__(16) uint8_t s_cs[T ? 512 : 16];
@@ -240,44 +243,80 @@ __global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : 4) fp4_quant_kernel
 // ---- values of the codes -------------------------------------------------
 struct Fp4Dequant {
     const uint8_t *q, *scales;
-    int64_t rows, cols, words;  // words: 8-element words a packed row
-    int64_t total;              // rows * words
+    int64_t rows, cols;
+    int words;  // VEC: 8-element words a packed row; else 256-element pieces of it
     void *out;
-    int vec;
 };
 
-// One packed word (8 elements) a thread.
+__device__ __forceinline__ uint32_t scale_at(const Fp4Dequant &P, int64_t r, int b) {
+    const int64_t tile = (r >> 7) * ((P.cols + kTile - 1) / kTile) + (b >> 2);
+    return P.scales[tile * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3)];
+}
+
+// Rows that are whole, aligned groups of 8: one packed word a thread and step,
+// four steps' loads before the first store.
 template <int XT>
-__global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(Fp4Dequant P) {
+__global__ void __launch_bounds__(kThreads) fp4_dequant_vec(Fp4Dequant P) {
     pdl_wait();
     pdl_trigger();
-    for (int64_t t = int64_t(blockIdx.x) * kThreads + threadIdx.x; t < P.total;
-         t += int64_t(gridDim.x) * kThreads) {
-        const int64_t r = t / P.words;
-        const int64_t w = t - r * P.words;
-        const int64_t col = 8 * w;
-        const int n = int(min(int64_t(8), P.cols - col));
-        if (n <= 0) continue;
-        const int64_t b = w >> 2;
-        const int64_t tile = (r >> 7) * ((P.cols + kTile - 1) / kTile) + (b >> 2);
-        const uint32_t e = P.scales[tile * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3)];
-        const uint32_t codes = reinterpret_cast<const uint32_t *>(P.q)[t];
-        const float s = mx_scale(e);
-        float y[8];
-        e2m1x8_to_f32x8(codes, y);
+    constexpr int U = 4;
+    RowWalk at(int64_t(blockIdx.x) * kThreads + threadIdx.x, int64_t(gridDim.x) * kThreads, P.words);
+    while (at.row < P.rows) {
+        uint32_t codes[U], e[U];
+        int64_t k[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(y[j], s);
-        const int64_t k = r * P.cols + col;
-        if (P.vec && n == 8) {
+        for (int i = 0; i < U; ++i) {
+            const bool in = at.row < P.rows && 8 * at.at < P.cols;
+            k[i] = in ? at.row * P.cols + 8 * at.at : -1;
+            if (in) {
+                codes[i] = reinterpret_cast<const uint32_t *>(P.q)[at.row * P.words + at.at];
+                e[i] = scale_at(P, at.row, at.at >> 2);
+            }
+            at.next();
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (k[i] < 0) continue;
+            const float s = mx_scale(e[i]);
+            float y[8];
+            e2m1x8_to_f32x8(codes[i], y);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) mul2_rn(y[j], y[j + 1], s, s, y[j], y[j + 1]);
             uint4 u[kWords8<XT>];
             f32_to_raw8<XT>(y, u);
 #pragma unroll
             for (int j = 0; j < kWords8<XT>; ++j)
-                st16(static_cast<char *>(P.out) + k * (XT == kF32 ? 4 : 2) + 16 * j, u[j]);
-        } else {
+                st16(static_cast<char *>(P.out) + k[i] * (XT == kF32 ? 4 : 2) + 16 * j, u[j]);
+        }
+    }
+}
+
+// Any row length and address: a warp takes 256 elements of a row, a lane one
+// packed word of them; the words then go round by shuffles so that each store
+// of the warp is 32 elements side by side.
+template <int XT>
+__global__ void __launch_bounds__(kThreads) fp4_dequant_elem(Fp4Dequant P) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t rowb = (P.cols + kMxBlock - 1) / kMxBlock * 16;
+    RowWalk at(int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), int64_t(gridDim.x) * (kThreads / 32),
+               P.words);
+    for (; at.row < P.rows; at.next()) {
+        const int c0 = 256 * at.at;
+        uint32_t codes = 0, e = 0;
+        if (c0 / 2 + 4 * lane < rowb) {
+            codes = *reinterpret_cast<const uint32_t *>(P.q + at.row * rowb + c0 / 2 + 4 * lane);
+            e = scale_at(P, at.row, c0 / 32 + lane / 4);
+        }
+        const int64_t k = at.row * P.cols + c0 + lane;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) store_elem<XT>(P.out, k + j, y[j]);
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t w = __shfl_sync(0xFFFFFFFFu, codes, 4 * j + lane / 8);
+            const uint32_t s = __shfl_sync(0xFFFFFFFFu, e, 4 * j);
+            float y[8];
+            e2m1x8_to_f32x8(w >> (4 * (lane & 7)), y);
+            if (c0 + 32 * j + lane < P.cols) store_elem<XT>(P.out, k + 32 * j, __fmul_rn(y[0], mx_scale(s)));
         }
     }
 }
@@ -315,22 +354,21 @@ cudaError_t launch_fp4_quant(const void *x, int xelem, int64_t rows, int64_t col
 
 cudaError_t launch_fp4_dequant(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t cols,
                                void *out, int oelem, int device, cudaStream_t s) {
-    Fp4Dequant P;
-    P.q = q;
-    P.scales = scales;
-    P.rows = rows;
-    P.cols = cols;
-    P.words = (cols + kMxBlock - 1) / kMxBlock * 4;
-    P.total = rows * P.words;
-    P.out = out;
     const int esz = oelem == kF32 ? 4 : 2;
-    P.vec = ((cols * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) ? 1 : 0;
-    const int64_t want = (P.total + kThreads - 1) / kThreads;
-    const dim3 grid((unsigned)std::min<int64_t>(want, int64_t(sm_count(device)) * 64)), block(kThreads);
+    const bool vec = cols % 8 == 0 && (cols * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    Fp4Dequant P{q, scales, rows, cols, 0, out};
+    P.words = int(vec ? (cols + kMxBlock - 1) / kMxBlock * 4 : (cols + 255) / 256);
+    const int64_t threads = rows * P.words * (vec ? 1 : 32);
+    const int64_t want = (threads + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)std::min<int64_t>(want, int64_t(sm_count(device)) * 8)), block(kThreads);
     cudaError_t e;
-    if (oelem == kF32) e = launch_pdl(fp4_dequant_kernel<kF32>, grid, block, 0, s, P);
-    else if (oelem == kF16) e = launch_pdl(fp4_dequant_kernel<kF16>, grid, block, 0, s, P);
-    else e = launch_pdl(fp4_dequant_kernel<kBF16>, grid, block, 0, s, P);
+#define FP4_D(XT)                                                             \
+    e = vec ? launch_pdl(fp4_dequant_vec<XT>, grid, block, 0, s, P)           \
+            : launch_pdl(fp4_dequant_elem<XT>, grid, block, 0, s, P)
+    if (oelem == kF32) FP4_D(kF32);
+    else if (oelem == kF16) FP4_D(kF16);
+    else FP4_D(kBF16);
+#undef FP4_D
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -179,4 +179,25 @@ __device__ __forceinline__ void load_raw8_tail(const void *x, int64_t k, int n, 
         u[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
+// Items 0 .. rows * per_row - 1 taken `step` apart: an item's row and place in
+// it, by one division at the start and additions from then on.
+struct RowWalk {
+    int64_t row, step_row;
+    int at, step_at, per_row;
+    __device__ __forceinline__ RowWalk(int64_t first, int64_t step, int per_row_) : per_row(per_row_) {
+        row = first / per_row;
+        at = int(first - row * per_row);
+        step_row = step / per_row;
+        step_at = int(step - step_row * per_row);
+    }
+    __device__ __forceinline__ void next() {
+        row += step_row;
+        at += step_at;
+        if (at >= per_row) {
+            at -= per_row;
+            ++row;
+        }
+    }
+};
+
 }  // namespace amp
