@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_vec(Fp4Dequant P) {
     pdl_wait();
     pdl_trigger();
     constexpr int U = 4;
-    RowWalk at(int64_t(blockIdx.x) * kThreads + threadIdx.x, int64_t(gridDim.x) * kThreads, P.words);
+    RowWalk at(blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads, P.words);
     while (at.row < P.rows) {
         uint32_t codes[U], e[U];
         int64_t k[U];
@@ -300,8 +300,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_elem(Fp4Dequant P) {
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int64_t rowb = (P.cols + kMxBlock - 1) / kMxBlock * 16;
-    RowWalk at(int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), int64_t(gridDim.x) * (kThreads / 32),
-               P.words);
+    RowWalk at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), P.words);
     for (; at.row < P.rows; at.next()) {
         const int c0 = 256 * at.at;
         uint32_t codes = 0, e = 0;
@@ -360,7 +359,7 @@ cudaError_t launch_fp4_dequant(const uint8_t *q, const uint8_t *scales, int64_t 
     P.words = int(vec ? (cols + kMxBlock - 1) / kMxBlock * 4 : (cols + 255) / 256);
     const int64_t threads = rows * P.words * (vec ? 1 : 32);
     const int64_t want = (threads + kThreads - 1) / kThreads;
-    const dim3 grid((unsigned)std::min<int64_t>(want, int64_t(sm_count(device)) * 8)), block(kThreads);
+    const dim3 grid((unsigned)std::min<int64_t>(want, int64_t(sm_count(device)) * 32)), block(kThreads);
     cudaError_t e;
 #define FP4_D(XT)                                                             \
     e = vec ? launch_pdl(fp4_dequant_vec<XT>, grid, block, 0, s, P)           \

@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 // ------------------------------------------------------------------ one CTA a tile
+constexpr uint32_t kMaxParts = 8;  // CTAs that share one tile's reduction
 constexpr int kSoloThreads = 256;  // load, issue, allocate, (idle), 4 store warps
 
 template <int BN>
@@ -509,18 +510,42 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
         tile_at(P, 16, first, tm, tn);
         const int64_t m0 = int64_t(tm) * BN;
         const int cols = int(min(int64_t(BN), P.m - m0));
-        const uint32_t part = smem_addr(smem);
-        const int l = threadIdx.x & 127;
-        const int64_t nn = int64_t(tn) * kLanes + l;
-        if (nn < P.n) {
-            // columns go round the CTAs and their two halves of threads
-            for (int c = int(rank) * 2 + (threadIdx.x >> 7); c < cols; c += 2 * int(parts)) {
-                float v = 0.0f;
-                for (uint32_t r = 0; r < parts; ++r) v += cluster_ld(part + (c * kLanes + l) * 4, r);
-                const int64_t k = (m0 + c) * P.n + nn;
-                if (P.ot == kF32) store_elem<kF32>(P.out, k, v);
-                else if (P.ot == kF16) store_elem<kF16>(P.out, k, v);
-                else store_elem<kBF16>(P.out, k, v);
+        uint32_t part[kMaxParts];
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxParts; ++r) part[r] = cluster_addr(smem, r < parts ? r : 0);
+        // groups of four neighbouring elements go round the CTAs' threads; the
+        // loads of one group's parts are issued together
+        for (int i = int(rank) * kSoloThreads + int(threadIdx.x); i < cols * (kLanes / 4);
+             i += int(parts) * kSoloThreads) {
+            const int c = i / (kLanes / 4), l = 4 * (i % (kLanes / 4));
+            float4 v[kMaxParts];
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxParts; ++r)
+                if (r < parts) v[r] = cluster_ld4(part[r] + uint32_t(c * kLanes + l) * 4);
+            float s[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (uint32_t r = 1; r < kMaxParts; ++r)
+                if (r < parts) {
+                    s[0] += v[r].x;
+                    s[1] += v[r].y;
+                    s[2] += v[r].z;
+                    s[3] += v[r].w;
+                }
+            const int64_t nn = int64_t(tn) * kLanes + l, k = (m0 + c) * P.n + nn;
+            if (P.packed && nn + 4 <= P.n) {
+                uint16_t *o = static_cast<uint16_t *>(P.out) + k;
+                const uint32_t a = P.ot == kF16 ? f32x2_to_16x2<kF16>(s[0], s[1]) : f32x2_to_16x2<kBF16>(s[0], s[1]);
+                const uint32_t b = P.ot == kF16 ? f32x2_to_16x2<kF16>(s[2], s[3]) : f32x2_to_16x2<kBF16>(s[2], s[3]);
+                reinterpret_cast<uint32_t *>(o)[0] = a;
+                reinterpret_cast<uint32_t *>(o)[1] = b;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (nn + j >= P.n) break;
+                    if (P.ot == kF32) store_elem<kF32>(P.out, k + j, s[j]);
+                    else if (P.ot == kF16) store_elem<kF16>(P.out, k + j, s[j]);
+                    else store_elem<kBF16>(P.out, k + j, s[j]);
+                }
             }
         }
         cluster_sync();  // nobody leaves while its shared memory is read
@@ -626,7 +651,7 @@ cudaError_t go(Fp4Product P, const void *a, const void *b, int64_t row_bytes, in
     const int64_t tiles = int64_t(P.tiles_m) * P.tiles_n, room = int64_t(sm_count(device)) * S::ctas;
     const int ks = (P.kt + 1) / 2;
     int parts = 1;
-    while (parts < 8 && tiles * parts * 2 <= room && parts * 2 <= ks) parts *= 2;
+    while (parts < int(kMaxParts) && tiles * parts * 2 <= room && parts * 2 <= ks) parts *= 2;
     void *args[] = {&mt, &mw, &P};
     if (parts > 1)
         return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, true>), unsigned(tiles * parts),
@@ -654,7 +679,7 @@ cudaError_t launch_fp4_product(const void *a, const uint8_t *sa, const void *b, 
     P.m = m;
     P.n = n;
     P.ot = oelem;
-    P.packed = n % 2 == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
+    P.packed = oelem != kF32 && n % 2 == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
     P.kt = int((k + 127) / 128);
     P.k64 = int((k + 63) / 64);
     const int64_t row_bytes = (k + kMxBlock - 1) / kMxBlock * 16;

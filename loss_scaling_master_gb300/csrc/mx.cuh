@@ -179,16 +179,18 @@ __device__ __forceinline__ void load_raw8_tail(const void *x, int64_t k, int n, 
         u[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
-// Items 0 .. rows * per_row - 1 taken `step` apart: an item's row and place in
-// it, by one division at the start and additions from then on.
+// Items 0 .. rows * per_row - 1 taken `step` apart (a grid's worth, so below
+// 2^32): an item's row and place in it, by 32-bit divisions at the start and
+// additions from then on.
 struct RowWalk {
-    int64_t row, step_row;
-    int at, step_at, per_row;
-    __device__ __forceinline__ RowWalk(int64_t first, int64_t step, int per_row_) : per_row(per_row_) {
-        row = first / per_row;
-        at = int(first - row * per_row);
-        step_row = step / per_row;
-        step_at = int(step - step_row * per_row);
+    int64_t row;
+    int at, step_row, step_at, per_row;
+    __device__ __forceinline__ RowWalk(uint32_t first, uint32_t step, int per_row_) : per_row(per_row_) {
+        const uint32_t r = first / uint32_t(per_row), s = step / uint32_t(per_row);
+        row = r;
+        at = int(first - r * uint32_t(per_row));
+        step_row = int(s);
+        step_at = int(step - s * uint32_t(per_row));
     }
     __device__ __forceinline__ void next() {
         row += step_row;

@@ -214,12 +214,12 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// the float at this shared-memory address of CTA `rank` of the cluster
-__device__ __forceinline__ float cluster_ld(uint32_t saddr, uint32_t rank) {
-    float v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-                 : "=f"(v)
-                 : "r"(saddr), "r"(rank)
+// four floats at an address of the cluster's shared memory
+__device__ __forceinline__ float4 cluster_ld4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
                  : "memory");
     return v;
 }
