@@ -21,9 +21,6 @@
 #include "mx.cuh"
 #include "pdl.cuh"
 
-#ifndef QMB
-#define QMB 3
-#endif
 namespace amp {
 namespace {
 
@@ -57,7 +54,7 @@ __device__ __forceinline__ void transposing_max4(uint32_t (&w)[N], uint32_t (&r)
 }
 
 template <int XT, bool T>
-__global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : T ? QMB : 4) fp4_quant_kernel(Fp4Quant P) {
+__global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : 4) fp4_quant_kernel(Fp4Quant P) {
     __shared__ __align__(16) uint32_t s_t[T ? 128 * 16 : 4];  // transposed codes, 64 B a column
     __shared__ __align__(16) uint8_t s_rs[512];
     __shared__ __align__(16) uint8_t s_cs[T ? 512 : 16];
@@ -150,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : T ? QMB : 4) fp4_qu
         }
     }
 
-    // ---- rows: scale bytes, codes
+    // ---- scale bytes
     const uint32_t e0 = mx_scale_code<MxE2M1>(rmax[0]), e1 = mx_scale_code<MxE2M1>(rmax[1]);
     {
         // byte (r % 32) * 16 + r / 32 * 4 + block, rows lr + 2 (cl % 4) + {0, 1}
@@ -158,62 +155,60 @@ __global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : T ? QMB : 4) fp4_qu
         s[0] = uint8_t(e0);
         s[16] = uint8_t(e1);
     }
+    float fc[T ? 8 : 1];  // the lane's columns' multipliers
+    if constexpr (T) {
+        const uint32_t d0 = mx_scale_code<MxE2M1>(cmax[0]), d1 = mx_scale_code<MxE2M1>(cmax[1]);
+        const int c = lc + 2 * rl;  // c and c + 1 are in the same group of 32 columns
+        uint8_t *s = s_cs + (c % 32) * 16 + (c / 32) * 4 + (warp >> 1);
+        s[0] = uint8_t(d0);
+        s[16] = uint8_t(d1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t e = __shfl_sync(0xFFFFFFFFu, d0 | (d1 << 16), cl + 8 * k);
+            fc[2 * k] = mx_unscale(e & 0xFFFFu);
+            fc[2 * k + 1] = mx_unscale(e >> 16);
+        }
+    }
+
+    // ---- codes, two rows at a time: each element is widened once for both
+    // orientations; the two rows make one byte of each column's word
     const int64_t rowb = (P.cols + kMxBlock - 1) / kMxBlock * 16;  // bytes a packed row
     const bool colin = col / 2 < rowb;
+    uint8_t *out = P.out + row * rowb + col / 2;
+    uint32_t cw[T ? 8 : 1];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const uint32_t e = __shfl_sync(0xFFFFFFFFu, e0 | (e1 << 16), (lane & ~3) + k);
+        float y[2][8], z[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = 2 * k + h;
             const float f = mx_unscale(h ? e >> 16 : e & 0xFFFFu);
-            float y[8];
-            raw8_to_f32<XT>(raw[i], y);
+            raw8_to_f32<XT>(raw[i], y[h]);
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) mul2_rn(y[j], y[j + 1], f, f, y[j], y[j + 1]);
-            const uint32_t w = f32x8_to_e2m1x8(y);
-            if (colin && row + i < P.rows)
-                *reinterpret_cast<uint32_t *>(P.out + (row + i) * rowb + col / 2) = w;
+            for (int j = 0; j < 8; j += 2) mul2_rn(y[h][j], y[h][j + 1], f, f, z[j], z[j + 1]);
+            const uint32_t w = f32x8_to_e2m1x8(z);
+            if (colin && row + i < P.rows) *reinterpret_cast<uint32_t *>(out + i * rowb) = w;
         }
-    }
-
-    // ---- columns
-    if constexpr (T) {
-        const uint32_t d0 = mx_scale_code<MxE2M1>(cmax[0]), d1 = mx_scale_code<MxE2M1>(cmax[1]);
-        {
-            const int c = lc + 2 * rl;  // c and c + 1 are in the same group of 32 columns
-            uint8_t *s = s_cs + (c % 32) * 16 + (c / 32) * 4 + (warp >> 1);
-            s[0] = uint8_t(d0);
-            s[16] = uint8_t(d1);
-        }
+        if constexpr (T) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t e = __shfl_sync(0xFFFFFFFFu, d0 | (d1 << 16), cl + 8 * k);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = 2 * k + h;
-                const float f = mx_unscale(h ? e >> 16 : e & 0xFFFFu);
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if constexpr (XT == kF32) {
-                        const uint4 q = raw[i][j / 4];
-                        y[i] = __uint_as_float(j % 4 == 0 ? q.x : j % 4 == 1 ? q.y : j % 4 == 2 ? q.z : q.w);
-                    } else {
-                        const uint4 q = raw[i][0];
-                        const uint32_t w = j / 2 == 0 ? q.x : j / 2 == 1 ? q.y : j / 2 == 2 ? q.z : q.w;
-                        if constexpr (XT == kBF16)
-                            y[i] = __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
-                        else
-                            y[i] = f16_bits_to_f32(j & 1 ? w >> 16 : w & 0xFFFFu);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) mul2_rn(y[i], y[i + 1], f, f, y[i], y[i + 1]);
-                // column lc + j, row group lr / 8, 16-byte pieces permuted by cl
-                s_t[(lc + j) * 16 + ((lr / 8) ^ ((cl & 3) << 2))] = f32x8_to_e2m1x8(y);
+            for (int j = 0; j < 8; j += 2) {
+                float a0, a1, b0, b1;
+                mul2_rn(y[0][j], y[0][j + 1], fc[j], fc[j + 1], a0, a1);
+                mul2_rn(y[1][j], y[1][j + 1], fc[j], fc[j + 1], b0, b1);
+                const uint32_t p = f32x2_to_e2m1x2(a0, b0), q = f32x2_to_e2m1x2(a1, b1);
+                cw[j] = k == 0 ? p : cw[j] + (p << (8 * k));
+                cw[j + 1] = k == 0 ? q : cw[j + 1] + (q << (8 * k));
             }
         }
+    }
+    if constexpr (T) {
+        // column lc + j, row group lr / 8; 16-byte pieces permuted by cl, and
+        // odd and even columns exchanged in every other group of 32, so that a
+        // warp's words fall into 32 banks
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s_t[((lc + j) ^ ((cl >> 2) & 1)) * 16 + ((lr / 8) ^ ((cl & 3) << 2))] = cw[j];
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -235,7 +230,8 @@ __global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : T ? QMB : 4) fp4_qu
             const int c = (threadIdx.x >> 2) + 64 * k;
             if (c0 + c < P.cols && at < rowb_t)
                 st16(P.out_t + (c0 + c) * rowb_t + at,
-                     *reinterpret_cast<const uint4 *>(&s_t[c * 16 + ((q ^ ((c >> 3) & 3)) << 2)]));
+                     *reinterpret_cast<const uint4 *>(
+                         &s_t[(c ^ ((c >> 5) & 1)) * 16 + ((q ^ ((c >> 3) & 3)) << 2)]));
         }
     }
 }

@@ -31,6 +31,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "internal.h"
 #include "mx.cuh"
@@ -604,10 +605,15 @@ cudaError_t scales_map(CUtensorMap *m, const void *base, int64_t tile_rows, int 
                     CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-cudaError_t launch(const void *kernel, unsigned grid, int threads, int smem, int cluster, cudaStream_t s,
-                   void **args) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+// ready: one bit a device, set once the kernel's shared memory is granted there
+cudaError_t launch(const void *kernel, std::atomic<uint64_t> &ready, int device, unsigned grid, int threads, int smem,
+                   int cluster, cudaStream_t s, void **args) {
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if ((ready.load(std::memory_order_relaxed) & bit) == 0) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(unsigned(threads));
@@ -635,7 +641,8 @@ cudaError_t go_pair(Fp4Product P, const void *a, const void *b, int64_t row_byte
     P.tiles_n = int((P.n + 255) / 256);
     const int64_t tiles = int64_t(P.tiles_m) * P.tiles_n;
     void *args[] = {&mt, &mw, &mst, &msw, &P};
-    return launch(reinterpret_cast<const void *>(&fp4_product_pair_kernel),
+    static std::atomic<uint64_t> ready{0};
+    return launch(reinterpret_cast<const void *>(&fp4_product_pair_kernel), ready, device,
                   unsigned(2 * std::min<int64_t>(tiles, sm_count(device) / 2)), kPairThreads, Pair::smem, 2, s, args);
 }
 
@@ -653,10 +660,11 @@ cudaError_t go(Fp4Product P, const void *a, const void *b, int64_t row_bytes, in
     int parts = 1;
     while (parts < int(kMaxParts) && tiles * parts * 2 <= room && parts * 2 <= ks) parts *= 2;
     void *args[] = {&mt, &mw, &P};
+    static std::atomic<uint64_t> ready[2];
     if (parts > 1)
-        return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, true>), unsigned(tiles * parts),
+        return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, true>), ready[1], device, unsigned(tiles * parts),
                       kSoloThreads, S::smem, parts, s, args);
-    return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, false>),
+    return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, false>), ready[0], device,
                   unsigned(std::min<int64_t>(tiles, room)), kSoloThreads, S::smem, 1, s, args);
 }
 
