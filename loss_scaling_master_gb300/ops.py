@@ -43,7 +43,7 @@ def _load():
     L.fp4_mx_check.argtypes = [P]
     L.amp_layer_norm_forward.argtypes = [P, i32, i64, i64, P, P, i32, dbl, P, P, P, P, P, P]
     L.amp_layer_norm_workspace_bytes.argtypes = [i64, i64]
-    L.amp_layer_norm_backward.argtypes = [P, P, i32, P, P, i64, i64, P, i32, P, P, P, P, P, P, i64, P]
+    L.amp_layer_norm_backward.argtypes = ([P, P, i32, P, P, i64, i64, P, i32] + [P] * 6 + [i64, P])
     L.amp_act_forward_mx8.argtypes = [i32, P, P, i32, i64, i64, P, P, P, P, P, P]
     L.amp_act_backward_mx8.argtypes = [i32, P, i32, i64, i64, P, P, P, P, P, P, P]
     L.amp_ckpt8_save.argtypes = [P, i32, i64, i64, P, P, P]
@@ -59,6 +59,8 @@ def _load():
 # there are conditions, and a refused tensor goes to _buf for its message.
 _ELEM = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}
 _F32, _I32, _U8, _E4M3 = torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+_ONE_BYTE = frozenset((torch.uint8, torch.int8, torch.float8_e4m3fn, torch.float8_e5m2, torch.bool))
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _mat(t, what: str):
@@ -82,25 +84,25 @@ def _ptr(t, what: str, numel: int, dtype=None):
     """Address of a contiguous GPU tensor of the dtype with at least numel elements (None: none)."""
     if t is None:
         return None
-    if not (t.is_cuda and t.is_contiguous()) or (dtype is not None and t.dtype is not dtype) \
-            or t.numel() < numel:
-        _buf(t, what, dtype, numel)
-    return t.data_ptr()
+    if t.is_cuda and t.is_contiguous() and t.numel() >= numel \
+            and (dtype is None or t.dtype is dtype):
+        return t.data_ptr()
+    return _buf(t, what, dtype, numel)
 
 
 def _bytes(t, what: str, nbytes: int):
     """Address of a contiguous GPU tensor of one-byte elements, at least nbytes of them."""
     if t is None:
         return None
-    if not (t.is_cuda and t.is_contiguous()) or t.element_size() != 1 or t.numel() < nbytes:
-        _buf(t, what, numel=nbytes, itemsize=1)
-    return t.data_ptr()
+    if t.is_cuda and t.is_contiguous() and t.numel() >= nbytes and t.dtype in _ONE_BYTE:
+        return t.data_ptr()
+    return _buf(t, what, numel=nbytes, itemsize=1)
 
 
 def _stream(stream):
     """Handle of the stream: the current one of the current device for None."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -110,7 +112,7 @@ def _fp4_sizes(rows: int, cols: int):
 
 
 def fp4_mx_buffers(rows: int, cols: int, device="cuda"):
-    """(q, scales) for a [rows, cols] matrix: uint8 [rows, 16 ceil(cols/32)] and the tiled scales."""
+    """(q, scales) for a [rows, cols] matrix: uint8 [rows, 16 ceil(cols/32)], the tiled scales."""
     nq, ns = _load().fp4_mx_bytes(rows, cols), _load().fp4_mx_scale_bytes(rows, cols)
     if nq < 0 or ns < 0:
         raise ValueError(f"[{rows}, {cols}]: negative or too large")
@@ -119,7 +121,7 @@ def fp4_mx_buffers(rows: int, cols: int, device="cuda"):
 
 
 def ckpt8_buffers(rows: int, cols: int, device="cuda"):
-    """(q, scales) of an 8-bit checkpoint: float8_e4m3fn [rows, cols], uint8 [rows, ceil(cols/32)]."""
+    """(q, scales) of a checkpoint: float8_e4m3fn [rows, cols], uint8 [rows, ceil(cols/32)]."""
     return (torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device),
             torch.empty((rows, -(-cols // 32)), dtype=torch.uint8, device=device))
 
@@ -128,11 +130,14 @@ def fp4_quant_mx(x, q, scales, qt=None, scales_t=None, skip_if=None, stream=None
     """x [rows, cols] -> 4-bit blocks along its rows (q, scales) and, with qt, of its transpose."""
     rows, cols = _mat(x, "x")
     nq, ns = _fp4_sizes(rows, cols)
-    nqt, nst = _fp4_sizes(cols, rows) if qt is not None else (0, 0)
+    if qt is not None or scales_t is not None:
+        nqt, nst = _fp4_sizes(cols, rows)
+        qt, scales_t = _bytes(qt, "qt", nqt), _bytes(scales_t, "scales_t", nst)
     st = (_ready or _load()).fp4_quant_mx(
         _ptr(x, "x", 0), _code(x, "x"), rows, cols, _bytes(q, "q", nq),
-        _bytes(scales, "scales", ns), _bytes(qt, "qt", nqt), _bytes(scales_t, "scales_t", nst),
-        _ptr(skip_if, "skip_if", 1, _I32), _stream(stream))
+        _bytes(scales, "scales", ns), qt, scales_t,
+        None if skip_if is None else _ptr(skip_if, "skip_if", 1, _I32),
+        _stream(stream))
     if st:
         _check("fp4_quant_mx", st)
 
