@@ -77,11 +77,21 @@ __device__ __forceinline__ int norm_count(int v, int t, int cols) {
     return left <= 0 ? 0 : min(8, (left + TPR - 1) / TPR);
 }
 
-// Raw words of the 8 elements from element k of the tensor, n of them in the
-// row; the rest are zeros.
+// Elements from a thread's first element of a row to element j of its group v.
+// (The kernels keep a pointer to that first element and move it on by a row:
+// with an index worked out for every access, address arithmetic was a quarter
+// of the instructions.)
+template <bool VEC, int TPR>
+__host__ __device__ constexpr int norm_step(int v, int j) {
+    return VEC ? 8 * v * TPR + j : (8 * v + j) * TPR;
+}
+
+// Raw words of the 8 elements of group v behind x, n of them in the row; the
+// rest are zeros.
 template <int XT, bool VEC, int TPR>
-__device__ __forceinline__ void ld8(const void *x, int64_t k, int n, uint4 (&u)[kWords8<XT>]) {
+__device__ __forceinline__ void ld8(const void *x, int v, int n, uint4 (&u)[kWords8<XT>]) {
     constexpr int esz = XT == kF32 ? 4 : 2;
+    const int k = norm_step<VEC, TPR>(v, 0);
     if constexpr (VEC) {
 #pragma unroll
         for (int i = 0; i < kWords8<XT>; ++i)
@@ -118,8 +128,9 @@ __device__ __forceinline__ void split8(const f2 (&y)[4], float (&f)[8]) {
     }
 }
 template <int XT, bool VEC, int TPR>
-__device__ __forceinline__ void st8(void *x, int64_t k, int n, const f2 (&y)[4]) {
+__device__ __forceinline__ void st8(void *x, int v, int n, const f2 (&y)[4]) {
     constexpr int esz = XT == kF32 ? 4 : 2;
+    const int k = norm_step<VEC, TPR>(v, 0);
     float f[8];
     split8(y, f);
     if constexpr (VEC) {
@@ -160,29 +171,36 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// The sums of N values over the TPR threads of a row, given to all of them.
-// Every thread of the CTA calls it (it synchronises); s: CTA scratch of N * 32
-// floats, another one for the next call.
+// The sums of one or two values over the TPR threads of a row, given to all of
+// them.  Every thread of the CTA calls it (it synchronises); s: CTA scratch of
+// N * 32 floats, another one for the next call.  Two values share the steps:
+// after the first, each half of a warp carries one of them.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float *s) {
+    static_assert(N == 1 || N == 2, "values");
+    constexpr uint32_t all = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float a = v[0];
+    if constexpr (N == 2) {
+        const bool hi = lane & 16;
+        a = (hi ? v[1] : v[0]) + __shfl_xor_sync(all, hi ? v[0] : v[1], 16);
+    } else {
+        a += __shfl_xor_sync(all, a, 16);
+    }
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(all, a, o);
     if constexpr (TPR > 32) {
         constexpr int W = TPR / 32;
-        const int warp = threadIdx.x >> 5, first = warp / W * W;
-        if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) s[i * 32 + warp] = v[i];
-        }
+        if ((lane & 15) == 0 && (N == 2 || lane == 0)) s[(lane >> 4) * 32 + warp] = a;
         __syncthreads();
+        // lane i of each half takes warp i's part of the half's value
+        const float p = s[(N == 2 ? lane & 16 : 0) * 2 + warp / W * W + (lane & (W - 1))];
+        a = p;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float t = 0.0f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) t += s[i * 32 + first + w];
-            v[i] = t;
-        }
+        for (int o = W / 2; o > 0; o >>= 1) a += __shfl_xor_sync(all, a, o);
     }
+    v[0] = N == 2 || TPR == 32 ? __shfl_sync(all, a, 0) : a;
+    if constexpr (N == 2) v[1] = __shfl_sync(all, a, 16);
 }
 
 __host__ __device__ constexpr int norm_cta(int tpr) { return tpr > 256 ? tpr : 256; }

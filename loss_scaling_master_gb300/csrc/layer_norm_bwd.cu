@@ -37,35 +37,31 @@ struct Group {
     uint4 x[CK ? 1 : kWords8<XT>];
 };
 
+// dy, x, q, s: the places of the thread's first element.
 template <int XT, bool CK, bool VEC, int TPR>
-__device__ __forceinline__ void load_pair(const NormBwd &P, int64_t r, int v, int t, int n, Group<XT, CK> &g) {
-    const int c = norm_col<VEC, TPR>(v, t, 0);
-    const int64_t k = r * P.cols + c;
-    ld8<XT, VEC, TPR>(P.dy, k, n, g.dy);
+__device__ __forceinline__ void load_pair(const char *dy, const char *x, const uint8_t *q, const uint8_t *s, int v,
+                                          int n, Group<XT, CK> &g) {
+    ld8<XT, VEC, TPR>(dy, v, n, g.dy);
     if constexpr (!CK) {
-        ld8<XT, VEC, TPR>(P.x, k, n, g.x);
-    } else {
-        const int64_t kb = (P.cols + kMxBlock - 1) / kMxBlock;
-        const uint8_t *s = P.s + r * kb;
-        if constexpr (VEC) {
-            uint2 u = make_uint2(0, 0);
-            uint32_t e = 0;
-            if (n > 0) {
-                u = *reinterpret_cast<const uint2 *>(P.q + k);
-                e = s[c / 32];
-            }
-            g.x[0] = make_uint4(u.x, u.y, e, 0);
-        } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = 0;
-                if (2 * i < n) w[i] = P.q[k + 2 * i * TPR] | uint32_t(s[(c + 2 * i * TPR) / 32]) << 16;
-                if (2 * i + 1 < n)
-                    w[i] |= uint32_t(P.q[k + (2 * i + 1) * TPR]) << 8 | uint32_t(s[(c + (2 * i + 1) * TPR) / 32]) << 24;
-            }
-            g.x[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        ld8<XT, VEC, TPR>(x, v, n, g.x);
+    } else if constexpr (VEC) {
+        uint2 u = make_uint2(0, 0);
+        uint32_t e = 0;
+        if (n > 0) {
+            u = *reinterpret_cast<const uint2 *>(q + norm_step<true, TPR>(v, 0));
+            e = s[norm_step<true, TPR>(v, 0) / kMxBlock];
         }
+        g.x[0] = make_uint4(u.x, u.y, e, 0);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int a = norm_step<false, TPR>(v, 2 * i), b = norm_step<false, TPR>(v, 2 * i + 1);
+            w[i] = 0;
+            if (2 * i < n) w[i] = q[a] | uint32_t(s[a / kMxBlock]) << 16;
+            if (2 * i + 1 < n) w[i] |= uint32_t(q[b]) << 8 | uint32_t(s[b / kMxBlock]) << 24;
+        }
+        g.x[0] = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 // dy and x - mean (a code times its power of two is exact, so one fused
@@ -105,14 +101,20 @@ __global__ void __launch_bounds__(norm_cta(TPR), norm_cta(TPR) == 256 && NV <= 2
     pdl_trigger();
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     f2 aw[NV][4], ab[NV][4], w[HOLD ? NV : 1][4];
-    const int64_t step = int64_t(gridDim.x) * RPC;
+    constexpr int esz = XT == kF32 ? 4 : 2;
+    const int64_t step = int64_t(gridDim.x) * RPC, hop = step * P.cols, kb = (P.cols + kMxBlock - 1) / kMxBlock;
     int64_t r = int64_t(blockIdx.x) * RPC + sub;
+    const int c0 = norm_col<VEC, TPR>(0, t, 0);
+    const int64_t k0 = r * P.cols + c0;
+    const char *dyp = static_cast<const char *>(P.dy) + k0 * esz, *xp = static_cast<const char *>(P.x) + k0 * esz;
+    const uint8_t *qp = P.q + k0, *sp = P.s + r * kb + c0 / kMxBlock;
+    char *dxp = static_cast<char *>(P.dx) + k0 * esz;
     int len[NV];
     Group<XT, CK> nxt[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         len[v] = norm_count<VEC, TPR>(v, t, int(P.cols));
-        load_pair<XT, CK, VEC, TPR>(P, r, v, t, r < P.rows ? len[v] : 0, nxt[v]);
+        load_pair<XT, CK, VEC, TPR>(dyp, xp, qp, sp, v, r < P.rows ? len[v] : 0, nxt[v]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) aw[v][i] = ab[v][i] = both(0.0f);
         if (HOLD) ld_params<VEC, TPR>(P.w, P.wt, v, t, len[v], 1.0f, w[HOLD ? v : 0]);
@@ -143,12 +145,16 @@ __global__ void __launch_bounds__(norm_cta(TPR), norm_cta(TPR) == 256 && NV <= 2
                 s1 = fma2(g[v][i], xh[v][i], s1);
             }
         }
-        const int64_t rn = r + step;
+        const bool more = r + step < P.rows;
+        dyp += hop * esz;
+        xp += hop * esz;
+        qp += hop;
+        sp += step * kb;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) load_pair<XT, CK, VEC, TPR>(P, rn, v, t, rn < P.rows ? len[v] : 0, nxt[v]);
-        if (rn < P.rows) {
-            nmean = P.mean[rn];
-            nrstd = P.rstd[rn];
+        for (int v = 0; v < NV; ++v) load_pair<XT, CK, VEC, TPR>(dyp, xp, qp, sp, v, more ? len[v] : 0, nxt[v]);
+        if (more) {
+            nmean = P.mean[r + step];
+            nrstd = P.rstd[r + step];
         }
         float sums[2] = {sum2(s0), sum2(s1)};
         row_sums<TPR>(sums, scratch[buf]);
@@ -160,9 +166,10 @@ __global__ void __launch_bounds__(norm_cta(TPR), norm_cta(TPR) == 256 && NV <= 2
                 f2 o[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[i] = fma2(g[v][i], rs, fma2(xh[v][i], c1, c0));
-                st8<XT, VEC, TPR>(P.dx, r * P.cols + norm_col<VEC, TPR>(v, t, 0), len[v], o);
+                st8<XT, VEC, TPR>(dxp, v, len[v], o);
             }
         }
+        dxp += hop * esz;
     }
     if (!P.part) return;
     float *out = P.part + int64_t(blockIdx.x) * 2 * P.cols;

@@ -34,11 +34,11 @@ __host__ __device__ constexpr int fwd_ctas(int tpr, int nv) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// The checkpoint of a thread's 8 elements of row r; the warp calls it together.
+// The checkpoint of a thread's group v; the warp calls it together.  q, sc: the
+// places of the thread's first element's code and scale byte.
 template <int XT, bool VEC, int TPR>
-__device__ __forceinline__ void keep8(const NormFwd &P, int64_t r, int v, int t, int n,
-                                      const uint4 (&raw)[kWords8<XT>], const f2 (&x)[4]) {
-    const int64_t kb = (P.cols + kMxBlock - 1) / kMxBlock;
+__device__ __forceinline__ void keep8(uint8_t *q, uint8_t *sc, int v, int n, const uint4 (&raw)[kWords8<XT>],
+                                      const f2 (&x)[4]) {
     float f[8];
     split8(x, f);
     if constexpr (VEC) {
@@ -62,17 +62,17 @@ __device__ __forceinline__ void keep8(const NormFwd &P, int64_t r, int v, int t,
             const float2 z = split(mul2(x[i], u));
             h[i] = f32x2_to_fp8x2_raw<kE4M3>(z.x, z.y);
         }
-        const int c = norm_col<true, TPR>(v, t, 0);
-        *reinterpret_cast<uint2 *>(P.q + r * P.cols + c) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-        if ((c & 31) == 0) P.s[r * kb + c / 32] = uint8_t(e);
+        *reinterpret_cast<uint2 *>(q + norm_step<true, TPR>(v, 0)) =
+            make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        if ((threadIdx.x & 3) == 0) sc[norm_step<true, TPR>(v, 0) / kMxBlock] = uint8_t(e);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t e = mx_scale_code<MxE4M3>(warp_max_u32(abs_bits(f[j])));
             if (j >= n) continue;
-            const int c = norm_col<false, TPR>(v, t, j);
-            P.q[r * P.cols + c] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(f[j], mx_unscale(e)), 0.0f));
-            if ((c & 31) == 0) P.s[r * kb + c / 32] = uint8_t(e);
+            q[norm_step<false, TPR>(v, j)] =
+                uint8_t(f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(f[j], mx_unscale(e)), 0.0f));
+            if ((threadIdx.x & 31) == 0) sc[norm_step<false, TPR>(v, j) / kMxBlock] = uint8_t(e);
         }
     }
 }
@@ -85,15 +85,21 @@ __global__ void __launch_bounds__(norm_cta(TPR), (fwd_ctas<XT, VEC>(TPR, NV)))
     pdl_trigger();
     constexpr int RPC = norm_rpc(TPR);
     const int t = threadIdx.x % TPR;
-    const int64_t step = int64_t(gridDim.x) * RPC;
+    constexpr int esz = XT == kF32 ? 4 : 2;
+    const int64_t step = int64_t(gridDim.x) * RPC, kb = (P.cols + kMxBlock - 1) / kMxBlock;
     int64_t r = int64_t(blockIdx.x) * RPC + threadIdx.x / TPR;
+    const int c0 = norm_col<VEC, TPR>(0, t, 0);
+    const int64_t hop = step * P.cols;
+    const char *xp = static_cast<const char *>(P.x) + (r * P.cols + c0) * esz;
+    char *yp = static_cast<char *>(P.y) + (r * P.cols + c0) * esz;
+    uint8_t *qp = P.q + r * P.cols + c0, *sp = P.s + r * kb + c0 / kMxBlock;
     int n[NV];
     f2 w[NV][4], b[NV][4];
     uint4 nxt[NV][kWords8<XT>];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         n[v] = norm_count<VEC, TPR>(v, t, int(P.cols));
-        ld8<XT, VEC, TPR>(P.x, r * P.cols + norm_col<VEC, TPR>(v, t, 0), r < P.rows ? n[v] : 0, nxt[v]);
+        ld8<XT, VEC, TPR>(xp, v, r < P.rows ? n[v] : 0, nxt[v]);
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -115,16 +121,18 @@ __global__ void __launch_bounds__(norm_cta(TPR), (fwd_ctas<XT, VEC>(TPR, NV)))
             to_f32<XT>(raw[v], x[v]);
             s2 = add2(s2, add2(add2(x[v][0], x[v][1]), add2(x[v][2], x[v][3])));
         }
-        const int64_t rn = r + step;
+        const bool more = r + step < P.rows;
+        xp += hop * esz;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            ld8<XT, VEC, TPR>(P.x, rn * P.cols + norm_col<VEC, TPR>(v, t, 0), rn < P.rows ? n[v] : 0, nxt[v]);
+        for (int v = 0; v < NV; ++v) ld8<XT, VEC, TPR>(xp, v, more ? n[v] : 0, nxt[v]);
         a[0] = sum2(s2);
         row_sums<TPR>(a, scratch[buf][0]);
         const float mean = a[0] * P.inv_d;
         if (P.q) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) keep8<XT, VEC, TPR>(P, r, v, t, in ? n[v] : 0, raw[v], x[v]);
+            for (int v = 0; v < NV; ++v) keep8<XT, VEC, TPR>(qp, sp, v, in ? n[v] : 0, raw[v], x[v]);
+            qp += hop;
+            sp += step * kb;
         }
         s2 = both(0.0f);
         const f2 off = both(-mean);
@@ -157,8 +165,9 @@ __global__ void __launch_bounds__(norm_cta(TPR), (fwd_ctas<XT, VEC>(TPR, NV)))
             f2 o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = fma2(mul2(x[v][i], rs), w[v][i], b[v][i]);
-            st8<XT, VEC, TPR>(P.y, r * P.cols + norm_col<VEC, TPR>(v, t, 0), in ? n[v] : 0, o);
+            st8<XT, VEC, TPR>(yp, v, in ? n[v] : 0, o);
         }
+        yp += hop * esz;
     }
 }
 
