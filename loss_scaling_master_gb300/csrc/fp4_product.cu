@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 // ------------------------------------------------------------------ one CTA a tile
-constexpr uint32_t kMaxParts = 8;  // CTAs that share one tile's reduction
+constexpr uint32_t kMaxParts = 4;  // CTAs that share one tile's reduction
 constexpr int kSoloThreads = 256;  // load, issue, allocate, (idle), 4 store warps
 
 template <int BN>
@@ -656,9 +656,16 @@ cudaError_t go(Fp4Product P, const void *a, const void *b, int64_t row_bytes, in
     P.tiles_m = int((P.m + BN - 1) / BN);
     P.tiles_n = int((P.n + kLanes - 1) / kLanes);
     const int64_t tiles = int64_t(P.tiles_m) * P.tiles_n, room = int64_t(sm_count(device)) * S::ctas;
-    const int ks = (P.kt + 1) / 2;
+    // Cutting the reduction pays where the CTAs still find an SM each and the
+    // stages saved (0.2 us each) outweigh the exchange (0.8 us for few tokens, 2
+    // us for 128): 48 x 4096 x 4096 6.8 us whole, 5.3 us in four; 1 x 14336 x 4096
+    // 6.5 us whole, 8.0 us in two on shared SMs; 1000 x 768 x 2304 5.9 us whole,
+    // 6.9 us in two.  Eight parts are slower than four (clusters of 8 large CTAs
+    // do not fill every part of the GPU: 512 x 512 x 8192 12.7 us, in four 7.1).
+    const int ks = (P.kt + 1) / 2, pays = BN == 128 ? 10 : 4;
     int parts = 1;
-    while (parts < int(kMaxParts) && tiles * parts * 2 <= room && parts * 2 <= ks) parts *= 2;
+    for (int p = 2; p <= int(kMaxParts) && tiles * p <= sm_count(device); p *= 2)
+        if (ks - (ks + p - 1) / p >= pays) parts = p;
     void *args[] = {&mt, &mw, &P};
     static std::atomic<uint64_t> ready[2];
     if (parts > 1)
