@@ -102,7 +102,9 @@ amp_status fp4_product_mx(const void *a, const void *a_scales, const void *b, co
                           amp_stream_t stream) {
     AMP_TRACE("fp4_product_mx");
     const char *fn = "fp4_product_mx";
-    if (bad_shape(m, n) || bad_shape(m, k) || bad_shape(n, k)) return fail(AMP_EINVAL, kShape, fn);
+    // k: tensor-map coordinates along the scales run to k
+    if (bad_shape(m, n) || bad_shape(m, k) || bad_shape(n, k) || k > (int64_t(1) << 30))
+        return fail(AMP_EINVAL, kShape, fn);
     const int oc = elem_code(out_dtype);
     if (oc < 0) return fail(AMP_EDTYPE, kType, fn);
     if (m * n == 0) return AMP_OK;

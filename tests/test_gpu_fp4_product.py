@@ -34,7 +34,7 @@ def bound(a, b, k):
 SHAPES = [(1, 1, 1), (1, 128, 32), (1, 14336, 4096), (3, 7, 33), (16, 128, 64), (17, 200, 96), (33, 130, 129),
           (48, 4096, 4096), (64, 64, 1000), (65, 129, 257), (128, 128, 256), (129, 1000, 777), (256, 384, 512),
           (300, 300, 300), (1000, 2304, 768), (4096, 4099, 160), (2049, 5121, 288), (2000, 131, 2080),
-          (128, 256, 20000)]
+          (128, 256, 20000), (3001, 3000, 1), (300, 20000, 64), (5000, 2600, 65)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
