@@ -87,7 +87,7 @@ amp_status fp4_dequant_mx(const void *q, const void *scales, int64_t rows, int64
  * of GPU time; the output of a call that did is unspecified and fp4_mx_check
  * reports it.
  * Errors: AMP_EINVAL (NULL or misaligned operands, negative or too large
- * size), AMP_EDTYPE, AMP_ECUDA. */
+ * size, k above 2^27), AMP_EDTYPE, AMP_ECUDA. */
 amp_status fp4_product_mx(const void *a, const void *a_scales, const void *b, const void *b_scales,
                           int64_t m, int64_t n, int64_t k, void *out, amp_dtype out_dtype,
                           amp_stream_t stream);

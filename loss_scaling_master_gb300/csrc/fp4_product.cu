@@ -25,9 +25,10 @@
 // from there (so the order of the sum is fixed and nothing goes through global
 // memory).
 //
-// Every wait gives up after a second of GPU time: the thread sets the error
-// word, the others see the CTA's flag, copies in flight are waited for, tensor
-// memory is freed, and the kernel returns.
+// Every wait gives up after a second of GPU time: the role sets the error word,
+// waits (again bounded) for the copies or products that it has in flight and
+// ends; the roles that wait for it give up in turn, tensor memory is freed, and
+// the kernel returns.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -135,7 +136,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], acc_full, acc_empty, drain;
     __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_fail;
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -148,7 +148,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         mbar_init(&acc_full, 1);
         mbar_init(&acc_empty, 32);  // the first CTA's: the 16 store warps of both
         mbar_init(&drain, 1);
-        s_fail = 0;
         mbar_fence_init();
         tma_prefetch_map(&map_t);
         tma_prefetch_map(&map_w);
@@ -167,10 +166,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int tiles = P.tiles_m * P.tiles_n;
     const int first = int(blockIdx.x >> 1), stride = int(gridDim.x >> 1);
     const int ks_all = (P.kt + 1) / 2;
-    auto give_up = [&]() {
-        s_fail = 1;
-        g_fp4_error = 1;
-    };
+    auto give_up = [&]() { g_fp4_error = 1; };
 
     if (warp == 0) {
         int st = 0, issued = 0;
@@ -338,7 +334,6 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], acc_full[NA], acc_empty[NA], drain;
     __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_fail;
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
@@ -352,7 +347,6 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
             mbar_init(&acc_empty[i], 128);
         }
         mbar_init(&drain, 1);
-        s_fail = 0;
         mbar_fence_init();
         tma_prefetch_map(&map_t);
         tma_prefetch_map(&map_w);
@@ -374,10 +368,7 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
     const int first = SPLIT ? int(blockIdx.x / parts) : int(blockIdx.x);
     const int ks_all = (P.kt + 1) / 2;
     const int ks0 = int(int64_t(ks_all) * rank / parts), ks1 = int(int64_t(ks_all) * (rank + 1) / parts);
-    auto give_up = [&]() {
-        s_fail = 1;
-        g_fp4_error = 1;
-    };
+    auto give_up = [&]() { g_fp4_error = 1; };
 
     if (warp == 0) {
         int st = 0, issued = 0;
@@ -474,9 +465,9 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
         for (int tile = first; tile < tiles; tile += stride) {
             int tm, tn;
             tile_at(P, 16, tile, tm, tn);
-            const bool ok = mbar_wait(&acc_full[ab], aph);
-            if (!__all_sync(0xFFFFFFFFu, ok && !s_fail)) {
-                if (!ok) give_up();
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[ab], aph));
+            if (!ok) {
+                give_up();
                 break;
             }
             tc_fence_after();

@@ -102,8 +102,8 @@ amp_status fp4_product_mx(const void *a, const void *a_scales, const void *b, co
                           amp_stream_t stream) {
     AMP_TRACE("fp4_product_mx");
     const char *fn = "fp4_product_mx";
-    // k: tensor-map coordinates along the scales run to k
-    if (bad_shape(m, n) || bad_shape(m, k) || bad_shape(n, k) || k > (int64_t(1) << 30))
+    // k: one tile's products have to end well within the second that a wait may take
+    if (bad_shape(m, n) || bad_shape(m, k) || bad_shape(n, k) || k > (int64_t(1) << 27))
         return fail(AMP_EINVAL, kShape, fn);
     const int oc = elem_code(out_dtype);
     if (oc < 0) return fail(AMP_EDTYPE, kType, fn);
