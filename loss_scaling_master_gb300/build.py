@@ -3,14 +3,18 @@
     python -m loss_scaling_master_gb300.build
 
 Each .cu file is compiled in parallel with nvcc, then linked into one shared
-library next to this file.  Objects go to ``_build/`` (git-ignored).
+library next to this file; the operators' Python argument marshalling
+(``csrc/ops_bind.cpp``) is compiled beside them with g++ into ``_ops_bind.so``.
+Objects go to ``_build/`` (git-ignored).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libampfp8.so")
+BIND_SRC = os.path.join(CSRC, "ops_bind.cpp")
+BIND = os.path.join(PKG, "_ops_bind.so")
 SOURCES = ["api.cu", "unscale_check.cu", "adamw_master.cu", "adamw_noalloc.cu", "emit_bf16.cu",
            "fp8_quant.cu",
            "fp8_rowwise.cu", "fp8_groupwise.cu", "update_scale.cu",
@@ -36,6 +42,19 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libampfp8")
+
+
+def _bind_command(target: str):
+    """g++ on the operators' argument marshalling, a Python extension against torch's headers
+    (found without importing torch)."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG",
+            "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+            "-isystem", os.path.join(torch, "include"),
+            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), BIND_SRC, "-o", target,
+            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def _stale(target: str, deps) -> bool:
@@ -61,15 +80,24 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 print(" ".join(cmd), flush=True)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                 stderr=subprocess.STDOUT, text=True)))
+    bind_tmp = BIND + f".tmp{os.getpid()}"
+    bind = None
+    if force or _stale(BIND, [BIND_SRC] + headers):
+        cmd = _bind_command(bind_tmp)
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        bind = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     failed = []
-    for src, p in procs:
+    for src, p in procs + ([("ops_bind.cpp", bind)] if bind else []):
         out, _ = p.communicate()
         if verbose or ptxas_info or p.returncode:
             sys.stdout.write(out)
         if p.returncode:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed for {failed}")
+        raise RuntimeError(f"compilation failed for {failed}")
+    if bind:
+        os.replace(bind_tmp, BIND)
     if force or procs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]

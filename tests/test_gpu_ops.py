@@ -421,3 +421,50 @@ def test_fp4_quant_offsets_past_32_bits(G, dev):
     full = torch.empty_like(x)
     G.fp4_dequant_mx(q, s, full)
     assert same(full[-2:], v) and not full[:1000].any()
+
+
+# ------------------------------------------------------------------ refusals
+def test_binding_refuses_what_would_not_fit(G, dev):
+    """Wrong types, sizes and layouts are refused with their name before any call."""
+    x = torch.zeros(40, 64, dtype=torch.bfloat16, device=dev)
+    q, s = G.fp4_mx_buffers(40, 64)
+    q8, s8 = G.ckpt8_buffers(40, 64)
+    f, w = torch.zeros(40, device=dev), torch.zeros(64, device=dev)
+    for match, call in (
+            ("q: 1279 elements, at least 1280", lambda: G.fp4_quant_mx(x, q.view(-1)[:1279], s)),
+            ("scales: 511 elements, at least 512", lambda: G.fp4_quant_mx(x, q, s[:511])),
+            ("q: 2-byte elements", lambda: G.fp4_quant_mx(x, q.view(torch.int16), s)),
+            ("x: dtype Int; f32, f16 or bf16", lambda: G.fp4_quant_mx(x.int(), q, s)),
+            ("x: needs a contiguous CUDA", lambda: G.fp4_quant_mx(x.t(), q, s)),
+            ("x: needs a tensor", lambda: G.fp4_quant_mx([1.0], q, s)),
+            ("skip_if: dtype Float", lambda: G.fp4_quant_mx(x, q, s, skip_if=f)),
+            ("stream: needs a stream", lambda: G.fp4_quant_mx(x, q, s, stream="s")),
+            ("out: needs a contiguous", lambda: G.fp4_dequant_mx(q, s, torch.zeros(64, 40, device=dev).t())),
+            ("b: 1280 elements, at least", lambda: G.fp4_product_mx(q, s, q, s, 64, torch.zeros(40, 41, device=dev))),
+            ("k = 1.5", lambda: G.fp4_product_mx(q, s, q, s, 1.5, torch.zeros(40, 40, device=dev))),
+            ("y: dtype Float, expected BFloat16", lambda: G.amp_layer_norm_forward(x, w, w, 1e-5, x.float())),
+            ("mean: 39 elements", lambda: G.amp_layer_norm_forward(x, w, w, 1e-5, x, f[:39])),
+            ("eps: needs a number", lambda: G.amp_layer_norm_forward(x, w, w, "e", x)),
+            ("saved: needs", lambda: G.amp_layer_norm_forward(x, w, w, 1e-5, x, saved=q8)),
+            ("saved: dtype Byte, expected Float8", lambda: G.amp_layer_norm_forward(x, w, w, 1e-5, x, saved=(q, s8))),
+            ("saved: 79 elements", lambda: G.amp_ckpt8_save(x, q8, s8.view(-1)[:79]) or G.amp_act_forward_mx8(
+                x, "silu", x, (q8, s8.view(-1)[:79]))),
+            ("dx: 64 elements", lambda: G.amp_layer_norm_backward(x, x, w, f, f, x[0])),
+            ("up: dtype Float", lambda: G.amp_act_forward_mx8(x, "silu", x, up=x.float())),
+    ):
+        if match.startswith("saved: 79"):
+            with pytest.raises(ValueError, match="79 elements, at least 80"):
+                call()
+            continue
+        with pytest.raises(ValueError, match=match):
+            call()
+    with pytest.raises(G.AmpError, match="workspace needs"):
+        G.amp_layer_norm_backward(x, x, w, f, f, None, w, w, torch.zeros(16, dtype=torch.uint8, device=dev))
+    with pytest.raises(G.AmpError, match="go together"):
+        G.fp4_quant_mx(x, q, s, G.fp4_mx_buffers(64, 40)[0])
+    with pytest.raises(G.AmpError, match="16-byte aligned"):
+        G.fp4_dequant_mx(torch.zeros(2000, dtype=torch.uint8, device=dev)[1:], s, x)
+    with pytest.raises(G.AmpError, match="both checkpoints or none"):
+        G.amp_act_forward_mx8(x, "silu", x.clone(), (q8, s8), up=x)
+    with pytest.raises(TypeError):
+        G.fp4_quant_mx(x)
