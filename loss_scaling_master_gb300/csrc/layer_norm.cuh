@@ -208,13 +208,16 @@ __host__ __device__ constexpr int norm_rpc(int tpr) { return norm_cta(tpr) / tpr
 
 }  // namespace amp
 
-// Runs F(TPR, NV) for the row length.  A warp a row up to 1024 elements (no
-// barrier), then the smallest CTA that holds the row in two groups a thread,
-// four for the longest rows, whose CTA could not be larger.
-#define AMP_NORM_SHAPE(cols, F)                 \
+// Runs F(TPR, NV) for the row length: the smallest CTA that holds the row in two
+// groups a thread, four for the longest rows, whose CTA could not be larger.
+// T1, V1: the shape up to 1024 elements.  Forward 128 x 1 (8 rows of 768 2.0 us,
+// with a warp a row 3.3 us, whose code is four times as long and run once; 16384
+// x 1024 15.7 against 18.9 us, 8192 x 768 8.5 against 8.0 us), backward 64 x 2 (4.3
+// against 5.5, 25.6 against 26.6, 14.7 against 15.0 us; 128 x 1 3.6, 28.5, 16.4 us).
+#define AMP_NORM_SHAPE(cols, F, T1, V1)         \
     do {                                        \
         if ((cols) <= 256) { F(32, 1); }        \
-        else if ((cols) <= 1024) { F(32, 4); }  \
+        else if ((cols) <= 1024) { F(T1, V1); } \
         else if ((cols) <= 2048) { F(128, 2); } \
         else if ((cols) <= 4096) { F(256, 2); } \
         else if ((cols) <= 8192) { F(512, 2); } \

@@ -306,7 +306,7 @@ cudaError_t go(const NormBwd &P, int64_t parts, cudaStream_t s) {
 #define F(TPR, NV)                                                                                           \
     return launch_pdl(norm_bwd_kernel<XT, CK, VEC, TPR, NV>, dim3((unsigned)parts), dim3(norm_cta(TPR)),     \
                       norm_rpc(TPR) > 1 ? size_t(P.cols) * 4 * norm_rpc(TPR) : 0, s, P)
-    AMP_NORM_SHAPE(P.cols, F);
+    AMP_NORM_SHAPE(P.cols, F, 64, 2);
 #undef F
 }
 template <int XT, bool CK>
@@ -334,7 +334,7 @@ int64_t norm_parts(int64_t rows, int64_t cols, int device) {
 #define F(TPR, NV)                                                                     \
     return std::max<int64_t>(1, std::min<int64_t>((rows + norm_rpc(TPR) - 1) / norm_rpc(TPR), \
                                                   norm_cta(TPR) == 256 && NV <= 2 ? 2 * sms : sms))
-    AMP_NORM_SHAPE(cols, F);
+    AMP_NORM_SHAPE(cols, F, 64, 2);
 #undef F
 }
 

@@ -231,7 +231,7 @@ cudaError_t go(const NormFwd &P, int device, cudaStream_t s) {
                       dim3((unsigned)std::min<int64_t>((P.rows + norm_rpc(TPR) - 1) / norm_rpc(TPR),     \
                                                        sms * (fwd_ctas<XT, VEC>(TPR, NV)))), \
                       dim3(norm_cta(TPR)), 0, s, P)
-    AMP_NORM_SHAPE(P.cols, F);
+    AMP_NORM_SHAPE(P.cols, F, 128, 1);
 #undef F
 }
 template <int XT>
