@@ -86,10 +86,14 @@ __host__ __device__ constexpr int norm_step(int v, int j) {
     return VEC ? 8 * v * TPR + j : (8 * v + j) * TPR;
 }
 
-// Raw words of the 8 elements of group v behind x, n of them in the row; the
-// rest are zeros.
+// The 8 elements of group v behind x as loaded (VEC: raw words; else one element
+// a word, so that nothing waits for the loads before the row's turn); n of them
+// are in the row, the rest are zeros.
+template <int XT, bool VEC>
+constexpr int kNormWords = VEC ? kWords8<XT> : 2;
+
 template <int XT, bool VEC, int TPR>
-__device__ __forceinline__ void ld8(const void *x, int v, int n, uint4 (&u)[kWords8<XT>]) {
+__device__ __forceinline__ void ld8(const void *x, int v, int n, uint4 (&u)[kNormWords<XT, VEC>]) {
     constexpr int esz = XT == kF32 ? 4 : 2;
     const int k = norm_step<VEC, TPR>(v, 0);
     if constexpr (VEC) {
@@ -97,19 +101,14 @@ __device__ __forceinline__ void ld8(const void *x, int v, int n, uint4 (&u)[kWor
         for (int i = 0; i < kWords8<XT>; ++i)
             u[i] = n > 0 ? ld16(static_cast<const char *>(x) + k * esz + 16 * i) : make_uint4(0, 0, 0, 0);
     } else {
-        uint32_t w[4 * kWords8<XT>];
+        uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 4 * kWords8<XT>; ++i) {
-            if constexpr (XT == kF32) {
-                w[i] = i < n ? static_cast<const uint32_t *>(x)[k + i * TPR] : 0u;
-            } else {
-                const uint16_t *p = static_cast<const uint16_t *>(x) + k;
-                const uint32_t a = 2 * i < n ? p[2 * i * TPR] : 0u, b = 2 * i + 1 < n ? p[(2 * i + 1) * TPR] : 0u;
-                w[i] = a | (b << 16);
-            }
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (XT == kF32) w[j] = j < n ? static_cast<const uint32_t *>(x)[k + j * TPR] : 0u;
+            else w[j] = j < n ? static_cast<const uint16_t *>(x)[k + j * TPR] : 0u;
         }
-#pragma unroll
-        for (int i = 0; i < kWords8<XT>; ++i) u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        u[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
 template <int XT>
@@ -118,6 +117,23 @@ __device__ __forceinline__ void to_f32(const uint4 (&u)[kWords8<XT>], f2 (&y)[4]
     raw8_to_f32<XT>(u, f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = make_f2(f[2 * i], f[2 * i + 1]);
+}
+// What ld8 loaded.
+template <int XT, bool VEC>
+__device__ __forceinline__ void widen8(const uint4 (&u)[kNormWords<XT, VEC>], f2 (&y)[4]) {
+    if constexpr (VEC) {
+        to_f32<XT>(u, y);
+    } else {
+        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (XT == kF32) f[j] = __uint_as_float(w[j]);
+            else f[j] = lowp_to_f32<XT>(w[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = make_f2(f[2 * i], f[2 * i + 1]);
+    }
 }
 __device__ __forceinline__ void split8(const f2 (&y)[4], float (&f)[8]) {
 #pragma unroll
@@ -220,6 +236,17 @@ __host__ __device__ constexpr int norm_rpc(int tpr) { return norm_cta(tpr) / tpr
         else if ((cols) <= 1024) { F(T1, V1); } \
         else if ((cols) <= 2048) { F(128, 2); } \
         else if ((cols) <= 4096) { F(256, 2); } \
+        else if ((cols) <= 8192) { F(512, 2); } \
+        else { F(512, 4); }                     \
+    } while (0)
+// Rows taken by single elements, whose loads each hold a register until their
+// turn: one group a thread as long as the CTA can grow.
+#define AMP_NORM_SHAPE_ODD(cols, F)             \
+    do {                                        \
+        if ((cols) <= 256) { F(32, 1); }        \
+        else if ((cols) <= 1024) { F(128, 1); } \
+        else if ((cols) <= 2048) { F(256, 1); } \
+        else if ((cols) <= 4096) { F(512, 1); } \
         else if ((cols) <= 8192) { F(512, 2); } \
         else { F(512, 4); }                     \
     } while (0)

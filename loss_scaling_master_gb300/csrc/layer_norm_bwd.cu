@@ -29,18 +29,22 @@ struct NormBwd {
     int wt;
 };
 
-// A thread's 8 elements of dy and of x, or of x's codes with their scale bytes
-// (VEC: 8 codes in x, y and one byte in z; else two codes and bytes a word).
-template <int XT, bool CK>
+// CTAs of the backward kernel an SM holds: 2 of 256 threads, 1 of 512.
+__host__ __device__ constexpr int bwd_ctas(int tpr, int nv) { return norm_cta(tpr) == 256 && nv <= 2 ? 2 : 1; }
+
+// A thread's 8 elements of dy and of x as loaded, or of x's codes with their
+// scale bytes (VEC: 8 codes in x, y and one byte in z; else one a word).
+template <int XT, bool CK, bool VEC>
 struct Group {
-    uint4 dy[kWords8<XT>];
-    uint4 x[CK ? 1 : kWords8<XT>];
+    uint4 dy[kNormWords<XT, VEC>];
+    uint4 x[!CK ? kNormWords<XT, VEC> : VEC ? 1 : 2];
+    uint4 s[CK && !VEC ? 2 : 1];
 };
 
 // dy, x, q, s: the places of the thread's first element.
 template <int XT, bool CK, bool VEC, int TPR>
 __device__ __forceinline__ void load_pair(const char *dy, const char *x, const uint8_t *q, const uint8_t *s, int v,
-                                          int n, Group<XT, CK> &g) {
+                                          int n, Group<XT, CK, VEC> &g) {
     ld8<XT, VEC, TPR>(dy, v, n, g.dy);
     if constexpr (!CK) {
         ld8<XT, VEC, TPR>(x, v, n, g.x);
@@ -53,24 +57,26 @@ __device__ __forceinline__ void load_pair(const char *dy, const char *x, const u
         }
         g.x[0] = make_uint4(u.x, u.y, e, 0);
     } else {
-        uint32_t w[4];
+        uint32_t w[8], e[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int a = norm_step<false, TPR>(v, 2 * i), b = norm_step<false, TPR>(v, 2 * i + 1);
-            w[i] = 0;
-            if (2 * i < n) w[i] = q[a] | uint32_t(s[a / kMxBlock]) << 16;
-            if (2 * i + 1 < n) w[i] |= uint32_t(q[b]) << 8 | uint32_t(s[b / kMxBlock]) << 24;
+        for (int j = 0; j < 8; ++j) {
+            const int k = norm_step<false, TPR>(v, j);
+            w[j] = j < n ? q[k] : 0u;
+            e[j] = j < n ? s[k / kMxBlock] : 0u;
         }
         g.x[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        g.x[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        g.s[0] = make_uint4(e[0], e[1], e[2], e[3]);
+        g.s[1] = make_uint4(e[4], e[5], e[6], e[7]);
     }
 }
 // dy and x - mean (a code times its power of two is exact, so one fused
 // multiply-add rounds as the subtraction does).
 template <int XT, bool CK, bool VEC>
-__device__ __forceinline__ void unpack_pair(const Group<XT, CK> &g, f2 off, f2 (&dy)[4], f2 (&x)[4]) {
-    to_f32<XT>(g.dy, dy);
+__device__ __forceinline__ void unpack_pair(const Group<XT, CK, VEC> &g, f2 off, f2 (&dy)[4], f2 (&x)[4]) {
+    widen8<XT, VEC>(g.dy, dy);
     if constexpr (!CK) {
-        to_f32<XT>(g.x, x);
+        widen8<XT, VEC>(g.x, x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = add2(x[i], off);
     } else if constexpr (VEC) {
@@ -81,18 +87,19 @@ __device__ __forceinline__ void unpack_pair(const Group<XT, CK> &g, f2 off, f2 (
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = fma2(make_f2(f[2 * i], f[2 * i + 1]), s, off);
     } else {
-        const uint32_t w[4] = {g.x[0].x, g.x[0].y, g.x[0].z, g.x[0].w};
+        const uint32_t w[8] = {g.x[0].x, g.x[0].y, g.x[0].z, g.x[0].w, g.x[1].x, g.x[1].y, g.x[1].z, g.x[1].w};
+        const uint32_t e[8] = {g.s[0].x, g.s[0].y, g.s[0].z, g.s[0].w, g.s[1].x, g.s[1].y, g.s[1].z, g.s[1].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float f[4];
-            e4m3x4_to_f32x4(w[i] & 0xFFFFu, f);
-            x[i] = fma2(make_f2(f[0], f[1]), make_f2(mx_scale((w[i] >> 16) & 0xFFu), mx_scale(w[i] >> 24)), off);
+            e4m3x4_to_f32x4(w[2 * i] | (w[2 * i + 1] << 8), f);
+            x[i] = fma2(make_f2(f[0], f[1]), make_f2(mx_scale(e[2 * i]), mx_scale(e[2 * i + 1])), off);
         }
     }
 }
 
 template <int XT, bool CK, bool VEC, int TPR, int NV>
-__global__ void __launch_bounds__(norm_cta(TPR), norm_cta(TPR) == 256 && NV <= 2 ? 2 : 1) norm_bwd_kernel(NormBwd P) {
+__global__ void __launch_bounds__(norm_cta(TPR), bwd_ctas(TPR, NV)) norm_bwd_kernel(NormBwd P) {
     constexpr int RPC = norm_rpc(TPR);
     constexpr bool HOLD = TPR < 512 || NV < 4;  // weights in registers
     __shared__ float scratch[2][2 * 32];
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(norm_cta(TPR), norm_cta(TPR) == 256 && NV <= 2
     const uint8_t *qp = P.q + k0, *sp = P.s + r * kb + c0 / kMxBlock;
     char *dxp = static_cast<char *>(P.dx) + k0 * esz;
     int len[NV];
-    Group<XT, CK> nxt[NV];
+    Group<XT, CK, VEC> nxt[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         len[v] = norm_count<VEC, TPR>(v, t, int(P.cols));
@@ -301,12 +308,26 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormJoin P) {
     }
 }
 
+// CTAs of the backward pass, and so rows of partial sums: as many as the device
+// holds at once, at most one for each group of rows.
+int64_t norm_grid(int64_t rows, int64_t cols, bool vec, int device) {
+    if (cols > kNormRegCols) return std::max<int64_t>(1, std::min<int64_t>(rows, 32));
+    const int64_t sms = sm_count(device);
+#define F(TPR, NV)                                                                             \
+    return std::max<int64_t>(1, std::min<int64_t>((rows + norm_rpc(TPR) - 1) / norm_rpc(TPR),  \
+                                                  sms * bwd_ctas(TPR, NV)))
+    if (vec) AMP_NORM_SHAPE(cols, F, 64, 2);
+    else AMP_NORM_SHAPE_ODD(cols, F);
+#undef F
+}
+
 template <int XT, bool CK, bool VEC>
 cudaError_t go(const NormBwd &P, int64_t parts, cudaStream_t s) {
 #define F(TPR, NV)                                                                                           \
     return launch_pdl(norm_bwd_kernel<XT, CK, VEC, TPR, NV>, dim3((unsigned)parts), dim3(norm_cta(TPR)),     \
                       norm_rpc(TPR) > 1 ? size_t(P.cols) * 4 * norm_rpc(TPR) : 0, s, P)
-    AMP_NORM_SHAPE(P.cols, F, 64, 2);
+    if constexpr (VEC) AMP_NORM_SHAPE(P.cols, F, 64, 2);
+    else AMP_NORM_SHAPE_ODD(P.cols, F);
 #undef F
 }
 template <int XT, bool CK>
@@ -325,17 +346,10 @@ cudaError_t go_x(const NormBwd &P, bool vec, int64_t parts, cudaStream_t s) {
 
 }  // namespace
 
-// Rows of partial sums: as many CTAs as the device holds at once (2 of 256
-// threads an SM, 1 of 512 or with four groups a thread), at most one for each
-// group of rows.
+// Rows of partial sums that a workspace has room for, whichever way the rows are
+// taken.
 int64_t norm_parts(int64_t rows, int64_t cols, int device) {
-    const int64_t sms = sm_count(device);
-    if (cols > kNormRegCols) return std::max<int64_t>(1, std::min<int64_t>(rows, 32));
-#define F(TPR, NV)                                                                     \
-    return std::max<int64_t>(1, std::min<int64_t>((rows + norm_rpc(TPR) - 1) / norm_rpc(TPR), \
-                                                  norm_cta(TPR) == 256 && NV <= 2 ? 2 * sms : sms))
-    AMP_NORM_SHAPE(cols, F, 64, 2);
-#undef F
+    return std::max(norm_grid(rows, cols, true, device), norm_grid(rows, cols, false, device));
 }
 
 cudaError_t launch_norm_bwd(const void *dy, const void *x, int elem, const uint8_t *q, const uint8_t *sc,
@@ -347,7 +361,7 @@ cudaError_t launch_norm_bwd(const void *dy, const void *x, int elem, const uint8
     const int esz = elem == kF32 ? 4 : 2;
     const bool vec = norm_vec(dy, cols, esz) && norm_vec(x, cols, esz) && norm_vec(dx, cols, esz) &&
                      (reinterpret_cast<uintptr_t>(q) & 7) == 0;
-    const int64_t parts = norm_parts(rows, cols, device);
+    const int64_t parts = norm_grid(rows, cols, vec, device);
     cudaError_t e = cudaSuccess;
     if (q)
         e = elem == kF32   ? go_x<kF32, true>(P, vec, parts, s)

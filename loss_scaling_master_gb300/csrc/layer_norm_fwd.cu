@@ -37,7 +37,7 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // The checkpoint of a thread's group v; the warp calls it together.  q, sc: the
 // places of the thread's first element's code and scale byte.
 template <int XT, bool VEC, int TPR>
-__device__ __forceinline__ void keep8(uint8_t *q, uint8_t *sc, int v, int n, const uint4 (&raw)[kWords8<XT>],
+__device__ __forceinline__ void keep8(uint8_t *q, uint8_t *sc, int v, int n, const uint4 (&raw)[kNormWords<XT, VEC>],
                                       const f2 (&x)[4]) {
     float f[8];
     split8(x, f);
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(norm_cta(TPR), (fwd_ctas<XT, VEC>(TPR, NV)))
     uint8_t *qp = P.q + r * P.cols + c0, *sp = P.s + r * kb + c0 / kMxBlock;
     int n[NV];
     f2 w[NV][4], b[NV][4];
-    uint4 nxt[NV][kWords8<XT>];
+    uint4 nxt[NV][kNormWords<XT, VEC>];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         n[v] = norm_count<VEC, TPR>(v, t, int(P.cols));
@@ -110,15 +110,15 @@ __global__ void __launch_bounds__(norm_cta(TPR), (fwd_ctas<XT, VEC>(TPR, NV)))
     // every thread of the CTA walks the same number of steps
     for (int64_t base = int64_t(blockIdx.x) * RPC; base < P.rows; base += step, r += step, buf ^= 1) {
         const bool in = r < P.rows;
-        uint4 raw[NV][kWords8<XT>];
+        uint4 raw[NV][kNormWords<XT, VEC>];
         f2 x[NV][4];
         float a[1];
         f2 s2 = both(0.0f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
 #pragma unroll
-            for (int i = 0; i < kWords8<XT>; ++i) raw[v][i] = nxt[v][i];
-            to_f32<XT>(raw[v], x[v]);
+            for (int i = 0; i < kNormWords<XT, VEC>; ++i) raw[v][i] = nxt[v][i];
+            widen8<XT, VEC>(raw[v], x[v]);
             s2 = add2(s2, add2(add2(x[v][0], x[v][1]), add2(x[v][2], x[v][3])));
         }
         const bool more = r + step < P.rows;
@@ -231,7 +231,8 @@ cudaError_t go(const NormFwd &P, int device, cudaStream_t s) {
                       dim3((unsigned)std::min<int64_t>((P.rows + norm_rpc(TPR) - 1) / norm_rpc(TPR),     \
                                                        sms * (fwd_ctas<XT, VEC>(TPR, NV)))), \
                       dim3(norm_cta(TPR)), 0, s, P)
-    AMP_NORM_SHAPE(P.cols, F, 128, 1);
+    if constexpr (VEC) AMP_NORM_SHAPE(P.cols, F, 128, 1);
+    else AMP_NORM_SHAPE_ODD(P.cols, F);
 #undef F
 }
 template <int XT>
