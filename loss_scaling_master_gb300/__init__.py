@@ -5,7 +5,7 @@ around it in the forward and backward pass: microscaled 4-bit quantisation and
 products, layer norm, activations kept in 8 bits.
 
 The compute lives in libampfp8.so (hand-written CUDA for sm_103a, C ABI in
-include/ampfp8.h and include/ampops.h); this package is its thin ctypes binding.
+include/ampfp8.h and include/ampops.h); this package is its thin binding.
 """
 from ._lib import (AmpError, TensorList, amp_abi_version, amp_adamw_master_step,
                    amp_adamw_master_step_clip, amp_adamw_master_step_fp8_delayed,
@@ -19,6 +19,7 @@ from ._lib import (AmpError, TensorList, amp_abi_version, amp_adamw_master_step,
                    amp_unscale_check_norm, amp_tensor_list_create, amp_tensor_list_destroy,
                    amp_tensor_list_set_amax_slots, amp_unscale_check, amp_update_scale,
                    fp8_quant_rowwise, fp8_quant_tensorwise, fp8_quant_tensorwise_list, load)
+from . import ops
 from .ops import (amp_act_backward_mx8, amp_act_forward_mx8, amp_ckpt8_restore, amp_ckpt8_save,
                   amp_layer_norm_backward, amp_layer_norm_forward, amp_layer_norm_workspace,
                   ckpt8_buffers, fp4_dequant_mx, fp4_mx_buffers, fp4_mx_check, fp4_product_mx,

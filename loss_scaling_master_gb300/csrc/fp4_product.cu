@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
 // ------------------------------------------------------------------ one CTA a tile
 constexpr uint32_t kMaxParts = 4;  // CTAs that share one tile's reduction
-constexpr int kSoloThreads = 256;  // load, issue, allocate, (idle), 4 store warps
+constexpr int kSoloThreads = 384;  // load, issue, allocate, (idle), 8 store warps
 
 template <int BN>
 struct Solo {
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
         }
         for (int i = 0; i < NA; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 128);
+            mbar_init(&acc_empty[i], 256);
         }
         mbar_init(&drain, 1);
         mbar_fence_init();
@@ -458,8 +458,9 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
             mbar_wait(&drain, 0);
         }
     } else if (warp >= 4) {
-        const int quarter = warp & 3;
-        constexpr int CH = BN < 32 ? BN : 32;  // columns at a time
+        // a quarter of the lanes and half of the columns a warp (all of 16)
+        constexpr int HALF = BN > 16 ? BN / 2 : BN, CH = HALF < 32 ? HALF : 32;  // CH: columns at a time
+        const int quarter = warp & 3, c0 = (warp - 4) / 4 * HALF;
         int ab = 0;
         uint32_t aph = 0;
         for (int tile = first; tile < tiles; tile += stride) {
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
             const int64_t nn = int64_t(tn) * kLanes + 32 * quarter + lane, m0 = int64_t(tm) * BN;
             const int rows = int(min(int64_t(BN), P.m - m0));
 #pragma unroll 1
-            for (int c = 0; c < rows; c += CH) {
+            for (int c = c0; c < min(rows, c0 + HALF) && c < BN; c += CH) {
                 uint32_t v[CH];
                 tmem_ld<CH>(acc + c, v);
                 if (SPLIT) {
