@@ -147,12 +147,6 @@ __device__ __forceinline__ void st_param(void *w, int wt, int64_t c, float v) {
     else store_elem<kBF16>(w, c, v);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
-
 // The sums of one or two values over the TPR threads of a row, given to all of
 // them.  Every thread of the CTA calls it (it synchronises); s: CTA scratch of
 // N * 32 floats, another one for the next call.  Two values share the steps:
