@@ -15,8 +15,9 @@
  * caller, asynchronous calls on `stream`, no allocation, no host
  * synchronisation, negative status = nothing enqueued, message in
  * amp_last_error(), programmatic dependent launches, one NVTX range per call.
- * Where a buffer has to be aligned its comment says so; all others may have
- * any address.  Empty shapes are accepted everywhere.
+ * A tensor is aligned to its element type (else AMP_EINVAL); where a buffer has
+ * to be aligned further its comment says so.  Empty shapes are accepted
+ * everywhere.
  *
  * Block formats (OCP Microscaling Formats specification 1.0: 32 consecutive
  * elements of a row share one E8M0 scale byte e, which stands for 2^(e-127)).

@@ -41,6 +41,12 @@ bool bad_shape(int64_t rows, int64_t cols) {
     return ((rows + 127) / 128) * ((cols + 127) / 128) > (int64_t(1) << 30);
 }
 bool misaligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+// Tensors of one element type (NULL passes): on the GPU an address between two
+// elements is a fault, not a status.
+template <class... Ps>
+bool off_type(int elem, Ps... p) {
+    return (misaligned(p, elem == amp::kF32 ? 4 : 2) || ...);
+}
 
 cudaStream_t cu(amp_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 uint8_t *u8(void *p) { return static_cast<uint8_t *>(p); }
@@ -49,6 +55,7 @@ const uint8_t *u8(const void *p) { return static_cast<const uint8_t *>(p); }
 const char *kShape = "%s: negative or too large size";
 const char *kNull = "%s: NULL argument";
 const char *kType = "%s: unsupported dtype";
+const char *kOff = "%s: a tensor is not aligned to its type";
 
 }  // namespace
 
@@ -75,6 +82,7 @@ amp_status fp4_quant_mx(const void *x, amp_dtype x_dtype, int64_t rows, int64_t 
     if (!x || !out || !scales) return fail(AMP_EINVAL, kNull, fn);
     if (misaligned(out, 16) || misaligned(scales, 16) || misaligned(out_t, 16) || misaligned(scales_t, 16))
         return fail(AMP_EINVAL, "%s: outputs must be 16-byte aligned", fn);
+    if (off_type(xc, x) || off_type(amp::kF32, skip_if_dev)) return fail(AMP_EINVAL, kOff, fn);
     return finish(amp::launch_fp4_quant(x, xc, rows, cols, u8(out), u8(scales), u8(out_t), u8(scales_t),
                                         skip_if_dev, cu(stream)),
                   fn);
@@ -91,6 +99,7 @@ amp_status fp4_dequant_mx(const void *q, const void *scales, int64_t rows, int64
     if (!q || !scales || !out) return fail(AMP_EINVAL, kNull, fn);
     if (misaligned(q, 16) || misaligned(scales, 16))
         return fail(AMP_EINVAL, "%s: q and scales must be 16-byte aligned", fn);
+    if (off_type(oc, out)) return fail(AMP_EINVAL, kOff, fn);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return finish(e, fn);
@@ -111,8 +120,7 @@ amp_status fp4_product_mx(const void *a, const void *a_scales, const void *b, co
     if (!out || (k > 0 && (!a || !a_scales || !b || !b_scales))) return fail(AMP_EINVAL, kNull, fn);
     if (misaligned(a, 16) || misaligned(a_scales, 16) || misaligned(b, 16) || misaligned(b_scales, 16))
         return fail(AMP_EINVAL, "%s: operands must be 16-byte aligned", fn);
-    if (misaligned(out, oc == amp::kF32 ? 4 : 2))
-        return fail(AMP_EINVAL, "%s: out is not aligned to its type", fn);
+    if (off_type(oc, out)) return fail(AMP_EINVAL, kOff, fn);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return finish(e, fn);
@@ -142,6 +150,8 @@ amp_status amp_layer_norm_forward(const void *x, amp_dtype x_dtype, int64_t rows
         return fail(AMP_EINVAL, "%s: ckpt and ckpt_scales go together", fn);
     if (rows * cols == 0) return AMP_OK;
     if (!x || !y) return fail(AMP_EINVAL, kNull, fn);
+    if (off_type(xc, x, y) || off_type(wc, weight, bias) || off_type(amp::kF32, mean, rstd))
+        return fail(AMP_EINVAL, kOff, fn);
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return finish(e, fn);
@@ -173,6 +183,8 @@ amp_status amp_layer_norm_backward(const void *dy, const void *x, amp_dtype dtyp
     if (cols == 0 || (rows == 0 && !params)) return AMP_OK;
     if (rows > 0 && (!dy || (!x && !ckpt) || !mean || !rstd)) return fail(AMP_EINVAL, kNull, fn);
     if (!dx && !params) return AMP_OK;
+    if (off_type(xc, dy, x, dx) || off_type(wc, weight, dweight, dbias) || off_type(amp::kF32, mean, rstd))
+        return fail(AMP_EINVAL, kOff, fn);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return finish(e, fn);
@@ -207,6 +219,7 @@ amp_status amp_act_forward_mx8(amp_act act, const void *x, const void *up, amp_d
         return fail(AMP_EINVAL, "%s: with up, both checkpoints or none", fn);
     if (rows * cols == 0) return AMP_OK;
     if (!x || !y) return fail(AMP_EINVAL, kNull, fn);
+    if (off_type(elem_code(dtype), x, up, y)) return fail(AMP_EINVAL, kOff, fn);
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return finish(e, fn);
@@ -226,6 +239,7 @@ amp_status amp_act_backward_mx8(amp_act act, const void *dy, amp_dtype dtype, in
         return fail(AMP_EINVAL, "%s: q_up, scales_up and dup go together", fn);
     if (rows * cols == 0) return AMP_OK;
     if (!dy || !q || !scales || !dx) return fail(AMP_EINVAL, kNull, fn);
+    if (off_type(elem_code(dtype), dy, dx, dup)) return fail(AMP_EINVAL, kOff, fn);
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return finish(e, fn);
@@ -241,6 +255,7 @@ amp_status amp_ckpt8_save(const void *x, amp_dtype x_dtype, int64_t rows, int64_
     const amp_status st = act_args(fn, 0, false, x_dtype, rows, cols);
     if (st != AMP_OK || rows * cols == 0) return st;
     if (!x || !q || !scales) return fail(AMP_EINVAL, kNull, fn);
+    if (off_type(elem_code(x_dtype), x)) return fail(AMP_EINVAL, kOff, fn);
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return finish(e, fn);
@@ -256,6 +271,7 @@ amp_status amp_ckpt8_restore(const void *q, const void *scales, int64_t rows, in
     const amp_status st = act_args(fn, 0, false, out_dtype, rows, cols);
     if (st != AMP_OK || rows * cols == 0) return st;
     if (!q || !scales || !out) return fail(AMP_EINVAL, kNull, fn);
+    if (off_type(elem_code(out_dtype), out)) return fail(AMP_EINVAL, kOff, fn);
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return finish(e, fn);

@@ -150,6 +150,44 @@ def test_act_backward_refusals(lib, args):
     assert lib.amp_act_backward_mx8(*args, None) in (EINVAL, EDTYPE)
 
 
+# one tensor a call whose address is between two elements (last argument: the stream)
+HALF = ctypes.c_void_p(4098)   # between two of four bytes
+
+
+@pytest.mark.parametrize("name,args", [
+    ("fp4_quant_mx", (ODD, BF16, 4, 4, D, D, None, None, None)),
+    ("fp4_quant_mx", (HALF, F32, 4, 4, D, D, None, None, None)),
+    ("fp4_quant_mx", (D, BF16, 4, 4, D, D, None, None, HALF)),
+    ("fp4_dequant_mx", (D, D, 4, 4, ODD, F16)),
+    ("fp4_dequant_mx", (D, D, 4, 4, HALF, F32)),
+    ("amp_layer_norm_forward", (ODD, BF16, 4, 4, D, D, F32, 1e-5, D, D, D, None, None)),
+    ("amp_layer_norm_forward", (D, BF16, 4, 4, HALF, D, F32, 1e-5, D, D, D, None, None)),
+    ("amp_layer_norm_forward", (D, BF16, 4, 4, D, HALF, F32, 1e-5, D, D, D, None, None)),
+    ("amp_layer_norm_forward", (D, BF16, 4, 4, D, D, F32, 1e-5, ODD, D, D, None, None)),
+    ("amp_layer_norm_forward", (D, BF16, 4, 4, D, D, F32, 1e-5, D, HALF, D, None, None)),
+    ("amp_layer_norm_forward", (D, BF16, 4, 4, D, D, F32, 1e-5, D, D, HALF, None, None)),
+    ("amp_layer_norm_backward", (ODD, D, BF16, None, None, 4, 4, D, F32, D, D, D, None, None, None, 0)),
+    ("amp_layer_norm_backward", (D, ODD, BF16, None, None, 4, 4, D, F32, D, D, D, None, None, None, 0)),
+    ("amp_layer_norm_backward", (D, D, BF16, None, None, 4, 4, HALF, F32, D, D, D, None, None, None, 0)),
+    ("amp_layer_norm_backward", (D, D, BF16, None, None, 4, 4, D, F32, HALF, D, D, None, None, None, 0)),
+    ("amp_layer_norm_backward", (D, D, BF16, None, None, 4, 4, D, F32, D, HALF, D, None, None, None, 0)),
+    ("amp_layer_norm_backward", (D, D, BF16, None, None, 4, 4, D, F32, D, D, ODD, None, None, None, 0)),
+    ("amp_layer_norm_backward", (D, D, BF16, None, None, 4, 4, D, F32, D, D, D, HALF, None, D, 1 << 20)),
+    ("amp_layer_norm_backward", (D, D, BF16, None, None, 4, 4, D, F32, D, D, D, None, HALF, D, 1 << 20)),
+    ("amp_act_forward_mx8", (0, ODD, None, F16, 4, 4, D, D, D, None, None)),
+    ("amp_act_forward_mx8", (0, D, HALF, F32, 4, 4, D, D, D, D, D)),
+    ("amp_act_forward_mx8", (0, D, None, F16, 4, 4, ODD, D, D, None, None)),
+    ("amp_act_backward_mx8", (0, ODD, F16, 4, 4, D, D, None, None, D, None)),
+    ("amp_act_backward_mx8", (0, D, F32, 4, 4, D, D, None, None, HALF, None)),
+    ("amp_act_backward_mx8", (0, D, F16, 4, 4, D, D, D, D, D, ODD)),
+    ("amp_ckpt8_save", (ODD, BF16, 4, 4, D, D)),
+    ("amp_ckpt8_restore", (D, D, 4, 4, HALF, F32)),
+])
+def test_addresses_between_elements_are_refused(lib, name, args):
+    assert getattr(lib, name)(*args, None) == EINVAL
+    assert b"not aligned to its type" in lib.amp_last_error()
+
+
 def test_binding_refusals(lib):
     import loss_scaling_master_gb300 as G
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
