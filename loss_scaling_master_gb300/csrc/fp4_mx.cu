@@ -16,6 +16,7 @@
 // exchange; only the 16-byte pieces of that copy go through shared memory, so
 // that a column's 64 bytes leave together.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "mx.cuh"
@@ -30,7 +31,6 @@ struct Fp4Quant {
     uint8_t *out, *scales, *out_t, *scales_t;
     const int32_t *skip;
     int64_t tiles_c;  // tiles along the columns
-    int vec;          // 16-byte access to every row of x
 };
 
 // Words w[0..N) over the 4 lanes of two lane bits -> the maxima of words
@@ -53,8 +53,56 @@ __device__ __forceinline__ void transposing_max4(uint32_t (&w)[N], uint32_t (&r)
     }
 }
 
-template <int XT, bool T>
+// A warp's 32 rows x 64 columns of x from rows at any address: loaded by single
+// elements, 32 of a row side by side, and turned over to the lanes' 8 x 8 pieces
+// in shared memory (s: the warp's 4 KB; fp32 takes two turns of 16 rows, its
+// 16-byte pieces exchanged in the right half of a row so that 8 lanes' reads
+// fall into 32 banks).  16383 x 5121 bf16, both orientations: 64 us, 87 us with a
+// lane loading its own piece element by element (a warp's load then touches 16 to
+// 32 sectors for 32 elements); 1537 x 1111 fp32 3.7 and 5.1 us.  x: the warp's
+// first element; rows, cols: how many of the matrix are there.
+template <int XT>
+__device__ __forceinline__ void load_any(const void *x, int64_t stride, int rows, int cols, uint8_t *s, int lane,
+                                         uint4 (&raw)[8][kWords8<XT>]) {
+    constexpr int TURNS = kWords8<XT>, R = 8 / TURNS;  // rows a lane and turn
+    constexpr int B = 8;                               // rows whose loads are issued together
+    using E = std::conditional_t<XT == kF32, uint32_t, uint16_t>;
+    const E *at = static_cast<const E *>(x) + lane;
+    const bool in0 = lane < cols, in1 = lane + 32 < cols;
+    E *put = reinterpret_cast<E *>(s) + lane;
+    E *put1 = XT == kF32 ? reinterpret_cast<E *>(s) + 32 + (lane ^ 4) : put + 32;
+#pragma unroll
+    for (int t = 0; t < TURNS; ++t) {
+        if (t) __syncwarp();
+#pragma unroll
+        for (int m0 = 0; m0 < 4 * R; m0 += B) {
+            E v[B][2];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int m = m0 + b, r = m / R * 8 + t * R + m % R;
+                v[b][0] = r < rows && in0 ? at[r * stride] : E(0);
+                v[b][1] = r < rows && in1 ? at[r * stride + 32] : E(0);
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                put[64 * (m0 + b)] = v[b][0];
+                put1[64 * (m0 + b)] = v[b][1];
+            }
+        }
+        __syncwarp();
+        const int cl = lane & 7, rl = lane >> 3;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int u = 0; u < kWords8<XT>; ++u)
+                raw[t * R + i][u] = reinterpret_cast<const uint4 *>(
+                    s + (rl * R + i) * 64 * sizeof(E))[XT == kF32 ? (2 * cl + u) ^ (cl >> 2) : cl];
+    }
+}
+
+template <int XT, bool T, bool VEC>
 __global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : 4) fp4_quant_kernel(Fp4Quant P) {
+    __shared__ __align__(16) uint8_t s_x[VEC ? 16 : 8 * 4096];
     __shared__ __align__(16) uint32_t s_t[T ? 128 * 16 : 4];  // transposed codes, 64 B a column
     __shared__ __align__(16) uint8_t s_rs[512];
     __shared__ __align__(16) uint8_t s_cs[T ? 512 : 16];
@@ -72,27 +120,20 @@ __global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : 4) fp4_quant_kernel
     constexpr int esz = XT == kF32 ? 4 : 2;
 
     uint4 raw[8][W];
+    if constexpr (VEC) {
+        // a row's length is a multiple of 8 here
+        const int n = col < P.cols ? int(max(int64_t(0), min(int64_t(8), P.rows - row))) : 0;
+        const char *p = static_cast<const char *>(P.x) + (row * P.cols + col) * esz;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int u = 0; u < W; ++u) raw[i][u] = make_uint4(0, 0, 0, 0);
-    if (P.vec) {
-        if (col < P.cols) {  // a row's length is a multiple of 8 here
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (row + i < P.rows) {
-                    const char *p = static_cast<const char *>(P.x) + ((row + i) * P.cols + col) * esz;
-#pragma unroll
-                    for (int u = 0; u < W; ++u) raw[i][u] = ld16(p + 16 * u);
-                }
-        }
+            for (int u = 0; u < W; ++u)
+                raw[i][u] = i < n ? ld16(p + i * P.cols * esz + 16 * u) : make_uint4(0, 0, 0, 0);
     } else {
-        const int n = int(min(int64_t(8), P.cols - col));
-        if (n > 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (row + i < P.rows) load_raw8_tail<XT>(P.x, (row + i) * P.cols + col, n, raw[i]);
-        }
+        const int64_t wr = r0 + 32 * (warp >> 1), wc = c0 + 64 * (warp & 1);
+        load_any<XT>(static_cast<const char *>(P.x) + (wr * P.cols + wc) * esz, P.cols,
+                     int(max(int64_t(0), min(int64_t(32), P.rows - wr))),
+                     int(max(int64_t(0), min(int64_t(64), P.cols - wc))), s_x + 4096 * warp, lane, raw);
     }
 
     // rmax[k]: fp32 bits of the maximum of row 2 (cl % 4) + k's block; cmax[k]:
@@ -240,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : 4) fp4_quant_kernel
 struct Fp4Dequant {
     const uint8_t *q, *scales;
     int64_t rows, cols;
-    int words;  // VEC: 8-element words a packed row; else 256-element pieces of it
+    int pieces;  // of a packed row: of 16 bytes of output, or of 256 elements
     void *out;
 };
 
@@ -249,24 +290,27 @@ __device__ __forceinline__ uint32_t scale_at(const Fp4Dequant &P, int64_t r, int
     return P.scales[tile * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3)];
 }
 
-// Rows that are whole, aligned groups of 8: one packed word a thread and step,
-// four steps' loads before the first store.
+// Rows that are whole, aligned 16-byte pieces: one of them a thread and step,
+// four steps' loads before the first store.  (Two pieces side by side a thread in
+// fp32 would write every sector by halves: 16384 x 5120 83 us, one 60 us, memory
+// 56 us; 16-bit 36 us of 31.)
 template <int XT>
 __global__ void __launch_bounds__(kThreads) fp4_dequant_vec(Fp4Dequant P) {
     pdl_wait();
     pdl_trigger();
-    constexpr int U = 4;
-    RowWalk at(blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads, P.words);
+    constexpr int U = 4, N = XT == kF32 ? 4 : 8;  // N elements a piece
+    using Codes = std::conditional_t<XT == kF32, uint16_t, uint32_t>;
+    RowWalk at(blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads, P.pieces);
     while (at.row < P.rows) {
         uint32_t codes[U], e[U];
         int64_t k[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const bool in = at.row < P.rows && 8 * at.at < P.cols;
-            k[i] = in ? at.row * P.cols + 8 * at.at : -1;
+            const bool in = at.row < P.rows && N * at.at < P.cols;
+            k[i] = in ? at.row * P.cols + N * at.at : -1;
             if (in) {
-                codes[i] = reinterpret_cast<const uint32_t *>(P.q)[at.row * P.words + at.at];
-                e[i] = scale_at(P, at.row, at.at >> 2);
+                codes[i] = reinterpret_cast<const Codes *>(P.q)[at.row * P.pieces + at.at];
+                e[i] = scale_at(P, at.row, at.at / (kMxBlock / N));
             }
             at.next();
         }
@@ -275,28 +319,38 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_vec(Fp4Dequant P) {
             if (k[i] < 0) continue;
             const float s = mx_scale(e[i]);
             float y[8];
-            e2m1x8_to_f32x8(codes[i], y);
+            if constexpr (N == 4) e2m1x4_to_f32x4(codes[i], y);
+            else e2m1x8_to_f32x8(codes[i], y);
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) mul2_rn(y[j], y[j + 1], s, s, y[j], y[j + 1]);
-            uint4 u[kWords8<XT>];
-            f32_to_raw8<XT>(y, u);
-#pragma unroll
-            for (int j = 0; j < kWords8<XT>; ++j)
-                st16(static_cast<char *>(P.out) + k[i] * (XT == kF32 ? 4 : 2) + 16 * j, u[j]);
+            for (int j = 0; j < N; j += 2) mul2_rn(y[j], y[j + 1], s, s, y[j], y[j + 1]);
+            if constexpr (N == 4) {
+                *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + k[i]) = make_float4(y[0], y[1], y[2], y[3]);
+            } else {
+                uint4 u[1];
+                f32_to_raw8<XT>(y, u);
+                st16(static_cast<uint16_t *>(P.out) + k[i], u[0]);
+            }
         }
     }
 }
 
 // Any row length and address: a warp takes 256 elements of a row, a lane one
-// packed word of them; the words then go round by shuffles so that each store
-// of the warp is 32 elements side by side.
+// packed word of them; the values are turned over in shared memory so that each
+// store of the warp is 32 elements side by side (fp32: 16-byte pieces exchanged
+// in every other 32 elements, against bank conflicts): 16383 x 5121 bf16 48 us,
+// 79 us with a word decoded for each element.
 template <int XT>
 __global__ void __launch_bounds__(kThreads) fp4_dequant_elem(Fp4Dequant P) {
+    using E = std::conditional_t<XT == kF32, uint32_t, uint16_t>;
+    constexpr int W = kWords8<XT>;
+    __shared__ uint4 s_y[kThreads / 32][32 * W];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
+    uint4 *const put = s_y[threadIdx.x >> 5];
+    const E *const get = reinterpret_cast<const E *>(put);
     const int64_t rowb = (P.cols + kMxBlock - 1) / kMxBlock * 16;
-    RowWalk at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), P.words);
+    RowWalk at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), P.pieces);
     for (; at.row < P.rows; at.next()) {
         const int c0 = 256 * at.at;
         uint32_t codes = 0, e = 0;
@@ -304,15 +358,22 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_elem(Fp4Dequant P) {
             codes = *reinterpret_cast<const uint32_t *>(P.q + at.row * rowb + c0 / 2 + 4 * lane);
             e = scale_at(P, at.row, c0 / 32 + lane / 4);
         }
-        const int64_t k = at.row * P.cols + c0 + lane;
+        const float s = mx_scale(e);
+        float y[8];
+        e2m1x8_to_f32x8(codes, y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t w = __shfl_sync(0xFFFFFFFFu, codes, 4 * j + lane / 8);
-            const uint32_t s = __shfl_sync(0xFFFFFFFFu, e, 4 * j);
-            float y[8];
-            e2m1x8_to_f32x8(w >> (4 * (lane & 7)), y);
-            if (c0 + 32 * j + lane < P.cols) store_elem<XT>(P.out, k + 32 * j, __fmul_rn(y[0], mx_scale(s)));
-        }
+        for (int j = 0; j < 8; j += 2) mul2_rn(y[j], y[j + 1], s, s, y[j], y[j + 1]);
+        uint4 u[W];
+        f32_to_raw8<XT>(y, u);
+        __syncwarp();  // the last step's words are out
+#pragma unroll
+        for (int j = 0; j < W; ++j) put[(W * lane + j) ^ (W == 2 ? (lane >> 2) & 1 : 0)] = u[j];
+        __syncwarp();
+        E *out = static_cast<E *>(P.out) + at.row * P.cols + c0 + lane;
+        const int n = int(P.cols) - c0 - lane;  // n > 32 j: element j is in the row
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (n > 32 * j) out[32 * j] = get[32 * j + (W == 2 ? lane ^ (4 * (j & 1)) : lane)];
     }
 }
 
@@ -333,27 +394,33 @@ cudaError_t launch_fp4_quant(const void *x, int xelem, int64_t rows, int64_t col
     P.tiles_c = (cols + kTile - 1) / kTile;
     const int esz = xelem == kF32 ? 4 : 2;
     // whole groups of 8 elements: every group of 8 columns lies inside the row
-    P.vec = (cols % 8 == 0 && (cols * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0) ? 1 : 0;
+    const bool vec = cols % 8 == 0 && (cols * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0;
     const int64_t tiles = ((rows + kTile - 1) / kTile) * P.tiles_c;
     const dim3 grid((unsigned)tiles), block(kThreads);
     cudaError_t e;
-#define FP4_Q(XT)                                                                   \
-    e = out_t ? launch_pdl(fp4_quant_kernel<XT, true>, grid, block, 0, s, P)        \
-              : launch_pdl(fp4_quant_kernel<XT, false>, grid, block, 0, s, P)
+#define FP4_Q1(XT, T)                                                               \
+    e = vec ? launch_pdl(fp4_quant_kernel<XT, T, true>, grid, block, 0, s, P)        \
+            : launch_pdl(fp4_quant_kernel<XT, T, false>, grid, block, 0, s, P)
+#define FP4_Q(XT)                    \
+    do {                             \
+        if (out_t) FP4_Q1(XT, true); \
+        else FP4_Q1(XT, false);      \
+    } while (0)
     if (xelem == kF32) FP4_Q(kF32);
     else if (xelem == kF16) FP4_Q(kF16);
     else FP4_Q(kBF16);
 #undef FP4_Q
+#undef FP4_Q1
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_fp4_dequant(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t cols,
                                void *out, int oelem, int device, cudaStream_t s) {
     const int esz = oelem == kF32 ? 4 : 2;
-    const bool vec = cols % 8 == 0 && (cols * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    const bool vec = (cols * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     Fp4Dequant P{q, scales, rows, cols, 0, out};
-    P.words = int(vec ? (cols + kMxBlock - 1) / kMxBlock * 4 : (cols + 255) / 256);
-    const int64_t threads = rows * P.words * (vec ? 1 : 32);
+    P.pieces = int(vec ? (cols + kMxBlock - 1) / kMxBlock * (kMxBlock * esz / 16) : (cols + 255) / 256);
+    const int64_t threads = rows * P.pieces * (vec ? 1 : 32);
     const int64_t want = (threads + kThreads - 1) / kThreads;
     const dim3 grid((unsigned)std::min<int64_t>(want, int64_t(sm_count(device)) * 32)), block(kThreads);
     cudaError_t e;

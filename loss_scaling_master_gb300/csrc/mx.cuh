@@ -64,7 +64,20 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&y)[8]) {
         : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
     return r;
 }
-// Eight e2m1 codes (one word) -> fp32 values.
+// Four e2m1 codes (the low half of w), or eight -> fp32 values.
+__device__ __forceinline__ void e2m1x4_to_f32x4(uint32_t w, float *y) {
+    uint32_t h0, h1;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
+        : "=r"(h0), "=r"(h1)
+        : "r"(w));
+    y[0] = f16_bits_to_f32(h0 & 0xFFFFu);
+    y[1] = f16_bits_to_f32(h0 >> 16);
+    y[2] = f16_bits_to_f32(h1 & 0xFFFFu);
+    y[3] = f16_bits_to_f32(h1 >> 16);
+}
 __device__ __forceinline__ void e2m1x8_to_f32x8(uint32_t w, float (&y)[8]) {
     uint32_t h[4];
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
@@ -156,27 +169,6 @@ template <int XT>
 __device__ __forceinline__ void store_elem(void *x, int64_t k, float v) {
     if constexpr (XT == kF32) static_cast<float *>(x)[k] = v;
     else static_cast<uint16_t *>(x)[k] = uint16_t(f32x2_to_16x2<XT>(v, 0.0f) & 0xFFFFu);
-}
-
-// Eight elements from p (any address) where only the first n are in the
-// tensor: raw words with zeros behind them.
-template <int XT>
-__device__ __forceinline__ void load_raw8_tail(const void *x, int64_t k, int n, uint4 *u) {
-    uint32_t w[4 * kWords8<XT>];
-#pragma unroll
-    for (int j = 0; j < 4 * kWords8<XT>; ++j) {
-        if constexpr (XT == kF32) {
-            w[j] = j < n ? __float_as_uint(static_cast<const float *>(x)[k + j]) : 0u;
-        } else {
-            const uint16_t *p = static_cast<const uint16_t *>(x) + k;
-            const uint32_t a = 2 * j < n ? p[2 * j] : 0u;
-            const uint32_t b = 2 * j + 1 < n ? p[2 * j + 1] : 0u;
-            w[j] = a | (b << 16);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < kWords8<XT>; ++j)
-        u[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
 // Items 0 .. rows * per_row - 1 taken `step` apart (a grid's worth, so below

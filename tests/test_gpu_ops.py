@@ -111,6 +111,24 @@ def test_fp4_quant(G, dev, dt, both, lead):
         assert torch.equal(xd.view(torch.uint8).cpu(), x.contiguous().view(torch.uint8))
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("r,c", [(130, 36), (129, 100), (5, 1028), (33, 1111), (5003, 1028), (20011, 301)])
+def test_fp4_rows_of_fours_and_walks(G, dev, dt, r, c):
+    """Rows that are whole 16-byte pieces in fp32 alone, and more rows than the
+    kernels have places for at once."""
+    x = values(r, c, TYPES[dt], r + c, special=True)
+    q, s = G.fp4_mx_buffers(r, c)
+    qt, st = G.fp4_mx_buffers(c, r)
+    G.fp4_quant_mx(x.to(dev), q, s, qt, st)
+    for a, b, codes, scales, m in ((r, c, q, s, x), (c, r, qt, st, x.t())):
+        v, e, _ = R.mx_blocks(m, "e2m1")
+        assert torch.equal(scales.cpu(), R.tiled_scales(e, a, b))
+        for od, t in TYPES.items():
+            out = Guarded(a * b, t, dev, shape=(a, b))
+            G.fp4_dequant_mx(codes, scales, out.view)
+            assert out.intact() and same(out.view, v.to(t)), (a, b, od)
+
+
 def test_fp4_quant_skips(G, dev):
     x = torch.randn(40, 70, device=dev)
     q, s = G.fp4_mx_buffers(40, 70)
