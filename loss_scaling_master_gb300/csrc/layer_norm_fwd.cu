@@ -26,10 +26,12 @@ struct NormFwd {
 };
 
 // CTAs an SM holds (and the register bound that lets it).  16384 x 4096 bf16
-// with a checkpoint: 2 CTAs 64 us, 3 59 us, 4 (spills) 68 us.
+// with a checkpoint: 2 CTAs 64 us, 3 59 us, 4 (spills) 68 us; 16383 x 4095, by
+// single elements, 1 CTA of 512 141 us, 2 117 us.
 template <int XT, bool VEC>
 __host__ __device__ constexpr int fwd_ctas(int tpr, int nv) {
-    return norm_cta(tpr) > 256 || (nv == 4) ? 1 : nv == 1 ? 4 : VEC && XT != kF32 ? 3 : 2;
+    if (nv == 1) return norm_cta(tpr) > 256 ? 2 : 4;
+    return norm_cta(tpr) > 256 ? 1 : VEC && XT != kF32 ? 3 : 2;
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
