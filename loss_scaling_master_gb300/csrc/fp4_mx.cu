@@ -158,26 +158,23 @@ __global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : 4) fp4_quant_kernel
         transposing_max4<8>(rw, rmax, 2, 1, lane, op);
         if (T) transposing_max4<8>(cw, cmax, 16, 8, lane, op);
     } else {
-        // 16-bit magnitudes order like their values (NaN above inf): maxima on
-        // packed pairs
-        uint32_t m[8], rw[4], cw[4] = {0, 0, 0, 0}, r1[1], c1[1] = {0};
-        auto op = [](uint32_t a, uint32_t b) { return max_u16x2(a, b); };
+        // maxima on packed pairs, their signs cleared when they are widened (on
+        // the bits as integers, signs cleared first: 45.7 against 45.4 us at 16384
+        // x 5120, 15.8 against 15.4 us at 8192 x 4096 rows only)
+        uint32_t m[8], rw[4], cw[4], r1[1], c1[1] = {0};
+        auto op = [](uint32_t a, uint32_t b) { return absmax2<XT>(a, b); };
         auto widen = [](uint32_t h) { return __float_as_uint(lowp_to_f32<XT>(h & 0xFFFFu)) & 0x7FFFFFFFu; };
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t w[4] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w};
-            m[i] = 0;
+            m[i] = op(op(w[0], w[1]), op(w[2], w[3]));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t a = w[j] & 0x7FFF7FFFu;
-                m[i] = max_u16x2(m[i], a);
-                if (T) cw[j] = max_u16x2(cw[j], a);
-            }
+            for (int j = 0; j < 4; ++j)
+                if (T) cw[j] = i ? op(cw[j], w[j]) : w[j];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            rw[i] = max_u16x2(__byte_perm(m[2 * i], m[2 * i + 1], 0x5410),
-                              __byte_perm(m[2 * i], m[2 * i + 1], 0x7632));
+            rw[i] = op(__byte_perm(m[2 * i], m[2 * i + 1], 0x5410), __byte_perm(m[2 * i], m[2 * i + 1], 0x7632));
         transposing_max4<4>(rw, r1, 2, 1, lane, op);
         rmax[0] = widen(r1[0]);
         rmax[1] = widen(r1[0] >> 16);

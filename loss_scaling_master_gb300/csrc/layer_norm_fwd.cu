@@ -48,10 +48,9 @@ __device__ __forceinline__ void keep8(uint8_t *q, uint8_t *sc, int v, int n, con
         if constexpr (XT == kF32) {
             m = max(max(max(abs_bits(f[0]), abs_bits(f[1])), max(abs_bits(f[2]), abs_bits(f[3]))),
                     max(max(abs_bits(f[4]), abs_bits(f[5])), max(abs_bits(f[6]), abs_bits(f[7]))));
-        } else {  // 16-bit magnitudes order like their values: maxima on packed pairs
-            const uint32_t k = 0x7FFF7FFFu;
-            const uint32_t p = max_u16x2(max_u16x2(raw[0].x & k, raw[0].y & k), max_u16x2(raw[0].z & k, raw[0].w & k));
-            m = abs_bits(lowp_to_f32<XT>(max(p & 0xFFFFu, p >> 16)));
+        } else {  // maxima on packed pairs
+            const uint32_t p = absmax2<XT>(absmax2<XT>(raw[0].x, raw[0].y), absmax2<XT>(raw[0].z, raw[0].w));
+            m = abs_bits(lowp_to_f32<XT>(absmax2<XT>(p, p >> 16) & 0xFFFFu));
         }
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));

@@ -40,6 +40,16 @@ __device__ __forceinline__ float mx_scale(uint32_t e) {
     return __uint_as_float(e == 255u ? 0x7FC00000u : b);
 }
 
+// Of two pairs of f16 or bf16, the larger magnitude each; its sign bit means
+// nothing, and a NaN wins.
+template <int XT>
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (XT == kF16) asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Two fp32 -> one byte of two e2m1 codes (lo in bits 0-3), RNE.  Only values
 // of magnitude at most 6 matter.
 __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
