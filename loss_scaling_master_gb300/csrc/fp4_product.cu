@@ -657,12 +657,14 @@ cudaError_t go(Fp4Product P, const void *a, const void *b, int64_t row_bytes, in
     P.tiles_n = int((P.n + kLanes - 1) / kLanes);
     const int64_t tiles = int64_t(P.tiles_m) * P.tiles_n, room = int64_t(sm_count(device)) * S::ctas;
     // Cutting the reduction pays where the CTAs still find an SM each and the
-    // stages saved (0.2 us each) outweigh the exchange (0.8 us for few tokens, 2
-    // us for 128): 48 x 4096 x 4096 6.8 us whole, 5.3 us in four; 1 x 14336 x 4096
-    // 6.5 us whole, 8.0 us in two on shared SMs; 1000 x 768 x 2304 5.9 us whole,
-    // 6.9 us in two.  Eight parts are slower than four (clusters of 8 large CTAs
-    // do not fill every part of the GPU: 512 x 512 x 8192 12.7 us, in four 7.1).
-    const int ks = (P.kt + 1) / 2, pays = BN == 128 ? 10 : 4;
+    // stages saved (0.2 us each) outweigh the exchange, which grows with the
+    // tokens: 1 x 2048 x 2560 4.4 us whole, 4.1 us in four; 64 x 1024 x 1536 3.7
+    // whole, 4.8 in four; 48 x 4096 x 4096 5.9 and 5.3; 128 x 4096 x 4096 6.5 and
+    // 6.7; 128 x 4096 x 5120 7.4 and 6.9.  On shared SMs it does not: 1 x 14336 x
+    // 4096 6.5 us whole, 8.0 us in two.  Eight parts are slower than four (clusters
+    // of 8 large CTAs do not fill every part of the GPU: 512 x 512 x 8192 12.7 us,
+    // in four 7.1).
+    const int ks = (P.kt + 1) / 2, pays = 7 + int(std::min<int64_t>(P.m, BN)) / 16;
     int parts = 1;
     for (int p = 2; p <= int(kMaxParts) && tiles * p <= sm_count(device); p *= 2)
         if (ks - (ks + p - 1) / p >= pays) parts = p;

@@ -55,6 +55,14 @@ def test_product(G, dev, shape):
         assert torch.equal(again, out.view)
 
 
+@pytest.mark.parametrize("shape", [(1, 300, 2600), (5, 130, 4001), (16, 1000, 5000), (20, 517, 3333), (32, 128, 7000),
+                                   (50, 301, 4100), (100, 700, 8191), (7, 6401, 4100), (128, 6401, 7700)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_product_of_few_tiles_and_a_long_reduction(G, dev, shape):
+    """Reductions that are cut in two or four, for each width of a tile."""
+    test_product(G, dev, shape)
+
+
 def test_product_is_exact_on_small_integers(G, dev):
     """Products and sums that fp32 holds exactly come out exactly."""
     g = torch.Generator().manual_seed(1)
