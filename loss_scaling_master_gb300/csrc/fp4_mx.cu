@@ -275,68 +275,88 @@ __global__ void __launch_bounds__(kThreads, XT == kF32 ? 2 : 4) fp4_quant_kernel
 }
 
 // ---- values of the codes -------------------------------------------------
+// With U = 4 a step takes the rows r, r + 32, r + 64 and r + 96 of a tile of 128
+// at one place: their scales are one 16-byte line of a scale tile, and their
+// addresses a fixed distance apart.  (With a row's place worked out for every 8
+// elements, 12 instructions an element bound the kernel: 16384 x 5120 bf16 36.2
+// against 33.4 us, memory 31.4 us; 1000 x 2304 3.2 against 2.1 us.)  Where that
+// leaves SMs without a CTA, U = 1: a row a step (32 x 4096 1.3 against 1.4 us, 33 x
+// 1111 1.3 against 1.6 us).
 struct Fp4Dequant {
     const uint8_t *q, *scales;
     int64_t rows, cols;
-    int pieces;  // of a packed row: of 16 bytes of output, or of 256 elements
+    int64_t groups;  // of rows: U = 4: 32 a whole tile; else the rows
+    int pieces;      // of a packed row: of 16 bytes of output, or of 256 elements
     void *out;
 };
-
-__device__ __forceinline__ uint32_t scale_at(const Fp4Dequant &P, int64_t r, int b) {
-    const int64_t tile = (r >> 7) * ((P.cols + kTile - 1) / kTile) + (b >> 2);
-    return P.scales[tile * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3)];
+template <int U>
+struct RowGroup {
+    int64_t row;  // the first
+    int n;        // how many of the U are there
+    __device__ __forceinline__ RowGroup(const Fp4Dequant &P, int64_t g) {
+        row = U == 4 ? (g >> 5) * kTile + (g & 31) : g;
+        n = U == 4 ? int(min(int64_t(4), (P.rows - row + 31) / 32)) : 1;
+    }
+};
+// the rows' scale bytes of block b
+template <int U>
+__device__ __forceinline__ void group_scales(const Fp4Dequant &P, int64_t row, int b, uint32_t (&e)[U]) {
+    const int64_t tile = (row >> 7) * ((P.cols + kTile - 1) / kTile) + (b >> 2);
+    const uint8_t *line = P.scales + tile * 512 + (row & 31) * 16;
+    if constexpr (U == 4) {
+        const uint4 w = ld16(line);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = (u[i] >> (8 * (b & 3))) & 0xFFu;
+    } else {
+        e[0] = line[((row >> 5) & 3) * 4 + (b & 3)];
+    }
 }
 
-// Rows that are whole, aligned 16-byte pieces: one of them a thread and step,
-// four steps' loads before the first store.  (Two pieces side by side a thread in
-// fp32 would write every sector by halves: 16384 x 5120 83 us, one 60 us, memory
-// 56 us; 16-bit 36 us of 31.)
-template <int XT>
+// Rows that are whole, aligned 16-byte pieces: one of them a thread, step and
+// row.  (Two pieces side by side a thread in fp32 would write every sector by
+// halves: 16384 x 5120 83 us, one 59 us, memory 56 us.)
+template <int XT, int U>
 __global__ void __launch_bounds__(kThreads) fp4_dequant_vec(Fp4Dequant P) {
     pdl_wait();
     pdl_trigger();
-    constexpr int U = 4, N = XT == kF32 ? 4 : 8;  // N elements a piece
+    constexpr int N = XT == kF32 ? 4 : 8;  // elements a piece
     using Codes = std::conditional_t<XT == kF32, uint16_t, uint32_t>;
     RowWalk at(blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads, P.pieces);
-    while (at.row < P.rows) {
+    for (; at.row < P.groups; at.next()) {
+        if (N * at.at >= P.cols) continue;
+        const RowGroup<U> r(P, at.row);
+        const Codes *q = reinterpret_cast<const Codes *>(P.q) + r.row * P.pieces + at.at;
         uint32_t codes[U], e[U];
-        int64_t k[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) codes[i] = i < r.n ? q[32 * i * int64_t(P.pieces)] : 0u;
+        group_scales<U>(P, r.row, at.at / (kMxBlock / N), e);
+        char *out = static_cast<char *>(P.out) + (r.row * P.cols + N * at.at) * (16 / N);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const bool in = at.row < P.rows && N * at.at < P.cols;
-            k[i] = in ? at.row * P.cols + N * at.at : -1;
-            if (in) {
-                codes[i] = reinterpret_cast<const Codes *>(P.q)[at.row * P.pieces + at.at];
-                e[i] = scale_at(P, at.row, at.at / (kMxBlock / N));
-            }
-            at.next();
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (k[i] < 0) continue;
+            if (i >= r.n) break;
             const float s = mx_scale(e[i]);
             float y[8];
             if constexpr (N == 4) e2m1x4_to_f32x4(codes[i], y);
             else e2m1x8_to_f32x8(codes[i], y);
 #pragma unroll
             for (int j = 0; j < N; j += 2) mul2_rn(y[j], y[j + 1], s, s, y[j], y[j + 1]);
-            if constexpr (N == 4) {
-                *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + k[i]) = make_float4(y[0], y[1], y[2], y[3]);
-            } else {
-                uint4 u[1];
-                f32_to_raw8<XT>(y, u);
-                st16(static_cast<uint16_t *>(P.out) + k[i], u[0]);
-            }
+            uint4 u[1];
+            if constexpr (N == 4)
+                u[0] = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                                  __float_as_uint(y[3]));
+            else f32_to_raw8<XT>(y, u);
+            st16(out + 32 * i * P.cols * (16 / N), u[0]);
         }
     }
 }
 
-// Any row length and address: a warp takes 256 elements of a row, a lane one
+// Any row length and address: a warp takes 256 elements of each row, a lane one
 // packed word of them; the values are turned over in shared memory so that each
 // store of the warp is 32 elements side by side (fp32: 16-byte pieces exchanged
-// in every other 32 elements, against bank conflicts): 16383 x 5121 bf16 48 us,
+// in every other 32 elements, against bank conflicts): 16383 x 5121 bf16 39 us,
 // 79 us with a word decoded for each element.
-template <int XT>
+template <int XT, int U>
 __global__ void __launch_bounds__(kThreads) fp4_dequant_elem(Fp4Dequant P) {
     using E = std::conditional_t<XT == kF32, uint32_t, uint16_t>;
     constexpr int W = kWords8<XT>;
@@ -348,29 +368,38 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_elem(Fp4Dequant P) {
     const E *const get = reinterpret_cast<const E *>(put);
     const int64_t rowb = (P.cols + kMxBlock - 1) / kMxBlock * 16;
     RowWalk at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), P.pieces);
-    for (; at.row < P.rows; at.next()) {
+    for (; at.row < P.groups; at.next()) {
+        const RowGroup<U> r(P, at.row);
         const int c0 = 256 * at.at;
-        uint32_t codes = 0, e = 0;
+        uint32_t codes[U] = {}, e[U] = {};
         if (c0 / 2 + 4 * lane < rowb) {
-            codes = *reinterpret_cast<const uint32_t *>(P.q + at.row * rowb + c0 / 2 + 4 * lane);
-            e = scale_at(P, at.row, c0 / 32 + lane / 4);
+            const uint8_t *q = P.q + r.row * rowb + c0 / 2 + 4 * lane;
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (i < r.n) codes[i] = *reinterpret_cast<const uint32_t *>(q + 32 * i * rowb);
+            group_scales<U>(P, r.row, c0 / 32 + lane / 4, e);
         }
-        const float s = mx_scale(e);
-        float y[8];
-        e2m1x8_to_f32x8(codes, y);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) mul2_rn(y[j], y[j + 1], s, s, y[j], y[j + 1]);
-        uint4 u[W];
-        f32_to_raw8<XT>(y, u);
-        __syncwarp();  // the last step's words are out
-#pragma unroll
-        for (int j = 0; j < W; ++j) put[(W * lane + j) ^ (W == 2 ? (lane >> 2) & 1 : 0)] = u[j];
-        __syncwarp();
-        E *out = static_cast<E *>(P.out) + at.row * P.cols + c0 + lane;
+        E *out = static_cast<E *>(P.out) + r.row * P.cols + c0 + lane;
         const int n = int(P.cols) - c0 - lane;  // n > 32 j: element j is in the row
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (n > 32 * j) out[32 * j] = get[32 * j + (W == 2 ? lane ^ (4 * (j & 1)) : lane)];
+        for (int i = 0; i < U; ++i) {
+            if (i >= r.n) break;
+            const float s = mx_scale(e[i]);
+            float y[8];
+            e2m1x8_to_f32x8(codes[i], y);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) mul2_rn(y[j], y[j + 1], s, s, y[j], y[j + 1]);
+            uint4 u[W];
+            f32_to_raw8<XT>(y, u);
+            __syncwarp();  // the last row's words are out
+#pragma unroll
+            for (int j = 0; j < W; ++j) put[(W * lane + j) ^ (W == 2 ? (lane >> 2) & 1 : 0)] = u[j];
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (n > 32 * j) out[32 * j] = get[32 * j + (W == 2 ? lane ^ (4 * (j & 1)) : lane)];
+            out += 32 * P.cols;
+        }
     }
 }
 
@@ -415,18 +444,26 @@ cudaError_t launch_fp4_dequant(const uint8_t *q, const uint8_t *scales, int64_t 
                                void *out, int oelem, int device, cudaStream_t s) {
     const int esz = oelem == kF32 ? 4 : 2;
     const bool vec = (cols * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-    Fp4Dequant P{q, scales, rows, cols, 0, out};
+    Fp4Dequant P{q, scales, rows, cols, rows / kTile * 32 + std::min<int64_t>(32, rows % kTile), 0, out};
     P.pieces = int(vec ? (cols + kMxBlock - 1) / kMxBlock * (kMxBlock * esz / 16) : (cols + 255) / 256);
-    const int64_t threads = rows * P.pieces * (vec ? 1 : 32);
-    const int64_t want = (threads + kThreads - 1) / kThreads;
-    const dim3 grid((unsigned)std::min<int64_t>(want, int64_t(sm_count(device)) * 32)), block(kThreads);
+    const int64_t sms = sm_count(device), per_cta = vec ? kThreads : kThreads / 32;
+    const bool four = P.groups * P.pieces >= sms * per_cta;
+    if (!four) P.groups = rows;
+    const int64_t want = (P.groups * P.pieces + per_cta - 1) / per_cta;
+    const dim3 grid((unsigned)std::min<int64_t>(want, sms * 32)), block(kThreads);
     cudaError_t e;
-#define FP4_D(XT)                                                             \
-    e = vec ? launch_pdl(fp4_dequant_vec<XT>, grid, block, 0, s, P)           \
-            : launch_pdl(fp4_dequant_elem<XT>, grid, block, 0, s, P)
+#define FP4_D1(XT, U)                                                         \
+    e = vec ? launch_pdl(fp4_dequant_vec<XT, U>, grid, block, 0, s, P)        \
+            : launch_pdl(fp4_dequant_elem<XT, U>, grid, block, 0, s, P)
+#define FP4_D(XT)                \
+    do {                         \
+        if (four) FP4_D1(XT, 4); \
+        else FP4_D1(XT, 1);      \
+    } while (0)
     if (oelem == kF32) FP4_D(kF32);
     else if (oelem == kF16) FP4_D(kF16);
     else FP4_D(kBF16);
+#undef FP4_D1
 #undef FP4_D
     return e != cudaSuccess ? e : cudaGetLastError();
 }

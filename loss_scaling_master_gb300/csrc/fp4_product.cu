@@ -649,6 +649,9 @@ cudaError_t go_pair(Fp4Product P, const void *a, const void *b, int64_t row_byte
 template <int BN>
 cudaError_t go(Fp4Product P, const void *a, const void *b, int64_t row_bytes, int device, cudaStream_t s) {
     using S = Solo<BN>;
+    // a narrower tile takes all tokens: the kernel finds a token tile's scales as
+    // the scale tile (128 rows) of the same index
+    if (BN < 128 && P.m > BN) return cudaErrorInvalidValue;
     CUtensorMap mt, mw;
     cudaError_t e = rows_map(&mt, a, P.m, row_bytes, BN);
     if (e == cudaSuccess) e = rows_map(&mw, b, P.n, row_bytes, kLanes);

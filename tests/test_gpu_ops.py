@@ -112,7 +112,7 @@ def test_fp4_quant(G, dev, dt, both, lead):
 
 
 @pytest.mark.parametrize("dt", TYPES)
-@pytest.mark.parametrize("r,c", [(130, 36), (129, 100), (5, 1028), (33, 1111), (5003, 1028), (20011, 301)])
+@pytest.mark.parametrize("r,c", [(130, 36), (129, 100), (5, 1028), (33, 1111), (5003, 1028), (2999, 1040), (20011, 301)])
 def test_fp4_rows_of_fours_and_walks(G, dev, dt, r, c):
     """Rows that are whole 16-byte pieces in fp32 alone, and more rows than the
     kernels have places for at once."""
