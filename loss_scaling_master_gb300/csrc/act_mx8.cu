@@ -14,6 +14,7 @@
 // takes two shuffles.  Rows that are not whole groups of 8 elements, or not
 // 16-byte aligned, take one element a lane and one block a warp instead.
 #include <algorithm>
+#include <type_traits>
 
 #include "ampops.h"
 #include "f32x2.cuh"
@@ -259,59 +260,95 @@ __global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P) {
     }
 }
 
-// Any size, any address: a warp takes four blocks of a row at a time, a lane one
-// element of each, so accesses stay side by side and a row's place is worked
-// out once for four elements (with one block a step, 100 instructions an element
-// bound the kernel: 8.6 us for 2047 x 1111).
-constexpr int kElemBlocks = 4;
+// Any size, any address: a warp takes EB blocks of a row at a time, a lane one
+// element of each, so accesses stay side by side and a row's place is worked out
+// once for EB elements (with one block a step, 100 instructions an element bound
+// the kernel: 2047 x 1111 f16 GELU 8.6 us, with four 5.7 us, with eight 4.9 us).  Eight
+// where rows are long and many enough; 20000 x 100 takes 6.0 us by four and 7.9 by
+// eight, 33 x 1111 1.5 and 1.8 us.
+template <int XT>
+using Elem = std::conditional_t<XT == kF32, uint32_t, uint16_t>;
+template <int XT>
+__device__ __forceinline__ float widen1(Elem<XT> v) {
+    if constexpr (XT == kF32) return __uint_as_float(v);
+    else return lowp_to_f32<XT>(v);
+}
 
-template <int XT, int ACT, bool GATED, bool KEEP>
+// The checkpoint of a warp's EB blocks, x[i] the lane's element of block i.  By
+// four: a block's maximum by one reduction over the warp.  By eight: the warp's
+// 256 elements go through shared memory (s, 1 KB, and b, 256 bytes) to 8
+// consecutive ones a lane and their codes come back as bytes, so that scales and
+// conversions serve 8 elements (fp32: 16-byte pieces exchanged in every other
+// block, against bank conflicts).  n > 32 i: element i is in the row; kb: blocks
+// left in it.
+template <int XT, int EB>
+__device__ __forceinline__ void keep_elems(const Elem<XT> (&x)[EB], int n, int kb, uint8_t *q, uint8_t *sc,
+                                           uint4 *s, uint2 *b) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (EB == 8) {
+        constexpr int W = kWords8<XT>;
+        __syncwarp();  // the last values of s and b are read
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            reinterpret_cast<Elem<XT> *>(s)[32 * i + (W == 2 ? lane ^ (4 * (i & 1)) : lane)] = x[i];
+        __syncwarp();
+        uint4 u[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) u[i] = s[(W * lane + i) ^ (W == 2 ? (lane >> 2) & 1 : 0)];
+        float y[8];
+        raw8_to_f32<XT>(u, y);
+        const uint32_t e = mx_scale_code<MxE4M3>(block_max8(y));
+        b[lane] = codes8(y, mx_unscale(e));
+        if ((lane & 3) == 0 && lane / 4 < kb) sc[lane / 4] = uint8_t(e);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (n > 32 * i) q[32 * i] = reinterpret_cast<const uint8_t *>(b)[32 * i + lane];
+    } else {
+        uint32_t mine = 0;  // lane i: block i's scale byte
+#pragma unroll
+        for (int i = 0; i < EB; ++i) {
+            const float v = widen1<XT>(x[i]);
+            const uint32_t e = mx_scale_code<MxE4M3>(warp_max_u32(__float_as_uint(v) & 0x7FFFFFFFu));
+            if (n > 32 * i) q[32 * i] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(v, mx_unscale(e)), 0.0f));
+            if (lane == i) mine = e;
+        }
+        if (lane < EB && lane < kb) sc[lane] = uint8_t(mine);
+    }
+}
+
+template <int XT, int ACT, bool GATED, bool KEEP, int EB>
 __global__ void __launch_bounds__(kThreads) act_fwd_elem(ActFwd P) {
+    __shared__ uint4 s_x[EB == 8 && KEEP ? kThreads / 32 : 1][32 * kWords8<XT>];
+    __shared__ uint2 s_q[EB == 8 && KEEP ? kThreads / 32 : 1][32];
     pdl_wait();
     pdl_trigger();
-    constexpr int esz = XT == kF32 ? 4 : 2;
-    const int lane = threadIdx.x & 31;
-    RowWalk at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32),
-               (P.kb + kElemBlocks - 1) / kElemBlocks);
+    const int lane = threadIdx.x & 31, warp = EB == 8 && KEEP ? threadIdx.x >> 5 : 0;
+    RowWalk at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), (P.kb + EB - 1) / EB);
     for (; at.row < P.rows; at.next()) {
-        const int b0 = at.at * kElemBlocks, n = int(P.cols) - b0 * kMxBlock - lane;  // n > 32 i: element i is in the row
+        const int b0 = at.at * EB, n = int(P.cols) - b0 * kMxBlock - lane;  // n > 32 i: element i is in the row
         const int64_t k = at.row * P.cols + b0 * kMxBlock + lane, sb = at.row * P.kb + b0;
-        const char *xp = static_cast<const char *>(P.x) + k * esz, *up = static_cast<const char *>(P.u) + k * esz;
-        char *yp = static_cast<char *>(P.y) + k * esz;
-        uint8_t *qp = P.q + k, *qup = P.qu + k;
-        float x[kElemBlocks], u[kElemBlocks];
+        const Elem<XT> *xp = static_cast<const Elem<XT> *>(P.x) + k, *up = static_cast<const Elem<XT> *>(P.u) + k;
+        Elem<XT> x[EB], u[EB];
 #pragma unroll
-        for (int i = 0; i < kElemBlocks; ++i) {
-            x[i] = n > 32 * i ? load_elem<XT>(xp, 32 * i) : 0.0f;
-            u[i] = GATED && n > 32 * i ? load_elem<XT>(up, 32 * i) : 0.0f;
+        for (int i = 0; i < EB; ++i) {
+            x[i] = n > 32 * i ? xp[32 * i] : Elem<XT>(0);
+            u[i] = GATED && n > 32 * i ? up[32 * i] : Elem<XT>(0);
         }
-        uint32_t e = 0, eu = 0;  // lane i < 4: block i's scale byte
-#pragma unroll
-        for (int i = 0; i < kElemBlocks; ++i) {
-            if (KEEP) {
-                const uint32_t c = mx_scale_code<MxE4M3>(warp_max_u32(__float_as_uint(x[i]) & 0x7FFFFFFFu));
-                if (n > 32 * i) qp[32 * i] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(x[i], mx_unscale(c)), 0.0f));
-                if (lane == i) e = c;
-                if (GATED) {
-                    const uint32_t d = mx_scale_code<MxE4M3>(warp_max_u32(__float_as_uint(u[i]) & 0x7FFFFFFFu));
-                    if (n > 32 * i)
-                        qup[32 * i] = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(u[i], mx_unscale(d)), 0.0f));
-                    if (lane == i) eu = d;
-                }
-            }
+        if constexpr (KEEP) {
+            keep_elems<XT, EB>(x, n, P.kb - b0, P.q + k, P.s + sb, s_x[warp], s_q[warp]);
+            if (GATED) keep_elems<XT, EB>(u, n, P.kb - b0, P.qu + k, P.su + sb, s_x[warp], s_q[warp]);
         }
         if constexpr (ACT != kSave) {
+            char *yp = static_cast<char *>(P.y) + k * int(sizeof(Elem<XT>));
 #pragma unroll
-            for (int i = 0; i < kElemBlocks; i += 2) {
+            for (int i = 0; i < EB; i += 2) {
                 if (n <= 32 * i) break;
-                const float2 v = act_apply<ACT, GATED>(x[i], x[i + 1], u[i], u[i + 1]);
+                const float2 v = act_apply<ACT, GATED>(widen1<XT>(x[i]), widen1<XT>(x[i + 1]), widen1<XT>(u[i]),
+                                                       widen1<XT>(u[i + 1]));
                 store_elem<XT>(yp, 32 * i, v.x);
                 if (n > 32 * (i + 1)) store_elem<XT>(yp, 32 * (i + 1), v.y);
             }
-        }
-        if (KEEP && lane < kElemBlocks && b0 + lane < P.kb) {
-            P.s[sb + lane] = uint8_t(e);
-            if (GATED) P.su[sb + lane] = uint8_t(eu);
         }
     }
 }
@@ -349,50 +386,53 @@ __global__ void __launch_bounds__(kThreads) act_bwd_vec(ActBwd P) {
     }
 }
 
-template <int XT, int ACT, bool GATED>
+template <int XT, int ACT, bool GATED, int EB>
 __global__ void __launch_bounds__(kThreads) act_bwd_elem(ActBwd P) {
     pdl_wait();
     pdl_trigger();
     constexpr int esz = XT == kF32 ? 4 : 2;
     const int lane = threadIdx.x & 31;
     RowWalk at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32),
-               (P.kb + kElemBlocks - 1) / kElemBlocks);
+               (P.kb + EB - 1) / EB);
     for (; at.row < P.rows; at.next()) {
-        const int b0 = at.at * kElemBlocks, n = int(P.cols) - b0 * kMxBlock - lane;
+        const int b0 = at.at * EB, n = int(P.cols) - b0 * kMxBlock - lane;
         const int64_t k = at.row * P.cols + b0 * kMxBlock + lane, sb = at.row * P.kb + b0;
         const char *gp = static_cast<const char *>(P.dy) + k * esz;
         char *dxp = static_cast<char *>(P.dx) + k * esz, *dup = static_cast<char *>(P.du) + k * esz;
         const uint8_t *qp = P.q + k, *qup = P.qu + k;
-        uint32_t q[kElemBlocks], qu[kElemBlocks], e[kElemBlocks], eu[kElemBlocks];
-        float g[kElemBlocks];
+        uint32_t q[EB], qu[EB];
+        float g[EB];
+        // lane i: block i's scale
+        const bool scales = lane < EB && lane < P.kb - b0;
+        const float sx = scales ? mx_scale(P.s[sb + lane]) : 0.0f;
+        const float su = GATED && scales ? mx_scale(P.su[sb + lane]) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < kElemBlocks; ++i) {
-            q[i] = qu[i] = e[i] = eu[i] = 0;
+        for (int i = 0; i < EB; ++i) {
+            q[i] = qu[i] = 0;
             g[i] = 0.0f;
             if (n <= 32 * i) continue;
             q[i] = qp[32 * i];
-            e[i] = P.s[sb + i];
-            if (GATED) {
-                qu[i] = qup[32 * i];
-                eu[i] = P.su[sb + i];
-            }
+            if (GATED) qu[i] = qup[32 * i];
             if (ACT != kSave) g[i] = load_elem<XT>(gp, 32 * i);
         }
 #pragma unroll
-        for (int i = 0; i < kElemBlocks; i += 2) {
-            if (n <= 32 * i) break;
+        for (int i = 0; i < EB; i += 2) {
+            constexpr uint32_t all = 0xFFFFFFFFu;
+            const float s0 = __shfl_sync(all, sx, i), s1 = __shfl_sync(all, sx, i + 1);
+            const float t0 = GATED ? __shfl_sync(all, su, i) : 0.0f, t1 = GATED ? __shfl_sync(all, su, i + 1) : 0.0f;
+            if (n <= 32 * i) continue;
             const bool two = n > 32 * (i + 1);
             float v[4], w[4];
             e4m3x4_to_f32x4(q[i] | (q[i + 1] << 8), v);
-            const float x0 = __fmul_rn(v[0], mx_scale(e[i])), x1 = __fmul_rn(v[1], mx_scale(e[i + 1]));
+            const float x0 = __fmul_rn(v[0], s0), x1 = __fmul_rn(v[1], s1);
             if constexpr (ACT == kSave) {
                 store_elem<XT>(dxp, 32 * i, x0);
                 if (two) store_elem<XT>(dxp, 32 * (i + 1), x1);
             } else {
                 float2 dx, du;
                 if (GATED) e4m3x4_to_f32x4(qu[i] | (qu[i + 1] << 8), w);
-                const float u0 = GATED ? __fmul_rn(w[0], mx_scale(eu[i])) : 0.0f;
-                const float u1 = GATED ? __fmul_rn(w[1], mx_scale(eu[i + 1])) : 0.0f;
+                const float u0 = GATED ? __fmul_rn(w[0], t0) : 0.0f;
+                const float u1 = GATED ? __fmul_rn(w[1], t1) : 0.0f;
                 act_grads<ACT, GATED>(x0, x1, u0, u1, g[i], g[i + 1], dx, du);
                 store_elem<XT>(dxp, 32 * i, dx.x);
                 if (two) store_elem<XT>(dxp, 32 * (i + 1), dx.y);
@@ -418,28 +458,41 @@ unsigned grid_of(int64_t threads, int most, int device) {
 // with 8 of them 83 us).
 constexpr int kVecCtas = 64, kElemCtas = 32;
 int64_t vec_threads(int64_t rows, int kb) { return rows * kb * 4; }
-int64_t elem_threads(int64_t rows, int kb) { return rows * ((kb + kElemBlocks - 1) / kElemBlocks) * 32; }
+int64_t elem_threads(int64_t rows, int kb, int eb) { return rows * ((kb + eb - 1) / eb) * 32; }
+// eight blocks a step: rows of 32 blocks or more, and 16 warps for every SM
+bool eight_blocks(int64_t rows, int kb, int device) {
+    return kb >= 32 && elem_threads(rows, kb, 8) >= int64_t(sm_count(device)) * 512;
+}
 
+template <int XT, int ACT, bool GATED, bool KEEP>
+cudaError_t fwd_keep(const ActFwd &P, bool vec, int dev, cudaStream_t s) {
+    const dim3 block(kThreads);
+    if (vec)
+        return launch_pdl(act_fwd_vec<XT, ACT, GATED, KEEP>, dim3(grid_of(vec_threads(P.rows, P.kb), kVecCtas, dev)),
+                          block, 0, s, P);
+    if (eight_blocks(P.rows, P.kb, dev))
+        return launch_pdl(act_fwd_elem<XT, ACT, GATED, KEEP, 8>,
+                          dim3(grid_of(elem_threads(P.rows, P.kb, 8), kElemCtas, dev)), block, 0, s, P);
+    return launch_pdl(act_fwd_elem<XT, ACT, GATED, KEEP, 4>,
+                      dim3(grid_of(elem_threads(P.rows, P.kb, 4), kElemCtas, dev)), block, 0, s, P);
+}
 template <int XT, int ACT, bool GATED>
 cudaError_t fwd(const ActFwd &P, bool keep, bool vec, int dev, cudaStream_t s) {
-    const dim3 block(kThreads), gv(grid_of(vec_threads(P.rows, P.kb), kVecCtas, dev)),
-        ge(grid_of(elem_threads(P.rows, P.kb), kElemCtas, dev));
-    if constexpr (ACT == kSave)
-        return vec ? launch_pdl(act_fwd_vec<XT, ACT, GATED, true>, gv, block, 0, s, P)
-                   : launch_pdl(act_fwd_elem<XT, ACT, GATED, true>, ge, block, 0, s, P);
-    else if (keep)
-        return vec ? launch_pdl(act_fwd_vec<XT, ACT, GATED, true>, gv, block, 0, s, P)
-                   : launch_pdl(act_fwd_elem<XT, ACT, GATED, true>, ge, block, 0, s, P);
-    else
-        return vec ? launch_pdl(act_fwd_vec<XT, ACT, GATED, false>, gv, block, 0, s, P)
-                   : launch_pdl(act_fwd_elem<XT, ACT, GATED, false>, ge, block, 0, s, P);
+    if constexpr (ACT != kSave)
+        if (!keep) return fwd_keep<XT, ACT, GATED, false>(P, vec, dev, s);
+    return fwd_keep<XT, ACT, GATED, true>(P, vec, dev, s);
 }
 template <int XT, int ACT, bool GATED>
 cudaError_t bwd(const ActBwd &P, bool vec, int dev, cudaStream_t s) {
-    const dim3 block(kThreads), gv(grid_of(vec_threads(P.rows, P.kb), kVecCtas, dev)),
-        ge(grid_of(elem_threads(P.rows, P.kb), kElemCtas, dev));
-    return vec ? launch_pdl(act_bwd_vec<XT, ACT, GATED>, gv, block, 0, s, P)
-               : launch_pdl(act_bwd_elem<XT, ACT, GATED>, ge, block, 0, s, P);
+    const dim3 block(kThreads);
+    if (vec)
+        return launch_pdl(act_bwd_vec<XT, ACT, GATED>, dim3(grid_of(vec_threads(P.rows, P.kb), kVecCtas, dev)), block, 0,
+                          s, P);
+    if (eight_blocks(P.rows, P.kb, dev))
+        return launch_pdl(act_bwd_elem<XT, ACT, GATED, 8>, dim3(grid_of(elem_threads(P.rows, P.kb, 8), kElemCtas, dev)),
+                          block, 0, s, P);
+    return launch_pdl(act_bwd_elem<XT, ACT, GATED, 4>, dim3(grid_of(elem_threads(P.rows, P.kb, 4), kElemCtas, dev)),
+                      block, 0, s, P);
 }
 
 template <int XT>

@@ -340,6 +340,24 @@ def test_activations(G, dev, dt, kind, gated):
         assert torch.equal(dyd, dx.view)
 
 
+# rows of more than a thousand elements, as many as give every SM work, not whole groups of eight
+LONG_SIZES = [(600, 1111), (301, 2999), (521, 1025)]
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("kind,gated", [("gelu", False), ("gelu_tanh", True), ("silu", True)])
+def test_activations_of_long_odd_rows(G, dev, dt, kind, gated, monkeypatch):
+    monkeypatch.setitem(globals(), "SIZES", LONG_SIZES)
+    test_activations(G, dev, dt, kind, gated)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("lead", [0, 1])
+def test_ckpt8_of_long_odd_rows(G, dev, dt, lead, monkeypatch):
+    monkeypatch.setitem(globals(), "SIZES", LONG_SIZES)
+    test_ckpt8_special_values(G, dev, dt, lead)
+
+
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("lead", [0, 1])
 def test_ckpt8_special_values(G, dev, dt, lead):
