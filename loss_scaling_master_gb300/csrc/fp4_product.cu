@@ -25,6 +25,12 @@
 // from there (so the order of the sum is fixed and nothing goes through global
 // memory).
 //
+// 8192 x 14336 x 4096 bf16 (pairs): 138 us, 6.97 PFLOP/s, the tensor pipe busy
+// 73 % of the time: a stage of four products takes 402 clocks alone and 550 while
+// the store warps write the previous tile, and the hand-over of the accumulators
+// (all of tensor memory that the scales leave is one tile) idles it 0.3 us a tile.
+// 48 x 4096 x 4096 (four parts): 5.3 us, of which 1.5 are memory.
+//
 // Every wait gives up after a second of GPU time: the role sets the error word,
 // waits (again bounded) for the copies or products that it has in flight and
 // ends; the roles that wait for it give up in turn, tensor memory is freed, and

@@ -136,8 +136,21 @@ __device__ __forceinline__ float ld_param(const void *w, int wt, int64_t c, floa
 template <bool VEC, int TPR>
 __device__ __forceinline__ void ld_params(const void *w, int wt, int v, int t, int n, float fill, f2 (&y)[4]) {
     float f[8];
+    // (by single elements, 1024 x 768 with fp32 parameters 3.5 us instead of 2.6)
+    if (VEC && w != nullptr && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+        const int c = norm_col<true, TPR>(v, t, 0);
+        uint4 u[2] = {};
+        if (n > 0) {
+            u[0] = ld16(static_cast<const char *>(w) + c * (wt == kF32 ? 4 : 2));
+            if (wt == kF32) u[1] = ld16(static_cast<const char *>(w) + c * 4 + 16);
+        }
+        if (wt == kF32) raw8_to_f32<kF32>(u, f);
+        else if (wt == kF16) raw8_to_f32<kF16>(u, f);
+        else raw8_to_f32<kBF16>(u, f);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = j < n ? ld_param(w, wt, norm_col<VEC, TPR>(v, t, j), fill) : 0.0f;
+        for (int j = 0; j < 8; ++j) f[j] = j < n ? ld_param(w, wt, norm_col<VEC, TPR>(v, t, j), fill) : 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = make_f2(f[2 * i], f[2 * i + 1]);
 }
@@ -186,15 +199,17 @@ __host__ __device__ constexpr int norm_rpc(int tpr) { return norm_cta(tpr) / tpr
 
 // Runs F(TPR, NV) for the row length: the smallest CTA that holds the row in two
 // groups a thread, four for the longest rows, whose CTA could not be larger.
-// T1, V1: the shape up to 1024 elements.  Forward 128 x 1 (8 rows of 768 2.0 us,
-// with a warp a row 3.3 us, whose code is four times as long and run once; 16384
-// x 1024 15.7 against 18.9 us, 8192 x 768 8.5 against 8.0 us), backward 64 x 2 (4.3
-// against 5.5, 25.6 against 26.6, 14.7 against 15.0 us; 128 x 1 3.6, 28.5, 16.4 us).
-#define AMP_NORM_SHAPE(cols, F, T1, V1)         \
+// T1, V1 and T2, V2: the shapes up to 1024 and 2048 elements.  Forward 128 x 1 (8
+// rows of 768 1.8 us, with a warp a row, whose code is four times as long and run
+// once, over 3 us; 8192 x 768 the same either way) and 256 x 1 (16384 x 2048 with a
+// checkpoint 33.3 us, 128 x 2 40.5 with spills, 100 x 2048 2.0 and 2.7 us); backward
+// 64 x 2 (8 x 768 4.3 us, 16384 x 1024 25.6, a warp a row 5.5 and 26.6, 128 x 1 3.6
+// and 28.5) and 128 x 2.
+#define AMP_NORM_SHAPE(cols, F, T1, V1, T2, V2) \
     do {                                        \
         if ((cols) <= 256) { F(32, 1); }        \
         else if ((cols) <= 1024) { F(T1, V1); } \
-        else if ((cols) <= 2048) { F(128, 2); } \
+        else if ((cols) <= 2048) { F(T2, V2); } \
         else if ((cols) <= 4096) { F(256, 2); } \
         else if ((cols) <= 8192) { F(512, 2); } \
         else { F(512, 4); }                     \

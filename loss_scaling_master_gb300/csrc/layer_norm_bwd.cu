@@ -11,6 +11,10 @@
 // groups' sums in a fixed order and writes one row of partial sums; a second
 // kernel adds those rows, again in a fixed order (no atomics, so equal calls
 // give equal bits).
+//
+// 16384 x 4096 bf16 from the checkpoint: 75 us with the join's 6, memory 50 us.
+// What bounds it is the latency of a row's phases (sums, barrier, sums) at 2 CTAs
+// an SM, which the column sums' registers allow.
 #include <algorithm>
 
 #include "layer_norm.cuh"
@@ -204,15 +208,29 @@ __global__ void __launch_bounds__(norm_cta(TPR), bwd_ctas(TPR, NV)) norm_bwd_ker
         }
     } else {
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v) {
+            float a[8], b[8];
+            split8(aw[v], a);
+            split8(ab[v], b);
+            const int c = norm_col<VEC, TPR>(v, t, 0);
+            if constexpr (VEC) {
+                // (by single elements, 32 bytes apart over a warp: 128 x 4096 13.9 us
+                // instead of 7.4, 16384 x 4096 82 instead of 75)
+                if (len[v] == 0) continue;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (j >= len[v]) continue;
-                const int c = norm_col<VEC, TPR>(v, t, j);
-                const float2 a = split(aw[v][j / 2]), b = split(ab[v][j / 2]);
-                out[c] = j & 1 ? a.y : a.x;
-                out[d + c] = j & 1 ? b.y : b.x;
+                for (int j = 0; j < 8; j += 4) {
+                    *reinterpret_cast<float4 *>(out + c + j) = make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]);
+                    *reinterpret_cast<float4 *>(out + d + c + j) = make_float4(b[j], b[j + 1], b[j + 2], b[j + 3]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (j >= len[v]) continue;
+                    out[c + j * TPR] = a[j];
+                    out[d + c + j * TPR] = b[j];
+                }
             }
+        }
     }
 }
 
@@ -278,16 +296,17 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_long_params(NormBwd P) {
 
 // Adds the partial rows.  A CTA takes 32 of the 2 cols columns, warp w the rows
 // w, w + 32, ...: the loads of a warp are independent, so a column costs a few
-// load latencies.
-constexpr int kJoinThreads = 1024;
+// load latencies.  16 warps up to 160 rows (32 x 4096 with its gradients 5.0 us, by 32
+// warps 6.3; 4096 x 8192 42 and 44 us), 32 above (1024 x 768 6.3 us, by 16 6.7).
 struct NormJoin {
     const float *part;
     int64_t parts, cols;
     void *dw, *db;
     int wt;
 };
-__global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormJoin P) {
-    __shared__ float s[kJoinThreads / 32][33];
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_join_kernel(NormJoin P) {
+    __shared__ float s[THREADS / 32][33];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -295,14 +314,14 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormJoin P) {
     float a = 0.0f;
     if (c < 2 * P.cols) {
 #pragma unroll 8
-        for (int64_t p = warp; p < P.parts; p += kJoinThreads / 32) a += P.part[p * 2 * P.cols + c];
+        for (int64_t p = warp; p < P.parts; p += THREADS / 32) a += P.part[p * 2 * P.cols + c];
     }
     s[warp][lane] = a;
     __syncthreads();
     if (warp == 0 && c < 2 * P.cols) {
         float t = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) t += s[w][lane];
+        for (int w = 0; w < THREADS / 32; ++w) t += s[w][lane];
         void *out = c < P.cols ? P.dw : P.db;
         if (out) st_param(out, P.wt, c < P.cols ? c : c - P.cols, t);
     }
@@ -316,7 +335,7 @@ int64_t norm_grid(int64_t rows, int64_t cols, bool vec, int device) {
 #define F(TPR, NV)                                                                             \
     return std::max<int64_t>(1, std::min<int64_t>((rows + norm_rpc(TPR) - 1) / norm_rpc(TPR),  \
                                                   sms * bwd_ctas(TPR, NV)))
-    if (vec) AMP_NORM_SHAPE(cols, F, 64, 2);
+    if (vec) AMP_NORM_SHAPE(cols, F, 64, 2, 128, 2);
     else AMP_NORM_SHAPE_ODD(cols, F);
 #undef F
 }
@@ -326,7 +345,7 @@ cudaError_t go(const NormBwd &P, int64_t parts, cudaStream_t s) {
 #define F(TPR, NV)                                                                                           \
     return launch_pdl(norm_bwd_kernel<XT, CK, VEC, TPR, NV>, dim3((unsigned)parts), dim3(norm_cta(TPR)),     \
                       norm_rpc(TPR) > 1 ? size_t(P.cols) * 4 * norm_rpc(TPR) : 0, s, P)
-    if constexpr (VEC) AMP_NORM_SHAPE(P.cols, F, 64, 2);
+    if constexpr (VEC) AMP_NORM_SHAPE(P.cols, F, 64, 2, 128, 2);
     else AMP_NORM_SHAPE_ODD(P.cols, F);
 #undef F
 }
@@ -373,7 +392,9 @@ cudaError_t launch_norm_bwd(const void *dy, const void *x, int elem, const uint8
                            : go_x<kBF16, false>(P, vec, parts, s);
     if (e == cudaSuccess && P.part) {
         const NormJoin J{part, parts, cols, dw, db, welem};
-        e = launch_pdl(norm_join_kernel, dim3((unsigned)((2 * cols + 31) / 32)), dim3(kJoinThreads), 0, s, J);
+        const dim3 grid((unsigned)((2 * cols + 31) / 32));
+        e = parts <= 160 ? launch_pdl(norm_join_kernel<512>, grid, dim3(512), 0, s, J)
+                         : launch_pdl(norm_join_kernel<1024>, grid, dim3(1024), 0, s, J);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }

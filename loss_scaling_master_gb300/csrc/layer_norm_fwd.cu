@@ -232,7 +232,7 @@ cudaError_t go(const NormFwd &P, int device, cudaStream_t s) {
                       dim3((unsigned)std::min<int64_t>((P.rows + norm_rpc(TPR) - 1) / norm_rpc(TPR),     \
                                                        sms * (fwd_ctas<XT, VEC>(TPR, NV)))), \
                       dim3(norm_cta(TPR)), 0, s, P)
-    if constexpr (VEC) AMP_NORM_SHAPE(P.cols, F, 128, 1);
+    if constexpr (VEC) AMP_NORM_SHAPE(P.cols, F, 128, 1, 256, 1);
     else AMP_NORM_SHAPE_ODD(P.cols, F);
 #undef F
 }
