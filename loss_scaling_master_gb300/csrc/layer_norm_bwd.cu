@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(norm_cta(TPR), bwd_ctas(TPR, NV)) norm_bwd_ker
     constexpr int RPC = norm_rpc(TPR);
     constexpr bool HOLD = TPR < 512 || NV < 4;  // weights in registers
     __shared__ float scratch[2][2 * 32];
-    extern __shared__ float s_join[];  // RPC > 1: RPC * cols floats
+    extern __shared__ __align__(16) float s_join[];  // RPC > 1: RPC * cols floats
     pdl_wait();
     pdl_trigger();
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
@@ -191,13 +191,20 @@ __global__ void __launch_bounds__(norm_cta(TPR), bwd_ctas(TPR, NV)) norm_bwd_ker
         for (int k = 0; k < 2; ++k) {
             __syncthreads();
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
+            for (int v = 0; v < NV; ++v) {
+                float a[8];
+                split8(k ? ab[v] : aw[v], a);
+                float *to = s_join + sub * d + norm_col<VEC, TPR>(v, t, 0);
+                if constexpr (VEC) {
+                    if (len[v] == 0) continue;
+                    reinterpret_cast<float4 *>(to)[0] = make_float4(a[0], a[1], a[2], a[3]);
+                    reinterpret_cast<float4 *>(to)[1] = make_float4(a[4], a[5], a[6], a[7]);
+                } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j >= len[v]) continue;
-                    const float2 p = split(k ? ab[v][j / 2] : aw[v][j / 2]);
-                    s_join[sub * d + norm_col<VEC, TPR>(v, t, j)] = j & 1 ? p.y : p.x;
+                    for (int j = 0; j < 8; ++j)
+                        if (j < len[v]) to[j * TPR] = a[j];
                 }
+            }
             __syncthreads();
             for (int c = threadIdx.x; c < d; c += norm_cta(TPR)) {
                 float a = 0.0f;
@@ -295,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_long_params(NormBwd P) {
 }
 
 // Adds the partial rows.  A CTA takes 32 of the 2 cols columns, warp w the rows
-// w, w + 32, ...: the loads of a warp are independent, so a column costs a few
+// w, w + warps, ...: the loads of a warp are independent, so a column costs a few
 // load latencies.  16 warps up to 160 rows (32 x 4096 with its gradients 5.0 us, by 32
 // warps 6.3; 4096 x 8192 42 and 44 us), 32 above (1024 x 768 6.3 us, by 16 6.7).
 struct NormJoin {
