@@ -42,11 +42,21 @@ struct ActBwd {
     int kb;
 };
 
-// The functions take two elements at a time, and in the GELUs what is not a
-// lookup of the special function unit, a comparison or a selection runs as one
-// instruction for both (f32x2.cuh; GELU over 4096 x 8192 bf16 34 instead of 39 us).
-// SiLU has too little of that to pay for the moves into pairs (8192 x 14336 gated
-// 143 us scalar, 149 us in pairs).
+// ---- f and f' ----------------------------------------------------------------
+// How far each is from 64 bits is in ampops.h.  The functions take two elements at a
+// time, and in the GELUs what is not a lookup of the special function unit, a comparison
+// or a selection runs as one instruction for both (f32x2.cuh; GELU over 4096 x 8192 bf16
+// 34 instead of 39 us).  SiLU has too little of that to pay for the moves into pairs
+// (8192 x 14336 gated 143 us scalar, 149 us in pairs).
+//
+// fp32 tensors have forms of their own, whose errors are as small as the type's rounding.
+// Relative norm of the error over N(0, 1.5), f and f' (in brackets: the elementary fp32
+// forms with erf, tanh and exp):
+//     GELU       3.3e-8 and 3.5e-8 (3.7e-8, 3.6e-8)
+//     GELU tanh  3.3e-8 and 4.5e-8 (3.6e-8, 7.9e-8)
+//     SiLU       3.5e-8 and 4.4e-8 (4.5e-8, 5.1e-8)
+// With normcdff() and expf() GELU is no nearer and takes 84 + 90 us for 4096 x 8192
+// instead of 45 + 47.
 //
 // 2^u and 1 / x, each within 2 ulp; exp2_flush gives 0 below 2^-126
 __device__ __forceinline__ float exp2_approx(float u) {
@@ -59,7 +69,7 @@ __device__ __forceinline__ float exp2_flush(float u) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(u));
     return r;
 }
-__device__ __forceinline__ float recip_approx(float x) {  // of normal x
+__device__ __forceinline__ float recip_approx(float x) {  // 0 above 2^126
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
@@ -69,104 +79,150 @@ __device__ __forceinline__ f2 recip2(f2 a) {
     return make_f2(recip_approx(s.x), recip_approx(s.y));
 }
 __device__ __forceinline__ f2 abs2(f2 a) { return a & 0x7FFFFFFF7FFFFFFFull; }
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.9259629911e-8f, kLn2 = 0.6931471805599453f;
 
 // 1 / (1 + exp(-t)) as 1 / (1 + e) or e / (1 + e), e = exp(-|t|): the
 // denominator stays in [1, 2], so neither overflow nor the flush to zero of a
 // large one's reciprocal cuts the tail off (it keeps its relative precision
-// down to the subnormals).
-__device__ __forceinline__ f2 sigmoid2(f2 t) {
+// down to the subnormals).  n = 1 - the result; in fp32 the larger of the two is
+// 1 - the smaller, which has no error of the division left (16 bits: the smaller
+// may be the difference, absolutely good to 2^-23).
+template <int XT>
+__device__ __forceinline__ f2 sigmoid2(f2 t, f2 &n) {
     const float2 u = split(mul2(abs2(t), both(-kLog2e))), s = split(t);
     const float ex = exp2_approx(u.x), ey = exp2_approx(u.y);
-    const f2 r = recip2(add2(make_f2(ex, ey), both(1.0f)));
-    return mul2(make_f2(s.x >= 0.0f ? 1.0f : ex, s.y >= 0.0f ? 1.0f : ey), r);
+    const f2 e = make_f2(ex, ey), one = both(1.0f), r = recip2(add2(e, one));
+    if constexpr (XT == kF32) {
+        const f2 lo = mul2(e, r);
+        const float2 l = split(lo), h = split(fma2(lo, both(-1.0f), one));
+        n = make_f2(s.x >= 0.0f ? l.x : h.x, s.y >= 0.0f ? l.y : h.y);
+        return make_f2(s.x >= 0.0f ? h.x : l.x, s.y >= 0.0f ? h.y : l.y);
+    }
+    const f2 v = mul2(make_f2(s.x >= 0.0f ? 1.0f : ex, s.y >= 0.0f ? 1.0f : ey), r);
+    n = fma2(v, both(-1.0f), one);
+    return v;
+}
+template <int XT>
+__device__ __forceinline__ float sigmoid1(float t, float &n) {
+    if constexpr (XT == kF32) {
+        // exp(-a) = 2^-(a log2 e), and what the product was rounded by made good
+        const float a = fminf(fabsf(t), 120.0f), u = a * kLog2e;
+        const float m = __fmaf_rn(a, -kLog2eLow, __fmaf_rn(a, -kLog2e, u)), e0 = exp2_approx(-u);
+        const float e = __fmaf_rn(e0 * m, kLn2, e0), lo = e * recip_approx(1.0f + e), hi = 1.0f - lo;
+        n = t >= 0.0f ? lo : hi;
+        return t >= 0.0f ? hi : lo;
+    }
+    const float e = exp2_approx(fabsf(t) * -kLog2e), v = (t >= 0.0f ? 1.0f : e) * recip_approx(1.0f + e);
+    n = 1.0f - v;
+    return v;
 }
 
-__device__ __forceinline__ float sigmoid1(float t) {
-    const float e = exp2_approx(fabsf(t) * -kLog2e);
-    return (t >= 0.0f ? 1.0f : e) * recip_approx(1.0f + e);
-}
-
-// The magnitude past which sigma(2z) and Phi are 0 or 1 to the last bit, so
-// cubes and squares of larger x need not be formed (they would overflow and
-// meet a zero factor).  NaN stays.
+// The magnitude past which sigma(2z) is 0 or 1 to the last bit, so cubes and squares of
+// larger x need not be formed (they would overflow and meet a zero factor).  NaN stays.
 __device__ __forceinline__ float act_clamp(float x) { return fabsf(x) > 30.0f ? copysignf(30.0f, x) : x; }
 __device__ __forceinline__ f2 act_clamp2(f2 x) {
     const float2 s = split(x);
     return make_f2(act_clamp(s.x), act_clamp(s.y));
 }
 
-// Phi(x) and exp(-x^2/2) of a clamped x.  Hastings' rational form of the error
-// function (Abramowitz and Stegun 7.1.26): for z >= 0
-//     erfc(z) = (a1 t + ... + a5 t^5) exp(-z^2) + eps, t = 1 / (1 + p z), |eps| <= 1.5e-7,
-// so Phi(-|x|) is half of that at z = |x| / sqrt 2, within 1e-7, and the
-// exponential is the one that the derivative needs.  (erff() in its place costs
-// a branch and a second exponential: 47 instead of 40 us for 4096 x 8192 bf16,
-// before two elements shared the rest.)
-__device__ __forceinline__ f2 gauss_cdf2(f2 c, f2 &e) {
-    const float2 u = split(mul2(mul2(c, c), both(-0.5f * kLog2e)));
-    e = make_f2(exp2_flush(u.x), exp2_flush(u.y));
-    const f2 t = recip2(fma2(abs2(c), both(0.3275911f * 0.70710678118654752f), both(1.0f)));
-    f2 q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
-    q = fma2(q, t, both(0.5f * 1.421413741f));
-    q = fma2(q, t, both(0.5f * -0.284496736f));
-    q = fma2(q, t, both(0.5f * 0.254829592f));
-    q = mul2(q, mul2(t, e));
-    const float2 s = split(c), v = split(q);
-    return make_f2(s.x >= 0.0f ? 1.0f - v.x : v.x, s.y >= 0.0f ? 1.0f - v.y : v.y);
+// Phi(x) and e = exp(-x^2/2).  Phi(-a) / e is a polynomial in t = 1 / (1 + p a) as far as
+// e goes, so Phi(-|x|) keeps its relative precision into the tail, and the exponential is
+// the one that the derivative needs.  (An error function of bounded absolute error, whose
+// Phi is 0.4 % off at x = -6 and 2 % at -10, takes as long.)  The coefficients here are
+// least-maximum fits of the relative error, made for this file.
+//
+// 16 bits: one polynomial, good to 1.9e-6.  e = 0 where x^2 overflows.
+// fp32: one good to 4.5e-8 for a >= 1.25; below, where Phi is not small and the roundings
+// of that one would show, 1/2 - a P(a^2) good to 9.6e-9 of a P.
+template <int XT>
+__device__ __forceinline__ f2 gauss_cdf2(f2 x, f2 &e) {
+    const float2 s = split(x);
+    f2 v;
+    if constexpr (XT == kF32) {
+        const f2 a = make_f2(fminf(fabsf(s.x), 15.0f), fminf(fabsf(s.y), 15.0f)), q = mul2(a, a);
+        const float2 u = split(mul2(q, both(-0.5f * kLog2e)));
+        e = make_f2(exp2_flush(u.x), exp2_flush(u.y));
+        const f2 t = recip2(fma2(a, both(0.625f), both(1.0f)));
+        f2 o = fma2(t, both(-0.2584007978f), both(0.7364913225f));
+        o = fma2(o, t, both(-0.7159850597f));
+        o = fma2(o, t, both(0.1085906923f));
+        o = fma2(o, t, both(0.1240824759f));
+        o = fma2(o, t, both(0.2523988783f));
+        o = fma2(o, t, both(0.2491545975f));
+        o = mul2(fma2(o, t, both(4.668735983e-06f)), e);
+        f2 i = fma2(q, both(-6.809503247e-06f), both(0.0001110411758f));
+        i = fma2(i, q, both(-0.001183837187f));
+        i = fma2(i, q, both(0.009972282685f));
+        i = fma2(i, q, both(-0.06649021059f));
+        i = fma2(mul2(fma2(i, q, both(0.3989422619f)), a), both(-1.0f), both(0.5f));
+        const float2 so = split(o), si = split(i), sa = split(a);
+        v = make_f2(sa.x < 1.25f ? si.x : so.x, sa.y < 1.25f ? si.y : so.y);
+    } else {
+        const float2 u = split(mul2(mul2(x, x), both(-0.5f * kLog2e)));
+        e = make_f2(exp2_flush(u.x), exp2_flush(u.y));
+        const f2 t = recip2(fma2(abs2(x), both(0.3f), both(1.0f)));
+        v = fma2(t, both(-0.0845924839f), both(0.2405701131f));
+        v = fma2(v, t, both(-0.0486405641f));
+        v = fma2(v, t, both(0.1647616178f));
+        v = fma2(v, t, both(0.1067056805f));
+        v = fma2(v, t, both(0.1212744638f));
+        v = mul2(fma2(v, t, both(-7.9769998e-05f)), e);
+    }
+    const float2 sv = split(v);
+    return make_f2(s.x >= 0.0f ? 1.0f - sv.x : sv.x, s.y >= 0.0f ? 1.0f - sv.y : sv.y);
 }
 
 // 2 sqrt(2/pi) = 1.5957691216, times 0.044715 = 0.0713548163
 constexpr float kTanhA = 1.5957691216057308f, kTanhB = 0.07135481627159954f;
 
-template <int ACT>
+template <int XT, int ACT>
 __device__ __forceinline__ f2 act_value2(f2 x) {
+    f2 e;
+    if constexpr (ACT == AMP_ACT_GELU) return mul2(x, gauss_cdf2<XT>(x, e));
     const f2 c = act_clamp2(x);
-    if constexpr (ACT == AMP_ACT_GELU) {
-        f2 e;
-        return mul2(x, gauss_cdf2(c, e));
-    }
-    return mul2(x, sigmoid2(mul2(c, fma2(mul2(c, c), both(kTanhB), both(kTanhA)))));
+    return mul2(x, sigmoid2<XT>(mul2(c, fma2(mul2(c, c), both(kTanhB), both(kTanhA))), e));
 }
 // f(x) and f'(x)
-template <int ACT>
+template <int XT, int ACT>
 __device__ __forceinline__ void act_both2(f2 x, f2 &f, f2 &d) {
     if constexpr (ACT == AMP_ACT_GELU) {
-        const f2 c = act_clamp2(x);
         f2 e;
-        const f2 p = gauss_cdf2(c, e);
+        const f2 p = gauss_cdf2<XT>(x, e);
         f = mul2(x, p);
-        d = fma2(mul2(c, both(0.3989422804014327f)), e, p);
+        d = fma2(mul2(x, both(0.3989422804014327f)), e, p);
     } else {
         const f2 c = act_clamp2(x), q = mul2(c, c);
-        const f2 s = sigmoid2(mul2(c, fma2(q, both(kTanhB), both(kTanhA))));
+        f2 n;
+        const f2 s = sigmoid2<XT>(mul2(c, fma2(q, both(kTanhB), both(kTanhA))), n);
         f = mul2(x, s);
-        d = fma2(mul2(mul2(c, s), fma2(s, both(-1.0f), both(1.0f))), fma2(q, both(3.0f * kTanhB), both(kTanhA)), s);
+        d = fma2(mul2(mul2(c, s), n), fma2(q, both(3.0f * kTanhB), both(kTanhA)), s);
     }
 }
 
 // y = f(x) [* u] for two elements.
-template <int ACT, bool GATED>
+template <int XT, int ACT, bool GATED>
 __device__ __forceinline__ float2 act_apply(float x0, float x1, float u0, float u1) {
     if constexpr (ACT == AMP_ACT_SILU) {
-        const float a = x0 * sigmoid1(x0), b = x1 * sigmoid1(x1);
+        float n;
+        const float a = x0 * sigmoid1<XT>(x0, n), b = x1 * sigmoid1<XT>(x1, n);
         return GATED ? make_float2(a * u0, b * u1) : make_float2(a, b);
     }
-    const f2 y = act_value2<ACT>(make_f2(x0, x1));
+    const f2 y = act_value2<XT, ACT>(make_f2(x0, x1));
     return split(GATED ? mul2(y, make_f2(u0, u1)) : y);
 }
 // dx = g f'(x) [* u] and du = g f(x) for two elements.
-template <int ACT, bool GATED>
+template <int XT, int ACT, bool GATED>
 __device__ __forceinline__ void act_grads(float x0, float x1, float u0, float u1, float g0, float g1, float2 &dx,
                                           float2 &du) {
     if constexpr (ACT == AMP_ACT_SILU) {
-        const float s0 = sigmoid1(x0), s1 = sigmoid1(x1);
-        du = make_float2(g0 * (x0 * s0), g1 * (x1 * s1));
-        dx = make_float2((GATED ? g0 * u0 : g0) * (s0 * __fmaf_rn(x0, 1.0f - s0, 1.0f)),
-                         (GATED ? g1 * u1 : g1) * (s1 * __fmaf_rn(x1, 1.0f - s1, 1.0f)));
+        float n0, n1;
+        const float s0 = sigmoid1<XT>(x0, n0), s1 = sigmoid1<XT>(x1, n1);
+        const float f0 = x0 * s0, f1 = x1 * s1;
+        du = make_float2(g0 * f0, g1 * f1);
+        dx = make_float2((GATED ? g0 * u0 : g0) * __fmaf_rn(f0, n0, s0), (GATED ? g1 * u1 : g1) * __fmaf_rn(f1, n1, s1));
     } else {
         f2 f, d, g = make_f2(g0, g1);
-        act_both2<ACT>(make_f2(x0, x1), f, d);
+        act_both2<XT, ACT>(make_f2(x0, x1), f, d);
         du = split(mul2(g, f));
         if (GATED) g = mul2(g, make_f2(u0, u1));
         dx = split(mul2(g, d));
@@ -217,9 +273,14 @@ __device__ __forceinline__ void stv(void *p, int64_t k, const float (&y)[8]) {
     for (int j = 0; j < kWords8<XT>; ++j) st16(static_cast<char *>(p) + k * esz + 16 * j, u[j]);
 }
 
+// CTAs an SM holds (0: as many as the compiler's registers leave): see bwd_vec_ctas.
+__host__ __device__ constexpr int fwd_vec_ctas(int xt, int act, bool gated) {
+    return act == AMP_ACT_GELU && !gated && xt == kF32 ? 8 : 0;
+}
 // 8 elements a thread; rows are whole groups of 8 and every address aligned.
 template <int XT, int ACT, bool GATED, bool KEEP>
-__global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P) {
+__global__ void __launch_bounds__(kThreads, fwd_vec_ctas(XT, ACT, GATED))
+    act_fwd_vec(ActFwd P) {
     pdl_wait();
     pdl_trigger();
     // the 4 threads of a block run together, so every thread of a warp walks
@@ -251,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P) {
         if (ACT != kSave && in) {
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
-                const float2 v = act_apply<ACT, GATED>(x[j], x[j + 1], u[j], u[j + 1]);
+                const float2 v = act_apply<XT, ACT, GATED>(x[j], x[j + 1], u[j], u[j + 1]);
                 x[j] = v.x;
                 x[j + 1] = v.y;
             }
@@ -344,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) act_fwd_elem(ActFwd P) {
 #pragma unroll
             for (int i = 0; i < EB; i += 2) {
                 if (n <= 32 * i) break;
-                const float2 v = act_apply<ACT, GATED>(widen1<XT>(x[i]), widen1<XT>(x[i + 1]), widen1<XT>(u[i]),
+                const float2 v = act_apply<XT, ACT, GATED>(widen1<XT>(x[i]), widen1<XT>(x[i + 1]), widen1<XT>(u[i]),
                                                        widen1<XT>(u[i + 1]));
                 store_elem<XT>(yp, 32 * i, v.x);
                 if (n > 32 * (i + 1)) store_elem<XT>(yp, 32 * (i + 1), v.y);
@@ -353,8 +414,15 @@ __global__ void __launch_bounds__(kThreads) act_fwd_elem(ActFwd P) {
     }
 }
 
+// CTAs an SM holds: GELU's backward is a register or more above 32 (gated: 40) where the
+// compiler is left to itself, and slower by an SM's missing CTAs (4096 x 8192 bf16 35.7
+// instead of 31.9 us, gated 44.8 and 42.4, fp32 53.4 and 46.6; fp32 forward 46.7 and 44.7).
+// The others are slower with any bound here.  0: none.
+__host__ __device__ constexpr int bwd_vec_ctas(int act, bool gated) {
+    return act == AMP_ACT_GELU ? (gated ? 6 : 8) : 0;
+}
 template <int XT, int ACT, bool GATED>
-__global__ void __launch_bounds__(kThreads) act_bwd_vec(ActBwd P) {
+__global__ void __launch_bounds__(kThreads, bwd_vec_ctas(ACT, GATED)) act_bwd_vec(ActBwd P) {
     pdl_wait();
     pdl_trigger();
     RowWalk at((blockIdx.x * kThreads + threadIdx.x) / 4, gridDim.x * (kThreads / 4), P.kb);
@@ -374,7 +442,7 @@ __global__ void __launch_bounds__(kThreads) act_bwd_vec(ActBwd P) {
                 g[j + 1] = x[j + 1];
             } else {
                 float2 dx, du;
-                act_grads<ACT, GATED>(x[j], x[j + 1], u[j], u[j + 1], g[j], g[j + 1], dx, du);
+                act_grads<XT, ACT, GATED>(x[j], x[j + 1], u[j], u[j + 1], g[j], g[j + 1], dx, du);
                 o[j] = du.x;
                 o[j + 1] = du.y;
                 g[j] = dx.x;
@@ -433,7 +501,7 @@ __global__ void __launch_bounds__(kThreads) act_bwd_elem(ActBwd P) {
                 if (GATED) e4m3x4_to_f32x4(qu[i] | (qu[i + 1] << 8), w);
                 const float u0 = GATED ? __fmul_rn(w[0], t0) : 0.0f;
                 const float u1 = GATED ? __fmul_rn(w[1], t1) : 0.0f;
-                act_grads<ACT, GATED>(x0, x1, u0, u1, g[i], g[i + 1], dx, du);
+                act_grads<XT, ACT, GATED>(x0, x1, u0, u1, g[i], g[i + 1], dx, du);
                 store_elem<XT>(dxp, 32 * i, dx.x);
                 if (two) store_elem<XT>(dxp, 32 * (i + 1), dx.y);
                 if (GATED) {
