@@ -6,10 +6,14 @@
 // they take 0.3 us in all.  ops.py holds the documented functions; each passes
 // its arguments on in order.  A tensor that does not fit raises ValueError
 // before anything is called; the return value is the entry point's status.
+// A call runs on the device of the tensor that gives it its shape, whichever is
+// current, and every other tensor has to be there too (an address of another
+// GPU would be a fault, not a status).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -45,27 +49,31 @@ const at::Tensor &tensor(PyObject *o, const char *what) {
     if (!THPVariable_Check(o)) refuse(std::string(what) + ": needs a tensor");
     return THPVariable_Unpack(o);
 }
-// Address of a contiguous GPU tensor of at least numel elements; None: NULL.
-void *address(const at::Tensor &t, const char *what, int64_t numel) {
+// Address of a contiguous GPU tensor on the call's device, of at least numel
+// elements; None: NULL.
+void *address(const at::Tensor &t, const char *what, int64_t numel, int64_t device) {
     if (!t.is_cuda() || !t.is_contiguous()) refuse(std::string(what) + ": needs a contiguous CUDA tensor");
+    if (device >= 0 && t.get_device() != device)  // (below 0: the shape's tensor will be refused)
+        refuse(std::string(what) + ": on cuda:" + std::to_string(t.get_device()) + ", the call is on cuda:" +
+               std::to_string(device));
     if (t.numel() < numel)
         refuse(std::string(what) + ": " + std::to_string(t.numel()) + " elements, at least " + std::to_string(numel) +
                " needed");
     return t.data_ptr();
 }
-void *typed(PyObject *o, const char *what, int64_t numel, at::ScalarType type) {
+void *typed_on(PyObject *o, const char *what, int64_t numel, at::ScalarType type, int64_t device) {
     if (o == Py_None) return nullptr;
     const at::Tensor &t = tensor(o, what);
     if (t.scalar_type() != type)
         refuse(std::string(what) + ": " + type_name(t.scalar_type()) + ", expected " + c10::toString(type));
-    return address(t, what, numel);
+    return address(t, what, numel, device);
 }
-void *bytes(PyObject *o, const char *what, int64_t n) {
+void *bytes_on(PyObject *o, const char *what, int64_t n, int64_t device) {
     if (o == Py_None) return nullptr;
     const at::Tensor &t = tensor(o, what);
     if (t.element_size() != 1)
         refuse(std::string(what) + ": " + std::to_string(t.element_size()) + "-byte elements, expected 1");
-    return address(t, what, n);
+    return address(t, what, n, device);
 }
 amp_dtype elem(const at::Tensor &t, const char *what) {
     switch (t.scalar_type()) {
@@ -76,11 +84,12 @@ amp_dtype elem(const at::Tensor &t, const char *what) {
     }
 }
 
-// The matrix that gives a call its shape: the last dimension are its columns.
+// The matrix that gives a call its shape (the last dimension are its columns) and
+// its device.
 struct Matrix {
     const at::Tensor &t;
     const char *what;
-    int64_t rows = 1, cols;
+    int64_t rows = 1, cols, device;
     amp_dtype type;
     Matrix(PyObject *o, const char *what_) : t(tensor(o, what_)), what(what_) {
         const auto s = t.sizes();
@@ -88,9 +97,15 @@ struct Matrix {
         cols = s.back();
         for (size_t i = 0; i + 1 < s.size(); ++i) rows *= s[i];
         type = elem(t, what);
+        device = t.is_cuda() ? t.get_device() : -1;
     }
-    void *p() const { return address(t, what, 0); }
-    // a tensor of the same type and at least its size
+    void *p() const { return address(t, what, 0, device); }
+    // the call's other tensors (None: NULL): of at least n elements of a type, or of
+    // bytes; of the same type and at least its size
+    void *typed(PyObject *o, const char *what, int64_t n, at::ScalarType of) const {
+        return typed_on(o, what, n, of, device);
+    }
+    void *bytes(PyObject *o, const char *what, int64_t n) const { return bytes_on(o, what, n, device); }
     void *like(PyObject *o, const char *what) const { return typed(o, what, rows * cols, t.scalar_type()); }
 };
 
@@ -101,15 +116,24 @@ int64_t fp4_scales(int64_t rows, int64_t cols) { return up(rows, 128) * up(cols,
 // An 8-bit checkpoint (q, scales) or None.
 struct Saved {
     void *q = nullptr, *s = nullptr;
-    Saved(PyObject *o, const char *what, int64_t rows, int64_t cols) {
+    Saved(PyObject *o, const char *what, const Matrix &m) {
         if (o == Py_None) return;
         if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 2) refuse(std::string(what) + ": needs (q, scales)");
-        q = typed(PyTuple_GET_ITEM(o, 0), what, rows * cols, at::kFloat8_e4m3fn);
-        s = typed(PyTuple_GET_ITEM(o, 1), what, rows * up(cols, 32), at::kByte);
+        q = m.typed(PyTuple_GET_ITEM(o, 0), what, m.rows * m.cols, at::kFloat8_e4m3fn);
+        s = m.typed(PyTuple_GET_ITEM(o, 1), what, m.rows * up(m.cols, 32), at::kByte);
     }
 };
 
-// A stream object or handle; None: the current stream.
+// Makes a device current for a call (at no cost where it is).
+struct OnDevice {
+    c10::cuda::OptionalCUDAGuard guard;
+    explicit OnDevice(int64_t device) {
+        const auto d = static_cast<c10::DeviceIndex>(device);
+        if (c10::cuda::current_device() != d) guard.set_index(d);
+    }
+};
+
+// A stream object or handle; None: the current device's current stream.
 amp_stream_t stream_of(PyObject *o) {
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
     PyObject *h = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Long(o);
@@ -127,7 +151,8 @@ amp_stream_t stream_of(PyObject *o) {
 struct Params {
     amp_dtype type = AMP_DT_F32;
     void *p[3] = {nullptr, nullptr, nullptr};
-    Params(int64_t cols, std::initializer_list<PyObject *> given) {
+    Params(const Matrix &m, std::initializer_list<PyObject *> given) {
+        const int64_t cols = m.cols;
         const at::Tensor *first = nullptr;
         int i = 0;
         for (PyObject *o : given) {
@@ -144,7 +169,7 @@ struct Params {
             }
         }
         for (PyObject *o : given) {
-            if (o != Py_None) p[i] = address(tensor(o, "weight"), "weight", cols);
+            if (o != Py_None) p[i] = address(tensor(o, "weight"), "weight", cols, m.device);
             ++i;
         }
     }
@@ -195,10 +220,12 @@ PyObject *quant(PyObject *, Args a, Py_ssize_t n) {  // x, q, scales, qt, scales
     return call(n, 7, g.quant, [&]() {
         const Matrix x(a[0], "x");
         const void *p = x.p();
-        void *q = bytes(a[1], "q", fp4_bytes(x.rows, x.cols)), *s = bytes(a[2], "scales", fp4_scales(x.rows, x.cols));
-        void *qt = bytes(a[3], "qt", fp4_bytes(x.cols, x.rows));
-        void *st = bytes(a[4], "scales_t", fp4_scales(x.cols, x.rows));
-        const auto *skip = static_cast<const int32_t *>(typed(a[5], "skip_if", 1, at::kInt));
+        void *q = x.bytes(a[1], "q", fp4_bytes(x.rows, x.cols));
+        void *s = x.bytes(a[2], "scales", fp4_scales(x.rows, x.cols));
+        void *qt = x.bytes(a[3], "qt", fp4_bytes(x.cols, x.rows));
+        void *st = x.bytes(a[4], "scales_t", fp4_scales(x.cols, x.rows));
+        const auto *skip = static_cast<const int32_t *>(x.typed(a[5], "skip_if", 1, at::kInt));
+        const OnDevice on(x.device);
         const amp_stream_t stream = stream_of(a[6]);
         Unlocked u;
         return g.quant(p, x.type, x.rows, x.cols, q, s, qt, st, skip, stream);
@@ -208,7 +235,9 @@ PyObject *dequant(PyObject *, Args a, Py_ssize_t n) {  // q, scales, out, stream
     return call(n, 4, g.dequant, [&]() {
         const Matrix o(a[2], "out");
         void *out = o.p();
-        void *q = bytes(a[0], "q", fp4_bytes(o.rows, o.cols)), *s = bytes(a[1], "scales", fp4_scales(o.rows, o.cols));
+        void *q = o.bytes(a[0], "q", fp4_bytes(o.rows, o.cols));
+        void *s = o.bytes(a[1], "scales", fp4_scales(o.rows, o.cols));
+        const OnDevice on(o.device);
         const amp_stream_t stream = stream_of(a[3]);
         Unlocked u;
         return g.dequant(q, s, o.rows, o.cols, out, o.type, stream);
@@ -228,8 +257,9 @@ PyObject *product(PyObject *, Args a, Py_ssize_t n) {  // a, a_scales, b, b_scal
         }
         const Matrix o(a[5], "out");
         void *out = o.p();
-        void *pa = bytes(a[0], "a", fp4_bytes(o.rows, k)), *sa = bytes(a[1], "a_scales", fp4_scales(o.rows, k));
-        void *pb = bytes(a[2], "b", fp4_bytes(o.cols, k)), *sb = bytes(a[3], "b_scales", fp4_scales(o.cols, k));
+        void *pa = o.bytes(a[0], "a", fp4_bytes(o.rows, k)), *sa = o.bytes(a[1], "a_scales", fp4_scales(o.rows, k));
+        void *pb = o.bytes(a[2], "b", fp4_bytes(o.cols, k)), *sb = o.bytes(a[3], "b_scales", fp4_scales(o.cols, k));
+        const OnDevice on(o.device);
         const amp_stream_t stream = stream_of(a[6]);
         Unlocked u;
         return g.product(pa, sa, pb, sb, o.rows, o.cols, k, out, o.type, stream);
@@ -238,13 +268,14 @@ PyObject *product(PyObject *, Args a, Py_ssize_t n) {  // a, a_scales, b, b_scal
 PyObject *norm_forward(PyObject *, Args a, Py_ssize_t n) {  // x, weight, bias, eps, y, mean, rstd, saved, stream
     return call(n, 9, g.norm_forward, [&]() {
         const Matrix x(a[0], "x");
-        const Params w(x.cols, {a[1], a[2]});
+        const Params w(x, {a[1], a[2]});
         const double eps = number(a[3], "eps");
         const void *p = x.p();
         void *y = x.like(a[4], "y");
-        auto *mean = static_cast<float *>(typed(a[5], "mean", x.rows, at::kFloat));
-        auto *rstd = static_cast<float *>(typed(a[6], "rstd", x.rows, at::kFloat));
-        const Saved c(a[7], "saved", x.rows, x.cols);
+        auto *mean = static_cast<float *>(x.typed(a[5], "mean", x.rows, at::kFloat));
+        auto *rstd = static_cast<float *>(x.typed(a[6], "rstd", x.rows, at::kFloat));
+        const Saved c(a[7], "saved", x);
+        const OnDevice on(x.device);
         const amp_stream_t stream = stream_of(a[8]);
         Unlocked u;
         return g.norm_forward(p, x.type, x.rows, x.cols, w.p[0], w.p[1], w.type, eps, y, mean, rstd, c.q, c.s, stream);
@@ -255,18 +286,19 @@ PyObject *norm_backward(PyObject *, Args a, Py_ssize_t n) {
     return call(n, 11, g.norm_backward, [&]() {
         const Matrix dy(a[0], "dy");
         if ((a[1] == Py_None) == (a[9] == Py_None)) refuse("either x or saved");
-        const Params w(dy.cols, {a[2], a[6], a[7]});
+        const Params w(dy, {a[2], a[6], a[7]});
         const void *p = dy.p(), *x = dy.like(a[1], "x");
-        const auto *mean = static_cast<const float *>(typed(a[3], "mean", dy.rows, at::kFloat));
-        const auto *rstd = static_cast<const float *>(typed(a[4], "rstd", dy.rows, at::kFloat));
+        const auto *mean = static_cast<const float *>(dy.typed(a[3], "mean", dy.rows, at::kFloat));
+        const auto *rstd = static_cast<const float *>(dy.typed(a[4], "rstd", dy.rows, at::kFloat));
         void *dx = dy.like(a[5], "dx"), *work = nullptr;
         int64_t room = 0;
         if (a[8] != Py_None) {
             const at::Tensor &t = tensor(a[8], "workspace");
-            work = address(t, "workspace", 0);
+            work = address(t, "workspace", 0, dy.device);
             room = t.numel() * t.element_size();
         }
-        const Saved c(a[9], "saved", dy.rows, dy.cols);
+        const Saved c(a[9], "saved", dy);
+        const OnDevice on(dy.device);
         const amp_stream_t stream = stream_of(a[10]);
         Unlocked u;
         return g.norm_backward(p, x, dy.type, c.q, c.s, dy.rows, dy.cols, w.p[0], w.type, mean, rstd, dx, w.p[1],
@@ -279,7 +311,8 @@ PyObject *act_forward(PyObject *, Args a, Py_ssize_t n) {  // x, kind, y, saved,
         const Matrix x(a[0], "x");
         const void *p = x.p();
         void *y = x.like(a[2], "y"), *up_ = x.like(a[4], "up");
-        const Saved c(a[3], "saved", x.rows, x.cols), cu(a[5], "saved_up", x.rows, x.cols);
+        const Saved c(a[3], "saved", x), cu(a[5], "saved_up", x);
+        const OnDevice on(x.device);
         const amp_stream_t stream = stream_of(a[6]);
         Unlocked u;
         return g.act_forward(act, p, up_, x.type, x.rows, x.cols, y, c.q, c.s, cu.q, cu.s, stream);
@@ -290,8 +323,9 @@ PyObject *act_backward(PyObject *, Args a, Py_ssize_t n) {  // dy, kind, saved, 
         const amp_act act = act_of(a[1]);
         const Matrix dy(a[0], "dy");
         const void *p = dy.p();
-        const Saved c(a[2], "saved", dy.rows, dy.cols), cu(a[4], "saved_up", dy.rows, dy.cols);
+        const Saved c(a[2], "saved", dy), cu(a[4], "saved_up", dy);
         void *dx = dy.like(a[3], "dx"), *du = dy.like(a[5], "dup");
+        const OnDevice on(dy.device);
         const amp_stream_t stream = stream_of(a[6]);
         Unlocked u;
         return g.act_backward(act, p, dy.type, dy.rows, dy.cols, c.q, c.s, cu.q, cu.s, dx, du, stream);
@@ -301,8 +335,9 @@ PyObject *save(PyObject *, Args a, Py_ssize_t n) {  // x, q, scales, stream
     return call(n, 4, g.save, [&]() {
         const Matrix x(a[0], "x");
         const void *p = x.p();
-        void *q = typed(a[1], "q", x.rows * x.cols, at::kFloat8_e4m3fn);
-        void *s = typed(a[2], "scales", x.rows * up(x.cols, 32), at::kByte);
+        void *q = x.typed(a[1], "q", x.rows * x.cols, at::kFloat8_e4m3fn);
+        void *s = x.typed(a[2], "scales", x.rows * up(x.cols, 32), at::kByte);
+        const OnDevice on(x.device);
         const amp_stream_t stream = stream_of(a[3]);
         Unlocked u;
         return g.save(p, x.type, x.rows, x.cols, q, s, stream);
@@ -312,8 +347,9 @@ PyObject *restore(PyObject *, Args a, Py_ssize_t n) {  // q, scales, out, stream
     return call(n, 4, g.restore, [&]() {
         const Matrix o(a[2], "out");
         void *out = o.p();
-        void *q = typed(a[0], "q", o.rows * o.cols, at::kFloat8_e4m3fn);
-        void *s = typed(a[1], "scales", o.rows * up(o.cols, 32), at::kByte);
+        void *q = o.typed(a[0], "q", o.rows * o.cols, at::kFloat8_e4m3fn);
+        void *s = o.typed(a[1], "scales", o.rows * up(o.cols, 32), at::kByte);
+        const OnDevice on(o.device);
         const amp_stream_t stream = stream_of(a[3]);
         Unlocked u;
         return g.restore(q, s, o.rows, o.cols, out, o.type, stream);

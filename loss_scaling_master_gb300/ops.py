@@ -4,12 +4,12 @@ kept in 8 bits.
 
 As in ``_lib``: argument marshalling only, here by ``csrc/ops_bind.cpp`` (built
 into ``_ops_bind.so``), because the smallest of these calls take microseconds.
-Each function checks its tensors (contiguous, on the GPU, of the right type and
-size: ``ValueError``), passes pointers, sizes and the stream (None: the current
-one) to the C entry point of the same name and raises ``AmpError`` on a non-OK
-status.  Outputs are the caller's tensors; nothing is allocated except by the
-two ``*_buffers`` helpers and ``amp_layer_norm_workspace``, which a program
-calls once.
+Each function checks its tensors (contiguous, on one GPU, of the right type and
+size: ``ValueError``), passes pointers, sizes and the stream (None: that GPU's
+current one) to the C entry point of the same name, with the tensors' GPU made
+current, and raises ``AmpError`` on a non-OK status.  Outputs are the caller's
+tensors; nothing is allocated except by the two ``*_buffers`` helpers and
+``amp_layer_norm_workspace``, which a program calls once.
 """
 from __future__ import annotations
 
