@@ -85,8 +85,8 @@ amp_status fp4_dequant_mx(const void *q, const void *scales, int64_t rows, int64
  * The order of the sum depends on the shape and the device alone, so equal
  * calls give equal bits.
  * The kernel's waits on its own copies and products give up after one second
- * of GPU time; the output of a call that did is unspecified and fp4_mx_check
- * reports it.
+ * of GPU time.  fp4_mx_check reports a call that did; the elements of out that
+ * it could not finish are NaN, so the gradient check sees them too.
  * Errors: AMP_EINVAL (NULL or misaligned operands, negative or too large
  * size, k above 2^27), AMP_EDTYPE, AMP_ECUDA. */
 amp_status fp4_product_mx(const void *a, const void *a_scales, const void *b, const void *b_scales,
@@ -97,6 +97,16 @@ amp_status fp4_product_mx(const void *a, const void *a_scales, const void *b, co
  * of fp4_product_mx: AMP_ETIMEOUT if a bounded wait gave up since the last
  * check, AMP_OK otherwise. */
 amp_status fp4_mx_check(amp_stream_t stream);
+
+/* fp4_product_mx with waits of at most 2^limit_log2_ns ns (0 to 30) and one of the
+ * kernel's roles ended after `stages` stages of 256 along the reduction, counted
+ * over all of a CTA's tiles, as if its wait had run out: 0 the loads (where two
+ * CTAs share a tile, the first's), 1 the loads of the second, 2 the products.  For
+ * tests of what a wait that gave up leaves behind; nothing faults or hangs. */
+amp_status fp4_product_mx_selftest(const void *a, const void *a_scales, const void *b,
+                                   const void *b_scales, int64_t m, int64_t n, int64_t k,
+                                   void *out, amp_dtype out_dtype, int32_t role, int32_t stages,
+                                   int32_t limit_log2_ns, amp_stream_t stream);
 
 /* Layer norm over the rows of x [rows, cols] (AMP_DT_BF16, AMP_DT_F16,
  * AMP_DT_F32), in fp32, with the mean taken first and the variance about it:

@@ -55,6 +55,27 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity,
         if (global_ns() - t0 > limit_ns) return false;
     }
 }
+// The phase wait of barriers that the cluster's other CTAs arrive on with release:
+// what they wrote before is visible after it.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *b, uint32_t parity, unsigned long long limit_ns) {
+    const unsigned long long t0 = global_ns();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; "
+            "selp.u32 %0, 1, 0, p; }"
+            : "=r"(ok)
+            : "r"(smem_addr(b)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (global_ns() - t0 > limit_ns) return false;
+    }
+}
+// Counts bytes as arrived that no copy will bring.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t *b, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes)
+                 : "memory");
+}
 // global -> shared, completion counted on the barrier (16-byte aligned, size % 16 == 0)
 __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile(

@@ -31,10 +31,11 @@
 // (all of tensor memory that the scales leave is one tile) idles it 0.3 us a tile.
 // 48 x 4096 x 4096 (four parts): 5.3 us, of which 1.5 are memory.
 //
-// Every wait gives up after a second of GPU time: the role sets the error word,
-// waits (again bounded) for the copies or products that it has in flight and
-// ends; the roles that wait for it give up in turn, tensor memory is freed, and
-// the kernel returns.
+// Every wait gives up after a second (2^30 ns) of GPU time: the role sets the error word and
+// ends, and the roles that wait for it give up in turn.  Whoever gave up, the CTA
+// (both of a pair) waits, again bounded, for every load and product that is in
+// flight, frees its tensor memory and returns.  An accumulator is handed over only
+// when all of its products were issued; what is not handed over is stored as NaN.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -56,13 +57,38 @@ constexpr int kStageBytes = 128;  // bytes of a row a stage: 256 elements
 struct Fp4Product {
     const uint8_t *sa, *sb;  // scale tiles of A and B
     void *out;
-    int64_t m, n;
-    int ot;      // ElemType of out
-    int packed;  // 16-bit out with even rows and 4-byte alignment: two elements a store
-    int kt;      // scale tiles (128 elements) along the reduction
-    int k64;     // products of 64 along the reduction
+    int64_t n;
+    int m;
+    int kt;   // scale tiles (128 elements) along the reduction
+    int k64;  // products of 64 along the reduction
     int tiles_m, tiles_n;
+    uint8_t ot;      // ElemType of out
+    uint8_t packed;  // 16-bit out with even rows and 4-byte alignment: two elements a store
+    Fp4Limits lim;
 };
+// One line of the constant cache: a second one is missed at every start (0.15 us a
+// call of a few tokens).
+static_assert(sizeof(Fp4Product) == 64, "one line of constants");
+
+// Stages after which a role ends early.
+__device__ __forceinline__ int stop_after(const Fp4Product &P, uint32_t role) {
+    return P.lim.role == role ? int(P.lim.stages) : INT32_MAX;
+}
+__device__ __forceinline__ unsigned long long limit_ns(const Fp4Product &P) { return 1ull << P.lim.log2_ns; }
+// A role's wait, by its whole warp.
+__device__ __forceinline__ bool role_wait(const Fp4Product &P, uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, limit_ns(P)));
+}
+constexpr uint32_t kNaN = 0x7FC00000u;
+// NaN for one column of C and cnt tokens from m0.
+__device__ __forceinline__ void store_nan(const Fp4Product &P, int64_t m0, int cnt, int64_t nn) {
+    if (nn >= P.n) return;
+#pragma unroll 1
+    for (int64_t m = m0; m < m0 + cnt && m < P.m; ++m) {
+        if (P.ot == kF32) static_cast<uint32_t *>(P.out)[m * P.n + nn] = kNaN;
+        else static_cast<uint16_t *>(P.out)[m * P.n + nn] = P.ot == kF16 ? 0x7E00 : 0x7FC0;
+    }
+}
 
 // tile -> (token tile, output tile): `side` output tiles side by side, so the
 // CTAs that run together share operands in L2
@@ -140,8 +166,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     using S = Pair;
     constexpr int NS = S::stages;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[NS], empty[NS], acc_full, acc_empty, drain;
-    __shared__ uint32_t s_tmem;
+    __shared__ __align__(8) uint64_t full[NS], empty[NS], acc_full, acc_empty, drain, loaded;
+    __shared__ uint32_t s_tmem, s_issued;
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -153,7 +179,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         mbar_init(&acc_full, 1);
         mbar_init(&acc_empty, 32);  // the first CTA's: the 16 store warps of both
-        mbar_init(&drain, 1);
+        mbar_init(&drain, 1);       // both: everything that was issued
+        mbar_init(&loaded, 2);      // the first CTA's: both loading warps have ended
         mbar_fence_init();
         tma_prefetch_map(&map_t);
         tma_prefetch_map(&map_w);
@@ -175,6 +202,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     auto give_up = [&]() { g_fp4_error = 1; };
 
     if (warp == 0) {
+        const int stop = stop_after(P, rank);
         int st = 0, issued = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -182,7 +210,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int tm, tn;
             tile_at(P, 8, tile, tm, tn);
             for (int ks = 0; ks < ks_all; ++ks) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ph ^ 1));
+                ok = role_wait(P, &empty[st], ph ^ 1) & (issued != stop);
                 if (!ok) break;
                 if (elect_one()) {
                     uint8_t *b = smem + st * S::stage;
@@ -204,23 +232,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
         }
         if (!ok) give_up();
-        if (!ok && rank == 0) {  // wait for the copies still in flight
-            for (int i = 0; i < min(issued, NS); ++i) {
-                st = st == 0 ? NS - 1 : st - 1;
-                if (st == NS - 1) ph ^= 1;
-                mbar_wait(&full[st], ph);
-            }
+        if (lane == 0) {
+            s_issued = issued;
+            cluster_arrive_release(cluster_addr(&loaded, 0));
         }
     } else if (warp == 1) {
         if (rank == 0) {
-            int st = 0;
+            const int stop = stop_after(P, 2);
+            int st = 0, taken = 0;
             uint32_t ph = 0, aph = 0;
             constexpr uint32_t instr = mxf4_instr(256, 256);
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += stride) {
                 for (int ks = 0; ks < ks_all; ++ks) {
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st], ph));
+                    ok = role_wait(P, &full[st], ph) & (taken != stop);
                     if (!ok) break;
+                    ++taken;
                     tc_fence_after();
                     const uint32_t b = smem_addr(smem) + st * S::stage;
                     const uint32_t sf = b + S::w_bytes + S::t_bytes;
@@ -239,7 +266,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (ks == 0) {
                         // only now are the accumulators needed: with this wait
                         // first, the products of a tile began 0.2 us later
-                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_empty, aph ^ 1));
+                        ok = role_wait(P, &acc_empty, aph ^ 1);
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -257,15 +284,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         ph ^= 1;
                     }
                 }
+                if (!ok) break;
                 if (elect_one()) tc_commit_pair(&acc_full);
                 __syncwarp();
                 aph ^= 1;
             }
-            if (!ok) {  // wait for the products still in flight
-                give_up();
-                if (elect_one()) tc_commit_pair(&drain);
-                __syncwarp();
-                mbar_wait(&drain, 0);
+            if (!ok) give_up();
+            if (elect_one()) tc_commit_pair(&drain);
+            __syncwarp();
+            mbar_wait(&drain, 0);
+            if (!ok) {
+                // Wait for the loads that no product waited for, of both CTAs: the
+                // last NS stages.  A stage that only one of the CTAs has loaded is
+                // made whole on its barrier first (the stage's last use is behind it:
+                // its products were committed before that CTA loaded it again).
+                const bool known =
+                    __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&loaded, 0, 2 * limit_ns(P) + kWaitLimitNs));
+                const int one = known ? int(s_issued) : 0, two = known ? int(cluster_ld(cluster_addr(&s_issued, 1))) : 0;
+                bool landed = true;  // after one that did not, the rest are only looked at
+                for (int f = max(0, max(one, two) - NS); f < max(one, two); ++f) {
+                    uint64_t *bar = &full[f % NS];
+                    if (elect_one()) {
+                        if (f >= one) mbar_arrive_expect_tx(bar, S::loads);
+                        else if (f >= two) mbar_complete_tx(bar, S::loads);
+                    }
+                    __syncwarp();
+                    landed = __all_sync(0xFFFFFFFFu, mbar_wait(bar, (f / NS) & 1, landed ? kWaitLimitNs : 0));
+                }
             }
         }
     } else if (warp >= 4) {
@@ -276,14 +321,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t acc = tmem + c0 + (uint32_t(32 * quarter) << 16);
         const uint32_t done = cluster_addr(&acc_empty, 0);
         uint32_t aph = 0;
-        for (int tile = first; tile < tiles; tile += stride) {
+        int tile = first;
+        for (; tile < tiles; tile += stride) {
             int tm, tn;
             tile_at(P, 8, tile, tm, tn);
-            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full, aph));
-            if (!ok) {
-                give_up();
-                break;
-            }
+            if (!role_wait(P, &acc_full, aph)) break;
             aph ^= 1;
             tc_fence_after();
             uint32_t v[64];
@@ -303,13 +345,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 store16<64>(P, m0, rows, nn, p);
             }
         }
+        if (tile < tiles) give_up();
+        for (; tile < tiles; tile += stride) {
+            int tm, tn;
+            tile_at(P, 8, tile, tm, tn);
+            store_nan(P, int64_t(tm) * 256 + c0, 64, int64_t(tn) * 256 + rank * 128 + 32 * quarter + lane);
+        }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // nobody leaves while the other's barriers or memory are in use
     tc_fence_after();
-    if (warp == 2) tmem_free<2, 512>(tmem);
+    if (warp == 2) {
+        if (rank == 1) mbar_wait(&drain, 0);  // the last arrival from the first CTA is in
+        tmem_free<2, 512>(tmem);
+    }
 }
 
 // ------------------------------------------------------------------ one CTA a tile
@@ -338,7 +389,7 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
     using S = Solo<BN>;
     constexpr int NS = S::stages, NA = 2;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[NS], empty[NS], acc_full[NA], acc_empty[NA], drain;
+    __shared__ __align__(8) uint64_t full[NS], empty[NS], acc_full[NA], acc_empty[NA], drain, ended;
     __shared__ uint32_t s_tmem;
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -352,7 +403,8 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], 256);
         }
-        mbar_init(&drain, 1);
+        mbar_init(&drain, 1);  // everything that was issued
+        mbar_init(&ended, 2);  // loads and products: nothing is in flight
         mbar_fence_init();
         tma_prefetch_map(&map_t);
         tma_prefetch_map(&map_w);
@@ -377,6 +429,7 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
     auto give_up = [&]() { g_fp4_error = 1; };
 
     if (warp == 0) {
+        const int stop = stop_after(P, 0);
         int st = 0, issued = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -384,7 +437,7 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
             int tm, tn;
             tile_at(P, 16, tile, tm, tn);
             for (int ks = ks0; ks < ks1; ++ks) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ph ^ 1));
+                ok = role_wait(P, &empty[st], ph ^ 1) & (issued != stop);
                 if (!ok) break;
                 if (elect_one()) {
                     uint8_t *b = smem + st * S::stage;
@@ -404,26 +457,30 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
                 }
             }
         }
-        if (!ok) {  // wait for the copies still in flight
-            give_up();
-            for (int i = 0; i < min(issued, NS); ++i) {
-                st = st == 0 ? NS - 1 : st - 1;
-                if (st == NS - 1) ph ^= 1;
-                mbar_wait(&full[st], ph);
-            }
+        if (!ok) give_up();
+        // every load lands before the CTA ends, whether its products wait for it or
+        // have given up
+        bool landed = true;  // after one that did not, the rest are only looked at
+        for (int i = 0; i < min(issued, NS); ++i) {
+            st = st == 0 ? NS - 1 : st - 1;
+            if (st == NS - 1) ph ^= 1;
+            landed = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st], ph, landed ? kWaitLimitNs : 0));
         }
+        if (lane == 0) mbar_arrive(&ended);
     } else if (warp == 1) {
-        int st = 0, ab = 0;
+        const int stop = stop_after(P, 2);
+        int st = 0, ab = 0, taken = 0;
         uint32_t ph = 0, aph = 0;
         constexpr uint32_t instr = mxf4_instr(kLanes, BN);
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += stride) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_empty[ab], aph ^ 1));
+            ok = role_wait(P, &acc_empty[ab], aph ^ 1);
             tc_fence_after();
             const uint32_t acc = tmem + ab * BN;
             for (int ks = ks0; ks < ks1 && ok; ++ks) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st], ph));
+                ok = role_wait(P, &full[st], ph) & (taken != stop);
                 if (!ok) break;
+                ++taken;
                 tc_fence_after();
                 const uint32_t b = smem_addr(smem) + st * S::stage;
                 const uint32_t tw = tmem + S::sf_base + st * S::sf_cols, tt = tw + 8;
@@ -450,6 +507,7 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
                     ph ^= 1;
                 }
             }
+            if (!ok) break;
             if (elect_one()) tc_commit(&acc_full[ab]);
             __syncwarp();
             if (++ab == NA) {
@@ -457,26 +515,22 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
                 aph ^= 1;
             }
         }
-        if (!ok) {  // wait for the products still in flight
-            give_up();
-            if (elect_one()) tc_commit(&drain);
-            __syncwarp();
-            mbar_wait(&drain, 0);
-        }
+        if (!ok) give_up();
+        if (elect_one()) tc_commit(&drain);
+        __syncwarp();
+        mbar_wait(&drain, 0);
+        if (lane == 0) mbar_arrive(&ended);
     } else if (warp >= 4) {
         // a quarter of the lanes and half of the columns a warp (all of 16)
         constexpr int HALF = BN > 16 ? BN / 2 : BN, CH = HALF < 32 ? HALF : 32;  // CH: columns at a time
         const int quarter = warp & 3, c0 = (warp - 4) / 4 * HALF;
         int ab = 0;
         uint32_t aph = 0;
-        for (int tile = first; tile < tiles; tile += stride) {
+        int tile = first;
+        for (; tile < tiles; tile += stride) {
             int tm, tn;
             tile_at(P, 16, tile, tm, tn);
-            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[ab], aph));
-            if (!ok) {
-                give_up();
-                break;
-            }
+            if (!role_wait(P, &acc_full[ab], aph)) break;
             tc_fence_after();
             const uint32_t acc = tmem + ab * BN + (uint32_t(32 * quarter) << 16);
             const int64_t nn = int64_t(tn) * kLanes + 32 * quarter + lane, m0 = int64_t(tm) * BN;
@@ -507,6 +561,18 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
                 ab = 0;
                 aph ^= 1;
             }
+        }
+        if (tile < tiles) give_up();
+        if (SPLIT && tile < tiles) {
+            // the partial tile takes the place of loads that may be in flight
+            mbar_wait(&ended, 0, 3 * limit_ns(P) + 3 * kWaitLimitNs);
+            for (int c = c0; c < c0 + HALF && c < BN; ++c)
+                reinterpret_cast<uint32_t *>(smem)[c * kLanes + 32 * quarter + lane] = kNaN;
+        }
+        for (; !SPLIT && tile < tiles; tile += stride) {
+            int tm, tn;
+            tile_at(P, 16, tile, tm, tn);
+            if (c0 < BN) store_nan(P, int64_t(tm) * BN + c0, HALF, int64_t(tn) * kLanes + 32 * quarter + lane);
         }
     }
 
@@ -689,7 +755,8 @@ cudaError_t go(Fp4Product P, const void *a, const void *b, int64_t row_bytes, in
 }  // namespace
 
 cudaError_t launch_fp4_product(const void *a, const uint8_t *sa, const void *b, const uint8_t *sb, int64_t m,
-                               int64_t n, int64_t k, void *out, int oelem, int device, cudaStream_t s) {
+                               int64_t n, int64_t k, void *out, int oelem, int device, cudaStream_t s,
+                               Fp4Limits limits) {
     cudaError_t e;
     if (k == 0) {
         const int64_t bytes = m * n * (oelem == kF32 ? 4 : 2);
@@ -702,9 +769,10 @@ cudaError_t launch_fp4_product(const void *a, const uint8_t *sa, const void *b, 
     P.sa = sa;
     P.sb = sb;
     P.out = out;
-    P.m = m;
+    P.m = int(m);
     P.n = n;
-    P.ot = oelem;
+    P.lim = limits;
+    P.ot = uint8_t(oelem);
     P.packed = oelem != kF32 && n % 2 == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
     P.kt = int((k + 127) / 128);
     P.k64 = int((k + 63) / 64);

@@ -153,9 +153,16 @@ cudaError_t launch_fp4_quant(const void *x, int xelem, int64_t rows, int64_t col
                              const int32_t *skip_if, cudaStream_t s);
 cudaError_t launch_fp4_dequant(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t cols,
                                void *out, int oelem, int device, cudaStream_t s);
+// How long a role of the product waits, 2^log2_ns nanoseconds, and after how many
+// stages one ends as if a wait had run out (for tests): 0 the loads of a CTA or of
+// a pair's first, 1 of a pair's second, 2 the products; 3 none.
+struct Fp4Limits {
+    uint8_t log2_ns, role;
+    uint32_t stages;
+};
 cudaError_t launch_fp4_product(const void *a, const uint8_t *sa, const void *b, const uint8_t *sb,
                                int64_t m, int64_t n, int64_t k, void *out, int oelem, int device,
-                               cudaStream_t s);
+                               cudaStream_t s, Fp4Limits limits = {30, 3, 0});
 // Reads and clears the product's sticky error word (waits for the stream).
 cudaError_t fp4_error_take(int32_t *v, cudaStream_t s);
 

@@ -106,11 +106,9 @@ amp_status fp4_dequant_mx(const void *q, const void *scales, int64_t rows, int64
     return finish(amp::launch_fp4_dequant(u8(q), u8(scales), rows, cols, out, oc, dev, cu(stream)), fn);
 }
 
-amp_status fp4_product_mx(const void *a, const void *a_scales, const void *b, const void *b_scales,
-                          int64_t m, int64_t n, int64_t k, void *out, amp_dtype out_dtype,
-                          amp_stream_t stream) {
-    AMP_TRACE("fp4_product_mx");
-    const char *fn = "fp4_product_mx";
+static amp_status product(const char *fn, const void *a, const void *a_scales, const void *b, const void *b_scales,
+                          int64_t m, int64_t n, int64_t k, void *out, amp_dtype out_dtype, amp_stream_t stream,
+                          amp::Fp4Limits limits) {
     // k: one tile's products have to end well within the second that a wait may take
     if (bad_shape(m, n) || bad_shape(m, k) || bad_shape(n, k) || k > (int64_t(1) << 27))
         return fail(AMP_EINVAL, kShape, fn);
@@ -124,7 +122,26 @@ amp_status fp4_product_mx(const void *a, const void *a_scales, const void *b, co
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return finish(e, fn);
-    return finish(amp::launch_fp4_product(a, u8(a_scales), b, u8(b_scales), m, n, k, out, oc, dev, cu(stream)), fn);
+    return finish(
+        amp::launch_fp4_product(a, u8(a_scales), b, u8(b_scales), m, n, k, out, oc, dev, cu(stream), limits), fn);
+}
+
+amp_status fp4_product_mx(const void *a, const void *a_scales, const void *b, const void *b_scales,
+                          int64_t m, int64_t n, int64_t k, void *out, amp_dtype out_dtype,
+                          amp_stream_t stream) {
+    AMP_TRACE("fp4_product_mx");
+    return product("fp4_product_mx", a, a_scales, b, b_scales, m, n, k, out, out_dtype, stream, {30, 3, 0});
+}
+
+amp_status fp4_product_mx_selftest(const void *a, const void *a_scales, const void *b, const void *b_scales,
+                                   int64_t m, int64_t n, int64_t k, void *out, amp_dtype out_dtype, int32_t role,
+                                   int32_t stages, int32_t limit_log2_ns, amp_stream_t stream) {
+    AMP_TRACE("fp4_product_mx_selftest");
+    const char *fn = "fp4_product_mx_selftest";
+    if (role < 0 || role > 2 || stages < 0) return fail(AMP_EINVAL, "%s: role not in [0, 2] or stages < 0", fn);
+    if (limit_log2_ns < 0 || limit_log2_ns > 30) return fail(AMP_EINVAL, "%s: limit above 2^30 ns", fn);
+    return product(fn, a, a_scales, b, b_scales, m, n, k, out, out_dtype, stream,
+                   {uint8_t(limit_log2_ns), uint8_t(role), uint32_t(stages)});
 }
 
 amp_status fp4_mx_check(amp_stream_t stream) {

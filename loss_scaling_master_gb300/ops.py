@@ -22,7 +22,7 @@ from ._lib import P, _check, _stream
 
 # every symbol include/ampops.h declares
 EXPORTS = ("fp4_mx_bytes", "fp4_mx_scale_bytes", "fp4_quant_mx", "fp4_dequant_mx",
-           "fp4_product_mx", "fp4_mx_check", "amp_layer_norm_forward",
+           "fp4_product_mx", "fp4_mx_check", "fp4_product_mx_selftest", "amp_layer_norm_forward",
            "amp_layer_norm_workspace_bytes", "amp_layer_norm_backward", "amp_act_forward_mx8",
            "amp_act_backward_mx8", "amp_ckpt8_save", "amp_ckpt8_restore")
 # those that _ops_bind calls, in the order it takes their addresses
@@ -47,6 +47,7 @@ def _load():
     L.fp4_dequant_mx.argtypes = [P, P, i64, i64, P, i32, P]
     L.fp4_product_mx.argtypes = [P, P, P, P, i64, i64, i64, P, i32, P]
     L.fp4_mx_check.argtypes = [P]
+    L.fp4_product_mx_selftest.argtypes = [P, P, P, P, i64, i64, i64, P, i32, i32, i32, i32, P]
     L.amp_layer_norm_forward.argtypes = [P, i32, i64, i64, P, P, i32, dbl, P, P, P, P, P, P]
     L.amp_layer_norm_workspace_bytes.argtypes = [i64, i64]
     L.amp_layer_norm_backward.argtypes = [P, P, i32, P, P, i64, i64, P, i32] + [P] * 6 + [i64, P]
@@ -123,7 +124,8 @@ def fp4_product_mx(a, a_scales, b, b_scales, k: int, out, stream=None):
 
 
 def fp4_mx_check(stream=None):
-    """Raise AmpError(AMP_ETIMEOUT) if a bounded wait of fp4_product_mx gave up (synchronises)."""
+    """Raise AmpError(AMP_ETIMEOUT) if a bounded wait of fp4_product_mx gave up on the current
+    device (synchronises)."""
     _check("fp4_mx_check", _load().fp4_mx_check(_stream(stream)))
 
 
