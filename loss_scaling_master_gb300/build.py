@@ -5,10 +5,13 @@
 Each .cu file is compiled in parallel with nvcc, then linked into one shared
 library next to this file; the operators' Python argument marshalling
 (``csrc/ops_bind.cpp``) is compiled beside them with g++ into ``_ops_bind.so``.
-Objects go to ``_build/`` (git-ignored).
+Objects go to ``_build/`` (git-ignored), and with them a stamp of what
+``_ops_bind.so`` was compiled for: it reads torch's tensors through torch's own
+inline accessors, so another torch or Python needs another one.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -24,6 +27,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libampfp8.so")
 BIND_SRC = os.path.join(CSRC, "ops_bind.cpp")
 BIND = os.path.join(PKG, "_ops_bind.so")
+BIND_STAMP = os.path.join(BUILD, "ops_bind.stamp")
 SOURCES = ["api.cu", "unscale_check.cu", "adamw_master.cu", "adamw_noalloc.cu", "emit_bf16.cu",
            "fp8_quant.cu",
            "fp8_rowwise.cu", "fp8_groupwise.cu", "update_scale.cu",
@@ -57,6 +61,21 @@ def _bind_command(target: str):
             "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
+def _bind_stamp() -> str:
+    """What _ops_bind.so depends on besides its sources: torch, Python and the command."""
+    return "\n".join([importlib.metadata.version("torch"), sysconfig.get_config_var("SOABI") or sys.version,
+                      *_bind_command(BIND)])
+
+
+def _bind_stale(deps) -> bool:
+    try:
+        with open(BIND_STAMP) as f:
+            same = f.read() == _bind_stamp()
+    except OSError:
+        same = False
+    return not same or _stale(BIND, deps)
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -82,7 +101,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                                                 stderr=subprocess.STDOUT, text=True)))
     bind_tmp = BIND + f".tmp{os.getpid()}"
     bind = None
-    if force or _stale(BIND, [BIND_SRC] + headers):
+    if force or _bind_stale([BIND_SRC] + headers):
         cmd = _bind_command(bind_tmp)
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -98,6 +117,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         raise RuntimeError(f"compilation failed for {failed}")
     if bind:
         os.replace(bind_tmp, BIND)
+        with open(bind_tmp + ".stamp", "w") as f:
+            f.write(_bind_stamp())
+        os.replace(bind_tmp + ".stamp", BIND_STAMP)
     if force or procs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]
