@@ -111,8 +111,9 @@ def main(steps=60, tokens=1024, d=256, hidden=1024):
         loss = block.train_step(x, target)
         if k % 10 == 0 or k == steps - 1:
             losses.append(loss.item())
+            # a product whose wait gave up is NaN, so its step was skipped; this says why
+            G.fp4_mx_check()
             print(f"step {k:4d}  loss {losses[-1]:.4f}")
-    G.fp4_mx_check()
     print(block.step.state())
     return losses
 

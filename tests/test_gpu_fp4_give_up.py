@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from test_gpu_fp4_product import operand
+from test_gpu_mlp_block import example  # noqa: F401  (fixture)
 from test_gpu_ops import G, dev  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
@@ -21,6 +22,14 @@ SOLO = [(1, 128, 4096), (1, 14336, 1500), (20, 300, 1024), (50, 301, 8192), (100
 PAIR = [(2049, 5121, 600), (4096, 4099, 2600), (700, 20000, 4100)]
 
 
+def give_up(G, a, sa, b, sb, k, out, role, stages):
+    """The product with a role ended early and waits of 2^22 ns."""
+    st = G.ops._load().fp4_product_mx_selftest(
+        *[x.data_ptr() for x in (a, sa, b, sb)], *out.shape, k, out.data_ptr(), DT[out.dtype], role, stages, 22,
+        ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == 0
+
+
 def run(G, dev, shape, role, stages, t):
     m, n, k = shape
     a, sa, _ = operand(G, m, k, 1)
@@ -29,10 +38,7 @@ def run(G, dev, shape, role, stages, t):
     G.fp4_product_mx(a, sa, b, sb, k, want)
     G.fp4_mx_check()
     assert not want.isnan().any()
-    st = G.ops._load().fp4_product_mx_selftest(
-        *[x.data_ptr() for x in (a, sa, b, sb)], m, n, k, out.data_ptr(), DT[t], role, stages, 22,
-        ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
-    assert st == 0
+    give_up(G, a, sa, b, sb, k, out, role, stages)
     with pytest.raises(G.AmpError) as e:
         G.fp4_mx_check()
     assert e.value.status == ETIMEOUT
@@ -74,6 +80,33 @@ def test_finished_tiles_stay(G, dev):
     """Roles that end after a whole tile leave it as it is."""
     assert not run(G, dev, (2049, 5121, 288), LOADS, 2, torch.float32).all()
     assert not run(G, dev, (128, 25600, 700), PRODUCTS, 4, torch.float32).all()
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_a_training_step_is_skipped(G, example, which, monkeypatch):
+    """Whichever of a step's six products gives up, the gradient check sees its NaN: the
+    weights stay, the scale is halved, and the check of the product says why."""
+    block = example.MlpBlock(300, 64, 96)
+    x, target = example.task(300, 64)
+    before = [t.clone() for t in block.step.master]
+    product, calls = G.fp4_product_mx, iter(range(6))
+
+    def one_gives_up(a, sa, b, sb, k, out):
+        if next(calls) == which:
+            return give_up(G, a, sa, b, sb, k, out, PRODUCTS, 0)
+        product(a, sa, b, sb, k, out)
+    monkeypatch.setattr(G, "fp4_product_mx", one_gives_up)
+    block.train_step(x, target)
+    assert next(calls, None) is None
+    st = block.step.state()
+    assert st["step"] == 0 and st["scale"] == 2.0 ** 11
+    assert all(torch.equal(a, b) for a, b in zip(before, block.step.master))
+    with pytest.raises(G.AmpError):
+        G.fp4_mx_check()
+    monkeypatch.undo()
+    block.train_step(x, target)
+    assert block.step.state()["step"] == 1
+    G.fp4_mx_check()
 
 
 def test_refusals(G, dev):
