@@ -114,7 +114,9 @@ amp_status fp4_product_mx_selftest(const void *a, const void *a_scales, const vo
  *     y    = (x - mean) * rstd * weight + bias       rounded to x's type
  *   weight, bias  [cols] of w_dtype (f32, or x's type); either may be NULL
  *                 (1 and 0)
- *   mean, rstd    fp32 [rows], for the backward pass; may be NULL
+ *   mean, rstd    fp32 [rows], for the backward pass; may be NULL (the inverse
+ *                 root is good to 2 units in its last place, and depends on the
+ *                 sum under it alone, not on the row's length or address)
  *   ckpt, ckpt_scales  both or neither: the 8-bit checkpoint of x
  * Errors: AMP_EINVAL (NULL x / y, half a checkpoint, negative or too large
  * size, eps < 0 or NaN), AMP_EDTYPE. */
