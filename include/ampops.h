@@ -1,11 +1,17 @@
 /*
  * ampops.h - C ABI of the forward/backward operators in libampfp8.so that sit
- * around the optimizer step of ampfp8.h: microscaled 4-bit quantisation and
- * products, layer norm, and activations whose inputs are kept in 8 bits for
- * the backward pass.
+ * around the optimizer step of ampfp8.h: microscaled 4-bit quantisation,
+ * products and linear layers, layer norm, activations whose inputs are kept in
+ * 8 bits for the backward pass, dropout, and the log probabilities of tokens.
  *
  *   fp4_quant_mx, fp4_dequant_mx     4-bit blocks (+ transposed copy), and back
  *   fp4_product_mx                   C = A B^T of two such matrices
+ *   fp4_linear_mx                    the same with bias, activation, residual and
+ *                                    the 8-bit checkpoint in its epilogue
+ *   amp_bias_act_backward_mx8        gradients of that bias and activation
+ *   amp_dropout_forward/backward     dropout whose mask is never stored
+ *   amp_token_logprobs_forward/backward  log probabilities of given tokens,
+ *                                    entropy, most probable tokens
  *   amp_layer_norm_forward/backward  layer norm, with both parameters' gradients
  *   amp_act_forward_mx8/backward_mx8 GELU / SiLU, plain or gated, from 8-bit
  *                                    checkpoints of their inputs
@@ -94,8 +100,8 @@ amp_status fp4_product_mx(const void *a, const void *a_scales, const void *b, co
                           amp_stream_t stream);
 
 /* Waits for `stream`, reads and clears the current device's sticky error word
- * of fp4_product_mx: AMP_ETIMEOUT if a bounded wait gave up since the last
- * check, AMP_OK otherwise. */
+ * of fp4_product_mx and fp4_linear_mx: AMP_ETIMEOUT if a bounded wait gave up
+ * since the last check, AMP_OK otherwise. */
 amp_status fp4_mx_check(amp_stream_t stream);
 
 /* fp4_product_mx with waits of at most 2^limit_log2_ns ns (0 to 30) and one of the
@@ -184,6 +190,123 @@ amp_status amp_ckpt8_save(const void *x, amp_dtype x_dtype, int64_t rows, int64_
                           void *scales, amp_stream_t stream);
 amp_status amp_ckpt8_restore(const void *q, const void *scales, int64_t rows, int64_t cols,
                              void *out, amp_dtype out_dtype, amp_stream_t stream);
+
+/* A linear layer in one launch, for 4-bit A [m, k] and B [n, k]:
+ *     z   = A B^T + bias                      in fp32, summed as fp4_product_mx
+ *     out = f(z) + residual                   rounded once to out_dtype
+ *   bias      [n] of bias_dtype (f32, or out's type), or NULL (0)
+ *   act       an amp_act, or AMP_ACT_NONE
+ *   residual  [m, n] of out_dtype, or NULL (0); may be out itself
+ *   q, scales the 8-bit checkpoint of z (before its rounding to any other
+ *             type), for amp_bias_act_backward_mx8; both or neither
+ * f is as accurate as amp_act_forward_mx8's for out's type.  k = 0: z = bias.
+ * Equal calls give equal bits.  Waits are bounded as fp4_product_mx's are:
+ * fp4_mx_check reports a call that gave up, what it could not finish is NaN in
+ * out and has the NaN scale in the checkpoint.
+ * Errors: as fp4_product_mx, AMP_EINVAL (half a checkpoint, unknown act). */
+enum { AMP_ACT_NONE = -1 };
+amp_status fp4_linear_mx(const void *a, const void *a_scales, const void *b, const void *b_scales,
+                         int64_t m, int64_t n, int64_t k, const void *bias, amp_dtype bias_dtype,
+                         int32_t act, const void *residual, void *out, amp_dtype out_dtype, void *q,
+                         void *scales, amp_stream_t stream);
+
+/* fp4_linear_mx as fp4_product_mx_selftest runs fp4_product_mx. */
+amp_status fp4_linear_mx_selftest(const void *a, const void *a_scales, const void *b,
+                                  const void *b_scales, int64_t m, int64_t n, int64_t k,
+                                  const void *bias, amp_dtype bias_dtype, int32_t act,
+                                  const void *residual, void *out, amp_dtype out_dtype, void *q,
+                                  void *scales, int32_t role, int32_t stages,
+                                  int32_t limit_log2_ns, amp_stream_t stream);
+
+/* Gradients behind a bias and an activation, from the checkpoint of z that
+ * fp4_linear_mx made (values zh):
+ *     dz = dy * f'(zh),   dbias = sum over rows of dz
+ * in fp32; dbias sums dz before its rounding, in an order that depends on the
+ * shape, the tensors' alignment and the device alone.  With AMP_ACT_NONE dz = dy: q, scales and dz are
+ * NULL and only dbias is written.
+ *   dy, dz  [rows, cols] of dtype; dz may be dy
+ *   dbias   [cols] of bias_dtype (f32, or dtype); zeros for no rows
+ * Errors: AMP_EINVAL (NULL, an activation without q, scales and dz or one of
+ * those without it, negative or too large size, unknown act), AMP_EDTYPE. */
+amp_status amp_bias_act_backward_mx8(int32_t act, const void *dy, amp_dtype dtype, int64_t rows,
+                                     int64_t cols, const void *q, const void *scales, void *dz,
+                                     void *dbias, amp_dtype bias_dtype, amp_stream_t stream);
+
+/* Dropout, added to a residual, over [rows, cols] (AMP_DT_BF16, AMP_DT_F16,
+ * AMP_DT_F32), in fp32 and rounded once:
+ *     y = residual + (u(k) >= T ? x * 65536 / (65536 - T) : 0)
+ * with T the whole number nearest to 65536 p (ties to even) and u(k) 16 random
+ * bits of element k = row * cols + column, which are a function of seed, step,
+ * site and k alone: half (k % 8) % 2, low first, of word (k % 8) / 2 of
+ * Philox4x32-10 for the counter {k / 8 low, k / 8 high, step, 2^30 + site}
+ * under the key seed.  Nothing is stored: the backward pass makes the same
+ * mask.  p = 1 drops everything.  What is dropped is not multiplied: a NaN or an
+ * infinity there leaves nothing behind.  The streams of the step's stochastic
+ * rounding under the same seed are others (their tensor words are below 2^30,
+ * or 2^31 and more).
+ *   step_dev  the step, one int32 on the device (so a captured graph draws
+ *             another mask each time it is changed); NULL: 0
+ *   site      which of a step's dropouts this is, in [0, 2^30)
+ *   residual  of the same type, or NULL (0); y may be x or residual
+ * Errors: AMP_EINVAL (NULL x / y, p outside [0, 1] or NaN, site out of range,
+ * negative or too large size), AMP_EDTYPE. */
+amp_status amp_dropout_forward(const void *x, amp_dtype dtype, int64_t rows, int64_t cols, double p,
+                               uint64_t seed, const int32_t *step_dev, int32_t site,
+                               const void *residual, void *y, amp_stream_t stream);
+
+/* Its gradients, with the mask of the same seed, step, site and shape:
+ *     dx = u(k) >= T ? dy * 65536 / (65536 - T) : 0,   dbias = sum over rows of dx
+ * (the residual's is dy).  dx may be dy.  dbias is the gradient of a bias that
+ * was added to x before: [cols] of bias_dtype (f32, or dtype), summed as
+ * amp_bias_act_backward_mx8's; or NULL.
+ * Errors: as amp_dropout_forward. */
+amp_status amp_dropout_backward(const void *dy, amp_dtype dtype, int64_t rows, int64_t cols,
+                                double p, uint64_t seed, const int32_t *step_dev, int32_t site,
+                                void *dx, void *dbias, amp_dtype bias_dtype, amp_stream_t stream);
+
+/* Log probabilities under softmax over the rows of z [rows, cols]
+ * (AMP_DT_BF16, AMP_DT_F16, AMP_DT_F32), whose rows start ld >= cols elements
+ * apart (what lies between is not read), in fp32:
+ *     m = max z_j,  s = sum exp(z_j - m),  log p_j = (z_j - m) - log s
+ *   targets  int64 [rows]: the row's token t.  A negative one marks a row that
+ *            is not used: it is not read, logp, entropy and stats are 0, and it
+ *            has no alternatives.  One of cols or more gives NaN.  NULL: none
+ *            (logp NULL too)
+ *   logp     fp32 [rows]: log p_t, or NULL
+ *   entropy  fp32 [rows]: -sum p_j log p_j, or NULL
+ *   stats    fp32 [rows, 2]: m and log s, for the backward pass, or NULL
+ *   top_ids, top_logp  int64 and fp32 [rows, top_n], both or neither: the top_n
+ *            most probable tokens (at most 32), larger logits first, equal ones
+ *            by index; -1 and -inf where there are no more.  Logits of -inf and
+ *            NaN are not listed
+ * A logit of -inf (a masked token) has probability 0 and log probability -inf.
+ * A row with a NaN, with +inf, or with nothing but -inf gives NaN.
+ * Errors: AMP_EINVAL (NULL z, logp without targets, top_n outside [0, 32], half
+ * of the alternatives, ld < cols, negative or too large size), AMP_EDTYPE. */
+amp_status amp_token_logprobs_forward(const void *z, amp_dtype dtype, int64_t rows, int64_t cols,
+                                      int64_t ld, const int64_t *targets, float *logp,
+                                      float *entropy, float *stats, int64_t *top_ids,
+                                      float *top_logp, int32_t top_n, amp_stream_t stream);
+
+/* The gradient at the logits, from what the forward call left in stats and
+ * entropy, in fp32:
+ *     dz_j = S * (dlogp * ([j = t] - p_j) - dentropy * p_j * (log p_j + H))
+ *   dlogp     fp32 [rows]: the gradient at logp, or NULL (0)
+ *   dentropy  fp32 [rows]: the gradient at the entropy H, or NULL (0); with it
+ *             entropy is needed
+ *   scale_dev the loss scale S, one fp32 on the device, or NULL (1)
+ *   dz        [rows, cols] of dtype, rows dld >= cols elements apart (what lies
+ *             between is left as it is); may be z itself with dld = ld
+ * Rows with a negative target get zeros, whatever their logits.
+ * Errors: AMP_EINVAL (NULL z / stats / dz, dlogp without targets, dentropy
+ * without entropy, ld or dld < cols, dz = z with another dld, negative or too
+ * large size), AMP_EDTYPE. */
+amp_status amp_token_logprobs_backward(const float *dlogp, const void *z, amp_dtype dtype,
+                                       int64_t rows, int64_t cols, int64_t ld,
+                                       const int64_t *targets, const float *stats,
+                                       const float *entropy, const float *dentropy,
+                                       const float *scale_dev, void *dz, int64_t dld,
+                                       amp_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,144 @@
+// bias_grad.cu - the gradient of a bias, alone or with that of the activation that
+// follows it (from the 8-bit checkpoint of the activation's input):
+//
+//   dz = dy f'(zh)  (or dz = dy),   db = sum over rows dz
+//
+// dy and the checkpoint are read once and dz is written once; the sums are of dz as
+// computed, before its rounding.  See column_sums.cuh.
+#include "act.cuh"
+#include "column_sums.cuh"
+#include "internal.h"
+
+namespace amp {
+namespace {
+
+enum : int { kNoAct = 3 };  // after the three amp_act values
+
+struct BiasBwd {
+    const void *dy;
+    const uint8_t *q, *s;
+    void *dz, *db;
+    int64_t rows, cols;
+    int kb, otype;
+};
+
+template <int XT, int ACT, bool VEC>
+__global__ void __launch_bounds__(kSumThreads) bias_bwd_kernel(BiasBwd P) {
+    using S = SumShape<VEC>;
+    constexpr int N = VEC ? 8 : 1, U = VEC ? 4 : 8;  // elements a thread and row, rows a step
+    pdl_wait();
+    pdl_trigger();
+    const SumShare at(P.rows);
+    const int64_t c = at.col0 + int(threadIdx.x) % S::across * N;
+    const bool in = c < P.cols;
+    float a[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) a[j] = 0.0f;
+    for (int64_t r0 = at.row0 + int(threadIdx.x) / S::across; in && r0 < at.row1; r0 += U * S::groups) {
+        if constexpr (VEC) {
+            uint4 g[U][kWords8<XT>];
+            uint2 q[U];
+            uint32_t e[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = r0 + u * S::groups, k = r * P.cols + c;
+                if (r >= at.row1) break;
+#pragma unroll
+                for (int w = 0; w < kWords8<XT>; ++w)
+                    g[u][w] = ld16(static_cast<const char *>(P.dy) + k * (XT == kF32 ? 4 : 2) + 16 * w);
+                if (ACT != kNoAct) {
+                    q[u] = *reinterpret_cast<const uint2 *>(P.q + k);
+                    e[u] = P.s[r * P.kb + c / kMxBlock];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = r0 + u * S::groups, k = r * P.cols + c;
+                if (r >= at.row1) break;
+                float y[8];
+                raw8_to_f32<XT>(g[u], y);
+                if constexpr (ACT != kNoAct) {
+                    float x[8];
+                    values8(q[u], mx_scale(e[u]), x);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        float2 dz, unused;
+                        act_grads<XT, ACT, false>(x[j], x[j + 1], 0.0f, 0.0f, y[j], y[j + 1], dz, unused);
+                        y[j] = dz.x;
+                        y[j + 1] = dz.y;
+                    }
+                    stv<XT>(P.dz, k, y);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a[j] += y[j];
+            }
+        } else {
+            float g[U];
+            uint32_t q[U], e[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = r0 + u * S::groups, k = r * P.cols + c;
+                g[u] = 0.0f;
+                q[u] = e[u] = 0;
+                if (r >= at.row1) continue;
+                g[u] = load_elem<XT>(P.dy, k);
+                if (ACT != kNoAct) {
+                    q[u] = P.q[k];
+                    e[u] = P.s[r * P.kb + c / kMxBlock];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; u += 2) {
+                float2 dz = make_float2(g[u], g[u + 1]);
+                if constexpr (ACT != kNoAct) {
+                    float x[4];
+                    float2 unused;
+                    e4m3x4_to_f32x4(q[u] | (q[u + 1] << 8), x);
+                    act_grads<XT, ACT, false>(__fmul_rn(x[0], mx_scale(e[u])), __fmul_rn(x[1], mx_scale(e[u + 1])),
+                                              0.0f, 0.0f, g[u], g[u + 1], dz, unused);
+                }
+                const int64_t r = r0 + u * S::groups, k = r * P.cols + c;
+                if (r < at.row1) {
+                    if (ACT != kNoAct) store_elem<XT>(P.dz, k, dz.x);
+                    a[0] += dz.x;
+                }
+                if (r + S::groups < at.row1) {
+                    if (ACT != kNoAct) store_elem<XT>(P.dz, k + S::groups * P.cols, dz.y);
+                    a[0] += dz.y;
+                }
+            }
+        }
+    }
+    sum_join<VEC>(at, P.cols, a, P.db, P.otype);
+}
+
+template <int XT, int ACT>
+cudaError_t go(const BiasBwd &P, bool vec, int sms, cudaStream_t s) {
+    return vec ? launch_sums(bias_bwd_kernel<XT, ACT, true>, P.rows, P.cols, SumShape<true>::groups, sms, s, P)
+               : launch_sums(bias_bwd_kernel<XT, ACT, false>, P.rows, P.cols, SumShape<false>::groups, sms, s, P);
+}
+template <int XT>
+cudaError_t go_x(const BiasBwd &P, int act, bool vec, int sms, cudaStream_t s) {
+    switch (act) {
+    case AMP_ACT_GELU: return go<XT, AMP_ACT_GELU>(P, vec, sms, s);
+    case AMP_ACT_GELU_TANH: return go<XT, AMP_ACT_GELU_TANH>(P, vec, sms, s);
+    case AMP_ACT_SILU: return go<XT, AMP_ACT_SILU>(P, vec, sms, s);
+    default: return go<XT, kNoAct>(P, vec, sms, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_bias_bwd(int act, const void *dy, int elem, int64_t rows, int64_t cols, const uint8_t *q,
+                            const uint8_t *sc, void *dz, void *db, int dbelem, int device, cudaStream_t s) {
+    const BiasBwd P{dy, q, sc, dz, db, rows, cols, int((cols + kMxBlock - 1) / kMxBlock), dbelem};
+    const auto off = [](const void *p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; };
+    const bool vec = cols % 8 == 0 && !off(dy, 15) && !off(dz, 15) && !off(q, 7);
+    const int a = act < 0 ? int(kNoAct) : act, sms = sm_count(device);
+    const cudaError_t e = elem == kF32   ? go_x<kF32>(P, a, vec, sms, s)
+                          : elem == kF16 ? go_x<kF16>(P, a, vec, sms, s)
+                                         : go_x<kBF16>(P, a, vec, sms, s);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace amp

@@ -1,0 +1,211 @@
+// dropout.cu - dropout whose mask is a function of the element's place and never
+// stored, added to a residual; its gradient, alone or with that of the bias that was
+// added before it.
+//
+//   y = residual + (bits(k) >= T ? x * 65536 / (65536 - T) : 0),  T = RNE(65536 p)
+//
+// bits(k): 16 bits of Philox4x32-10 (philox.cuh), one call of the generator for 8
+// consecutive elements, so the backward pass makes the same mask again in whichever
+// order it walks.  The generator's 20 wide multiplications and 60 other instructions
+// for 8 elements are a third of what the issue rate leaves an element at the rate of
+// memory.
+#include "column_sums.cuh"
+#include "internal.h"
+#include "philox.cuh"
+
+namespace amp {
+namespace {
+
+struct Dropout {
+    const void *x, *res;
+    void *y, *db;
+    const int32_t *step;
+    uint64_t seed;
+    int64_t rows, cols;  // flat: rows = 1
+    float scale;
+    uint32_t drop;  // T
+    uint32_t site;
+    int otype;
+};
+
+// Bit j: element j of the group stays.
+__device__ __forceinline__ uint32_t keep8(const Dropout &P, int32_t step, int64_t group) {
+    const uint4 r = sr_random8(P.seed, step, int32_t(P.site), group);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if ((w[j] & 0xFFFFu) >= P.drop) m |= 1u << (2 * j);
+        if ((w[j] >> 16) >= P.drop) m |= 2u << (2 * j);
+    }
+    return m;
+}
+
+// 8 elements a thread, every address aligned; the last ones one at a time.
+template <int XT, bool RES>
+__global__ void __launch_bounds__(kThreads) dropout_vec_kernel(Dropout P) {
+    pdl_wait();
+    pdl_trigger();
+    const int32_t step = P.step ? *P.step : 0;
+    const int64_t groups = P.cols >> 3;
+    for (int64_t g = int64_t(blockIdx.x) * kThreads + threadIdx.x; g < groups; g += int64_t(gridDim.x) * kThreads) {
+        float x[8], r[8];
+        ldv<XT>(P.x, 8 * g, x);
+        if (RES) ldv<XT>(P.res, 8 * g, r);
+        const uint32_t m = keep8(P, step, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            x[j] = (m >> j) & 1 ? x[j] * P.scale : 0.0f;
+            if (RES) x[j] = r[j] + x[j];
+        }
+        stv<XT>(P.y, 8 * g, x);
+    }
+    const int64_t k = 8 * groups + threadIdx.x;
+    if (blockIdx.x == 0 && k < P.cols) {
+        float v = (keep8(P, step, groups) >> threadIdx.x) & 1 ? load_elem<XT>(P.x, k) * P.scale : 0.0f;
+        if (RES) v = load_elem<XT>(P.res, k) + v;
+        store_elem<XT>(P.y, k, v);
+    }
+}
+
+// Any address: a warp takes 256 elements, a lane makes the mask of 8 consecutive ones
+// and applies that of every 32nd.
+template <int XT, bool RES>
+__global__ void __launch_bounds__(kThreads) dropout_elem_kernel(Dropout P) {
+    pdl_wait();
+    pdl_trigger();
+    const int32_t step = P.step ? *P.step : 0;
+    const int lane = threadIdx.x & 31;
+    const int64_t stride = int64_t(gridDim.x) * kThreads * 8;
+    for (int64_t k0 = (int64_t(blockIdx.x) * kThreads + (threadIdx.x & ~31)) * 8; k0 < P.cols; k0 += stride) {
+        const uint32_t m = keep8(P, step, (k0 >> 3) + lane);
+        float x[8], r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t k = k0 + 32 * j + lane;
+            x[j] = k < P.cols ? load_elem<XT>(P.x, k) : 0.0f;
+            r[j] = RES && k < P.cols ? load_elem<XT>(P.res, k) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t k = k0 + 32 * j + lane;
+            const uint32_t b = __shfl_sync(0xFFFFFFFFu, m, 4 * j + lane / 8);
+            float v = (b >> (lane & 7)) & 1 ? x[j] * P.scale : 0.0f;
+            if (RES) v = r[j] + v;
+            if (k < P.cols) store_elem<XT>(P.y, k, v);
+        }
+    }
+}
+
+// The gradient with the bias's: by columns (column_sums.cuh).
+template <int XT>
+__global__ void __launch_bounds__(kSumThreads) dropout_bias_vec_kernel(Dropout P) {
+    using S = SumShape<true>;
+    constexpr int U = 4;
+    pdl_wait();
+    pdl_trigger();
+    const SumShare at(P.rows);
+    const int32_t step = P.step ? *P.step : 0;
+    const int64_t c = at.col0 + int(threadIdx.x) % S::across * 8;
+    const bool in = c < P.cols;
+    float a[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t r0 = at.row0 + int(threadIdx.x) / S::across; in && r0 < at.row1; r0 += U * S::groups) {
+        uint4 g[U][kWords8<XT>];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u * S::groups;
+            if (r >= at.row1) break;
+#pragma unroll
+            for (int w = 0; w < kWords8<XT>; ++w)
+                g[u][w] = ld16(static_cast<const char *>(P.x) + (r * P.cols + c) * (XT == kF32 ? 4 : 2) + 16 * w);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u * S::groups, k = r * P.cols + c;
+            if (r >= at.row1) break;
+            const uint32_t m = keep8(P, step, k >> 3);
+            float y[8];
+            raw8_to_f32<XT>(g[u], y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                y[j] = (m >> j) & 1 ? y[j] * P.scale : 0.0f;
+                a[j] += y[j];
+            }
+            stv<XT>(P.y, k, y);
+        }
+    }
+    sum_join<true>(at, P.cols, a, P.db, P.otype);
+}
+// Any size and address.  A warp's 32 columns of a row lie in at most 5 of the
+// generator's groups: 30 lanes make the masks of 6 rows.
+template <int XT>
+__global__ void __launch_bounds__(kSumThreads) dropout_bias_elem_kernel(Dropout P) {
+    using S = SumShape<false>;
+    constexpr int U = 6;
+    pdl_wait();
+    pdl_trigger();
+    const SumShare at(P.rows);
+    const int32_t step = P.step ? *P.step : 0;
+    const int lane = threadIdx.x & 31;
+    const int64_t c0 = at.col0 + (int(threadIdx.x) % S::across & ~31), c = c0 + lane;
+    const bool in = c < P.cols;
+    float a[1] = {0.0f};
+    for (int64_t r0 = at.row0 + int(threadIdx.x) / S::across; r0 < at.row1; r0 += U * S::groups) {
+        float x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u * S::groups;
+            x[u] = in && r < at.row1 ? load_elem<XT>(P.x, r * P.cols + c) : 0.0f;
+        }
+        const int64_t k0 = (r0 + int64_t(min(lane / 5, U - 1)) * S::groups) * P.cols + c0;
+        const uint32_t m = keep8(P, step, (k0 >> 3) + lane % 5);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u * S::groups, k = r * P.cols + c0;
+            const int off = int(k & 7) + lane;
+            const uint32_t b = __shfl_sync(0xFFFFFFFFu, m, 5 * u + off / 8);
+            const float v = (b >> (off & 7)) & 1 ? x[u] * P.scale : 0.0f;
+            if (in && r < at.row1) {
+                a[0] += v;
+                store_elem<XT>(P.y, k + lane, v);
+            }
+        }
+    }
+    sum_join<false>(at, P.cols, a, P.db, P.otype);
+}
+
+bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+template <int XT>
+cudaError_t go(const Dropout &P, int sms, cudaStream_t s) {
+    const bool vec = !off16(P.x) && !off16(P.res) && !off16(P.y);
+    if (P.db) {
+        return vec && P.cols % 8 == 0
+                   ? launch_sums(dropout_bias_vec_kernel<XT>, P.rows, P.cols, SumShape<true>::groups, sms, s, P)
+                   : launch_sums(dropout_bias_elem_kernel<XT>, P.rows, P.cols, SumShape<false>::groups, sms, s, P);
+    }
+    Dropout F = P;
+    F.cols = P.rows * P.cols;
+    F.rows = 1;
+    const int64_t want = (F.cols + kThreads * 8 - 1) / (kThreads * 8);
+    const dim3 grid(unsigned(std::min<int64_t>(want, int64_t(sms) * 64))), block(kThreads);
+    if (vec)
+        return F.res ? launch_pdl(dropout_vec_kernel<XT, true>, grid, block, 0, s, F)
+                     : launch_pdl(dropout_vec_kernel<XT, false>, grid, block, 0, s, F);
+    return F.res ? launch_pdl(dropout_elem_kernel<XT, true>, grid, block, 0, s, F)
+                 : launch_pdl(dropout_elem_kernel<XT, false>, grid, block, 0, s, F);
+}
+
+}  // namespace
+
+cudaError_t launch_dropout(const void *x, const void *res, int elem, int64_t rows, int64_t cols, uint32_t drop,
+                           uint64_t seed, const int32_t *step, uint32_t site, void *y, void *db, int dbelem,
+                           int device, cudaStream_t s) {
+    const float scale = drop < 65536u ? float(65536.0 / double(65536u - drop)) : 0.0f;
+    const Dropout P{x, res, y, db, step, seed, rows, cols, scale, drop, site, dbelem};
+    const int sms = sm_count(device);
+    const cudaError_t e = elem == kF32 ? go<kF32>(P, sms, s) : elem == kF16 ? go<kF16>(P, sms, s) : go<kBF16>(P, sms, s);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace amp

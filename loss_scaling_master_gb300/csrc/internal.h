@@ -163,8 +163,34 @@ struct Fp4Limits {
 cudaError_t launch_fp4_product(const void *a, const uint8_t *sa, const void *b, const uint8_t *sb,
                                int64_t m, int64_t n, int64_t k, void *out, int oelem, int device,
                                cudaStream_t s, Fp4Limits limits = {30, 3, 0});
-// Reads and clears the product's sticky error word (waits for the stream).
+// Reads and clears the sticky error words of the product and of the linear layer (waits for
+// the stream); the second one the linear layer's alone.
 cudaError_t fp4_error_take(int32_t *v, cudaStream_t s);
+cudaError_t fp4_linear_error_take(int32_t *v, cudaStream_t s);
+
+cudaError_t launch_fp4_linear(const void *a, const uint8_t *sa, const void *b, const uint8_t *sb,
+                              int64_t m, int64_t n, int64_t k, const void *bias, int belem, int act,
+                              const void *res, void *out, int oelem, uint8_t *q, uint8_t *sc,
+                              int device, cudaStream_t s, Fp4Limits limits = {30, 3, 0});
+
+// act: an amp_act, or -1 for none (dz, q and sc unused).
+cudaError_t launch_bias_bwd(int act, const void *dy, int elem, int64_t rows, int64_t cols,
+                            const uint8_t *q, const uint8_t *sc, void *dz, void *db, int dbelem,
+                            int device, cudaStream_t s);
+
+// db: the column sums of y (res is NULL then), or NULL.  drop: of 65536.
+cudaError_t launch_dropout(const void *x, const void *res, int elem, int64_t rows, int64_t cols,
+                           uint32_t drop, uint64_t seed, const int32_t *step, uint32_t site, void *y,
+                           void *db, int dbelem, int device, cudaStream_t s);
+
+// ld, dld: elements from a row to the next.
+cudaError_t launch_logprobs_fwd(const void *z, int elem, int64_t rows, int64_t cols, int64_t ld,
+                                const int64_t *t, float *logp, float *ent, float *stats, int64_t *ids,
+                                float *top, int k, int device, cudaStream_t s);
+cudaError_t launch_logprobs_bwd(const void *z, int elem, int64_t rows, int64_t cols, int64_t ld,
+                                const int64_t *t, const float *stats, const float *dlogp,
+                                const float *ent, const float *dent, const float *scale, void *dz,
+                                int64_t dld, cudaStream_t s);
 
 cudaError_t launch_norm_fwd(const void *x, int xelem, int64_t rows, int64_t cols, const void *w,
                             const void *b, int welem, float eps, void *y, float *mean, float *rstd,

@@ -181,6 +181,52 @@ __device__ __forceinline__ void store_elem(void *x, int64_t k, float v) {
     else static_cast<uint16_t *>(x)[k] = uint16_t(f32x2_to_16x2<XT>(v, 0.0f) & 0xFFFFu);
 }
 
+// fp32 bits of max |y| over 8 elements a lane and the 4 lanes of a block
+__device__ __forceinline__ uint32_t block_max8(const float (&y)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+}
+
+// 8 elements -> e4m3 codes by a block's factor, and back
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float f) {
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float a, b;
+        mul2_rn(y[2 * j], y[2 * j + 1], f, f, a, b);
+        h[j] = f32x2_to_fp8x2_raw<kE4M3>(a, b);
+    }
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+__device__ __forceinline__ void values8(uint2 q, float s, float (&y)[8]) {
+    e4m3x4_to_f32x4(q.x, y);
+    e4m3x4_to_f32x4(q.y, y + 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(y[j], s);
+}
+
+// 8 consecutive elements from k on, 16-byte aligned
+template <int XT>
+__device__ __forceinline__ void ldv(const void *p, int64_t k, float (&y)[8]) {
+    constexpr int esz = XT == kF32 ? 4 : 2;
+    uint4 u[kWords8<XT>];
+#pragma unroll
+    for (int j = 0; j < kWords8<XT>; ++j) u[j] = ld16(static_cast<const char *>(p) + k * esz + 16 * j);
+    raw8_to_f32<XT>(u, y);
+}
+template <int XT>
+__device__ __forceinline__ void stv(void *p, int64_t k, const float (&y)[8]) {
+    constexpr int esz = XT == kF32 ? 4 : 2;
+    uint4 u[kWords8<XT>];
+    f32_to_raw8<XT>(y, u);
+#pragma unroll
+    for (int j = 0; j < kWords8<XT>; ++j) st16(static_cast<char *>(p) + k * esz + 16 * j, u[j]);
+}
+
 // Items 0 .. rows * per_row - 1 taken `step` apart (a grid's worth, so below
 // 2^32): an item's row and place in it, by 32-bit divisions at the start and
 // additions from then on.

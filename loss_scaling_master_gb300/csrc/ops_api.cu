@@ -149,7 +149,7 @@ amp_status fp4_mx_check(amp_stream_t stream) {
     int32_t v = 0;
     const cudaError_t e = amp::fp4_error_take(&v, cu(stream));
     if (e != cudaSuccess) return finish(e, "fp4_mx_check");
-    return v == 0 ? AMP_OK : fail(AMP_ETIMEOUT, "fp4_mx_check: a bounded wait of fp4_product_mx gave up; "
+    return v == 0 ? AMP_OK : fail(AMP_ETIMEOUT, "fp4_mx_check: a bounded wait of fp4_product_mx or fp4_linear_mx gave up; "
                                                 "the output of that call is unspecified");
 }
 
@@ -294,6 +294,190 @@ amp_status amp_ckpt8_restore(const void *q, const void *scales, int64_t rows, in
     if (e != cudaSuccess) return finish(e, fn);
     return finish(amp::launch_act_bwd(-1, nullptr, elem_code(out_dtype), rows, cols, u8(q), u8(scales), nullptr,
                                       nullptr, out, nullptr, dev, cu(stream)),
+                  fn);
+}
+
+static bool known_act(int32_t act) { return act == AMP_ACT_NONE || (act >= AMP_ACT_GELU && act <= AMP_ACT_SILU); }
+
+static amp_status linear(const char *fn, const void *a, const void *a_scales, const void *b, const void *b_scales,
+                         int64_t m, int64_t n, int64_t k, const void *bias, amp_dtype bias_dtype, int32_t act,
+                         const void *residual, void *out, amp_dtype out_dtype, void *q, void *scales,
+                         amp_stream_t stream, amp::Fp4Limits limits) {
+    if (bad_shape(m, n) || bad_shape(m, k) || bad_shape(n, k) || k > (int64_t(1) << 27))
+        return fail(AMP_EINVAL, kShape, fn);
+    const int oc = elem_code(out_dtype), bc = bias ? elem_code(bias_dtype) : int(amp::kF32);
+    if (oc < 0 || bc < 0 || (bc != amp::kF32 && bc != oc)) return fail(AMP_EDTYPE, kType, fn);
+    if (!known_act(act)) return fail(AMP_EINVAL, "%s: unknown act", fn);
+    if ((q == nullptr) != (scales == nullptr)) return fail(AMP_EINVAL, "%s: q and scales go together", fn);
+    if (m * n == 0) return AMP_OK;
+    if (!out || (k > 0 && (!a || !a_scales || !b || !b_scales))) return fail(AMP_EINVAL, kNull, fn);
+    if (misaligned(a, 16) || misaligned(a_scales, 16) || misaligned(b, 16) || misaligned(b_scales, 16))
+        return fail(AMP_EINVAL, "%s: operands must be 16-byte aligned", fn);
+    if (off_type(oc, out, residual) || off_type(bc, bias)) return fail(AMP_EINVAL, kOff, fn);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return finish(e, fn);
+    return finish(amp::launch_fp4_linear(a, u8(a_scales), b, u8(b_scales), m, n, k, bias, bc, act, residual, out, oc,
+                                         u8(q), u8(scales), dev, cu(stream), limits),
+                  fn);
+}
+
+amp_status fp4_linear_mx(const void *a, const void *a_scales, const void *b, const void *b_scales, int64_t m,
+                         int64_t n, int64_t k, const void *bias, amp_dtype bias_dtype, int32_t act,
+                         const void *residual, void *out, amp_dtype out_dtype, void *q, void *scales,
+                         amp_stream_t stream) {
+    AMP_TRACE("fp4_linear_mx");
+    return linear("fp4_linear_mx", a, a_scales, b, b_scales, m, n, k, bias, bias_dtype, act, residual, out, out_dtype,
+                  q, scales, stream, {30, 3, 0});
+}
+
+amp_status fp4_linear_mx_selftest(const void *a, const void *a_scales, const void *b, const void *b_scales, int64_t m,
+                                  int64_t n, int64_t k, const void *bias, amp_dtype bias_dtype, int32_t act,
+                                  const void *residual, void *out, amp_dtype out_dtype, void *q, void *scales,
+                                  int32_t role, int32_t stages, int32_t limit_log2_ns, amp_stream_t stream) {
+    AMP_TRACE("fp4_linear_mx_selftest");
+    const char *fn = "fp4_linear_mx_selftest";
+    if (role < 0 || role > 2 || stages < 0) return fail(AMP_EINVAL, "%s: role not in [0, 2] or stages < 0", fn);
+    if (limit_log2_ns < 0 || limit_log2_ns > 30) return fail(AMP_EINVAL, "%s: limit above 2^30 ns", fn);
+    return linear(fn, a, a_scales, b, b_scales, m, n, k, bias, bias_dtype, act, residual, out, out_dtype, q, scales,
+                  stream, {uint8_t(limit_log2_ns), uint8_t(role), uint32_t(stages)});
+}
+
+// The element codes of a tensor and of a bias gradient next to it (f32, or the tensor's).
+static bool bias_types(amp_dtype dtype, amp_dtype bias_dtype, bool bias, int &ec, int &bc) {
+    ec = elem_code(dtype);
+    bc = bias ? elem_code(bias_dtype) : int(amp::kF32);
+    return ec >= 0 && bc >= 0 && (bc == amp::kF32 || bc == ec);
+}
+// Zeros for a bias gradient over no rows.
+static amp_status no_rows(const char *fn, void *dbias, int bc, int64_t cols, cudaStream_t s) {
+    if (!dbias || cols == 0) return AMP_OK;
+    return finish(cudaMemsetAsync(dbias, 0, size_t(cols) * (bc == amp::kF32 ? 4 : 2), s), fn);
+}
+
+amp_status amp_bias_act_backward_mx8(int32_t act, const void *dy, amp_dtype dtype, int64_t rows, int64_t cols,
+                                     const void *q, const void *scales, void *dz, void *dbias, amp_dtype bias_dtype,
+                                     amp_stream_t stream) {
+    AMP_TRACE("amp_bias_act_backward_mx8");
+    const char *fn = "amp_bias_act_backward_mx8";
+    if (bad_shape(rows, cols)) return fail(AMP_EINVAL, kShape, fn);
+    int ec, bc;
+    if (!bias_types(dtype, bias_dtype, true, ec, bc)) return fail(AMP_EDTYPE, kType, fn);
+    if (!known_act(act)) return fail(AMP_EINVAL, "%s: unknown act", fn);
+    const bool none = act == AMP_ACT_NONE;
+    if (none ? (q || scales || dz) : ((q == nullptr) != (scales == nullptr)))
+        return fail(AMP_EINVAL, "%s: q, scales and dz go with an activation", fn);
+    if (cols == 0) return AMP_OK;
+    if (!dbias) return fail(AMP_EINVAL, kNull, fn);
+    if (off_type(ec, dy, dz) || off_type(bc, dbias)) return fail(AMP_EINVAL, kOff, fn);
+    if (rows == 0) return no_rows(fn, dbias, bc, cols, cu(stream));
+    if (!dy || (!none && (!q || !dz))) return fail(AMP_EINVAL, kNull, fn);
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return finish(e, fn);
+    return finish(amp::launch_bias_bwd(act, dy, ec, rows, cols, u8(q), u8(scales), dz, dbias, bc, dev, cu(stream)),
+                  fn);
+}
+
+// p as the number of 65536 that drops, or -1.
+static int64_t drop_of(double p) { return p >= 0.0 && p <= 1.0 ? int64_t(std::nearbyint(p * 65536.0)) : -1; }
+static amp_status dropout_args(const char *fn, int64_t rows, int64_t cols, double p, int32_t site) {
+    if (bad_shape(rows, cols)) return fail(AMP_EINVAL, kShape, fn);
+    if (drop_of(p) < 0) return fail(AMP_EINVAL, "%s: p must be in [0, 1]", fn);
+    if (site < 0 || site >= (1 << 30)) return fail(AMP_EINVAL, "%s: site must be in [0, 2^30)", fn);
+    return AMP_OK;
+}
+
+amp_status amp_dropout_forward(const void *x, amp_dtype dtype, int64_t rows, int64_t cols, double p, uint64_t seed,
+                               const int32_t *step_dev, int32_t site, const void *residual, void *y,
+                               amp_stream_t stream) {
+    AMP_TRACE("amp_dropout_forward");
+    const char *fn = "amp_dropout_forward";
+    const amp_status st = dropout_args(fn, rows, cols, p, site);
+    if (st != AMP_OK) return st;
+    const int ec = elem_code(dtype);
+    if (ec < 0) return fail(AMP_EDTYPE, kType, fn);
+    if (rows * cols == 0) return AMP_OK;
+    if (!x || !y) return fail(AMP_EINVAL, kNull, fn);
+    if (off_type(ec, x, residual, y) || off_type(amp::kF32, step_dev)) return fail(AMP_EINVAL, kOff, fn);
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return finish(e, fn);
+    return finish(amp::launch_dropout(x, residual, ec, rows, cols, uint32_t(drop_of(p)), seed, step_dev,
+                                      (1u << 30) + uint32_t(site), y, nullptr, amp::kF32, dev, cu(stream)),
+                  fn);
+}
+
+amp_status amp_dropout_backward(const void *dy, amp_dtype dtype, int64_t rows, int64_t cols, double p, uint64_t seed,
+                                const int32_t *step_dev, int32_t site, void *dx, void *dbias, amp_dtype bias_dtype,
+                                amp_stream_t stream) {
+    AMP_TRACE("amp_dropout_backward");
+    const char *fn = "amp_dropout_backward";
+    const amp_status st = dropout_args(fn, rows, cols, p, site);
+    if (st != AMP_OK) return st;
+    int ec, bc;
+    if (!bias_types(dtype, bias_dtype, dbias != nullptr, ec, bc)) return fail(AMP_EDTYPE, kType, fn);
+    if (off_type(ec, dy, dx) || off_type(amp::kF32, step_dev) || off_type(bc, dbias)) return fail(AMP_EINVAL, kOff, fn);
+    if (rows * cols == 0) return no_rows(fn, dbias, bc, cols, cu(stream));
+    if (!dy || !dx) return fail(AMP_EINVAL, kNull, fn);
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return finish(e, fn);
+    return finish(amp::launch_dropout(dy, nullptr, ec, rows, cols, uint32_t(drop_of(p)), seed, step_dev,
+                                      (1u << 30) + uint32_t(site), dx, dbias, bc, dev, cu(stream)),
+                  fn);
+}
+
+// A matrix whose rows lie ld elements apart.
+static bool bad_rows(int64_t rows, int64_t cols, int64_t ld) {
+    return bad_shape(rows, cols) || ld < cols || bad_shape(rows, ld);
+}
+
+amp_status amp_token_logprobs_forward(const void *z, amp_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                                      const int64_t *targets, float *logp, float *entropy, float *stats,
+                                      int64_t *top_ids, float *top_logp, int32_t top_n, amp_stream_t stream) {
+    AMP_TRACE("amp_token_logprobs_forward");
+    const char *fn = "amp_token_logprobs_forward";
+    if (bad_rows(rows, cols, ld)) return fail(AMP_EINVAL, kShape, fn);
+    const int ec = elem_code(dtype);
+    if (ec < 0) return fail(AMP_EDTYPE, kType, fn);
+    if (top_n < 0 || top_n > 32) return fail(AMP_EINVAL, "%s: top_n must be in [0, 32]", fn);
+    if ((top_ids == nullptr) != (top_logp == nullptr) || (top_n == 0 && top_ids))
+        return fail(AMP_EINVAL, "%s: top_ids, top_logp and top_n go together", fn);
+    if (rows == 0) return AMP_OK;
+    if (cols == 0) return fail(AMP_EINVAL, "%s: a row needs a logit", fn);
+    if (logp && !targets) return fail(AMP_EINVAL, "%s: logp needs targets", fn);
+    if (!z || (top_n > 0 && !top_ids)) return fail(AMP_EINVAL, kNull, fn);
+    if (off_type(ec, z) || off_type(amp::kF32, logp, entropy, stats, top_logp) || misaligned(targets, 8) ||
+        misaligned(stats, 8) || misaligned(top_ids, 8))
+        return fail(AMP_EINVAL, kOff, fn);
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return finish(e, fn);
+    return finish(amp::launch_logprobs_fwd(z, ec, rows, cols, ld, targets, logp, entropy, stats, top_ids, top_logp,
+                                           top_n, dev, cu(stream)),
+                  fn);
+}
+
+amp_status amp_token_logprobs_backward(const float *dlogp, const void *z, amp_dtype dtype, int64_t rows, int64_t cols,
+                                       int64_t ld, const int64_t *targets, const float *stats, const float *entropy,
+                                       const float *dentropy, const float *scale_dev, void *dz, int64_t dld,
+                                       amp_stream_t stream) {
+    AMP_TRACE("amp_token_logprobs_backward");
+    const char *fn = "amp_token_logprobs_backward";
+    if (bad_rows(rows, cols, ld) || bad_rows(rows, cols, dld)) return fail(AMP_EINVAL, kShape, fn);
+    const int ec = elem_code(dtype);
+    if (ec < 0) return fail(AMP_EDTYPE, kType, fn);
+    if (rows * cols == 0) return AMP_OK;
+    if (dlogp && !targets) return fail(AMP_EINVAL, "%s: dlogp needs targets", fn);
+    if (dentropy && !entropy) return fail(AMP_EINVAL, "%s: dentropy needs the entropy", fn);
+    if (!z || !stats || !dz) return fail(AMP_EINVAL, kNull, fn);
+    if (dz == z && dld != ld) return fail(AMP_EINVAL, "%s: in place, the rows need one stride", fn);
+    if (off_type(ec, z, dz) || off_type(amp::kF32, dlogp, entropy, dentropy, scale_dev) || misaligned(targets, 8) ||
+        misaligned(stats, 8))
+        return fail(AMP_EINVAL, kOff, fn);
+    return finish(amp::launch_logprobs_bwd(z, ec, rows, cols, ld, targets, stats, dlogp, entropy, dentropy, scale_dev,
+                                           dz, dld, cu(stream)),
                   fn);
 }
 

@@ -36,6 +36,12 @@ struct Entries {
     decltype(&amp_act_backward_mx8) act_backward;
     decltype(&amp_ckpt8_save) save;
     decltype(&amp_ckpt8_restore) restore;
+    decltype(&fp4_linear_mx) linear;
+    decltype(&amp_bias_act_backward_mx8) bias_act_backward;
+    decltype(&amp_dropout_forward) dropout_forward;
+    decltype(&amp_dropout_backward) dropout_backward;
+    decltype(&amp_token_logprobs_forward) logprobs_forward;
+    decltype(&amp_token_logprobs_backward) logprobs_backward;
 } g{};
 
 struct Refused {
@@ -175,6 +181,68 @@ struct Params {
     }
 };
 
+// One vector of n elements next to a matrix (None: NULL and f32): a bias or its gradient.
+struct Vector {
+    void *p = nullptr;
+    amp_dtype type = AMP_DT_F32;
+    Vector(PyObject *o, const char *what, const Matrix &m) {
+        if (o == Py_None) return;
+        const at::Tensor &t = tensor(o, what);
+        if (t.numel() != m.cols)
+            refuse(std::string(what) + ": " + std::to_string(t.numel()) + " elements, " + std::to_string(m.cols) +
+                   " needed");
+        type = elem(t, what);
+        p = address(t, what, m.cols, m.device);
+    }
+};
+
+// A matrix whose rows may lie apart, `ld` elements from one to the next (leading
+// dimensions have to be rows of one stride).
+struct Rows {
+    const at::Tensor &t;
+    int64_t rows = 1, cols, ld, device;
+    amp_dtype type;
+    Rows(PyObject *o, const char *what) : t(tensor(o, what)) {
+        const auto s = t.sizes(), st = t.strides();
+        if (s.empty()) refuse(std::string(what) + ": needs at least one dimension");
+        cols = ld = s.back();
+        bool fits = t.is_cuda() && (st.back() == 1 || cols <= 1);
+        int64_t next = -1;  // the stride that the next dimension to the left has to have
+        for (size_t i = s.size() - 1; i-- > 0;) {
+            rows *= s[i];
+            if (s[i] <= 1) continue;
+            if (next < 0) ld = st[i];
+            else if (st[i] != next) fits = false;
+            next = st[i] * s[i];
+        }
+        if (!fits || (rows > 1 && ld < cols))
+            refuse(std::string(what) + ": needs a CUDA tensor with contiguous rows, one stride apart");
+        type = elem(t, what);
+        device = t.get_device();
+    }
+    // the call's vectors of n elements a row
+    void *of(PyObject *o, const char *what, int64_t n, at::ScalarType type) const {
+        return typed_on(o, what, rows * n, type, device);
+    }
+};
+
+uint64_t seed_of(PyObject *o) {
+    const uint64_t v = PyLong_Check(o) ? PyLong_AsUnsignedLongLong(o) : 0;
+    if (!PyLong_Check(o) || PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse("seed: needs a whole number in [0, 2^64)");
+    }
+    return v;
+}
+int32_t site_of(PyObject *o) {
+    const long v = PyLong_Check(o) ? PyLong_AsLong(o) : -1;
+    if (v < 0 || v >= (1l << 30)) {
+        PyErr_Clear();
+        refuse("site: needs a whole number in [0, 2^30)");
+    }
+    return int32_t(v);
+}
+
 amp_act act_of(PyObject *o) {
     const char *s = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : nullptr;
     if (s && !std::strcmp(s, "gelu")) return AMP_ACT_GELU;
@@ -183,6 +251,7 @@ amp_act act_of(PyObject *o) {
     PyErr_Clear();
     refuse(std::string("activation '") + (s ? s : "?") + "'; one of ['gelu', 'gelu_tanh', 'silu']");
 }
+int32_t act_or_none(PyObject *o) { return o == Py_None ? int32_t(AMP_ACT_NONE) : int32_t(act_of(o)); }
 double number(PyObject *o, const char *what) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) {
@@ -216,6 +285,20 @@ struct Unlocked {
 
 using Args = PyObject *const *;
 
+int64_t reduction(PyObject *o) {
+    const int64_t k = PyLong_Check(o) ? PyLong_AsLongLong(o) : -1;
+    if (k < 0 || k > (int64_t(1) << 32)) {  // sizes are formed in 64 bits
+        PyErr_Clear();
+        PyObject *s = PyObject_Str(o);
+        const char *c = s ? PyUnicode_AsUTF8(s) : nullptr;
+        const std::string why = std::string("k = ") + (c ? c : "?");
+        Py_XDECREF(s);
+        PyErr_Clear();
+        refuse(why);
+    }
+    return k;
+}
+
 PyObject *quant(PyObject *, Args a, Py_ssize_t n) {  // x, q, scales, qt, scales_t, skip_if, stream
     return call(n, 7, g.quant, [&]() {
         const Matrix x(a[0], "x");
@@ -245,16 +328,7 @@ PyObject *dequant(PyObject *, Args a, Py_ssize_t n) {  // q, scales, out, stream
 }
 PyObject *product(PyObject *, Args a, Py_ssize_t n) {  // a, a_scales, b, b_scales, k, out, stream
     return call(n, 7, g.product, [&]() {
-        const int64_t k = PyLong_Check(a[4]) ? PyLong_AsLongLong(a[4]) : -1;
-        if (k < 0 || k > (int64_t(1) << 32)) {  // sizes below are formed in 64 bits
-            PyErr_Clear();
-            PyObject *s = PyObject_Str(a[4]);
-            const char *c = s ? PyUnicode_AsUTF8(s) : nullptr;
-            const std::string why = std::string("k = ") + (c ? c : "?");
-            Py_XDECREF(s);
-            PyErr_Clear();
-            refuse(why);
-        }
+        const int64_t k = reduction(a[4]);
         const Matrix o(a[5], "out");
         void *out = o.p();
         void *pa = o.bytes(a[0], "a", fp4_bytes(o.rows, k)), *sa = o.bytes(a[1], "a_scales", fp4_scales(o.rows, k));
@@ -356,15 +430,125 @@ PyObject *restore(PyObject *, Args a, Py_ssize_t n) {  // q, scales, out, stream
     });
 }
 
-// bind(addresses of the nine entry points, in the order of Entries)
+// a, a_scales, b, b_scales, k, out, bias, kind, residual, saved, stream
+PyObject *linear(PyObject *, Args a, Py_ssize_t n) {
+    return call(n, 11, g.linear, [&]() {
+        const int64_t k = reduction(a[4]);
+        const int32_t act = act_or_none(a[7]);
+        const Matrix o(a[5], "out");
+        void *out = o.p();
+        void *pa = o.bytes(a[0], "a", fp4_bytes(o.rows, k)), *sa = o.bytes(a[1], "a_scales", fp4_scales(o.rows, k));
+        void *pb = o.bytes(a[2], "b", fp4_bytes(o.cols, k)), *sb = o.bytes(a[3], "b_scales", fp4_scales(o.cols, k));
+        const Vector bias(a[6], "bias", o);
+        const void *res = o.like(a[8], "residual");
+        const Saved c(a[9], "saved", o);
+        const OnDevice on(o.device);
+        const amp_stream_t stream = stream_of(a[10]);
+        Unlocked u;
+        return g.linear(pa, sa, pb, sb, o.rows, o.cols, k, bias.p, bias.type, act, res, out, o.type, c.q, c.s, stream);
+    });
+}
+PyObject *bias_act_backward(PyObject *, Args a, Py_ssize_t n) {  // dy, dbias, kind, saved, dx, stream
+    return call(n, 6, g.bias_act_backward, [&]() {
+        const int32_t act = act_or_none(a[2]);
+        const Matrix dy(a[0], "dy");
+        const void *p = dy.p();
+        const Vector db(a[1], "dbias", dy);
+        const Saved c(a[3], "saved", dy);
+        void *dx = dy.like(a[4], "dx");
+        const OnDevice on(dy.device);
+        const amp_stream_t stream = stream_of(a[5]);
+        Unlocked u;
+        return g.bias_act_backward(act, p, dy.type, dy.rows, dy.cols, c.q, c.s, dx, db.p, db.type, stream);
+    });
+}
+PyObject *dropout_forward(PyObject *, Args a, Py_ssize_t n) {  // x, p, seed, site, y, residual, step, stream
+    return call(n, 8, g.dropout_forward, [&]() {
+        const double p = number(a[1], "p");
+        const uint64_t seed = seed_of(a[2]);
+        const int32_t site = site_of(a[3]);
+        const Matrix x(a[0], "x");
+        const void *px = x.p();
+        void *y = x.like(a[4], "y");
+        const void *res = x.like(a[5], "residual");
+        const auto *step = static_cast<const int32_t *>(x.typed(a[6], "step", 1, at::kInt));
+        const OnDevice on(x.device);
+        const amp_stream_t stream = stream_of(a[7]);
+        Unlocked u;
+        return g.dropout_forward(px, x.type, x.rows, x.cols, p, seed, step, site, res, y, stream);
+    });
+}
+PyObject *dropout_backward(PyObject *, Args a, Py_ssize_t n) {  // dy, p, seed, site, dx, step, dbias, stream
+    return call(n, 8, g.dropout_backward, [&]() {
+        const double p = number(a[1], "p");
+        const uint64_t seed = seed_of(a[2]);
+        const int32_t site = site_of(a[3]);
+        const Matrix dy(a[0], "dy");
+        const void *pd = dy.p();
+        void *dx = dy.like(a[4], "dx");
+        const auto *step = static_cast<const int32_t *>(dy.typed(a[5], "step", 1, at::kInt));
+        const Vector db(a[6], "dbias", dy);
+        const OnDevice on(dy.device);
+        const amp_stream_t stream = stream_of(a[7]);
+        Unlocked u;
+        return g.dropout_backward(pd, dy.type, dy.rows, dy.cols, p, seed, step, site, dx, db.p, db.type, stream);
+    });
+}
+// logits, targets, logp, entropy, stats, top_ids, top_logp, stream
+PyObject *logprobs_forward(PyObject *, Args a, Py_ssize_t n) {
+    return call(n, 8, g.logprobs_forward, [&]() {
+        const Rows z(a[0], "logits");
+        const auto *t = static_cast<const int64_t *>(z.of(a[1], "targets", 1, at::kLong));
+        auto *logp = static_cast<float *>(z.of(a[2], "logp", 1, at::kFloat));
+        auto *ent = static_cast<float *>(z.of(a[3], "entropy", 1, at::kFloat));
+        auto *stats = static_cast<float *>(z.of(a[4], "stats", 2, at::kFloat));
+        int64_t top = 0;
+        if (a[5] != Py_None) {
+            const at::Tensor &ids = tensor(a[5], "top_ids");
+            if (ids.dim() < 1) refuse("top_ids: needs at least one dimension");
+            top = ids.size(-1);
+            if (top < 1 || top > 32) refuse("top_ids: 1 to 32 alternatives a row");
+        }
+        auto *ids = static_cast<int64_t *>(z.of(a[5], "top_ids", top, at::kLong));
+        auto *lp = static_cast<float *>(z.of(a[6], "top_logp", top, at::kFloat));
+        const OnDevice on(z.device);
+        const amp_stream_t stream = stream_of(a[7]);
+        Unlocked u;
+        return g.logprobs_forward(z.t.data_ptr(), z.type, z.rows, z.cols, z.ld, t, logp, ent, stats, ids, lp,
+                                  int32_t(top), stream);
+    });
+}
+// dlogp, logits, targets, stats, dlogits, entropy, dentropy, scale, stream
+PyObject *logprobs_backward(PyObject *, Args a, Py_ssize_t n) {
+    return call(n, 9, g.logprobs_backward, [&]() {
+        const Rows z(a[1], "logits"), dz(a[4], "dlogits");
+        if (dz.rows != z.rows || dz.cols != z.cols || dz.type != z.type)
+            refuse("dlogits: needs the shape and dtype of logits");
+        if (dz.device != z.device)
+            refuse("dlogits: on cuda:" + std::to_string(dz.device) + ", the call is on cuda:" + std::to_string(z.device));
+        const auto *dlogp = static_cast<const float *>(z.of(a[0], "dlogp", 1, at::kFloat));
+        const auto *t = static_cast<const int64_t *>(z.of(a[2], "targets", 1, at::kLong));
+        const auto *stats = static_cast<const float *>(z.of(a[3], "stats", 2, at::kFloat));
+        const auto *ent = static_cast<const float *>(z.of(a[5], "entropy", 1, at::kFloat));
+        const auto *dent = static_cast<const float *>(z.of(a[6], "dentropy", 1, at::kFloat));
+        const auto *scale = static_cast<const float *>(typed_on(a[7], "scale", 1, at::kFloat, z.device));
+        const OnDevice on(z.device);
+        const amp_stream_t stream = stream_of(a[8]);
+        Unlocked u;
+        return g.logprobs_backward(dlogp, z.t.data_ptr(), z.type, z.rows, z.cols, z.ld, t, stats, ent, dent, scale,
+                                   dz.t.data_ptr(), dz.ld, stream);
+    });
+}
+
+// bind(addresses of the fifteen entry points, in the order of Entries)
 PyObject *bind(PyObject *, Args a, Py_ssize_t n) {
-    void *p[9];
+    void *p[15];
     static_assert(sizeof(p) == sizeof(Entries), "entries");
-    if (n != 9) {
-        PyErr_SetString(PyExc_TypeError, "nine addresses");
+    if (n != 15) {
+        PyErr_SetString(PyExc_TypeError, "fifteen addresses");
         return nullptr;
     }
-    for (int i = 0; i < 9; ++i) {
+    for (int i = 0; i < 15; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -376,7 +560,9 @@ PyObject *bind(PyObject *, Args a, Py_ssize_t n) {
     { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {METHOD(bind), METHOD(quant), METHOD(dequant), METHOD(product), METHOD(norm_forward),
                          METHOD(norm_backward), METHOD(act_forward), METHOD(act_backward), METHOD(save),
-                         METHOD(restore), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(restore), METHOD(linear), METHOD(bias_act_backward), METHOD(dropout_forward),
+                         METHOD(dropout_backward), METHOD(logprobs_forward), METHOD(logprobs_backward),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

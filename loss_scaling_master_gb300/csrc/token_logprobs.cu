@@ -1,0 +1,446 @@
+// token_logprobs.cu - log probabilities of given tokens, the entropy of each row
+// and its most probable tokens; and the gradient at the logits.
+//
+//   m = max z, s = sum exp(z - m), w = sum exp(z - m) (z - m)
+//   log p_j = (z_j - m) - log s,  H = log s - w / s
+//   dz_j = S (dlogp (1[j = t] - p_j) - dent p_j (log p_j + H))
+//
+// Forward.  The logits are read once: each thread keeps a running maximum and the
+// two sums relative to it, which are rescaled when the maximum grows, at most once
+// for four 16-byte loads.  The most probable tokens are kept by warps, an entry a
+// lane in order; the maximum of the four loads, needed anyway, tells whether any of
+// their elements can enter, which after the first loads is rare.  Few rows are cut
+// over the CTAs of a cluster, whose results the first of them joins from shared
+// memory.
+//
+// Every row starts where its address lies: a first and a last piece of less than 16
+// bytes are taken by single elements, padded with -inf, which adds nothing.
+#include <algorithm>
+
+#include "internal.h"
+#include "mx.cuh"
+#include "pdl.cuh"
+#include "tcgen05.cuh"
+
+namespace amp {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.402823466e+38f;
+constexpr int kMaxTop = 32;
+constexpr int kLoads = 4;  // 16-byte loads a thread has in flight
+
+struct LogprobsFwd {
+    const void *z;
+    const int64_t *t;
+    float *logp, *ent;
+    float2 *stats;  // m, log s
+    int64_t *ids;
+    float *top;
+    int64_t rows, ld;
+    int cols, k;
+};
+
+__device__ __forceinline__ float exp2_flush(float u) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(u));
+    return r;
+}
+
+// A row in pieces of 16 bytes: piece i holds the elements base + i * VN and on, of
+// which those in [0, cols) exist; only the first and the last may lack some.
+template <int XT>
+struct Pieces {
+    static constexpr int VN = XT == kF32 ? 4 : 8;
+    const char *row;
+    int base, count, cols;
+    __device__ __forceinline__ Pieces(const void *z, int64_t at, int cols_) : cols(cols_) {
+        constexpr int esz = XT == kF32 ? 4 : 2;
+        row = static_cast<const char *>(z) + at * esz;
+        const int past = int(reinterpret_cast<uintptr_t>(row) & 15) / esz;
+        base = -past;
+        count = int((int64_t(cols) + past + VN - 1) / VN);
+    }
+    __device__ __forceinline__ int first(int i) const { return base + i * VN; }
+    __device__ __forceinline__ bool whole(int i) const { return first(i) >= 0 && first(i) <= cols - VN; }
+    // the raw words; -inf for what does not exist
+    __device__ __forceinline__ uint4 load(int i) const {
+        constexpr uint32_t none = XT == kF32 ? 0xFF800000u : XT == kF16 ? 0xFC00FC00u : 0xFF80FF80u;
+        uint4 u = make_uint4(none, none, none, none);
+        if (i >= count) return u;
+        const int f = first(i);
+        if (whole(i)) return ld16(row + int64_t(f) * (XT == kF32 ? 4 : 2));
+        uint32_t w[4] = {none, none, none, none};
+#pragma unroll
+        for (int e = 0; e < VN; ++e) {
+            if (f + e < 0 || f + e >= cols) continue;
+            if constexpr (XT == kF32) {
+                w[e] = reinterpret_cast<const uint32_t *>(row)[f + e];
+            } else {
+                const uint32_t v = reinterpret_cast<const uint16_t *>(row)[f + e];
+                w[e / 2] = e % 2 ? (w[e / 2] & 0xFFFFu) | (v << 16) : (w[e / 2] & 0xFFFF0000u) | v;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+template <int XT>
+__device__ __forceinline__ void widen(uint4 u, float (&y)[XT == kF32 ? 4 : 8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (XT == kF32) {
+            y[j] = __uint_as_float(w[j]);
+        } else if constexpr (XT == kBF16) {
+            y[2 * j] = __uint_as_float(w[j] << 16);
+            y[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        } else {
+            y[2 * j] = f16_bits_to_f32(w[j] & 0xFFFFu);
+            y[2 * j + 1] = f16_bits_to_f32(w[j] >> 16);
+        }
+    }
+}
+// Largest of a piece's elements, NaN aside.
+template <int XT>
+__device__ __forceinline__ float largest(uint4 u) {
+    if constexpr (XT == kF32) {
+        return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)),
+                     fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+    } else {
+        uint32_t a, b, c;
+        if constexpr (XT == kF16) {
+            asm("max.f16x2 %0, %1, %2;" : "=r"(a) : "r"(u.x), "r"(u.y));
+            asm("max.f16x2 %0, %1, %2;" : "=r"(b) : "r"(u.z), "r"(u.w));
+            asm("max.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+        } else {
+            asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(u.x), "r"(u.y));
+            asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(u.z), "r"(u.w));
+            asm("max.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+        }
+        return fmaxf(lowp_to_f32<XT>(c & 0xFFFFu), lowp_to_f32<XT>(c >> 16));
+    }
+}
+
+// Differences are taken no lower than this in factors (its exponential is 0), so
+// that a zero weight never meets an infinity.
+constexpr float kFar = -1e4f;
+
+// The running maximum and the sums relative to it.  A NaN reaches the sums.
+struct Sums {
+    float m = kLowest, s = 0.0f, w = 0.0f;
+    __device__ __forceinline__ void raise(float to) {  // to >= m
+        const float d = fmaxf(m - to, kFar), c = exp2_flush(d * kLog2e);
+        w = __fmaf_rn(s, d, w) * c;
+        s *= c;
+        m = to;
+    }
+    template <bool ENT>
+    __device__ __forceinline__ void add(float z) {
+        const float d = z - m, e = exp2_flush(d * kLog2e);
+        s += e;
+        if (ENT) w = __fmaf_rn(e, fmaxf(d, kFar), w);
+    }
+    __device__ __forceinline__ void join(float m2, float s2, float w2) {
+        raise(fmaxf(m, m2));
+        const float d = fmaxf(m2 - m, kFar), c = exp2_flush(d * kLog2e);
+        s = __fmaf_rn(s2, c, s);
+        w = __fmaf_rn(__fmaf_rn(s2, d, w2), c, w);
+    }
+};
+
+// An alternative: larger first, of equals the lower index.
+struct Entry {
+    float v;
+    int i;
+};
+__device__ __forceinline__ bool before(float v, int i, Entry b) { return v > b.v || (v == b.v && i < b.i); }
+
+// A warp's k best, lane l the l-th; k - 1 is the bound to pass.
+struct Best {
+    Entry mine{-INFINITY, -1};
+    // one candidate, the same on all lanes
+    __device__ __forceinline__ void insert(float v, int i) {
+        const int lane = threadIdx.x & 31;
+        const bool stays = !before(v, i, mine);
+        const int at = __popc(__ballot_sync(0xFFFFFFFFu, stays));  // lanes that stay come first
+        const float uv = __shfl_up_sync(0xFFFFFFFFu, mine.v, 1);
+        const int ui = __shfl_up_sync(0xFFFFFFFFu, mine.i, 1);
+        if (lane > at) mine = {uv, ui};
+        if (lane == at) mine = {v, i};
+    }
+    __device__ __forceinline__ Entry last(int k) const {
+        return {__shfl_sync(0xFFFFFFFFu, mine.v, k - 1), __shfl_sync(0xFFFFFFFFu, mine.i, k - 1)};
+    }
+    // a candidate of each lane
+    __device__ __forceinline__ void offer(float v, int i, int k) {
+        Entry b = last(k);
+        uint32_t in = __ballot_sync(0xFFFFFFFFu, before(v, i, b));
+        while (in) {
+            const int src = __ffs(in) - 1;
+            insert(__shfl_sync(0xFFFFFFFFu, v, src), __shfl_sync(0xFFFFFFFFu, i, src));
+            b = last(k);
+            in &= ~(1u << src);
+            in &= __ballot_sync(0xFFFFFFFFu, before(v, i, b));
+        }
+    }
+    // the pieces of the lanes whose largest element reaches the bound
+    template <int XT>
+    __device__ __forceinline__ void offer_piece(uint4 u, int first, int k) {
+        constexpr int VN = Pieces<XT>::VN;
+        const int lane = threadIdx.x & 31;
+        const float big = largest<XT>(u);
+        Entry b = last(k);
+        uint32_t hits = __ballot_sync(0xFFFFFFFFu, big >= b.v && big > -INFINITY);
+        while (hits) {
+            const int src = __ffs(hits) - 1;
+            hits &= hits - 1;
+            const uint4 x = make_uint4(__shfl_sync(0xFFFFFFFFu, u.x, src), __shfl_sync(0xFFFFFFFFu, u.y, src),
+                                       __shfl_sync(0xFFFFFFFFu, u.z, src), __shfl_sync(0xFFFFFFFFu, u.w, src));
+            const int f = __shfl_sync(0xFFFFFFFFu, first, src);
+            float y[VN], v = -INFINITY;
+            widen<XT>(x, y);
+#pragma unroll
+            for (int e = 0; e < VN; ++e)
+                if (lane == e) v = y[e];
+            // what is not there is -inf, which never enters
+            offer(v, v > -INFINITY ? f + lane : INT32_MAX, k);
+        }
+    }
+};
+
+template <int XT, int THREADS, bool TOP>
+__global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
+    constexpr int WARPS = THREADS / 32, VN = Pieces<XT>::VN;
+    __shared__ float s_m[WARPS], s_s[WARPS], s_w[WARPS];
+    __shared__ Entry s_top[TOP ? WARPS : 1][kMaxTop];
+    __shared__ float3 s_cta;
+    pdl_wait();
+    pdl_trigger();
+    uint32_t parts;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
+    const uint32_t rank = parts > 1 ? cluster_rank() : 0;
+    const int64_t r = int64_t(blockIdx.x / parts);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = P.t ? P.t[r] : 0;
+    if (P.t && t < 0) {  // the same in all CTAs of the cluster
+        if (rank == 0) {
+            if (threadIdx.x == 0) {
+                if (P.logp) P.logp[r] = 0.0f;
+                if (P.ent) P.ent[r] = 0.0f;
+                if (P.stats) P.stats[r] = make_float2(0.0f, 0.0f);
+            }
+            if (TOP && threadIdx.x < unsigned(P.k)) {
+                P.ids[r * P.k + threadIdx.x] = -1;
+                P.top[r * P.k + threadIdx.x] = -INFINITY;
+            }
+        }
+        return;
+    }
+    const Pieces<XT> row(P.z, r * P.ld, P.cols);
+    Sums a;
+    Best best;
+    const int step = int(parts) * THREADS;
+    for (int i0 = int(rank) * THREADS; i0 < row.count; i0 += kLoads * step) {
+        uint4 u[kLoads];
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) u[j] = row.load(i0 + j * step + int(threadIdx.x));
+        float big = a.m;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) big = fmaxf(big, largest<XT>(u[j]));
+        a.raise(big);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            float y[VN];
+            widen<XT>(u[j], y);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) a.add<true>(y[e]);
+        }
+        if constexpr (TOP) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                best.offer_piece<XT>(u[j], row.first(i0 + j * step + int(threadIdx.x)), P.k);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        a.join(__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
+               __shfl_xor_sync(0xFFFFFFFFu, a.w, o));
+    if (lane == 0) {
+        s_m[warp] = a.m;
+        s_s[warp] = a.s;
+        s_w[warp] = a.w;
+    }
+    if (TOP) s_top[warp][lane] = best.mine;
+    __syncthreads();
+    if (warp == 0) {
+        a = Sums();
+        for (int w = 0; w < WARPS; ++w) a.join(s_m[w], s_s[w], s_w[w]);
+        if (TOP) {
+            for (int w = 1; w < WARPS; ++w) {
+                const Entry e = s_top[w][lane];
+                best.offer(lane < P.k ? e.v : -INFINITY, lane < P.k && e.v > -INFINITY ? e.i : INT32_MAX, P.k);
+            }
+            __syncwarp();
+            s_top[0][lane] = best.mine;
+        }
+        if (lane == 0) s_cta = make_float3(a.m, a.s, a.w);
+    }
+    if (parts > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (rank == 0 && warp == 0) {
+            for (uint32_t q = 1; q < parts; ++q) {
+                const uint32_t at = cluster_addr(&s_cta, q);
+                a.join(__uint_as_float(cluster_ld(at)), __uint_as_float(cluster_ld(at + 4)),
+                       __uint_as_float(cluster_ld(at + 8)));
+                if (TOP) {
+                    const uint32_t e = cluster_addr(&s_top[0][lane], q);
+                    const float v = __uint_as_float(cluster_ld(e));
+                    const int i = int(cluster_ld(e + 4));
+                    best.offer(lane < P.k ? v : -INFINITY, lane < P.k && v > -INFINITY ? i : INT32_MAX, P.k);
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // nobody leaves while its shared memory is read
+    }
+    if (rank != 0 || warp != 0) return;
+    const float logs = logf(a.s);
+    if (lane == 0) {
+        if (P.logp)
+            P.logp[r] = !P.t ? 0.0f
+                        : t >= P.cols ? NAN
+                                      : (load_elem<XT>(P.z, r * P.ld + t) - a.m) - logs;
+        if (P.ent) P.ent[r] = logs - a.w / a.s;
+        if (P.stats) P.stats[r] = make_float2(a.m, logs);
+    }
+    if (TOP && lane < P.k) {
+        P.ids[r * P.k + lane] = best.mine.i;
+        P.top[r * P.k + lane] = best.mine.v == -INFINITY ? -INFINITY : (best.mine.v - a.m) - logs;
+    }
+}
+
+// ------------------------------------------------------------------ the gradient
+struct LogprobsBwd {
+    const void *z;
+    const int64_t *t;
+    const float2 *stats;
+    const float *dlogp, *ent, *dent, *scale;
+    void *dz;
+    int64_t rows, ld, dld;
+    int cols, chunks;
+};
+
+// One CTA a share of a row: every element is read and written once, and what the row
+// adds are five numbers.  With u = log p:
+//   dz = p (A + B u) [+ S dlogp for the token],  A = -S (dlogp + dent H), B = -S dent
+template <int XT, int THREADS>
+__global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(LogprobsBwd P) {
+    constexpr int VN = Pieces<XT>::VN, esz = XT == kF32 ? 4 : 2;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t r = blockIdx.x / unsigned(P.chunks);
+    const int chunk = int(blockIdx.x - unsigned(r) * unsigned(P.chunks));
+    const Pieces<XT> row(P.z, r * P.ld, P.cols);
+    char *out = static_cast<char *>(P.dz) + r * P.dld * esz;
+    const bool aligned = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.row)) & 15) == 0;
+    const int64_t t = P.t ? P.t[r] : 0;
+    const bool used = t >= 0;
+    const int i0 = chunk * (kLoads * THREADS) + int(threadIdx.x);
+    uint4 u[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) u[j] = used ? row.load(i0 + j * THREADS) : make_uint4(0, 0, 0, 0);
+    const float scale = P.scale ? *P.scale : 1.0f;
+    const float dlogp = P.dlogp && used ? P.dlogp[r] * scale : 0.0f;
+    const float dent = P.dent && used ? P.dent[r] * scale : 0.0f;
+    const float2 st = P.stats[r];
+    const float B = -dent, BH = P.dent ? B * P.ent[r] : 0.0f;
+    float A = BH - dlogp;
+    if (t >= P.cols && P.t) A = NAN;
+    const int at = P.dlogp && used && t < P.cols ? int(t) : -1;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+        const int i = i0 + j * THREADS;
+        if (i >= row.count) break;
+        const int f = row.first(i);
+        float y[VN];
+        if (used) {
+            widen<XT>(u[j], y);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) {
+                const float lp = (y[e] - st.x) - st.y, p = exp2_flush(lp * kLog2e);
+                y[e] = p * __fmaf_rn(B, fmaxf(lp, kFar), A);
+                if (f + e == at)  // dlogp (1 - p), without the difference's rounding where p is near 1
+                    y[e] = __fmaf_rn(-dlogp, expm1f(lp), p * __fmaf_rn(B, fmaxf(lp, kFar), BH));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < VN; ++e) y[e] = 0.0f;
+        }
+        if (aligned && row.whole(i)) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (XT == kF32) w[q] = __float_as_uint(y[q]);
+                else w[q] = f32x2_to_16x2<XT>(y[2 * q], y[2 * q + 1]);
+            }
+            st16(out + int64_t(f) * esz, make_uint4(w[0], w[1], w[2], w[3]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < VN; ++e)
+                if (f + e >= 0 && f + e < P.cols) store_elem<XT>(out, f + e, y[e]);
+        }
+    }
+}
+
+template <int XT, int THREADS, bool TOP>
+cudaError_t fwd(const LogprobsFwd &P, int parts, cudaStream_t s) {
+    return launch_pdl_cluster(logprobs_fwd_kernel<XT, THREADS, TOP>, dim3(unsigned(P.rows * parts)), dim3(THREADS), 0,
+                              parts, s, P);
+}
+template <int XT>
+cudaError_t fwd_x(const LogprobsFwd &P, int device, cudaStream_t s) {
+    const int pieces = P.cols / Pieces<XT>::VN + 1, sms = sm_count(device);
+    if (pieces <= 1024 && P.rows >= sms)
+        return P.k ? fwd<XT, 128, true>(P, 1, s) : fwd<XT, 128, false>(P, 1, s);
+    int parts = 1;
+    while (parts < 8 && P.rows * parts * 2 <= 2 * sms && pieces > parts * 512) parts *= 2;
+    return P.k ? fwd<XT, 512, true>(P, parts, s) : fwd<XT, 512, false>(P, parts, s);
+}
+template <int XT>
+cudaError_t bwd_x(LogprobsBwd P, cudaStream_t s) {
+    constexpr int VN = Pieces<XT>::VN;
+    const int64_t pieces = P.cols / VN + 2;  // a row that starts inside a piece has one more
+    if (pieces <= 512) {
+        P.chunks = int((pieces + 4 * 128 - 1) / (4 * 128));
+        return launch_pdl(logprobs_bwd_kernel<XT, 128>, dim3(unsigned(P.rows * P.chunks)), dim3(128), 0, s, P);
+    }
+    P.chunks = int((pieces + 4 * 256 - 1) / (4 * 256));
+    return launch_pdl(logprobs_bwd_kernel<XT, 256>, dim3(unsigned(P.rows * P.chunks)), dim3(256), 0, s, P);
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs_fwd(const void *z, int elem, int64_t rows, int64_t cols, int64_t ld, const int64_t *t,
+                                float *logp, float *ent, float *stats, int64_t *ids, float *top, int k, int device,
+                                cudaStream_t s) {
+    const LogprobsFwd P{z, t, logp, ent, reinterpret_cast<float2 *>(stats), ids, top, rows, ld, int(cols), k};
+    const cudaError_t e = elem == kF32   ? fwd_x<kF32>(P, device, s)
+                          : elem == kF16 ? fwd_x<kF16>(P, device, s)
+                                         : fwd_x<kBF16>(P, device, s);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_logprobs_bwd(const void *z, int elem, int64_t rows, int64_t cols, int64_t ld, const int64_t *t,
+                                const float *stats, const float *dlogp, const float *ent, const float *dent,
+                                const float *scale, void *dz, int64_t dld, cudaStream_t s) {
+    const LogprobsBwd P{z, t, reinterpret_cast<const float2 *>(stats), dlogp, ent, dent, scale, dz, rows, ld, dld,
+                        int(cols), 1};
+    const cudaError_t e = elem == kF32   ? bwd_x<kF32>(P, s)
+                          : elem == kF16 ? bwd_x<kF16>(P, s)
+                                         : bwd_x<kBF16>(P, s);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace amp

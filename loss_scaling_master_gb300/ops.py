@@ -1,6 +1,6 @@
 """The forward/backward operators (declared in include/ampops.h): microscaled
-4-bit quantisation and products, layer norm, and activations whose inputs are
-kept in 8 bits.
+4-bit quantisation, products and linear layers, layer norm, activations whose
+inputs are kept in 8 bits, dropout, and log probabilities of tokens.
 
 As in ``_lib``: argument marshalling only, here by ``csrc/ops_bind.cpp`` (built
 into ``_ops_bind.so``), because the smallest of these calls take microseconds.
@@ -24,11 +24,15 @@ from ._lib import P, _check, _stream
 EXPORTS = ("fp4_mx_bytes", "fp4_mx_scale_bytes", "fp4_quant_mx", "fp4_dequant_mx",
            "fp4_product_mx", "fp4_mx_check", "fp4_product_mx_selftest", "amp_layer_norm_forward",
            "amp_layer_norm_workspace_bytes", "amp_layer_norm_backward", "amp_act_forward_mx8",
-           "amp_act_backward_mx8", "amp_ckpt8_save", "amp_ckpt8_restore")
+           "amp_act_backward_mx8", "amp_ckpt8_save", "amp_ckpt8_restore", "fp4_linear_mx",
+           "fp4_linear_mx_selftest", "amp_bias_act_backward_mx8", "amp_dropout_forward",
+           "amp_dropout_backward", "amp_token_logprobs_forward", "amp_token_logprobs_backward")
 # those that _ops_bind calls, in the order it takes their addresses
 _BOUND = ("fp4_quant_mx", "fp4_dequant_mx", "fp4_product_mx", "amp_layer_norm_forward",
           "amp_layer_norm_backward", "amp_act_forward_mx8", "amp_act_backward_mx8",
-          "amp_ckpt8_save", "amp_ckpt8_restore")
+          "amp_ckpt8_save", "amp_ckpt8_restore", "fp4_linear_mx", "amp_bias_act_backward_mx8",
+          "amp_dropout_forward", "amp_dropout_backward", "amp_token_logprobs_forward",
+          "amp_token_logprobs_backward")
 
 _library = None
 _native = None
@@ -40,7 +44,7 @@ def _load():
     if _library is not None:
         return _library
     L = A.load()
-    i32, i64, dbl = ctypes.c_int, ctypes.c_int64, ctypes.c_double
+    i32, i64, dbl, u64 = ctypes.c_int, ctypes.c_int64, ctypes.c_double, ctypes.c_uint64
     L.fp4_mx_bytes.argtypes = [i64, i64]
     L.fp4_mx_scale_bytes.argtypes = [i64, i64]
     L.fp4_quant_mx.argtypes = [P, i32, i64, i64, P, P, P, P, P, P]
@@ -55,6 +59,14 @@ def _load():
     L.amp_act_backward_mx8.argtypes = [i32, P, i32, i64, i64, P, P, P, P, P, P, P]
     L.amp_ckpt8_save.argtypes = [P, i32, i64, i64, P, P, P]
     L.amp_ckpt8_restore.argtypes = [P, P, i64, i64, P, i32, P]
+    linear = [P, P, P, P, i64, i64, i64, P, i32, i32, P, P, i32, P, P]
+    L.fp4_linear_mx.argtypes = linear + [P]
+    L.fp4_linear_mx_selftest.argtypes = linear + [i32, i32, i32, P]
+    L.amp_bias_act_backward_mx8.argtypes = [i32, P, i32, i64, i64, P, P, P, P, i32, P]
+    L.amp_dropout_forward.argtypes = [P, i32, i64, i64, dbl, u64, P, i32, P, P, P]
+    L.amp_dropout_backward.argtypes = [P, i32, i64, i64, dbl, u64, P, i32, P, P, i32, P]
+    L.amp_token_logprobs_forward.argtypes = [P, i32, i64, i64, i64, P, P, P, P, P, P, i32, P]
+    L.amp_token_logprobs_backward.argtypes = [P, P, i32, i64, i64, i64, P, P, P, P, P, P, i64, P]
     for name in EXPORTS:
         getattr(L, name).restype = i64 if name.endswith("_bytes") else ctypes.c_int
     _library = L
@@ -124,8 +136,8 @@ def fp4_product_mx(a, a_scales, b, b_scales, k: int, out, stream=None):
 
 
 def fp4_mx_check(stream=None):
-    """Raise AmpError(AMP_ETIMEOUT) if a bounded wait of fp4_product_mx gave up on the current
-    device (synchronises)."""
+    """Raise AmpError(AMP_ETIMEOUT) if a bounded wait of fp4_product_mx or fp4_linear_mx gave up
+    on the current device (synchronises)."""
     _check("fp4_mx_check", _load().fp4_mx_check(_stream(stream)))
 
 
@@ -173,3 +185,58 @@ def amp_ckpt8_restore(q, scales, out, stream=None):
     st = (_native or _bound()).restore(q, scales, out, stream)
     if st:
         _check("amp_ckpt8_restore", st)
+
+
+def fp4_linear_mx(a, a_scales, b, b_scales, k: int, out, bias=None, kind=None, residual=None,
+                  saved=None, stream=None):
+    """out [m, n] = residual + f(A B^T + bias) of packed A [m, k] and B [n, k]; kind None: f(z) = z;
+    saved: (q, scales) that take z = A B^T + bias in 8 bits."""
+    st = (_native or _bound()).linear(a, a_scales, b, b_scales, k, out, bias, kind, residual, saved,
+                                      stream)
+    if st:
+        _check("fp4_linear_mx", st)
+
+
+def amp_bias_act_backward_mx8(dy, dbias, kind=None, saved=None, dx=None, stream=None):
+    """dx = dy f'(z) and dbias = its sums over the rows, from the 8-bit checkpoint of z; kind None:
+    dbias = the sums of dy (no saved, no dx)."""
+    st = (_native or _bound()).bias_act_backward(dy, dbias, kind, saved, dx, stream)
+    if st:
+        _check("amp_bias_act_backward_mx8", st)
+
+
+def amp_dropout_forward(x, p: float, seed: int, site: int, y, residual=None, step=None, stream=None):
+    """y = residual + dropout(x), the mask a function of (seed, step, site, element); step: one
+    int32 on the device (AmpOptimizerStep.step_count, say; None: 0)."""
+    st = (_native or _bound()).dropout_forward(x, p, seed, site, y, residual, step, stream)
+    if st:
+        _check("amp_dropout_forward", st)
+
+
+def amp_dropout_backward(dy, p: float, seed: int, site: int, dx, step=None, dbias=None, stream=None):
+    """dx from dy with the mask of the forward call (same p, seed, site, step value and shape);
+    dbias: the sums of dx over the rows."""
+    st = (_native or _bound()).dropout_backward(dy, p, seed, site, dx, step, dbias, stream)
+    if st:
+        _check("amp_dropout_backward", st)
+
+
+def amp_token_logprobs_forward(logits, targets, logp, entropy=None, stats=None, top_ids=None,
+                               top_logp=None, stream=None):
+    """Log probabilities of the targets (int64, negative: row not used; or None) under softmax of
+    each row of the logits, whose rows may lie apart; entropy, stats (fp32 [rows, 2], for the
+    backward pass) and the most probable tokens (int64 and fp32 [rows, n]) where given."""
+    st = (_native or _bound()).logprobs_forward(logits, targets, logp, entropy, stats, top_ids,
+                                                top_logp, stream)
+    if st:
+        _check("amp_token_logprobs_forward", st)
+
+
+def amp_token_logprobs_backward(dlogp, logits, targets, stats, dlogits, entropy=None, dentropy=None,
+                                scale=None, stream=None):
+    """dlogits from the gradients at logp and at the entropy ([rows], None: 0), times the loss
+    scale (one fp32 on the device); dlogits may be logits."""
+    st = (_native or _bound()).logprobs_backward(dlogp, logits, targets, stats, dlogits, entropy,
+                                                 dentropy, scale, stream)
+    if st:
+        _check("amp_token_logprobs_backward", st)
