@@ -28,6 +28,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
 constexpr int kMaxTop = 32;
+constexpr int kMaxParts = 8;  // CTAs of a cluster that share a row
 constexpr int kLoads = 4;  // 16-byte loads a thread has in flight
 
 struct LogprobsFwd {
@@ -156,9 +157,40 @@ struct Entry {
 };
 __device__ __forceinline__ bool before(float v, int i, Entry b) { return v > b.v || (v == b.v && i < b.i); }
 
-// A warp's k best, lane l the l-th; k - 1 is the bound to pass.
+// A warp's k best, lane l the l-th (32 are kept: what is behind the k-th does no harm).
 struct Best {
     Entry mine{-INFINITY, -1};
+
+    static __device__ __forceinline__ Entry other(Entry e, int mask) {
+        return {__shfl_xor_sync(0xFFFFFFFFu, e.v, mask), __shfl_xor_sync(0xFFFFFFFFu, e.i, mask)};
+    }
+    // the earlier of the two in the lanes that `first` says, the later in the others
+    static __device__ __forceinline__ Entry exchange(Entry e, int mask, bool first) {
+        const Entry o = other(e, mask);
+        return before(o.v, o.i, e) == first ? o : e;
+    }
+    // sorts a sequence that rises and falls
+    static __device__ __forceinline__ Entry settle(Entry e) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int j = 16; j > 0; j >>= 1) e = exchange(e, j, (lane & j) == 0);
+        return e;
+    }
+    static __device__ __forceinline__ Entry sorted(Entry e) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int n = 2; n < 32; n *= 2)
+#pragma unroll
+            for (int j = n / 2; j > 0; j >>= 1) e = exchange(e, j, ((lane & j) == 0) == ((lane & n) == 0));
+        return settle(e);
+    }
+    // with another sorted list
+    __device__ __forceinline__ void merge(Entry e) {
+        e = other(e, 31);
+        if (before(e.v, e.i, mine)) mine = e;
+        mine = settle(mine);
+    }
+
     // one candidate, the same on all lanes
     __device__ __forceinline__ void insert(float v, int i) {
         const int lane = threadIdx.x & 31;
@@ -172,10 +204,11 @@ struct Best {
     __device__ __forceinline__ Entry last(int k) const {
         return {__shfl_sync(0xFFFFFFFFu, mine.v, k - 1), __shfl_sync(0xFFFFFFFFu, mine.i, k - 1)};
     }
-    // a candidate of each lane
+    // a candidate of each lane; sorting takes as long as ten insertions
     __device__ __forceinline__ void offer(float v, int i, int k) {
         Entry b = last(k);
         uint32_t in = __ballot_sync(0xFFFFFFFFu, before(v, i, b));
+        if (__popc(in) > 10) return merge(sorted({v, i}));
         while (in) {
             const int src = __ffs(in) - 1;
             insert(__shfl_sync(0xFFFFFFFFu, v, src), __shfl_sync(0xFFFFFFFFu, i, src));
@@ -184,36 +217,79 @@ struct Best {
             in &= __ballot_sync(0xFFFFFFFFu, before(v, i, b));
         }
     }
-    // the pieces of the lanes whose largest element reaches the bound
-    template <int XT>
-    __device__ __forceinline__ void offer_piece(uint4 u, int first, int k) {
-        constexpr int VN = Pieces<XT>::VN;
-        const int lane = threadIdx.x & 31;
-        const float big = largest<XT>(u);
-        Entry b = last(k);
-        uint32_t hits = __ballot_sync(0xFFFFFFFFu, big >= b.v && big > -INFINITY);
-        while (hits) {
-            const int src = __ffs(hits) - 1;
-            hits &= hits - 1;
-            const uint4 x = make_uint4(__shfl_sync(0xFFFFFFFFu, u.x, src), __shfl_sync(0xFFFFFFFFu, u.y, src),
-                                       __shfl_sync(0xFFFFFFFFu, u.z, src), __shfl_sync(0xFFFFFFFFu, u.w, src));
-            const int f = __shfl_sync(0xFFFFFFFFu, first, src);
-            float y[VN], v = -INFINITY;
-            widen<XT>(x, y);
+};
+
+// What may enter a warp's list: the elements of up to 32 a lane that reach the list's
+// last value, put side by side in shared memory.
+constexpr int kQueue = 64;
+
+// Offers the elements of kLoads pieces a lane, big the largest of the lane's.
+template <int XT>
+__device__ __forceinline__ void offer_pieces(Best &best, const uint4 (&u)[kLoads], const int (&first)[kLoads], float big,
+                                             int k, Entry *queue) {
+    constexpr int VN = Pieces<XT>::VN;
+    const int lane = threadIdx.x & 31;
+    float bound = best.last(k).v;
+    if (bound == -INFINITY) {
+        // nothing yet: the k-th of the lanes' largest is reached by k elements
+        const Entry e = Best::sorted({big, lane});
+        bound = __shfl_sync(0xFFFFFFFFu, e.v, k - 1);
+    }
+    if (!__any_sync(0xFFFFFFFFu, big >= bound)) return;
+    int n = 0;
 #pragma unroll
-            for (int e = 0; e < VN; ++e)
-                if (lane == e) v = y[e];
-            // what is not there is -inf, which never enters
-            offer(v, v > -INFINITY ? f + lane : INT32_MAX, k);
+    for (int j = 0; j < kLoads; ++j) {
+        float y[VN];
+        widen<XT>(u[j], y);
+#pragma unroll
+        for (int e = 0; e < VN; ++e) n += y[e] >= bound && y[e] > -INFINITY;
+    }
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    const int total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    if (total <= kQueue) {
+        int at = upto - n;
+        if (n) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                float y[VN];
+                widen<XT>(u[j], y);
+#pragma unroll
+                for (int e = 0; e < VN; ++e)
+                    if (y[e] >= bound && y[e] > -INFINITY) queue[at++] = {y[e], first[j] + e};
+            }
+        }
+        __syncwarp();
+        for (int i = lane; i - lane < total; i += 32)
+            best.offer(i < total ? queue[i].v : -INFINITY, i < total ? queue[i].i : INT32_MAX, k);
+        __syncwarp();
+        return;
+    }
+    // too many (equal values, say): one element of each lane at a time
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+        float y[VN];
+        widen<XT>(u[j], y);
+#pragma unroll 1
+        for (int e = 0; e < VN; ++e) {
+            float v = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < VN; ++q)
+                if (q == e) v = y[q];
+            best.offer(v, v > -INFINITY ? first[j] + e : INT32_MAX, k);
         }
     }
-};
+}
 
 template <int XT, int THREADS, bool TOP>
 __global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
     constexpr int WARPS = THREADS / 32, VN = Pieces<XT>::VN;
     __shared__ float s_m[WARPS], s_s[WARPS], s_w[WARPS];
-    __shared__ Entry s_top[TOP ? WARPS : 1][kMaxTop];
+    __shared__ Entry s_top[TOP ? WARPS : 1][kMaxTop], s_queue[TOP ? WARPS : 1][TOP ? kQueue : 1];
     __shared__ float3 s_cta;
     pdl_wait();
     pdl_trigger();
@@ -245,10 +321,10 @@ __global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
         uint4 u[kLoads];
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) u[j] = row.load(i0 + j * step + int(threadIdx.x));
-        float big = a.m;
+        float big = largest<XT>(u[0]);
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) big = fmaxf(big, largest<XT>(u[j]));
-        a.raise(big);
+        for (int j = 1; j < kLoads; ++j) big = fmaxf(big, largest<XT>(u[j]));
+        a.raise(fmaxf(a.m, big));
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             float y[VN];
@@ -257,9 +333,10 @@ __global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
             for (int e = 0; e < VN; ++e) a.add<true>(y[e]);
         }
         if constexpr (TOP) {
+            int first[kLoads];
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j)
-                best.offer_piece<XT>(u[j], row.first(i0 + j * step + int(threadIdx.x)), P.k);
+            for (int j = 0; j < kLoads; ++j) first[j] = row.first(i0 + j * step + int(threadIdx.x));
+            offer_pieces<XT>(best, u, first, fmaxf(big, -INFINITY), P.k, s_queue[warp]);  // not NaN
         }
     }
 #pragma unroll
@@ -271,53 +348,82 @@ __global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
         s_s[warp] = a.s;
         s_w[warp] = a.w;
     }
-    if (TOP) s_top[warp][lane] = best.mine;
-    __syncthreads();
-    if (warp == 0) {
-        a = Sums();
-        for (int w = 0; w < WARPS; ++w) a.join(s_m[w], s_s[w], s_w[w]);
-        if (TOP) {
-            for (int w = 1; w < WARPS; ++w) {
-                const Entry e = s_top[w][lane];
-                best.offer(lane < P.k ? e.v : -INFINITY, lane < P.k && e.v > -INFINITY ? e.i : INT32_MAX, P.k);
+    if constexpr (TOP) {
+        // half of the warps take the other half's lists, until one is left
+        s_top[warp][lane] = best.mine;
+#pragma unroll
+        for (int half = WARPS / 2; half > 0; half /= 2) {
+            __syncthreads();
+            if (warp < half) {
+                best.merge(s_top[warp + half][lane]);
+                s_top[warp][lane] = best.mine;
             }
-            __syncwarp();
-            s_top[0][lane] = best.mine;
         }
+    } else {
+        __syncthreads();
+    }
+    if (warp == 0) {
+        // the warps' sums, a lane each, in one order
+        a = Sums();
+        if (lane < WARPS) {
+            a.m = s_m[lane];
+            a.s = s_s[lane];
+            a.w = s_w[lane];
+        }
+#pragma unroll
+        for (int o = WARPS / 2; o > 0; o >>= 1)
+            a.join(__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
+                   __shfl_xor_sync(0xFFFFFFFFu, a.w, o));
         if (lane == 0) s_cta = make_float3(a.m, a.s, a.w);
     }
     if (parts > 1) {
         __syncwarp();
         cluster_sync();
         if (rank == 0 && warp == 0) {
-            for (uint32_t q = 1; q < parts; ++q) {
-                const uint32_t at = cluster_addr(&s_cta, q);
-                a.join(__uint_as_float(cluster_ld(at)), __uint_as_float(cluster_ld(at + 4)),
-                       __uint_as_float(cluster_ld(at + 8)));
-                if (TOP) {
-                    const uint32_t e = cluster_addr(&s_top[0][lane], q);
-                    const float v = __uint_as_float(cluster_ld(e));
-                    const int i = int(cluster_ld(e + 4));
-                    best.offer(lane < P.k ? v : -INFINITY, lane < P.k && v > -INFINITY ? i : INT32_MAX, P.k);
+            // lane q: the sums of CTA q
+            a = Sums();
+            if (lane < int(parts)) {
+                const uint32_t at = cluster_addr(&s_cta, lane);
+                a.m = __uint_as_float(cluster_ld(at));
+                a.s = __uint_as_float(cluster_ld(at + 4));
+                a.w = __uint_as_float(cluster_ld(at + 8));
+            }
+#pragma unroll
+            for (int o = kMaxParts / 2; o > 0; o >>= 1)
+                a.join(__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
+                       __shfl_xor_sync(0xFFFFFFFFu, a.w, o));
+            if constexpr (TOP) {
+                Entry e[kMaxParts - 1];
+#pragma unroll
+                for (int q = 1; q < kMaxParts; ++q) {
+                    e[q - 1] = {-INFINITY, -1};
+                    if (q < int(parts)) {
+                        const uint32_t at = cluster_addr(&s_top[0][lane], q);
+                        e[q - 1] = {__uint_as_float(cluster_ld(at)), int(cluster_ld(at + 4))};
+                    }
                 }
+#pragma unroll
+                for (int q = 1; q < kMaxParts; ++q)
+                    if (q < int(parts)) best.merge(e[q - 1]);
             }
         }
         __syncwarp();
         cluster_sync();  // nobody leaves while its shared memory is read
     }
     if (rank != 0 || warp != 0) return;
-    const float logs = logf(a.s);
+    const float m = __shfl_sync(0xFFFFFFFFu, a.m, 0), logs = logf(__shfl_sync(0xFFFFFFFFu, a.s, 0));
     if (lane == 0) {
         if (P.logp)
             P.logp[r] = !P.t ? 0.0f
                         : t >= P.cols ? NAN
-                                      : (load_elem<XT>(P.z, r * P.ld + t) - a.m) - logs;
+                                      : (load_elem<XT>(P.z, r * P.ld + t) - m) - logs;
         if (P.ent) P.ent[r] = logs - a.w / a.s;
-        if (P.stats) P.stats[r] = make_float2(a.m, logs);
+        if (P.stats) P.stats[r] = make_float2(m, logs);
     }
     if (TOP && lane < P.k) {
-        P.ids[r * P.k + lane] = best.mine.i;
-        P.top[r * P.k + lane] = best.mine.v == -INFINITY ? -INFINITY : (best.mine.v - a.m) - logs;
+        const bool none = best.mine.v == -INFINITY;
+        P.ids[r * P.k + lane] = none ? -1 : best.mine.i;
+        P.top[r * P.k + lane] = none ? -INFINITY : (best.mine.v - m) - logs;
     }
 }
 
@@ -405,7 +511,7 @@ cudaError_t fwd_x(const LogprobsFwd &P, int device, cudaStream_t s) {
     if (pieces <= 1024 && P.rows >= sms)
         return P.k ? fwd<XT, 128, true>(P, 1, s) : fwd<XT, 128, false>(P, 1, s);
     int parts = 1;
-    while (parts < 8 && P.rows * parts * 2 <= 2 * sms && pieces > parts * 512) parts *= 2;
+    while (parts < kMaxParts && P.rows * parts * 2 <= 2 * sms && pieces > parts * 512) parts *= 2;
     return P.k ? fwd<XT, 512, true>(P, parts, s) : fwd<XT, 512, false>(P, parts, s);
 }
 template <int XT>
