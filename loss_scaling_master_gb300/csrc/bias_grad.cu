@@ -23,9 +23,9 @@ struct BiasBwd {
 };
 
 template <int XT, int ACT, bool VEC>
-__global__ void __launch_bounds__(kSumThreads) bias_bwd_kernel(BiasBwd P) {
+__global__ void __launch_bounds__(kSumThreads, kSumCtas) bias_bwd_kernel(BiasBwd P) {
     using S = SumShape<VEC>;
-    constexpr int N = VEC ? 8 : 1, U = VEC ? 4 : 8;  // elements a thread and row, rows a step
+    constexpr int N = VEC ? 8 : 1, U = VEC ? 2 : 8;  // elements a thread and row, rows a step
     pdl_wait();
     pdl_trigger();
     const SumShare at(P.rows);

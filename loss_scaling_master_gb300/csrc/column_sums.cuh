@@ -17,7 +17,7 @@
 
 namespace amp {
 
-constexpr int kSumThreads = 512, kSumCols = 64;
+constexpr int kSumThreads = 256, kSumCols = 64, kSumCtas = 4;  // CTAs an SM holds
 // Threads beside one another on a row and row groups: 8 columns a thread, or one.
 template <bool VEC>
 struct SumShape {
@@ -77,8 +77,8 @@ __device__ __forceinline__ void sum_join(const SumShare &at, int64_t cols, const
     }
     __syncwarp();
     if (at.parts > 1) cluster_sync();  // every CTA's sums are written
-    const int mine = kSumCols / int(at.parts), c = int(at.rank) * mine + int(threadIdx.x);
-    if (threadIdx.x < unsigned(mine) && at.col0 + c < cols) {
+    const int mine = (kSumCols + int(at.parts) - 1) / int(at.parts), c = int(at.rank) * mine + int(threadIdx.x);
+    if (threadIdx.x < unsigned(mine) && c < kSumCols && at.col0 + c < cols) {
         float t = s_part[c];
         if (at.parts > 1) {
             t = 0.0f;
@@ -92,11 +92,19 @@ __device__ __forceinline__ void sum_join(const SumShare &at, int64_t cols, const
     if (at.parts > 1) cluster_sync();  // nobody leaves while its shared memory is read
 }
 
-// Shares of the rows: enough for four CTAs an SM, of at least a row a group, at most 8.
+// Shares of the rows, at most 8 of at least a row a group: as many as make the rounds
+// of CTAs that the GPU holds at once shortest.
 inline int sum_parts(int64_t rows, int64_t cols, int groups, int sms) {
-    const int64_t tiles = (cols + kSumCols - 1) / kSumCols;
+    const int64_t tiles = (cols + kSumCols - 1) / kSumCols, room = int64_t(sms) * kSumCtas;
     int parts = 1;
-    while (parts < 8 && tiles * parts < 4 * sms && rows > int64_t(groups) * parts) parts *= 2;
+    double least = 0.0;
+    for (int p = 1; p <= 8 && (p == 1 || rows > int64_t(groups) * (p - 1)); ++p) {
+        const double t = double((tiles * p + room - 1) / room) / p;
+        if (p == 1 || t < least) {
+            least = t;
+            parts = p;
+        }
+    }
     return parts;
 }
 template <class K, class A>

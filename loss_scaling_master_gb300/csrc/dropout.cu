@@ -23,26 +23,41 @@ struct Dropout {
     uint64_t seed;
     int64_t rows, cols;  // flat: rows = 1
     float scale;
-    uint32_t drop;  // T
+    uint32_t drop, last;  // T, and 65536 T - 1: of 32 bits whose upper half is u, u >= T where they are above it
     uint32_t site;
     int otype;
 };
 
+// What becomes of 8 elements x of the group.  ALL: T = 0.
+template <bool ALL>
+__device__ __forceinline__ void drop8(const Dropout &P, int32_t step, int64_t group, float (&x)[8]) {
+    if constexpr (ALL) return;
+    const uint4 r = sr_random8(P.seed, step, int32_t(P.site), group);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float a = x[2 * j] * P.scale, b = x[2 * j + 1] * P.scale;
+        x[2 * j] = (w[j] << 16) > P.last ? a : 0.0f;
+        x[2 * j + 1] = w[j] > P.last ? b : 0.0f;
+    }
+}
 // Bit j: element j of the group stays.
+template <bool ALL>
 __device__ __forceinline__ uint32_t keep8(const Dropout &P, int32_t step, int64_t group) {
+    if constexpr (ALL) return 0xFFu;
     const uint4 r = sr_random8(P.seed, step, int32_t(P.site), group);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if ((w[j] & 0xFFFFu) >= P.drop) m |= 1u << (2 * j);
-        if ((w[j] >> 16) >= P.drop) m |= 2u << (2 * j);
+        if ((w[j] << 16) > P.last) m |= 1u << (2 * j);
+        if (w[j] > P.last) m |= 2u << (2 * j);
     }
     return m;
 }
 
 // 8 elements a thread, every address aligned; the last ones one at a time.
-template <int XT, bool RES>
+template <int XT, bool RES, bool ALL>
 __global__ void __launch_bounds__(kThreads) dropout_vec_kernel(Dropout P) {
     pdl_wait();
     pdl_trigger();
@@ -52,17 +67,15 @@ __global__ void __launch_bounds__(kThreads) dropout_vec_kernel(Dropout P) {
         float x[8], r[8];
         ldv<XT>(P.x, 8 * g, x);
         if (RES) ldv<XT>(P.res, 8 * g, r);
-        const uint32_t m = keep8(P, step, g);
+        drop8<ALL>(P, step, g, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = (m >> j) & 1 ? x[j] * P.scale : 0.0f;
+        for (int j = 0; j < 8; ++j)
             if (RES) x[j] = r[j] + x[j];
-        }
         stv<XT>(P.y, 8 * g, x);
     }
     const int64_t k = 8 * groups + threadIdx.x;
     if (blockIdx.x == 0 && k < P.cols) {
-        float v = (keep8(P, step, groups) >> threadIdx.x) & 1 ? load_elem<XT>(P.x, k) * P.scale : 0.0f;
+        float v = (keep8<ALL>(P, step, groups) >> threadIdx.x) & 1 ? load_elem<XT>(P.x, k) * P.scale : 0.0f;
         if (RES) v = load_elem<XT>(P.res, k) + v;
         store_elem<XT>(P.y, k, v);
     }
@@ -70,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) dropout_vec_kernel(Dropout P) {
 
 // Any address: a warp takes 256 elements, a lane makes the mask of 8 consecutive ones
 // and applies that of every 32nd.
-template <int XT, bool RES>
+template <int XT, bool RES, bool ALL>
 __global__ void __launch_bounds__(kThreads) dropout_elem_kernel(Dropout P) {
     pdl_wait();
     pdl_trigger();
@@ -78,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) dropout_elem_kernel(Dropout P) {
     const int lane = threadIdx.x & 31;
     const int64_t stride = int64_t(gridDim.x) * kThreads * 8;
     for (int64_t k0 = (int64_t(blockIdx.x) * kThreads + (threadIdx.x & ~31)) * 8; k0 < P.cols; k0 += stride) {
-        const uint32_t m = keep8(P, step, (k0 >> 3) + lane);
+        const uint32_t m = keep8<ALL>(P, step, (k0 >> 3) + lane);
         float x[8], r[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -98,10 +111,10 @@ __global__ void __launch_bounds__(kThreads) dropout_elem_kernel(Dropout P) {
 }
 
 // The gradient with the bias's: by columns (column_sums.cuh).
-template <int XT>
-__global__ void __launch_bounds__(kSumThreads) dropout_bias_vec_kernel(Dropout P) {
+template <int XT, bool ALL>
+__global__ void __launch_bounds__(kSumThreads, kSumCtas) dropout_bias_vec_kernel(Dropout P) {
     using S = SumShape<true>;
-    constexpr int U = 4;
+    constexpr int U = XT == kF32 ? 2 : 4;
     pdl_wait();
     pdl_trigger();
     const SumShare at(P.rows);
@@ -123,14 +136,11 @@ __global__ void __launch_bounds__(kSumThreads) dropout_bias_vec_kernel(Dropout P
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + u * S::groups, k = r * P.cols + c;
             if (r >= at.row1) break;
-            const uint32_t m = keep8(P, step, k >> 3);
             float y[8];
             raw8_to_f32<XT>(g[u], y);
+            drop8<ALL>(P, step, k >> 3, y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                y[j] = (m >> j) & 1 ? y[j] * P.scale : 0.0f;
-                a[j] += y[j];
-            }
+            for (int j = 0; j < 8; ++j) a[j] += y[j];
             stv<XT>(P.y, k, y);
         }
     }
@@ -138,8 +148,8 @@ __global__ void __launch_bounds__(kSumThreads) dropout_bias_vec_kernel(Dropout P
 }
 // Any size and address.  A warp's 32 columns of a row lie in at most 5 of the
 // generator's groups: 30 lanes make the masks of 6 rows.
-template <int XT>
-__global__ void __launch_bounds__(kSumThreads) dropout_bias_elem_kernel(Dropout P) {
+template <int XT, bool ALL>
+__global__ void __launch_bounds__(kSumThreads, kSumCtas) dropout_bias_elem_kernel(Dropout P) {
     using S = SumShape<false>;
     constexpr int U = 6;
     pdl_wait();
@@ -158,7 +168,7 @@ __global__ void __launch_bounds__(kSumThreads) dropout_bias_elem_kernel(Dropout 
             x[u] = in && r < at.row1 ? load_elem<XT>(P.x, r * P.cols + c) : 0.0f;
         }
         const int64_t k0 = (r0 + int64_t(min(lane / 5, U - 1)) * S::groups) * P.cols + c0;
-        const uint32_t m = keep8(P, step, (k0 >> 3) + lane % 5);
+        const uint32_t m = keep8<ALL>(P, step, (k0 >> 3) + lane % 5);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + u * S::groups, k = r * P.cols + c0;
@@ -176,13 +186,13 @@ __global__ void __launch_bounds__(kSumThreads) dropout_bias_elem_kernel(Dropout 
 
 bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
-template <int XT>
+template <int XT, bool ALL>
 cudaError_t go(const Dropout &P, int sms, cudaStream_t s) {
     const bool vec = !off16(P.x) && !off16(P.res) && !off16(P.y);
     if (P.db) {
         return vec && P.cols % 8 == 0
-                   ? launch_sums(dropout_bias_vec_kernel<XT>, P.rows, P.cols, SumShape<true>::groups, sms, s, P)
-                   : launch_sums(dropout_bias_elem_kernel<XT>, P.rows, P.cols, SumShape<false>::groups, sms, s, P);
+                   ? launch_sums(dropout_bias_vec_kernel<XT, ALL>, P.rows, P.cols, SumShape<true>::groups, sms, s, P)
+                   : launch_sums(dropout_bias_elem_kernel<XT, ALL>, P.rows, P.cols, SumShape<false>::groups, sms, s, P);
     }
     Dropout F = P;
     F.cols = P.rows * P.cols;
@@ -190,10 +200,14 @@ cudaError_t go(const Dropout &P, int sms, cudaStream_t s) {
     const int64_t want = (F.cols + kThreads * 8 - 1) / (kThreads * 8);
     const dim3 grid(unsigned(std::min<int64_t>(want, int64_t(sms) * 64))), block(kThreads);
     if (vec)
-        return F.res ? launch_pdl(dropout_vec_kernel<XT, true>, grid, block, 0, s, F)
-                     : launch_pdl(dropout_vec_kernel<XT, false>, grid, block, 0, s, F);
-    return F.res ? launch_pdl(dropout_elem_kernel<XT, true>, grid, block, 0, s, F)
-                 : launch_pdl(dropout_elem_kernel<XT, false>, grid, block, 0, s, F);
+        return F.res ? launch_pdl(dropout_vec_kernel<XT, true, ALL>, grid, block, 0, s, F)
+                     : launch_pdl(dropout_vec_kernel<XT, false, ALL>, grid, block, 0, s, F);
+    return F.res ? launch_pdl(dropout_elem_kernel<XT, true, ALL>, grid, block, 0, s, F)
+                 : launch_pdl(dropout_elem_kernel<XT, false, ALL>, grid, block, 0, s, F);
+}
+template <int XT>
+cudaError_t go_all(const Dropout &P, int sms, cudaStream_t s) {
+    return P.drop == 0 ? go<XT, true>(P, sms, s) : go<XT, false>(P, sms, s);
 }
 
 }  // namespace
@@ -202,9 +216,11 @@ cudaError_t launch_dropout(const void *x, const void *res, int elem, int64_t row
                            uint64_t seed, const int32_t *step, uint32_t site, void *y, void *db, int dbelem,
                            int device, cudaStream_t s) {
     const float scale = drop < 65536u ? float(65536.0 / double(65536u - drop)) : 0.0f;
-    const Dropout P{x, res, y, db, step, seed, rows, cols, scale, drop, site, dbelem};
+    const Dropout P{x, res, y, db, step, seed, rows, cols, scale, drop, (drop << 16) - 1, site, dbelem};
     const int sms = sm_count(device);
-    const cudaError_t e = elem == kF32 ? go<kF32>(P, sms, s) : elem == kF16 ? go<kF16>(P, sms, s) : go<kBF16>(P, sms, s);
+    const cudaError_t e = elem == kF32   ? go_all<kF32>(P, sms, s)
+                          : elem == kF16 ? go_all<kF16>(P, sms, s)
+                                         : go_all<kBF16>(P, sms, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
