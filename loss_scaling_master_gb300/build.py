@@ -32,7 +32,7 @@ SOURCES = ["api.cu", "unscale_check.cu", "adamw_master.cu", "adamw_noalloc.cu", 
            "fp8_quant.cu",
            "fp8_rowwise.cu", "fp8_groupwise.cu", "update_scale.cu",
            "ops_api.cu", "fp4_mx.cu", "fp4_product.cu", "layer_norm_fwd.cu", "layer_norm_bwd.cu",
-           "act_mx8.cu", "fp4_linear.cu", "bias_grad.cu", "dropout.cu", "token_logprobs.cu"]
+           "act_mx8.cu", "fp4_linear.cu", "fp4_linear_pair.cu", "bias_grad.cu", "dropout.cu", "token_logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # --fmad=false: no multiply-add is fused behind the code's back; the kernels
 # spell out the rounding of every operation.  IEEE division and square root

@@ -1,5 +1,6 @@
 // fp4_linear.cu - a linear layer of two 4-bit block-scaled matrices with bias,
-// activation and residual (fp4_linear.cuh) on the kernels of fp4_product.cuh.
+// activation and residual (fp4_linear.cuh) on the kernels of fp4_product.cuh; those of
+// pairs of CTAs are compiled in fp4_linear_pair.cu.
 #include "fp4_linear.cuh"
 
 namespace amp {
@@ -7,6 +8,7 @@ namespace {
 
 // z = bias for an empty reduction: a warp takes 32 columns of 16 tokens.
 __global__ void __launch_bounds__(kThreads) linear_empty_kernel(Fp4Linear P) {
+    __shared__ __align__(16) uint8_t s_stage[kThreads / 32][EpAny::staged];
     pdl_wait();
     pdl_trigger();
     const int64_t items = (int64_t(P.m) + 15) / 16 * P.kb;
@@ -15,17 +17,8 @@ __global__ void __launch_bounds__(kThreads) linear_empty_kernel(Fp4Linear P) {
         const int64_t m0 = i / P.kb * 16;
         const uint32_t zero[16] = {};
         EpAny::State ep;
-        EpAny::finish<16>(P, m0, int(min(int64_t(16), P.m - m0)), i % P.kb * kMxBlock + (threadIdx.x & 31), zero, ep);
-    }
-}
-
-template <int OT>
-cudaError_t pair_of(const Fp4Linear &P, const void *a, const void *b, int64_t row_bytes, int device, cudaStream_t s) {
-    switch (P.act) {
-    case AMP_ACT_GELU: return go_pair<EpOne<OT, AMP_ACT_GELU>>(P, a, b, row_bytes, device, s);
-    case AMP_ACT_GELU_TANH: return go_pair<EpOne<OT, AMP_ACT_GELU_TANH>>(P, a, b, row_bytes, device, s);
-    case AMP_ACT_SILU: return go_pair<EpOne<OT, AMP_ACT_SILU>>(P, a, b, row_bytes, device, s);
-    default: return go_pair<EpOne<OT, kNoAct>>(P, a, b, row_bytes, device, s);
+        EpAny::finish<16>(P, m0, int(min(int64_t(16), P.m - m0)), i % P.kb * kMxBlock + (threadIdx.x & 31), zero, ep,
+                          s_stage[threadIdx.x / 32]);
     }
 }
 
@@ -44,7 +37,8 @@ cudaError_t launch_fp4_linear(const void *a, const uint8_t *sa, const void *b, c
     P.bt = uint8_t(belem);
     P.act = uint8_t(act < 0 ? int(kNoAct) : act);
     P.rpacked = P.packed && (reinterpret_cast<uintptr_t>(res) & 3) == 0;
-    P.qpacked = n % 4 == 0 && (reinterpret_cast<uintptr_t>(q) & 3) == 0;
+    const auto off = [](const void *p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; };
+    P.vec = n % 8 == 0 && !off(out, 15) && !off(res, 15) && !off(q, 7);
     cudaError_t e;
     const int64_t row_bytes = (k + kMxBlock - 1) / kMxBlock * 16;
     if (k == 0) {
@@ -53,13 +47,17 @@ cudaError_t launch_fp4_linear(const void *a, const uint8_t *sa, const void *b, c
     } else if (!takes_pairs(m, n, device)) {
         e = go_solo<EpAny>(P, a, b, row_bytes, device, s);
     } else {
-        e = oelem == kF32   ? pair_of<kF32>(P, a, b, row_bytes, device, s)
-            : oelem == kF16 ? pair_of<kF16>(P, a, b, row_bytes, device, s)
-                            : pair_of<kBF16>(P, a, b, row_bytes, device, s);
+        e = linear_pairs(P, a, b, row_bytes, device, s);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t fp4_linear_error_take(int32_t *v, cudaStream_t s) { return error_take(v, s); }
+cudaError_t fp4_linear_error_take(int32_t *v, cudaStream_t s) {
+    int32_t pairs = 0;
+    cudaError_t e = error_take(v, s);
+    if (e == cudaSuccess) e = linear_pairs_error_take(&pairs, s);
+    *v |= pairs;
+    return e;
+}
 
 }  // namespace amp

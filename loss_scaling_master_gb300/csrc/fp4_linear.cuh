@@ -15,9 +15,6 @@
 #include "fp4_product.cuh"
 
 namespace amp {
-namespace {
-
-enum : int { kNoAct = 3 };  // after the three amp_act values
 
 struct Fp4Linear : Fp4Product {
     const void *bias, *res;
@@ -26,8 +23,17 @@ struct Fp4Linear : Fp4Product {
     uint8_t bt;      // ElemType of bias
     uint8_t act;     // amp_act or kNoAct
     uint8_t rpacked; // packed, and the residual 4-byte aligned too
-    uint8_t qpacked; // q 4-byte aligned, and n % 4 == 0
+    uint8_t vec;     // rows are whole groups of 8 elements, and every address is aligned for one
 };
+
+// The kernels of pairs of CTAs (fp4_linear_pair.cu), and that file's error word.
+cudaError_t linear_pairs(const Fp4Linear &P, const void *a, const void *b, int64_t row_bytes, int device,
+                         cudaStream_t s);
+cudaError_t linear_pairs_error_take(int32_t *v, cudaStream_t s);
+
+namespace {
+
+enum : int { kNoAct = 3 };  // after the three amp_act values
 
 template <int OT>
 __device__ __forceinline__ float bias_at(const Fp4Linear &P, int64_t nn) {
@@ -46,7 +52,8 @@ template <int OT, int ACT>
 struct EpOne {
     using Args = Fp4Linear;
     static constexpr bool none = false;
-    static constexpr int CH = 16, WORDS = OT == kF32 ? CH : CH / 2;
+    static constexpr int staged = 0;
+    static constexpr int CH = OT == kF32 ? 8 : 16, WORDS = 8;
     struct State {
         uint32_t r[WORDS];  // the residual of CH tokens
         float bias;
@@ -130,7 +137,7 @@ struct EpOne {
     // ep: as begin() left it for the same place
     template <int CNT>
     static __device__ __forceinline__ void finish(const Args &P, int64_t m0, int rows, int64_t nn,
-                                                  const uint32_t (&v)[CNT], State &ep) {
+                                                  const uint32_t (&v)[CNT], State &ep, uint8_t *) {
 #pragma unroll
         for (int c = 0; c < CNT; c += CH) {
             if (c >= rows) break;
@@ -169,48 +176,201 @@ struct EpOne {
     }
 };
 
-// The element type and the activation looked up for every 16 tokens: for the kernels of
-// one CTA a tile, whose time is the operands'.
+// Eight neighbouring columns of one token, four lanes a block of the checkpoint.
+template <int OT>
+struct Eight {
+    uint4 r[kWords8<OT>];  // the residual's
+    // vec: the whole row is groups of eight, and aligned
+    __device__ __forceinline__ void load(const Fp4Linear &P, bool in, int64_t k, int left) {
+#pragma unroll
+        for (int w = 0; w < kWords8<OT>; ++w) r[w] = make_uint4(0, 0, 0, 0);
+        if (!P.res || !in) return;
+        if (P.vec) {
+#pragma unroll
+            for (int w = 0; w < kWords8<OT>; ++w)
+                r[w] = ld16(static_cast<const char *>(P.res) + k * (OT == kF32 ? 4 : 2) + 16 * w);
+        } else {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = j < left ? load_elem<OT>(P.res, k + j) : 0.0f;
+            f32_to_raw8<OT>(y, r);
+        }
+    }
+    // z: with the bias, 0 where in is false or behind the last column (left: columns from here)
+    template <int ACT>
+    __device__ __forceinline__ void finish(const Fp4Linear &P, bool in, int64_t k, int left, int64_t scale_at,
+                                           float (&z)[8]) const {
+        if (P.q) {
+            const uint32_t e = mx_scale_code<MxE4M3>(block_max8(z));
+            const uint2 c = codes8(z, mx_unscale(e));
+            if (in) {
+                if (P.vec) {
+                    *reinterpret_cast<uint2 *>(P.q + k) = c;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < left) P.q[k + j] = uint8_t((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
+                }
+                if ((threadIdx.x & 3) == 0) P.s[scale_at] = uint8_t(e);
+            }
+        }
+        float y[8], b[8];
+        raw8_to_f32<OT>(r, b);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            float2 v = make_float2(z[j], z[j + 1]);
+            if constexpr (ACT != kNoAct) v = act_apply<OT, ACT, false>(v.x, v.y, 0.0f, 0.0f);
+            y[j] = v.x;
+            y[j + 1] = v.y;
+        }
+        if (P.res) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] += b[j];
+        }
+        if (!in) return;
+        if (P.vec) {
+            stv<OT>(P.out, k, y);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < left) store_elem<OT>(P.out, k + j, y[j]);
+        }
+    }
+};
+
+// For pairs of CTAs: 16 tokens at a time go through shared memory, so that a lane gets
+// eight neighbouring columns: scales serve eight elements, and accesses are 16 bytes.
+// (4096 x 8192 x 2048 bf16 with bias, GELU and checkpoint STG1 us, a column a lane 81.8.)
+// The rows of 36 floats keep both accesses free of bank conflicts.
+template <int OT, int ACT>
+struct EpStaged {
+    using Args = Fp4Linear;
+    static constexpr bool none = false;
+    static constexpr int CH = 16, PITCH = 36, staged = CH * PITCH * 4;
+    struct State {
+        Eight<OT> e[2];
+        float bias;
+    };
+    static __device__ __forceinline__ void residual(const Args &P, int64_t m0, int rows, int64_t nn, Eight<OT> (&e)[2]) {
+        const int lane = threadIdx.x & 31;
+        const int64_t c = nn - lane + 8 * (lane & 3);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = 8 * h + lane / 4;
+            e[h].load(P, t < rows && c < P.n, (m0 + t) * P.n + c, 8);
+        }
+    }
+    static __device__ __forceinline__ void begin(const Args &P, int64_t m0, int rows, int64_t nn, State &ep) {
+        ep.bias = bias_at<OT>(P, nn);
+        residual(P, m0, rows, nn, ep.e);
+    }
+    template <int CNT>
+    static __device__ __forceinline__ void finish(const Args &P, int64_t m0, int rows, int64_t nn,
+                                                  const uint32_t (&v)[CNT], State &ep, uint8_t *mem) {
+        float *stage = reinterpret_cast<float *>(mem);
+        const int lane = threadIdx.x & 31;
+        const int64_t c = nn - lane + 8 * (lane & 3);
+#pragma unroll
+        for (int s = 0; s < CNT; s += CH) {
+            if (s >= rows) break;
+            __syncwarp();  // the last tokens are read
+#pragma unroll
+            for (int i = 0; i < CH; ++i) stage[i * PITCH + lane] = __uint_as_float(v[s + i]) + ep.bias;
+            __syncwarp();
+            // 16-bit types: 16 tokens ahead (fp32 has no registers for that)
+            Eight<OT> nxt[OT == kF32 ? 1 : 2];
+            if constexpr (OT != kF32)
+                if (s + CH < CNT) residual(P, m0 + s + CH, rows - s - CH, nn, nxt);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int t = 8 * h + lane / 4;
+                const bool in = s + t < rows && c < P.n;
+                const float4 *at = reinterpret_cast<const float4 *>(stage + t * PITCH + 8 * (lane & 3));
+                const float4 a = at[0], b = at[1];
+                float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                ep.e[h].template finish<ACT>(P, in, (m0 + s + t) * P.n + c, 8, (m0 + s + t) * P.kb + c / kMxBlock, z);
+            }
+            if (s + CH < CNT) {
+                if constexpr (OT == kF32) {
+                    residual(P, m0 + s + CH, rows - s - CH, nn, ep.e);
+                } else {
+                    ep.e[0] = nxt[0];
+                    ep.e[1] = nxt[1];
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ void saved_nan(const Args &P, int64_t m0, int cnt, int64_t nn) {
+        scales_nan(P, m0, cnt, nn);
+    }
+};
+
+// For one CTA a tile: as EpStaged, with the element type and the activation looked up for
+// every 16 tokens, and rows of any length.
 struct EpAny {
     using Args = Fp4Linear;
     static constexpr bool none = false;
+    static constexpr int CH = 16, PITCH = 36, staged = CH * PITCH * 4;
     struct State {};
     static __device__ __forceinline__ void begin(const Args &, int64_t, int, int64_t, State &) {}
-    template <int OT, int ACT, int CNT>
-    static __device__ __forceinline__ void run(const Args &P, int64_t m0, int rows, int64_t nn,
-                                               const uint32_t (&v)[CNT]) {
-        typename EpOne<OT, ACT>::State ep;
-        EpOne<OT, ACT>::begin(P, m0, rows, nn, ep);
-        EpOne<OT, ACT>::template finish<CNT>(P, m0, rows, nn, v, ep);
+
+    // 16 tokens from m0; stage: their z, a row of PITCH a token
+    template <int OT, int ACT>
+    static __device__ __forceinline__ void tokens(const Args &P, int64_t m0, int rows, int64_t c,
+                                                  const float *stage, const Eight<OT> (&e)[2]) {
+        const int lane = threadIdx.x & 31, left = int(min(int64_t(8), P.n - c));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = 8 * h + lane / 4;
+            const float4 *at = reinterpret_cast<const float4 *>(stage + t * PITCH + 8 * (lane & 3));
+            const float4 a = at[0], b = at[1];
+            float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            e[h].template finish<ACT>(P, t < rows && left > 0, (m0 + t) * P.n + c, left, (m0 + t) * P.kb + c / kMxBlock,
+                                      z);
+        }
     }
-    template <int OT, int CNT>
-    static __device__ __forceinline__ void run_act(const Args &P, int64_t m0, int rows, int64_t nn,
-                                                   const uint32_t (&v)[CNT]) {
+    template <int OT>
+    static __device__ __forceinline__ void run(const Args &P, int64_t m0, int rows, int64_t nn,
+                                               const uint32_t (&v)[CH], float *stage) {
+        const int lane = threadIdx.x & 31;
+        const int64_t c = nn - lane + 8 * (lane & 3);
+        Eight<OT> e[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = 8 * h + lane / 4;
+            e[h].load(P, t < rows && c < P.n, (m0 + t) * P.n + c, int(min(int64_t(8), P.n - c)));
+        }
+        const float bias = bias_at<OT>(P, nn);
+        __syncwarp();  // the last tokens are read
+#pragma unroll
+        for (int i = 0; i < CH; ++i) stage[i * PITCH + lane] = __uint_as_float(v[i]) + bias;
+        __syncwarp();
         switch (P.act) {
-        case AMP_ACT_GELU: return run<OT, AMP_ACT_GELU, CNT>(P, m0, rows, nn, v);
-        case AMP_ACT_GELU_TANH: return run<OT, AMP_ACT_GELU_TANH, CNT>(P, m0, rows, nn, v);
-        case AMP_ACT_SILU: return run<OT, AMP_ACT_SILU, CNT>(P, m0, rows, nn, v);
-        default: return run<OT, kNoAct, CNT>(P, m0, rows, nn, v);
+        case AMP_ACT_GELU: return tokens<OT, AMP_ACT_GELU>(P, m0, rows, c, stage, e);
+        case AMP_ACT_GELU_TANH: return tokens<OT, AMP_ACT_GELU_TANH>(P, m0, rows, c, stage, e);
+        case AMP_ACT_SILU: return tokens<OT, AMP_ACT_SILU>(P, m0, rows, c, stage, e);
+        default: return tokens<OT, kNoAct>(P, m0, rows, c, stage, e);
         }
     }
     template <int CNT>
     static __device__ __forceinline__ void finish(const Args &P, int64_t m0, int rows, int64_t nn,
-                                                  const uint32_t (&v)[CNT], State &) {
-        if (P.ot == kF32) run_act<kF32, CNT>(P, m0, rows, nn, v);
-        else if (P.ot == kF16) run_act<kF16, CNT>(P, m0, rows, nn, v);
-        else run_act<kBF16, CNT>(P, m0, rows, nn, v);
+                                                  const uint32_t (&v)[CNT], State &, uint8_t *mem) {
+        static_assert(CNT == CH, "16 tokens");
+        float *stage = reinterpret_cast<float *>(mem);
+        if (P.ot == kF32) run<kF32>(P, m0, rows, nn, v, stage);
+        else if (P.ot == kF16) run<kF16>(P, m0, rows, nn, v, stage);
+        else run<kBF16>(P, m0, rows, nn, v, stage);
     }
 
-    // Four neighbouring columns of one token; a warp holds 128, so 8 lanes a block.
+    // Four neighbouring columns of one token, for tiles whose reduction was cut (a warp
+    // holds 128 columns, so 8 lanes a block of the checkpoint; eight columns a thread,
+    // half of the threads idle, took 1.3 us longer at 48 x 4096 x 4096).
     template <int OT>
-    static __device__ __forceinline__ void four(const Args &P, int64_t m, int64_t nn, float (&z)[4]) {
+    static __device__ __forceinline__ void four(const Args &P, int64_t m, int64_t nn, float (&z)[4],
+                                                const float (&bias)[4], const float (&r)[4]) {
         const int64_t k = m * P.n + nn;
-        float r[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            z[j] += bias_at<OT>(P, nn + j);
-            r[j] = P.res && nn + j < P.n ? load_elem<OT>(P.res, k + j) : 0.0f;
-        }
+        for (int j = 0; j < 4; ++j) z[j] += bias[j];
         if (P.q) {
             uint32_t b = 0;
 #pragma unroll
@@ -221,7 +381,7 @@ struct EpAny {
             const float f = mx_unscale(e);
             const uint32_t c = f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(z[0], f), __fmul_rn(z[1], f)) |
                                (f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(z[2], f), __fmul_rn(z[3], f)) << 16);
-            if (P.qpacked && nn < P.n) {
+            if (P.vec && nn < P.n) {
                 *reinterpret_cast<uint32_t *>(P.q + k) = c;
             } else {
 #pragma unroll
@@ -252,10 +412,45 @@ struct EpAny {
                 if (nn + j < P.n) store_elem<OT>(P.out, k + j, y[j]);
         }
     }
-    static __device__ __forceinline__ void finish4(const Args &P, int64_t m, int64_t nn, float (&z)[4]) {
-        if (P.ot == kF32) four<kF32>(P, m, nn, z);
-        else if (P.ot == kF16) four<kF16>(P, m, nn, z);
-        else four<kBF16>(P, m, nn, z);
+    // The partial tiles of a cluster's CTAs in shared memory, [token][128 columns]: rank by
+    // rank, so the order of the sum is fixed; one group's loads are issued together.
+    template <int THREADS, int OT>
+    static __device__ __forceinline__ void join_as(const Args &P, const uint32_t (&part)[kMaxParts], uint32_t parts,
+                                                   uint32_t rank, int64_t m0, int64_t n0, int cols) {
+        // a thread's columns stay: the step is whole rows of 32 groups
+        const int l = 4 * (threadIdx.x % (kLanes / 4));
+        const int64_t nn = n0 + l;
+        float bias[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bias[j] = bias_at<OT>(P, nn + j);
+        for (int i = int(rank) * THREADS + int(threadIdx.x); i < cols * (kLanes / 4); i += int(parts) * THREADS) {
+            const int t = i / (kLanes / 4);
+            float4 v[kMaxParts];
+            float r[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                r[j] = P.res && nn + j < P.n ? load_elem<OT>(P.res, (m0 + t) * P.n + nn + j) : 0.0f;
+#pragma unroll
+            for (uint32_t q = 0; q < kMaxParts; ++q)
+                if (q < parts) v[q] = cluster_ld4(part[q] + uint32_t(t * kLanes + l) * 4);
+            float z[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (uint32_t q = 1; q < kMaxParts; ++q)
+                if (q < parts) {
+                    z[0] += v[q].x;
+                    z[1] += v[q].y;
+                    z[2] += v[q].z;
+                    z[3] += v[q].w;
+                }
+            four<OT>(P, m0 + t, nn, z, bias, r);
+        }
+    }
+    template <int THREADS>
+    static __device__ __forceinline__ void join(const Args &P, const uint32_t (&part)[kMaxParts], uint32_t parts,
+                                                uint32_t rank, int64_t m0, int64_t n0, int cols) {
+        if (P.ot == kF32) join_as<THREADS, kF32>(P, part, parts, rank, m0, n0, cols);
+        else if (P.ot == kF16) join_as<THREADS, kF16>(P, part, parts, rank, m0, n0, cols);
+        else join_as<THREADS, kBF16>(P, part, parts, rank, m0, n0, cols);
     }
     static __device__ __forceinline__ void saved_nan(const Args &P, int64_t m0, int cnt, int64_t nn) {
         scales_nan(P, m0, cnt, nn);

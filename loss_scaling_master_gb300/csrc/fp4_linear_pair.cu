@@ -1,0 +1,37 @@
+// fp4_linear_pair.cu - the linear layer's kernels of pairs of CTAs (fp4_linear.cuh), one
+// for each element type and activation.
+#include "fp4_linear.cuh"
+
+namespace amp {
+namespace {
+
+// Pairs of CTAs: staged where there is something to compute and rows are whole groups of
+// eight; a bias or a residual alone is added as the columns come (8192 x 4096 x 14336 bf16
+// with a residual PRM0 us, staged PRM1), and so are rows of any length.
+template <int OT, int ACT>
+cudaError_t pair_act(const Fp4Linear &P, const void *a, const void *b, int64_t row_bytes, int device, cudaStream_t s) {
+    if (P.vec && (ACT != kNoAct || P.q)) return go_pair<EpStaged<OT, ACT>>(P, a, b, row_bytes, device, s);
+    return go_pair<EpOne<OT, ACT>>(P, a, b, row_bytes, device, s);
+}
+template <int OT>
+cudaError_t pair_of(const Fp4Linear &P, const void *a, const void *b, int64_t row_bytes, int device, cudaStream_t s) {
+    switch (P.act) {
+    case AMP_ACT_GELU: return pair_act<OT, AMP_ACT_GELU>(P, a, b, row_bytes, device, s);
+    case AMP_ACT_GELU_TANH: return pair_act<OT, AMP_ACT_GELU_TANH>(P, a, b, row_bytes, device, s);
+    case AMP_ACT_SILU: return pair_act<OT, AMP_ACT_SILU>(P, a, b, row_bytes, device, s);
+    default: return pair_act<OT, kNoAct>(P, a, b, row_bytes, device, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t linear_pairs(const Fp4Linear &P, const void *a, const void *b, int64_t row_bytes, int device,
+                         cudaStream_t s) {
+    return P.ot == kF32   ? pair_of<kF32>(P, a, b, row_bytes, device, s)
+           : P.ot == kF16 ? pair_of<kF16>(P, a, b, row_bytes, device, s)
+                          : pair_of<kBF16>(P, a, b, row_bytes, device, s);
+}
+
+cudaError_t linear_pairs_error_take(int32_t *v, cudaStream_t s) { return error_take(v, s); }
+
+}  // namespace amp

@@ -53,12 +53,6 @@
 #include "tcgen05.cuh"
 
 namespace amp {
-namespace {
-
-__device__ int32_t g_fp4_error;
-
-constexpr int kLanes = 128;       // rows of B a CTA
-constexpr int kStageBytes = 128;  // bytes of a row a stage: 256 elements
 
 struct Fp4Product {
     const uint8_t *sa, *sb;  // scale tiles of A and B
@@ -72,9 +66,18 @@ struct Fp4Product {
     uint8_t packed;  // 16-bit out with even rows and 4-byte alignment: two elements a store
     Fp4Limits lim;
 };
+
+namespace {
+
+__device__ int32_t g_fp4_error;
+
+constexpr int kLanes = 128;       // rows of B a CTA
+constexpr int kStageBytes = 128;  // bytes of a row a stage: 256 elements
+
 struct EpNone {
     using Args = Fp4Product;
     static constexpr bool none = true;
+    static constexpr int staged = 0;  // bytes of shared memory a store warp
     struct State {};
 };
 // One line of the constant cache: a second one is missed at every start (0.15 us a
@@ -161,15 +164,18 @@ __device__ __forceinline__ void pack16(const uint32_t (&v)[CNT], uint32_t *p) {
 
 // ------------------------------------------------------------------ a pair of CTAs a tile
 constexpr int kPairThreads = 640;  // load, issue, allocate, (idle), 16 store warps
+template <class EP>
 struct Pair {
     static constexpr int w_bytes = kLanes * kStageBytes;  // this CTA's half of the tile's rows of B
     static constexpr int t_bytes = 128 * kStageBytes;     // and of its rows of A
     static constexpr int loads = w_bytes + t_bytes + 1024 + 2048;
     static constexpr int stage = loads;
-    static constexpr int stages = 6;
+    static constexpr int stages = EP::staged ? 5 : 6;
     static constexpr int sf_base = 256, sf_cols = 8 + 16;  // columns of a stage's scales
-    static constexpr int smem = stages * stage + 1024;
+    static constexpr int store_warps = 16;
+    static constexpr int smem = stages * stage + store_warps * EP::staged + 1024;
     static_assert(sf_base + stages * sf_cols <= 512, "tensor memory");
+    static_assert(smem <= 232448 - 256, "shared memory");
 };
 
 template <class EP>
@@ -177,7 +183,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     fp4_product_pair_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
                             const __grid_constant__ CUtensorMap map_st,
                             const __grid_constant__ CUtensorMap map_sw, typename EP::Args P) {
-    using S = Pair;
+    using S = Pair<EP>;
     constexpr int NS = S::stages;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], acc_full, acc_empty, drain, loaded;
@@ -353,7 +359,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             __syncwarp();
             if (lane == 0) cluster_arrive(done);
             if constexpr (!EP::none) {
-                EP::template finish<64>(P, m0, rows, nn, v, ep);
+                EP::template finish<64>(P, m0, rows, nn, v, ep,
+                                        smem + NS * S::stage + (warp - 4) * EP::staged);
             } else if (P.ot == kF32) {
                 store32<64>(P, m0, rows, nn, v);
             } else {
@@ -385,26 +392,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 constexpr uint32_t kMaxParts = 4;  // CTAs that share one tile's reduction
 constexpr int kSoloThreads = 384;  // load, issue, allocate, (idle), 8 store warps
 
-template <int BN>
+template <int BN, bool SPLIT, class EP>
 struct Solo {
+    static constexpr int staged = SPLIT ? 0 : EP::staged;
     static constexpr int w_bytes = kLanes * kStageBytes;
     static constexpr int t_bytes = BN * kStageBytes;
     static constexpr int stage = w_bytes + t_bytes + 2048;  // and 1 KB of scales of each operand
-    static constexpr int stages = BN == 128 ? 6 : BN == 64 ? 4 : 5;
+    // an epilogue's shared memory takes the place of a stage where two CTAs share an SM
+    static constexpr int stages = BN == 128 ? 6 : (BN == 64 ? 4 : 5) - (staged ? 1 : 0);
     static constexpr int ctas = BN == 128 ? 1 : 2;  // CTAs an SM holds
     static constexpr int sf_base = 2 * BN;          // two accumulators
     static constexpr int sf_cols = 16;
     static constexpr int tmem_cols = BN == 128 ? 512 : 256;
     static_assert(sf_base + stages * sf_cols <= tmem_cols, "tensor memory");
-    static constexpr int smem = stages * stage + 1024;  // and the alignment to 1024
+    static constexpr int smem = stages * stage + 8 * staged + 1024;  // and the alignment to 1024
     static_assert(BN * kLanes * 4 <= stages * stage, "the partial tile");
+    static_assert(ctas * (smem + 1024 + 256) <= 228 * 1024, "shared memory");
 };
 
 template <int BN, bool SPLIT, class EP>
-__global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
+__global__ void __launch_bounds__(kSoloThreads, Solo<BN, SPLIT, EP>::ctas)
     fp4_product_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
                        typename EP::Args P) {
-    using S = Solo<BN>;
+    using S = Solo<BN, SPLIT, EP>;
     constexpr int NS = S::stages, NA = 2;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], acc_full[NA], acc_empty[NA], drain, ended;
@@ -542,6 +552,7 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
         // a quarter of the lanes and half of the columns a warp (all of 16)
         constexpr int HALF = BN > 16 ? BN / 2 : BN;
         constexpr int CH = HALF < 32 ? HALF : EP::none || SPLIT ? 32 : 16;  // columns at a time
+        [[maybe_unused]] typename EP::State ep;
         const int quarter = warp & 3, c0 = (warp - 4) / 4 * HALF;
         int ab = 0;
         uint32_t aph = 0;
@@ -557,8 +568,9 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
 #pragma unroll 1
             for (int c = c0; c < min(rows, c0 + HALF) && c < BN; c += CH) {
                 uint32_t v[CH];
+                if constexpr (!EP::none && !SPLIT) EP::begin(P, m0 + c, rows - c, nn, ep);
                 tmem_ld<CH>(acc + c, v);
-                if (SPLIT) {
+                if constexpr (SPLIT) {
                     // partial tile [column][lane] over the stages' buffers: every
                     // product of this CTA has finished reading them
                     float *part = reinterpret_cast<float *>(smem);
@@ -566,9 +578,8 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
                     for (int i = 0; i < CH; ++i)
                         part[(c + i) * kLanes + 32 * quarter + lane] = __uint_as_float(v[i]);
                 } else if constexpr (!EP::none) {
-                    typename EP::State ep;
-                    EP::begin(P, m0 + c, rows - c, nn, ep);
-                    EP::template finish<CH>(P, m0 + c, rows - c, nn, v, ep);
+                    EP::template finish<CH>(P, m0 + c, rows - c, nn, v, ep,
+                                            smem + NS * S::stage + (warp - 4) * EP::staged);
                 } else if (P.ot == kF32) {
                     store32<CH>(P, m0 + c, rows - c, nn, v);
                 } else {
@@ -609,40 +620,42 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN>::ctas)
         uint32_t part[kMaxParts];
 #pragma unroll
         for (uint32_t r = 0; r < kMaxParts; ++r) part[r] = cluster_addr(smem, r < parts ? r : 0);
-        // groups of four neighbouring elements go round the CTAs' threads; the
-        // loads of one group's parts are issued together
-        for (int i = int(rank) * kSoloThreads + int(threadIdx.x); i < cols * (kLanes / 4);
-             i += int(parts) * kSoloThreads) {
-            const int c = i / (kLanes / 4), l = 4 * (i % (kLanes / 4));
-            float4 v[kMaxParts];
+        if constexpr (!EP::none) {
+            EP::template join<kSoloThreads>(P, part, parts, rank, m0, int64_t(tn) * kLanes, cols);
+        } else {
+            // groups of four neighbouring elements go round the CTAs' threads; the
+            // loads of one group's parts are issued together
+            for (int i = int(rank) * kSoloThreads + int(threadIdx.x); i < cols * (kLanes / 4);
+                 i += int(parts) * kSoloThreads) {
+                const int c = i / (kLanes / 4), l = 4 * (i % (kLanes / 4));
+                float4 v[kMaxParts];
 #pragma unroll
-            for (uint32_t r = 0; r < kMaxParts; ++r)
-                if (r < parts) v[r] = cluster_ld4(part[r] + uint32_t(c * kLanes + l) * 4);
-            float s[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                for (uint32_t r = 0; r < kMaxParts; ++r)
+                    if (r < parts) v[r] = cluster_ld4(part[r] + uint32_t(c * kLanes + l) * 4);
+                float s[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-            for (uint32_t r = 1; r < kMaxParts; ++r)
-                if (r < parts) {
-                    s[0] += v[r].x;
-                    s[1] += v[r].y;
-                    s[2] += v[r].z;
-                    s[3] += v[r].w;
-                }
-            const int64_t nn = int64_t(tn) * kLanes + l, k = (m0 + c) * P.n + nn;
-            if constexpr (!EP::none) {
-                EP::finish4(P, m0 + c, nn, s);
-            } else if (P.packed && nn + 4 <= P.n) {
-                uint16_t *o = static_cast<uint16_t *>(P.out) + k;
-                const uint32_t a = P.ot == kF16 ? f32x2_to_16x2<kF16>(s[0], s[1]) : f32x2_to_16x2<kBF16>(s[0], s[1]);
-                const uint32_t b = P.ot == kF16 ? f32x2_to_16x2<kF16>(s[2], s[3]) : f32x2_to_16x2<kBF16>(s[2], s[3]);
-                reinterpret_cast<uint32_t *>(o)[0] = a;
-                reinterpret_cast<uint32_t *>(o)[1] = b;
-            } else {
+                for (uint32_t r = 1; r < kMaxParts; ++r)
+                    if (r < parts) {
+                        s[0] += v[r].x;
+                        s[1] += v[r].y;
+                        s[2] += v[r].z;
+                        s[3] += v[r].w;
+                    }
+                const int64_t nn = int64_t(tn) * kLanes + l, k = (m0 + c) * P.n + nn;
+                if (P.packed && nn + 4 <= P.n) {
+                    uint16_t *o = static_cast<uint16_t *>(P.out) + k;
+                    const uint32_t a = P.ot == kF16 ? f32x2_to_16x2<kF16>(s[0], s[1]) : f32x2_to_16x2<kBF16>(s[0], s[1]);
+                    const uint32_t b = P.ot == kF16 ? f32x2_to_16x2<kF16>(s[2], s[3]) : f32x2_to_16x2<kBF16>(s[2], s[3]);
+                    reinterpret_cast<uint32_t *>(o)[0] = a;
+                    reinterpret_cast<uint32_t *>(o)[1] = b;
+                } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (nn + j >= P.n) break;
-                    if (P.ot == kF32) store_elem<kF32>(P.out, k + j, s[j]);
-                    else if (P.ot == kF16) store_elem<kF16>(P.out, k + j, s[j]);
-                    else store_elem<kBF16>(P.out, k + j, s[j]);
+                    for (int j = 0; j < 4; ++j) {
+                        if (nn + j >= P.n) break;
+                        if (P.ot == kF32) store_elem<kF32>(P.out, k + j, s[j]);
+                        else if (P.ot == kF16) store_elem<kF16>(P.out, k + j, s[j]);
+                        else store_elem<kBF16>(P.out, k + j, s[j]);
+                    }
                 }
             }
         }
@@ -733,12 +746,12 @@ cudaError_t go_pair(typename EP::Args P, const void *a, const void *b, int64_t r
     void *args[] = {&mt, &mw, &mst, &msw, &P};
     static std::atomic<uint64_t> ready{0};
     return launch(reinterpret_cast<const void *>(&fp4_product_pair_kernel<EP>), ready, device,
-                  unsigned(2 * std::min<int64_t>(tiles, sm_count(device) / 2)), kPairThreads, Pair::smem, 2, s, args);
+                  unsigned(2 * std::min<int64_t>(tiles, sm_count(device) / 2)), kPairThreads, Pair<EP>::smem, 2, s, args);
 }
 
 template <int BN, class EP>
 cudaError_t go(typename EP::Args P, const void *a, const void *b, int64_t row_bytes, int device, cudaStream_t s) {
-    using S = Solo<BN>;
+    using S = Solo<BN, false, EP>;
     // a narrower tile takes all tokens: the kernel finds a token tile's scales as
     // the scale tile (128 rows) of the same index
     if (BN < 128 && P.m > BN) return cudaErrorInvalidValue;
@@ -765,7 +778,7 @@ cudaError_t go(typename EP::Args P, const void *a, const void *b, int64_t row_by
     static std::atomic<uint64_t> ready[2];
     if (parts > 1)
         return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, true, EP>), ready[1], device, unsigned(tiles * parts),
-                      kSoloThreads, S::smem, parts, s, args);
+                      kSoloThreads, Solo<BN, true, EP>::smem, parts, s, args);
     return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, false, EP>), ready[0], device,
                   unsigned(std::min<int64_t>(tiles, room)), kSoloThreads, S::smem, 1, s, args);
 }
