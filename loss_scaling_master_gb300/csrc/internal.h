@@ -190,7 +190,7 @@ cudaError_t launch_logprobs_fwd(const void *z, int elem, int64_t rows, int64_t c
 cudaError_t launch_logprobs_bwd(const void *z, int elem, int64_t rows, int64_t cols, int64_t ld,
                                 const int64_t *t, const float *stats, const float *dlogp,
                                 const float *ent, const float *dent, const float *scale, void *dz,
-                                int64_t dld, cudaStream_t s);
+                                int64_t dld, int device, cudaStream_t s);
 
 cudaError_t launch_norm_fwd(const void *x, int xelem, int64_t rows, int64_t cols, const void *w,
                             const void *b, int welem, float eps, void *y, float *mean, float *rstd,

@@ -476,8 +476,11 @@ amp_status amp_token_logprobs_backward(const float *dlogp, const void *z, amp_dt
     if (off_type(ec, z, dz) || off_type(amp::kF32, dlogp, entropy, dentropy, scale_dev) || misaligned(targets, 8) ||
         misaligned(stats, 8))
         return fail(AMP_EINVAL, kOff, fn);
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return finish(e, fn);
     return finish(amp::launch_logprobs_bwd(z, ec, rows, cols, ld, targets, stats, dlogp, entropy, dentropy, scale_dev,
-                                           dz, dld, cu(stream)),
+                                           dz, dld, dev, cu(stream)),
                   fn);
 }
 

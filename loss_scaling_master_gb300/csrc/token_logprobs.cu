@@ -7,11 +7,15 @@
 //
 // Forward.  The logits are read once: each thread keeps a running maximum and the
 // two sums relative to it, which are rescaled when the maximum grows, at most once
-// for four 16-byte loads.  The most probable tokens are kept by warps, an entry a
-// lane in order; the maximum of the four loads, needed anyway, tells whether any of
-// their elements can enter, which after the first loads is rare.  Few rows are cut
-// over the CTAs of a cluster, whose results the first of them joins from shared
-// memory.
+// for four 16-byte loads.  Few rows are cut over the CTAs of a cluster, whose results
+// the first of them joins from shared memory.
+//
+// The k most probable tokens.  The k-th largest of the threads' maxima is reached by at
+// least k elements, so only threads whose maximum reaches it hold any of the k, and
+// these are hardly more than k.  What they read is read once more (a thread's share of
+// the row each, from L2), and what reaches the bound there is put in order.  (Lists kept
+// by warps along the row took 703 us for 5 of 4096 x 128256 bf16, 179 without; this
+// way TOPA.)
 //
 // Every row starts where its address lies: a first and a last piece of less than 16
 // bytes are taken by single elements, padded with -inf, which adds nothing.
@@ -27,9 +31,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
-constexpr int kMaxTop = 32;
 constexpr int kMaxParts = 8;  // CTAs of a cluster that share a row
-constexpr int kLoads = 4;  // 16-byte loads a thread has in flight
+constexpr int kLoads = 4, kBwdLoads = 2;  // 16-byte loads a thread has in flight (and as many ahead in the gradient)
 
 struct LogprobsFwd {
     const void *z;
@@ -204,11 +207,10 @@ struct Best {
     __device__ __forceinline__ Entry last(int k) const {
         return {__shfl_sync(0xFFFFFFFFu, mine.v, k - 1), __shfl_sync(0xFFFFFFFFu, mine.i, k - 1)};
     }
-    // a candidate of each lane; sorting takes as long as ten insertions
+    // a candidate of each lane
     __device__ __forceinline__ void offer(float v, int i, int k) {
         Entry b = last(k);
         uint32_t in = __ballot_sync(0xFFFFFFFFu, before(v, i, b));
-        if (__popc(in) > 10) return merge(sorted({v, i}));
         while (in) {
             const int src = __ffs(in) - 1;
             insert(__shfl_sync(0xFFFFFFFFu, v, src), __shfl_sync(0xFFFFFFFFu, i, src));
@@ -217,79 +219,108 @@ struct Best {
             in &= __ballot_sync(0xFFFFFFFFu, before(v, i, b));
         }
     }
+    // the elements of a piece a lane that reach the bound
+    template <int XT>
+    __device__ __forceinline__ void offer_piece(uint4 u, int first, float bound, int k) {
+        constexpr int VN = Pieces<XT>::VN;
+        const int lane = threadIdx.x & 31;
+        const float big = largest<XT>(u);
+        uint32_t hits = __ballot_sync(0xFFFFFFFFu, big >= bound && big > -INFINITY);
+        while (hits) {
+            const int src = __ffs(hits) - 1;
+            hits &= hits - 1;
+            const uint4 x = make_uint4(__shfl_sync(0xFFFFFFFFu, u.x, src), __shfl_sync(0xFFFFFFFFu, u.y, src),
+                                       __shfl_sync(0xFFFFFFFFu, u.z, src), __shfl_sync(0xFFFFFFFFu, u.w, src));
+            const int f = __shfl_sync(0xFFFFFFFFu, first, src);
+            float y[VN], v = -INFINITY;
+            widen<XT>(x, y);
+#pragma unroll
+            for (int e = 0; e < VN; ++e)
+                if (lane == e) v = y[e];
+            // what is not there is -inf, which never enters
+            offer(v >= bound ? v : -INFINITY, v >= bound && v > -INFINITY ? f + lane : INT32_MAX, k);
+        }
+    }
 };
 
-// What may enter a warp's list: the elements of up to 32 a lane that reach the list's
-// last value, put side by side in shared memory.
-constexpr int kQueue = 64;
-
-// Offers the elements of kLoads pieces a lane, big the largest of the lane's.
-template <int XT>
-__device__ __forceinline__ void offer_pieces(Best &best, const uint4 (&u)[kLoads], const int (&first)[kLoads], float big,
-                                             int k, Entry *queue) {
-    constexpr int VN = Pieces<XT>::VN;
+// Values alone, larger first, as Best does it with entries.
+__device__ __forceinline__ float settle_values(float v) {
     const int lane = threadIdx.x & 31;
-    float bound = best.last(k).v;
-    if (bound == -INFINITY) {
-        // nothing yet: the k-th of the lanes' largest is reached by k elements
-        const Entry e = Best::sorted({big, lane});
-        bound = __shfl_sync(0xFFFFFFFFu, e.v, k - 1);
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) {
+        const float o = __shfl_xor_sync(0xFFFFFFFFu, v, j);
+        v = (lane & j) == 0 ? fmaxf(v, o) : fminf(v, o);
     }
-    if (!__any_sync(0xFFFFFFFFu, big >= bound)) return;
-    int n = 0;
+    return v;
+}
+__device__ __forceinline__ float sort_values(float v) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-        float y[VN];
-        widen<XT>(u[j], y);
+    for (int n = 2; n < 32; n *= 2)
 #pragma unroll
-        for (int e = 0; e < VN; ++e) n += y[e] >= bound && y[e] > -INFINITY;
-    }
-    int upto = n;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    const int total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    if (total <= kQueue) {
-        int at = upto - n;
-        if (n) {
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                float y[VN];
-                widen<XT>(u[j], y);
-#pragma unroll
-                for (int e = 0; e < VN; ++e)
-                    if (y[e] >= bound && y[e] > -INFINITY) queue[at++] = {y[e], first[j] + e};
-            }
+        for (int j = n / 2; j > 0; j >>= 1) {
+            const float o = __shfl_xor_sync(0xFFFFFFFFu, v, j);
+            v = ((lane & j) == 0) == ((lane & n) == 0) ? fmaxf(v, o) : fminf(v, o);
         }
-        __syncwarp();
-        for (int i = lane; i - lane < total; i += 32)
-            best.offer(i < total ? queue[i].v : -INFINITY, i < total ? queue[i].i : INT32_MAX, k);
-        __syncwarp();
-        return;
-    }
-    // too many (equal values, say): one element of each lane at a time
+    return settle_values(v);
+}
+
+// The k best of what this CTA's threads have read, big the largest that each has seen
+// (not NaN): in warp 0's list.
+template <int XT, int THREADS>
+__device__ __forceinline__ Best top_of(const Pieces<XT> &row, int first_piece, int step, float big, int k) {
+    constexpr int WARPS = THREADS / 32;
+    __shared__ float s_big[WARPS][32];
+    __shared__ int s_hot[THREADS], s_count;
+    __shared__ Entry s_list[WARPS][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the k-th largest of the threads' largest
+    float v = sort_values(big);
+    s_big[warp][lane] = v;
+    if (threadIdx.x == 0) s_count = 0;
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-        float y[VN];
-        widen<XT>(u[j], y);
-#pragma unroll 1
-        for (int e = 0; e < VN; ++e) {
-            float v = -INFINITY;
-#pragma unroll
-            for (int q = 0; q < VN; ++q)
-                if (q == e) v = y[q];
-            best.offer(v, v > -INFINITY ? first[j] + e : INT32_MAX, k);
+    for (int half = WARPS / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (warp < half) {
+            v = settle_values(fmaxf(v, s_big[warp + half][31 - lane]));
+            s_big[warp][lane] = v;
         }
     }
+    __syncthreads();
+    const float bound = s_big[0][k - 1];
+    // who reached it (in any order: lists are in one order whatever comes first)
+    const uint32_t hot = __ballot_sync(0xFFFFFFFFu, big >= bound && big > -INFINITY);
+    if (hot) {
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&s_count, __popc(hot));
+        at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(hot & ((1u << lane) - 1));
+        if ((hot >> lane) & 1) s_hot[at] = int(threadIdx.x);
+    }
+    __syncthreads();
+    Best best;
+    const int n = s_count;
+    for (int h = warp; h < n; h += WARPS) {
+        const int i0 = first_piece + s_hot[h];
+        for (int j = lane; i0 + (j - lane) * step < row.count; j += 32)
+            best.offer_piece<XT>(row.load(i0 + j * step), row.first(i0 + j * step), bound, k);
+    }
+    s_list[warp][lane] = best.mine;
+#pragma unroll
+    for (int half = WARPS / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (warp < half) {
+            best.merge(s_list[warp + half][lane]);
+            s_list[warp][lane] = best.mine;
+        }
+    }
+    return best;
 }
 
 template <int XT, int THREADS, bool TOP>
-__global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
+__global__ void __launch_bounds__(THREADS, TOP ? 1024 / THREADS : 2048 / THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
     constexpr int WARPS = THREADS / 32, VN = Pieces<XT>::VN;
     __shared__ float s_m[WARPS], s_s[WARPS], s_w[WARPS];
-    __shared__ Entry s_top[TOP ? WARPS : 1][kMaxTop], s_queue[TOP ? WARPS : 1][TOP ? kQueue : 1];
+    __shared__ Entry s_top[32], s_tops[TOP ? kMaxParts : 1][32];
     __shared__ float3 s_cta;
     pdl_wait();
     pdl_trigger();
@@ -315,7 +346,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
     }
     const Pieces<XT> row(P.z, r * P.ld, P.cols);
     Sums a;
-    Best best;
+    float most = -INFINITY;  // the thread's largest
     const int step = int(parts) * THREADS;
     for (int i0 = int(rank) * THREADS; i0 < row.count; i0 += kLoads * step) {
         uint4 u[kLoads];
@@ -324,6 +355,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
         float big = largest<XT>(u[0]);
 #pragma unroll
         for (int j = 1; j < kLoads; ++j) big = fmaxf(big, largest<XT>(u[j]));
+        if (TOP) most = fmaxf(most, big);
         a.raise(fmaxf(a.m, big));
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
@@ -332,12 +364,11 @@ __global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
 #pragma unroll
             for (int e = 0; e < VN; ++e) a.add<true>(y[e]);
         }
-        if constexpr (TOP) {
-            int first[kLoads];
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) first[j] = row.first(i0 + j * step + int(threadIdx.x));
-            offer_pieces<XT>(best, u, first, fmaxf(big, -INFINITY), P.k, s_queue[warp]);  // not NaN
-        }
+    }
+    Best best;
+    if constexpr (TOP) {
+        best = top_of<XT, THREADS>(row, int(rank) * THREADS, step, most, P.k);
+        if (warp == 0) s_top[lane] = best.mine;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -348,20 +379,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
         s_s[warp] = a.s;
         s_w[warp] = a.w;
     }
-    if constexpr (TOP) {
-        // half of the warps take the other half's lists, until one is left
-        s_top[warp][lane] = best.mine;
-#pragma unroll
-        for (int half = WARPS / 2; half > 0; half /= 2) {
-            __syncthreads();
-            if (warp < half) {
-                best.merge(s_top[warp + half][lane]);
-                s_top[warp][lane] = best.mine;
-            }
-        }
-    } else {
-        __syncthreads();
-    }
+    __syncthreads();
     if (warp == 0) {
         // the warps' sums, a lane each, in one order
         a = Sums();
@@ -392,19 +410,22 @@ __global__ void __launch_bounds__(THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
             for (int o = kMaxParts / 2; o > 0; o >>= 1)
                 a.join(__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
                        __shfl_xor_sync(0xFFFFFFFFu, a.w, o));
-            if constexpr (TOP) {
-                Entry e[kMaxParts - 1];
-#pragma unroll
-                for (int q = 1; q < kMaxParts; ++q) {
-                    e[q - 1] = {-INFINITY, -1};
-                    if (q < int(parts)) {
-                        const uint32_t at = cluster_addr(&s_top[0][lane], q);
-                        e[q - 1] = {__uint_as_float(cluster_ld(at)), int(cluster_ld(at + 4))};
+        }
+        if constexpr (TOP && WARPS >= kMaxParts) {
+            // warp q: the list of CTA q; then in halves
+            if (rank == 0) {
+                if (warp < int(parts)) {
+                    const uint32_t at = cluster_addr(&s_top[lane], warp);
+                    best.mine = {__uint_as_float(cluster_ld(at)), int(cluster_ld(at + 4))};
+                    s_tops[warp][lane] = best.mine;
+                }
+                for (int half = kMaxParts / 2; half > 0; half /= 2) {
+                    __syncthreads();
+                    if (warp < half && warp + half < int(parts)) {
+                        best.merge(s_tops[warp + half][lane]);
+                        s_tops[warp][lane] = best.mine;
                     }
                 }
-#pragma unroll
-                for (int q = 1; q < kMaxParts; ++q)
-                    if (q < int(parts)) best.merge(e[q - 1]);
             }
         }
         __syncwarp();
@@ -443,7 +464,7 @@ struct LogprobsBwd {
 //   dz = p (A + B u) [+ S dlogp for the token],  A = -S (dlogp + dent H), B = -S dent
 template <int XT, int THREADS>
 __global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(LogprobsBwd P) {
-    constexpr int VN = Pieces<XT>::VN, esz = XT == kF32 ? 4 : 2;
+    constexpr int VN = Pieces<XT>::VN, esz = XT == kF32 ? 4 : 2, U = kBwdLoads;
     pdl_wait();
     pdl_trigger();
     const int64_t r = blockIdx.x / unsigned(P.chunks);
@@ -452,51 +473,69 @@ __global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(LogprobsBwd P) {
     char *out = static_cast<char *>(P.dz) + r * P.dld * esz;
     const bool aligned = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.row)) & 15) == 0;
     const int64_t t = P.t ? P.t[r] : 0;
-    const bool used = t >= 0;
-    const int i0 = chunk * (kLoads * THREADS) + int(threadIdx.x);
-    uint4 u[kLoads];
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) u[j] = used ? row.load(i0 + j * THREADS) : make_uint4(0, 0, 0, 0);
     const float scale = P.scale ? *P.scale : 1.0f;
-    const float dlogp = P.dlogp && used ? P.dlogp[r] * scale : 0.0f;
-    const float dent = P.dent && used ? P.dent[r] * scale : 0.0f;
+    const float dl = P.dlogp ? P.dlogp[r] : 0.0f, de = P.dent ? P.dent[r] : 0.0f, ent = P.dent ? P.ent[r] : 0.0f;
     const float2 st = P.stats[r];
-    const float B = -dent, BH = P.dent ? B * P.ent[r] : 0.0f;
+    const bool used = t >= 0;
+    const int per = (row.count + P.chunks - 1) / P.chunks, end = min(row.count, (chunk + 1) * per);
+    int i = chunk * per + int(threadIdx.x);
+    uint4 u[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) u[j] = used && i + j * THREADS < end ? row.load(i + j * THREADS) : make_uint4(0, 0, 0, 0);
+    const float dlogp = dl * scale, dent = de * scale, B = -dent, BH = B * ent;
     float A = BH - dlogp;
     if (t >= P.cols && P.t) A = NAN;
-    const int at = P.dlogp && used && t < P.cols ? int(t) : -1;
+    const int at = P.dlogp && used && t < P.cols ? int(t) : -VN;
+    for (; i < end; i += U * THREADS) {
+        uint4 nxt[U];
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-        const int i = i0 + j * THREADS;
-        if (i >= row.count) break;
-        const int f = row.first(i);
-        float y[VN];
-        if (used) {
-            widen<XT>(u[j], y);
-#pragma unroll
-            for (int e = 0; e < VN; ++e) {
-                const float lp = (y[e] - st.x) - st.y, p = exp2_flush(lp * kLog2e);
-                y[e] = p * __fmaf_rn(B, fmaxf(lp, kFar), A);
-                if (f + e == at)  // dlogp (1 - p), without the difference's rounding where p is near 1
-                    y[e] = __fmaf_rn(-dlogp, expm1f(lp), p * __fmaf_rn(B, fmaxf(lp, kFar), BH));
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < VN; ++e) y[e] = 0.0f;
+        for (int j = 0; j < U; ++j) {
+            const int n = i + (U + j) * THREADS;
+            nxt[j] = used && n < end ? row.load(n) : make_uint4(0, 0, 0, 0);
         }
-        if (aligned && row.whole(i)) {
-            uint32_t w[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if constexpr (XT == kF32) w[q] = __float_as_uint(y[q]);
-                else w[q] = f32x2_to_16x2<XT>(y[2 * q], y[2 * q + 1]);
+        for (int j = 0; j < U; ++j) {
+            const int n = i + j * THREADS;
+            if (n >= end) break;
+            const int f = row.first(n);
+            float y[VN];
+            if (used) {
+                widen<XT>(u[j], y);
+                float token = 0.0f;
+#pragma unroll
+                for (int e = 0; e < VN; ++e) {
+                    const float lp = (y[e] - st.x) - st.y;
+                    if (f + e == at) token = lp;
+                    y[e] = exp2_flush(lp * kLog2e) * __fmaf_rn(B, fmaxf(lp, kFar), A);
+                }
+                if (unsigned(at - f) < unsigned(VN)) {
+                    // dlogp (1 - p), without the difference's rounding where p is near 1
+                    const float g = __fmaf_rn(-dlogp, expm1f(token),
+                                              exp2_flush(token * kLog2e) * __fmaf_rn(B, fmaxf(token, kFar), BH));
+#pragma unroll
+                    for (int e = 0; e < VN; ++e)
+                        if (f + e == at) y[e] = g;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VN; ++e) y[e] = 0.0f;
             }
-            st16(out + int64_t(f) * esz, make_uint4(w[0], w[1], w[2], w[3]));
-        } else {
+            if (aligned && row.whole(n)) {
+                uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < VN; ++e)
-                if (f + e >= 0 && f + e < P.cols) store_elem<XT>(out, f + e, y[e]);
+                for (int q = 0; q < 4; ++q) {
+                    if constexpr (XT == kF32) w[q] = __float_as_uint(y[q]);
+                    else w[q] = f32x2_to_16x2<XT>(y[2 * q], y[2 * q + 1]);
+                }
+                st16(out + int64_t(f) * esz, make_uint4(w[0], w[1], w[2], w[3]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < VN; ++e)
+                    if (f + e >= 0 && f + e < P.cols) store_elem<XT>(out, f + e, y[e]);
+            }
         }
+#pragma unroll
+        for (int j = 0; j < U; ++j) u[j] = nxt[j];
     }
 }
 
@@ -508,21 +547,23 @@ cudaError_t fwd(const LogprobsFwd &P, int parts, cudaStream_t s) {
 template <int XT>
 cudaError_t fwd_x(const LogprobsFwd &P, int device, cudaStream_t s) {
     const int pieces = P.cols / Pieces<XT>::VN + 1, sms = sm_count(device);
-    if (pieces <= 1024 && P.rows >= sms)
+    if (pieces <= 512 && P.rows >= sms)
         return P.k ? fwd<XT, 128, true>(P, 1, s) : fwd<XT, 128, false>(P, 1, s);
     int parts = 1;
-    while (parts < kMaxParts && P.rows * parts * 2 <= 2 * sms && pieces > parts * 512) parts *= 2;
-    return P.k ? fwd<XT, 512, true>(P, parts, s) : fwd<XT, 512, false>(P, parts, s);
+    while (parts < kMaxParts && P.rows * parts <= 2 * sms && pieces > parts * 256) parts *= 2;
+    return P.k ? fwd<XT, 256, true>(P, parts, s) : fwd<XT, 256, false>(P, parts, s);
 }
 template <int XT>
-cudaError_t bwd_x(LogprobsBwd P, cudaStream_t s) {
-    constexpr int VN = Pieces<XT>::VN;
-    const int64_t pieces = P.cols / VN + 2;  // a row that starts inside a piece has one more
+cudaError_t bwd_x(LogprobsBwd P, int sms, cudaStream_t s) {
+    const int64_t pieces = P.cols / Pieces<XT>::VN + 2;  // a row that starts inside a piece has one more
     if (pieces <= 512) {
-        P.chunks = int((pieces + 4 * 128 - 1) / (4 * 128));
-        return launch_pdl(logprobs_bwd_kernel<XT, 128>, dim3(unsigned(P.rows * P.chunks)), dim3(128), 0, s, P);
+        P.chunks = 1;
+        return launch_pdl(logprobs_bwd_kernel<XT, 128>, dim3(unsigned(P.rows)), dim3(128), 0, s, P);
     }
-    P.chunks = int((pieces + 4 * 256 - 1) / (4 * 256));
+    // shares of 8 loads a thread, smaller ones where rows are few
+    int64_t chunks = (pieces + 8 * 256 - 1) / (8 * 256);
+    while (chunks * P.rows < 4 * sms && chunks * 512 < pieces) chunks *= 2;
+    P.chunks = int(chunks);
     return launch_pdl(logprobs_bwd_kernel<XT, 256>, dim3(unsigned(P.rows * P.chunks)), dim3(256), 0, s, P);
 }
 
@@ -540,12 +581,13 @@ cudaError_t launch_logprobs_fwd(const void *z, int elem, int64_t rows, int64_t c
 
 cudaError_t launch_logprobs_bwd(const void *z, int elem, int64_t rows, int64_t cols, int64_t ld, const int64_t *t,
                                 const float *stats, const float *dlogp, const float *ent, const float *dent,
-                                const float *scale, void *dz, int64_t dld, cudaStream_t s) {
+                                const float *scale, void *dz, int64_t dld, int device, cudaStream_t s) {
     const LogprobsBwd P{z, t, reinterpret_cast<const float2 *>(stats), dlogp, ent, dent, scale, dz, rows, ld, dld,
                         int(cols), 1};
-    const cudaError_t e = elem == kF32   ? bwd_x<kF32>(P, s)
-                          : elem == kF16 ? bwd_x<kF16>(P, s)
-                                         : bwd_x<kBF16>(P, s);
+    const int sms = sm_count(device);
+    const cudaError_t e = elem == kF32   ? bwd_x<kF32>(P, sms, s)
+                          : elem == kF16 ? bwd_x<kF16>(P, sms, s)
+                                         : bwd_x<kBF16>(P, sms, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
