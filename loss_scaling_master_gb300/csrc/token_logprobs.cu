@@ -21,6 +21,7 @@
 // bytes are taken by single elements, padded with -inf, which adds nothing.
 #include <algorithm>
 
+#include "f32x2.cuh"
 #include "internal.h"
 #include "mx.cuh"
 #include "pdl.cuh"
@@ -32,7 +33,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
 constexpr int kMaxParts = 8;  // CTAs of a cluster that share a row
-constexpr int kLoads = 4, kBwdLoads = 2;  // 16-byte loads a thread has in flight (and as many ahead in the gradient)
+constexpr int kLoads = 4;  // 16-byte loads a thread has in flight
 
 struct LogprobsFwd {
     const void *z;
@@ -67,13 +68,16 @@ struct Pieces {
     }
     __device__ __forceinline__ int first(int i) const { return base + i * VN; }
     __device__ __forceinline__ bool whole(int i) const { return first(i) >= 0 && first(i) <= cols - VN; }
+    __device__ __forceinline__ uint4 load_whole(int i) const {
+        return ld16(row + int64_t(first(i)) * (XT == kF32 ? 4 : 2));
+    }
     // the raw words; -inf for what does not exist
     __device__ __forceinline__ uint4 load(int i) const {
         constexpr uint32_t none = XT == kF32 ? 0xFF800000u : XT == kF16 ? 0xFC00FC00u : 0xFF80FF80u;
         uint4 u = make_uint4(none, none, none, none);
         if (i >= count) return u;
         const int f = first(i);
-        if (whole(i)) return ld16(row + int64_t(f) * (XT == kF32 ? 4 : 2));
+        if (whole(i)) return load_whole(i);
         uint32_t w[4] = {none, none, none, none};
 #pragma unroll
         for (int e = 0; e < VN; ++e) {
@@ -90,18 +94,16 @@ struct Pieces {
 };
 
 template <int XT>
-__device__ __forceinline__ void widen(uint4 u, float (&y)[XT == kF32 ? 4 : 8]) {
+__device__ __forceinline__ void widen(uint4 u, f2 (&y)[Pieces<XT>::VN / 2]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (XT == kF32) {
+        y[0] = make_f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        y[1] = make_f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if constexpr (XT == kF32) {
-            y[j] = __uint_as_float(w[j]);
-        } else if constexpr (XT == kBF16) {
-            y[2 * j] = __uint_as_float(w[j] << 16);
-            y[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        } else {
-            y[2 * j] = f16_bits_to_f32(w[j] & 0xFFFFu);
-            y[2 * j + 1] = f16_bits_to_f32(w[j] >> 16);
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (XT == kBF16) y[j] = make_f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+            else y[j] = make_f2(f16_bits_to_f32(w[j] & 0xFFFFu), f16_bits_to_f32(w[j] >> 16));
         }
     }
 }
@@ -130,6 +132,15 @@ __device__ __forceinline__ float largest(uint4 u) {
 // that a zero weight never meets an infinity.
 constexpr float kFar = -1e4f;
 
+__device__ __forceinline__ f2 exp2_both(f2 u) {
+    const float2 s = split(u);
+    return make_f2(exp2_flush(s.x), exp2_flush(s.y));
+}
+__device__ __forceinline__ f2 at_least(f2 u, float low) {
+    const float2 s = split(u);
+    return make_f2(fmaxf(s.x, low), fmaxf(s.y, low));
+}
+
 // The running maximum and the sums relative to it.  A NaN reaches the sums.
 struct Sums {
     float m = kLowest, s = 0.0f, w = 0.0f;
@@ -139,11 +150,26 @@ struct Sums {
         s *= c;
         m = to;
     }
-    template <bool ENT>
-    __device__ __forceinline__ void add(float z) {
-        const float d = z - m, e = exp2_flush(d * kLog2e);
-        s += e;
-        if (ENT) w = __fmaf_rn(e, fmaxf(d, kFar), w);
+    // n pieces' elements, of which big is the largest; ENT: with w
+    template <int XT, bool ENT>
+    __device__ __forceinline__ void add(const uint4 (&u)[kLoads], int n, float big) {
+        raise(fmaxf(m, big));
+        const f2 nm = both(-m);
+        f2 s2 = both(0.0f), w2 = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            if (j >= n) break;
+            f2 y[Pieces<XT>::VN / 2];
+            widen<XT>(u[j], y);
+#pragma unroll
+            for (int e = 0; e < Pieces<XT>::VN / 2; ++e) {
+                const f2 d = add2(y[e], nm), x = exp2_both(mul2(d, both(kLog2e)));
+                s2 = add2(s2, x);
+                if (ENT) w2 = fma2(x, at_least(d, kFar), w2);
+            }
+        }
+        s += sum2(s2);
+        if (ENT) w += sum2(w2);
     }
     __device__ __forceinline__ void join(float m2, float s2, float w2) {
         raise(fmaxf(m, m2));
@@ -232,11 +258,12 @@ struct Best {
             const uint4 x = make_uint4(__shfl_sync(0xFFFFFFFFu, u.x, src), __shfl_sync(0xFFFFFFFFu, u.y, src),
                                        __shfl_sync(0xFFFFFFFFu, u.z, src), __shfl_sync(0xFFFFFFFFu, u.w, src));
             const int f = __shfl_sync(0xFFFFFFFFu, first, src);
-            float y[VN], v = -INFINITY;
+            f2 y[VN / 2];
+            float v = -INFINITY;
             widen<XT>(x, y);
 #pragma unroll
             for (int e = 0; e < VN; ++e)
-                if (lane == e) v = y[e];
+                if (lane == e) v = e % 2 ? split(y[e / 2]).y : split(y[e / 2]).x;
             // what is not there is -inf, which never enters
             offer(v >= bound ? v : -INFINITY, v >= bound && v > -INFINITY ? f + lane : INT32_MAX, k);
         }
@@ -267,12 +294,22 @@ __device__ __forceinline__ float sort_values(float v) {
 
 // The k best of what this CTA's threads have read, big the largest that each has seen
 // (not NaN): in warp 0's list.
-template <int XT, int THREADS>
+// Of the threads that share a row.
+template <int THREADS>
+__device__ __forceinline__ void row_sync() {
+    if constexpr (THREADS == 32) __syncwarp();
+    else __syncthreads();
+}
+
+template <int XT, int THREADS, int ROWS>
 __device__ __forceinline__ Best top_of(const Pieces<XT> &row, int first_piece, int step, float big, int k) {
     constexpr int WARPS = THREADS / 32;
-    __shared__ float s_big[WARPS][32];
-    __shared__ int s_hot[THREADS], s_count;
+    __shared__ float s_bigs[ROWS][WARPS][32];
+    __shared__ int s_hots[ROWS][THREADS], s_counts[ROWS];
     __shared__ Entry s_list[WARPS][32];
+    auto &s_big = s_bigs[threadIdx.y];
+    auto &s_hot = s_hots[threadIdx.y];
+    int &s_count = s_counts[threadIdx.y];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the k-th largest of the threads' largest
     float v = sort_values(big);
@@ -280,13 +317,13 @@ __device__ __forceinline__ Best top_of(const Pieces<XT> &row, int first_piece, i
     if (threadIdx.x == 0) s_count = 0;
 #pragma unroll
     for (int half = WARPS / 2; half > 0; half /= 2) {
-        __syncthreads();
+        row_sync<THREADS>();
         if (warp < half) {
             v = settle_values(fmaxf(v, s_big[warp + half][31 - lane]));
             s_big[warp][lane] = v;
         }
     }
-    __syncthreads();
+    row_sync<THREADS>();
     const float bound = s_big[0][k - 1];
     // who reached it (in any order: lists are in one order whatever comes first)
     const uint32_t hot = __ballot_sync(0xFFFFFFFFu, big >= bound && big > -INFINITY);
@@ -296,7 +333,7 @@ __device__ __forceinline__ Best top_of(const Pieces<XT> &row, int first_piece, i
         at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(hot & ((1u << lane) - 1));
         if ((hot >> lane) & 1) s_hot[at] = int(threadIdx.x);
     }
-    __syncthreads();
+    row_sync<THREADS>();
     Best best;
     const int n = s_count;
     for (int h = warp; h < n; h += WARPS) {
@@ -304,10 +341,10 @@ __device__ __forceinline__ Best top_of(const Pieces<XT> &row, int first_piece, i
         for (int j = lane; i0 + (j - lane) * step < row.count; j += 32)
             best.offer_piece<XT>(row.load(i0 + j * step), row.first(i0 + j * step), bound, k);
     }
-    s_list[warp][lane] = best.mine;
+    if (WARPS > 1) s_list[warp][lane] = best.mine;
 #pragma unroll
     for (int half = WARPS / 2; half > 0; half /= 2) {
-        __syncthreads();
+        row_sync<THREADS>();
         if (warp < half) {
             best.merge(s_list[warp + half][lane]);
             s_list[warp][lane] = best.mine;
@@ -316,8 +353,10 @@ __device__ __forceinline__ Best top_of(const Pieces<XT> &row, int first_piece, i
     return best;
 }
 
-template <int XT, int THREADS, bool TOP>
-__global__ void __launch_bounds__(THREADS, TOP ? 1024 / THREADS : 2048 / THREADS) logprobs_fwd_kernel(LogprobsFwd P) {
+// THREADS share a row (x), ROWS rows a CTA (y; one where a row has more than a warp).
+template <int XT, int THREADS, int ROWS, bool TOP>
+__global__ void __launch_bounds__(THREADS *ROWS, (TOP ? 1024 : 1536) / (THREADS * ROWS))
+    logprobs_fwd_kernel(LogprobsFwd P) {
     constexpr int WARPS = THREADS / 32, VN = Pieces<XT>::VN;
     __shared__ float s_m[WARPS], s_s[WARPS], s_w[WARPS];
     __shared__ Entry s_top[32], s_tops[TOP ? kMaxParts : 1][32];
@@ -327,7 +366,8 @@ __global__ void __launch_bounds__(THREADS, TOP ? 1024 / THREADS : 2048 / THREADS
     uint32_t parts;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
     const uint32_t rank = parts > 1 ? cluster_rank() : 0;
-    const int64_t r = int64_t(blockIdx.x / parts);
+    const int64_t r = int64_t(blockIdx.x / parts) * ROWS + threadIdx.y;
+    if (ROWS > 1 && r >= P.rows) return;  // whole warps, which wait for no other
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = P.t ? P.t[r] : 0;
     if (P.t && t < 0) {  // the same in all CTAs of the cluster
@@ -350,37 +390,44 @@ __global__ void __launch_bounds__(THREADS, TOP ? 1024 / THREADS : 2048 / THREADS
     const int step = int(parts) * THREADS;
     for (int i0 = int(rank) * THREADS; i0 < row.count; i0 += kLoads * step) {
         uint4 u[kLoads];
+        int n = kLoads;  // loads that any thread has
+        // (one test for all: with one a load, a load waited for the last)
+        if (row.whole(i0) && row.whole(i0 + (kLoads - 1) * step + THREADS - 1)) {
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) u[j] = row.load(i0 + j * step + int(threadIdx.x));
+            for (int j = 0; j < kLoads; ++j) u[j] = row.load_whole(i0 + j * step + int(threadIdx.x));
+        } else {
+            n = 0;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                u[j] = row.load(i0 + j * step + int(threadIdx.x));
+                n += i0 + j * step < row.count;
+            }
+        }
         float big = largest<XT>(u[0]);
 #pragma unroll
         for (int j = 1; j < kLoads; ++j) big = fmaxf(big, largest<XT>(u[j]));
         if (TOP) most = fmaxf(most, big);
-        a.raise(fmaxf(a.m, big));
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            float y[VN];
-            widen<XT>(u[j], y);
-#pragma unroll
-            for (int e = 0; e < VN; ++e) a.add<true>(y[e]);
-        }
+        if (P.ent) a.add<XT, true>(u, n, big);
+        else a.add<XT, false>(u, n, big);
     }
     Best best;
     if constexpr (TOP) {
-        best = top_of<XT, THREADS>(row, int(rank) * THREADS, step, most, P.k);
-        if (warp == 0) s_top[lane] = best.mine;
+        best = top_of<XT, THREADS, ROWS>(row, int(rank) * THREADS, step, most, P.k);
+        if (WARPS > 1 && warp == 0) s_top[lane] = best.mine;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         a.join(__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
                __shfl_xor_sync(0xFFFFFFFFu, a.w, o));
-    if (lane == 0) {
-        s_m[warp] = a.m;
-        s_s[warp] = a.s;
-        s_w[warp] = a.w;
+    if constexpr (WARPS > 1) {
+        if (lane == 0) {
+            s_m[warp] = a.m;
+            s_s[warp] = a.s;
+            s_w[warp] = a.w;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    if (warp == 0) {
+    if (WARPS > 1 && warp == 0) {
         // the warps' sums, a lane each, in one order
         a = Sums();
         if (lane < WARPS) {
@@ -394,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, TOP ? 1024 / THREADS : 2048 / THREADS
                    __shfl_xor_sync(0xFFFFFFFFu, a.w, o));
         if (lane == 0) s_cta = make_float3(a.m, a.s, a.w);
     }
-    if (parts > 1) {
+    if (WARPS > 1 && parts > 1) {
         __syncwarp();
         cluster_sync();
         if (rank == 0 && warp == 0) {
@@ -462,13 +509,14 @@ struct LogprobsBwd {
 // One CTA a share of a row: every element is read and written once, and what the row
 // adds are five numbers.  With u = log p:
 //   dz = p (A + B u) [+ S dlogp for the token],  A = -S (dlogp + dent H), B = -S dent
-template <int XT, int THREADS>
-__global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(LogprobsBwd P) {
-    constexpr int VN = Pieces<XT>::VN, esz = XT == kF32 ? 4 : 2, U = kBwdLoads;
+template <int XT, int THREADS, int ROWS>
+__global__ void __launch_bounds__(THREADS *ROWS) logprobs_bwd_kernel(LogprobsBwd P) {
+    constexpr int VN = Pieces<XT>::VN, esz = XT == kF32 ? 4 : 2, U = kLoads;
     pdl_wait();
     pdl_trigger();
-    const int64_t r = blockIdx.x / unsigned(P.chunks);
-    const int chunk = int(blockIdx.x - unsigned(r) * unsigned(P.chunks));
+    const int64_t r = int64_t(blockIdx.x / unsigned(P.chunks)) * ROWS + threadIdx.y;
+    if (ROWS > 1 && r >= P.rows) return;
+    const int chunk = int(blockIdx.x % unsigned(P.chunks));
     const Pieces<XT> row(P.z, r * P.ld, P.cols);
     char *out = static_cast<char *>(P.dz) + r * P.dld * esz;
     const bool aligned = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.row)) & 15) == 0;
@@ -478,93 +526,116 @@ __global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(LogprobsBwd P) {
     const float2 st = P.stats[r];
     const bool used = t >= 0;
     const int per = (row.count + P.chunks - 1) / P.chunks, end = min(row.count, (chunk + 1) * per);
-    int i = chunk * per + int(threadIdx.x);
-    uint4 u[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) u[j] = used && i + j * THREADS < end ? row.load(i + j * THREADS) : make_uint4(0, 0, 0, 0);
     const float dlogp = dl * scale, dent = de * scale, B = -dent, BH = B * ent;
     float A = BH - dlogp;
     if (t >= P.cols && P.t) A = NAN;
     const int at = P.dlogp && used && t < P.cols ? int(t) : -VN;
-    for (; i < end; i += U * THREADS) {
-        uint4 nxt[U];
+    const f2 nm = both(-st.x), nl = both(-st.y), nl2 = both(-st.y * kLog2e), A2 = both(A), B2 = both(B);
+
+    auto gradient = [&](const uint4 &u, int f, f2 (&y)[VN / 2]) {
+        if (!used) {
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int n = i + (U + j) * THREADS;
-            nxt[j] = used && n < end ? row.load(n) : make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < VN / 2; ++e) y[e] = both(0.0f);
+            return;
+        }
+        widen<XT>(u, y);
+        float token = 0.0f;
+        const bool here = unsigned(at - f) < unsigned(VN);
+        if (here) {
+#pragma unroll
+            for (int e = 0; e < VN; ++e)
+                if (f + e == at) token = e % 2 ? split(y[e / 2]).y : split(y[e / 2]).x;
         }
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int n = i + j * THREADS;
-            if (n >= end) break;
-            const int f = row.first(n);
-            float y[VN];
-            if (used) {
-                widen<XT>(u[j], y);
-                float token = 0.0f;
+        for (int e = 0; e < VN / 2; ++e) {
+            const f2 d = add2(y[e], nm), p = exp2_both(fma2(d, both(kLog2e), nl2));
+            y[e] = mul2(p, P.dent ? fma2(B2, at_least(add2(d, nl), kFar), A2) : A2);
+        }
+        if (here) {
+            // dlogp (1 - p), without the difference's rounding where p is near 1
+            const float lp = (token - st.x) - st.y;
+            const float g =
+                __fmaf_rn(-dlogp, expm1f(lp), exp2_flush(lp * kLog2e) * __fmaf_rn(B, fmaxf(lp, kFar), BH));
 #pragma unroll
-                for (int e = 0; e < VN; ++e) {
-                    const float lp = (y[e] - st.x) - st.y;
-                    if (f + e == at) token = lp;
-                    y[e] = exp2_flush(lp * kLog2e) * __fmaf_rn(B, fmaxf(lp, kFar), A);
-                }
-                if (unsigned(at - f) < unsigned(VN)) {
-                    // dlogp (1 - p), without the difference's rounding where p is near 1
-                    const float g = __fmaf_rn(-dlogp, expm1f(token),
-                                              exp2_flush(token * kLog2e) * __fmaf_rn(B, fmaxf(token, kFar), BH));
-#pragma unroll
-                    for (int e = 0; e < VN; ++e)
-                        if (f + e == at) y[e] = g;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < VN; ++e) y[e] = 0.0f;
-            }
-            if (aligned && row.whole(n)) {
-                uint32_t w[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if constexpr (XT == kF32) w[q] = __float_as_uint(y[q]);
-                    else w[q] = f32x2_to_16x2<XT>(y[2 * q], y[2 * q + 1]);
-                }
-                st16(out + int64_t(f) * esz, make_uint4(w[0], w[1], w[2], w[3]));
-            } else {
-#pragma unroll
-                for (int e = 0; e < VN; ++e)
-                    if (f + e >= 0 && f + e < P.cols) store_elem<XT>(out, f + e, y[e]);
+            for (int e = 0; e < VN / 2; ++e) {
+                const float2 v = split(y[e]);
+                y[e] = make_f2(f + 2 * e == at ? g : v.x, f + 2 * e + 1 == at ? g : v.y);
             }
         }
+    };
+    auto store_whole = [&](int f, const f2 (&y)[VN / 2]) {
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < U; ++j) u[j] = nxt[j];
+        for (int q = 0; q < 4; ++q) {
+            const float2 v = split(y[XT == kF32 ? q / 2 : q]);
+            if constexpr (XT == kF32) w[q] = __float_as_uint(q % 2 ? v.y : v.x);
+            else w[q] = f32x2_to_16x2<XT>(v.x, v.y);
+        }
+        st16(out + int64_t(f) * esz, make_uint4(w[0], w[1], w[2], w[3]));
+    };
+    for (int i0 = chunk * per; i0 < end; i0 += U * THREADS) {
+        const int last = i0 + U * THREADS - 1;
+        if (aligned && last < end && row.whole(i0) && row.whole(last)) {
+            uint4 u[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                u[j] = used ? row.load_whole(i0 + j * THREADS + int(threadIdx.x)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int f = row.first(i0 + j * THREADS + int(threadIdx.x));
+                f2 y[VN / 2];
+                gradient(u[j], f, y);
+                store_whole(f, y);
+            }
+            continue;
+        }
+#pragma unroll 1
+        for (int i = i0 + int(threadIdx.x); i < min(end, i0 + U * THREADS); i += THREADS) {
+            const int f = row.first(i);
+            f2 y[VN / 2];
+            gradient(used ? row.load(i) : make_uint4(0, 0, 0, 0), f, y);
+            if (aligned && row.whole(i)) {
+                store_whole(f, y);
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < VN; ++e)
+                if (f + e >= 0 && f + e < P.cols)
+                    store_elem<XT>(out, f + e, e % 2 ? split(y[e / 2]).y : split(y[e / 2]).x);
+        }
     }
 }
 
-template <int XT, int THREADS, bool TOP>
+constexpr int kShortRows = 4;  // a CTA, a warp each
+template <int XT, int THREADS, int ROWS>
 cudaError_t fwd(const LogprobsFwd &P, int parts, cudaStream_t s) {
-    return launch_pdl_cluster(logprobs_fwd_kernel<XT, THREADS, TOP>, dim3(unsigned(P.rows * parts)), dim3(THREADS), 0,
-                              parts, s, P);
+    const dim3 grid(unsigned((P.rows + ROWS - 1) / ROWS * parts)), block(THREADS, ROWS);
+    return P.k ? launch_pdl_cluster(logprobs_fwd_kernel<XT, THREADS, ROWS, true>, grid, block, 0, parts, s, P)
+               : launch_pdl_cluster(logprobs_fwd_kernel<XT, THREADS, ROWS, false>, grid, block, 0, parts, s, P);
 }
 template <int XT>
 cudaError_t fwd_x(const LogprobsFwd &P, int device, cudaStream_t s) {
     const int pieces = P.cols / Pieces<XT>::VN + 1, sms = sm_count(device);
-    if (pieces <= 512 && P.rows >= sms)
-        return P.k ? fwd<XT, 128, true>(P, 1, s) : fwd<XT, 128, false>(P, 1, s);
+    if (pieces <= 260 || (pieces <= 520 && P.rows >= 16 * sms)) return fwd<XT, 32, kShortRows>(P, 1, s);
+    if (pieces <= 1030 && P.rows >= 2 * sms) return fwd<XT, 128, 1>(P, 1, s);
     int parts = 1;
     while (parts < kMaxParts && P.rows * parts <= 2 * sms && pieces > parts * 256) parts *= 2;
-    return P.k ? fwd<XT, 256, true>(P, parts, s) : fwd<XT, 256, false>(P, parts, s);
+    return fwd<XT, 256, 1>(P, parts, s);
 }
 template <int XT>
 cudaError_t bwd_x(LogprobsBwd P, int sms, cudaStream_t s) {
     const int64_t pieces = P.cols / Pieces<XT>::VN + 2;  // a row that starts inside a piece has one more
-    if (pieces <= 512) {
-        P.chunks = 1;
-        return launch_pdl(logprobs_bwd_kernel<XT, 128>, dim3(unsigned(P.rows)), dim3(128), 0, s, P);
-    }
+    P.chunks = 1;
+    if (pieces <= 260)
+        return launch_pdl(logprobs_bwd_kernel<XT, 32, kShortRows>, dim3(unsigned((P.rows + kShortRows - 1) / kShortRows)),
+                          dim3(32, kShortRows), 0, s, P);
+    if (pieces <= 1030 && P.rows >= 2 * sms)
+        return launch_pdl(logprobs_bwd_kernel<XT, 128, 1>, dim3(unsigned(P.rows)), dim3(128), 0, s, P);
     // shares of 8 loads a thread, smaller ones where rows are few
     int64_t chunks = (pieces + 8 * 256 - 1) / (8 * 256);
     while (chunks * P.rows < 4 * sms && chunks * 512 < pieces) chunks *= 2;
     P.chunks = int(chunks);
-    return launch_pdl(logprobs_bwd_kernel<XT, 256>, dim3(unsigned(P.rows * P.chunks)), dim3(256), 0, s, P);
+    return launch_pdl(logprobs_bwd_kernel<XT, 256, 1>, dim3(unsigned(P.rows * P.chunks)), dim3(256), 0, s, P);
 }
 
 }  // namespace
