@@ -33,7 +33,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
 constexpr int kMaxParts = 8;  // CTAs of a cluster that share a row
-constexpr int kLoads = 4;  // 16-byte loads a thread has in flight
+constexpr int kLoads = 8, kBwdLoads = 2;  // 16-byte loads a thread has in flight
 
 struct LogprobsFwd {
     const void *z;
@@ -153,7 +153,7 @@ struct Sums {
     // n pieces' elements, of which big is the largest; ENT: with w
     template <int XT, bool ENT>
     __device__ __forceinline__ void add(const uint4 (&u)[kLoads], int n, float big) {
-        raise(fmaxf(m, big));
+        if (__any_sync(0xFFFFFFFFu, big > m)) raise(fmaxf(m, big));  // soon rare
         const f2 nm = both(-m);
         f2 s2 = both(0.0f), w2 = both(0.0f);
 #pragma unroll
@@ -292,8 +292,6 @@ __device__ __forceinline__ float sort_values(float v) {
     return settle_values(v);
 }
 
-// The k best of what this CTA's threads have read, big the largest that each has seen
-// (not NaN): in warp 0's list.
 // Of the threads that share a row.
 template <int THREADS>
 __device__ __forceinline__ void row_sync() {
@@ -301,65 +299,120 @@ __device__ __forceinline__ void row_sync() {
     else __syncthreads();
 }
 
+// Entries in order by counting those before each: `put(rank, entry)` for the first 32.
+template <int THREADS, class F>
+__device__ __forceinline__ void by_rank(const Entry *list, int n, F put) {
+    for (int e = int(threadIdx.x); e < n; e += THREADS) {
+        const Entry mine = list[e];
+        int rank = 0;
+#pragma unroll 4
+        for (int o = 0; o < n; ++o) rank += before(list[o].v, list[o].i, mine);
+        if (rank < 32) put(rank, mine);
+    }
+}
+
+// The k best of what the row's threads of this CTA have read, big the largest that each
+// has seen (not NaN), into s_top; filled up with -inf.
 template <int XT, int THREADS, int ROWS>
-__device__ __forceinline__ Best top_of(const Pieces<XT> &row, int first_piece, int step, float big, int k) {
-    constexpr int WARPS = THREADS / 32;
-    __shared__ float s_bigs[ROWS][WARPS][32];
-    __shared__ int s_hots[ROWS][THREADS], s_counts[ROWS];
-    __shared__ Entry s_list[WARPS][32];
-    auto &s_big = s_bigs[threadIdx.y];
-    auto &s_hot = s_hots[threadIdx.y];
-    int &s_count = s_counts[threadIdx.y];
+__device__ __forceinline__ void top_of(const Pieces<XT> &row, int first_piece, int step, float big, int k,
+                                       Entry (&s_top)[32]) {
+    constexpr int WARPS = THREADS / 32, VN = Pieces<XT>::VN, QUEUE = WARPS == 1 ? 64 : 256;
+    __shared__ float s_bigs[ROWS][THREADS];
+    __shared__ int s_hots[ROWS][THREADS], s_counts[ROWS][2];
+    __shared__ Entry s_queues[ROWS][QUEUE];
+    float *s_big = s_bigs[threadIdx.y];
+    int *s_hot = s_hots[threadIdx.y], *s_count = s_counts[threadIdx.y];
+    Entry *queue = s_queues[threadIdx.y];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x < 2) s_count[threadIdx.x] = 0;
+    if (threadIdx.x < 32) s_top[threadIdx.x] = {-INFINITY, -1};
+
     // the k-th largest of the threads' largest
-    float v = sort_values(big);
-    s_big[warp][lane] = v;
-    if (threadIdx.x == 0) s_count = 0;
+    float bound;
+    {
+        float v = sort_values(big);
+        if constexpr (WARPS > 1) {
+            s_big[threadIdx.x] = v;
 #pragma unroll
-    for (int half = WARPS / 2; half > 0; half /= 2) {
-        row_sync<THREADS>();
-        if (warp < half) {
-            v = settle_values(fmaxf(v, s_big[warp + half][31 - lane]));
-            s_big[warp][lane] = v;
+            for (int half = WARPS / 2; half > 0; half /= 2) {
+                row_sync<THREADS>();
+                if (warp < half) {
+                    v = settle_values(fmaxf(v, s_big[32 * (warp + half) + 31 - lane]));
+                    s_big[threadIdx.x] = v;
+                }
+            }
+            row_sync<THREADS>();
+            bound = s_big[k - 1];
+        } else {
+            bound = __shfl_sync(0xFFFFFFFFu, v, k - 1);
+            __syncwarp();
         }
     }
-    row_sync<THREADS>();
-    const float bound = s_big[0][k - 1];
-    // who reached it (in any order: lists are in one order whatever comes first)
+    // who reached it (in any order: what follows is in one order whatever comes first)
     const uint32_t hot = __ballot_sync(0xFFFFFFFFu, big >= bound && big > -INFINITY);
     if (hot) {
         int at = 0;
-        if (lane == 0) at = atomicAdd(&s_count, __popc(hot));
+        if (lane == 0) at = atomicAdd(&s_count[0], __popc(hot));
         at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(hot & ((1u << lane) - 1));
         if ((hot >> lane) & 1) s_hot[at] = int(threadIdx.x);
     }
     row_sync<THREADS>();
+    const int hots = s_count[0];
+    for (int h = warp; h < hots; h += WARPS) {
+        const int i0 = first_piece + s_hot[h];
+        for (int i = i0 + lane * step; i < row.count; i += 32 * step) {
+            const uint4 u = row.load(i);
+            if (!(largest<XT>(u) >= bound)) continue;
+            f2 y[VN / 2];
+            widen<XT>(u, y);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) {
+                const float v = e % 2 ? split(y[e / 2]).y : split(y[e / 2]).x;
+                if (v >= bound && v > -INFINITY) {
+                    const int at = atomicAdd(&s_count[1], 1);
+                    if (at < QUEUE) queue[at] = {v, row.first(i) + e};
+                }
+            }
+        }
+    }
+    row_sync<THREADS>();
+    const int n = s_count[1];
+    if (n <= QUEUE) {
+        by_rank<THREADS>(queue, n, [&](int rank, Entry e) { s_top[rank] = e; });
+        row_sync<THREADS>();
+        return;
+    }
+    // too many (equal values, say): lists kept by warps, then joined in halves
     Best best;
-    const int n = s_count;
-    for (int h = warp; h < n; h += WARPS) {
+    for (int h = warp; h < hots; h += WARPS) {
         const int i0 = first_piece + s_hot[h];
         for (int j = lane; i0 + (j - lane) * step < row.count; j += 32)
             best.offer_piece<XT>(row.load(i0 + j * step), row.first(i0 + j * step), bound, k);
     }
-    if (WARPS > 1) s_list[warp][lane] = best.mine;
+    if constexpr (WARPS > 1) {
+        Entry(*list)[32] = reinterpret_cast<Entry(*)[32]>(queue);
+        static_assert(QUEUE >= 32 * WARPS, "a list a warp");
+        list[warp][lane] = best.mine;
 #pragma unroll
-    for (int half = WARPS / 2; half > 0; half /= 2) {
-        row_sync<THREADS>();
-        if (warp < half) {
-            best.merge(s_list[warp + half][lane]);
-            s_list[warp][lane] = best.mine;
+        for (int half = WARPS / 2; half > 0; half /= 2) {
+            row_sync<THREADS>();
+            if (warp < half) {
+                best.merge(list[warp + half][lane]);
+                list[warp][lane] = best.mine;
+            }
         }
     }
-    return best;
+    if (warp == 0) s_top[lane] = best.mine;
+    row_sync<THREADS>();
 }
 
 // THREADS share a row (x), ROWS rows a CTA (y; one where a row has more than a warp).
 template <int XT, int THREADS, int ROWS, bool TOP>
-__global__ void __launch_bounds__(THREADS *ROWS, (TOP ? 1024 : 1536) / (THREADS * ROWS))
+__global__ void __launch_bounds__(THREADS *ROWS, 1024 / (THREADS * ROWS))
     logprobs_fwd_kernel(LogprobsFwd P) {
     constexpr int WARPS = THREADS / 32, VN = Pieces<XT>::VN;
     __shared__ float s_m[WARPS], s_s[WARPS], s_w[WARPS];
-    __shared__ Entry s_top[32], s_tops[TOP ? kMaxParts : 1][32];
+    __shared__ Entry s_tops[TOP ? ROWS : 1][32], s_all[TOP && WARPS > 1 ? kMaxParts * 32 : 1];
     __shared__ float3 s_cta;
     pdl_wait();
     pdl_trigger();
@@ -410,11 +463,9 @@ __global__ void __launch_bounds__(THREADS *ROWS, (TOP ? 1024 : 1536) / (THREADS 
         if (P.ent) a.add<XT, true>(u, n, big);
         else a.add<XT, false>(u, n, big);
     }
-    Best best;
-    if constexpr (TOP) {
-        best = top_of<XT, THREADS, ROWS>(row, int(rank) * THREADS, step, most, P.k);
-        if (WARPS > 1 && warp == 0) s_top[lane] = best.mine;
-    }
+    Entry(&s_top)[32] = s_tops[TOP ? threadIdx.y : 0];
+    if constexpr (TOP)
+        top_of<XT, THREADS, ROWS>(row, int(rank) * THREADS, step, most, P.k, s_top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         a.join(__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
@@ -458,21 +509,25 @@ __global__ void __launch_bounds__(THREADS *ROWS, (TOP ? 1024 : 1536) / (THREADS 
                 a.join(__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
                        __shfl_xor_sync(0xFFFFFFFFu, a.w, o));
         }
-        if constexpr (TOP && WARPS >= kMaxParts) {
-            // warp q: the list of CTA q; then in halves
+        if constexpr (TOP && WARPS > 1) {
             if (rank == 0) {
+                // warp q: the list of CTA q; then in halves
+                static_assert(WARPS >= kMaxParts || THREADS == 128, "a list a warp");
+                Best best;
                 if (warp < int(parts)) {
                     const uint32_t at = cluster_addr(&s_top[lane], warp);
                     best.mine = {__uint_as_float(cluster_ld(at)), int(cluster_ld(at + 4))};
-                    s_tops[warp][lane] = best.mine;
+                    s_all[32 * warp + lane] = best.mine;
                 }
+#pragma unroll
                 for (int half = kMaxParts / 2; half > 0; half /= 2) {
                     __syncthreads();
                     if (warp < half && warp + half < int(parts)) {
-                        best.merge(s_tops[warp + half][lane]);
-                        s_tops[warp][lane] = best.mine;
+                        best.merge(s_all[32 * (warp + half) + lane]);
+                        s_all[32 * warp + lane] = best.mine;
                     }
                 }
+                if (warp == 0) s_top[lane] = best.mine;
             }
         }
         __syncwarp();
@@ -489,9 +544,10 @@ __global__ void __launch_bounds__(THREADS *ROWS, (TOP ? 1024 : 1536) / (THREADS 
         if (P.stats) P.stats[r] = make_float2(m, logs);
     }
     if (TOP && lane < P.k) {
-        const bool none = best.mine.v == -INFINITY;
-        P.ids[r * P.k + lane] = none ? -1 : best.mine.i;
-        P.top[r * P.k + lane] = none ? -INFINITY : (best.mine.v - m) - logs;
+        const Entry e = s_top[lane];
+        const bool none = e.v == -INFINITY;
+        P.ids[r * P.k + lane] = none ? -1 : e.i;
+        P.top[r * P.k + lane] = none ? -INFINITY : (e.v - m) - logs;
     }
 }
 
@@ -511,7 +567,7 @@ struct LogprobsBwd {
 //   dz = p (A + B u) [+ S dlogp for the token],  A = -S (dlogp + dent H), B = -S dent
 template <int XT, int THREADS, int ROWS>
 __global__ void __launch_bounds__(THREADS *ROWS) logprobs_bwd_kernel(LogprobsBwd P) {
-    constexpr int VN = Pieces<XT>::VN, esz = XT == kF32 ? 4 : 2, U = kLoads;
+    constexpr int VN = Pieces<XT>::VN, esz = XT == kF32 ? 4 : 2, U = kBwdLoads;
     pdl_wait();
     pdl_trigger();
     const int64_t r = int64_t(blockIdx.x / unsigned(P.chunks)) * ROWS + threadIdx.y;
@@ -616,10 +672,10 @@ cudaError_t fwd(const LogprobsFwd &P, int parts, cudaStream_t s) {
 template <int XT>
 cudaError_t fwd_x(const LogprobsFwd &P, int device, cudaStream_t s) {
     const int pieces = P.cols / Pieces<XT>::VN + 1, sms = sm_count(device);
-    if (pieces <= 260 || (pieces <= 520 && P.rows >= 16 * sms)) return fwd<XT, 32, kShortRows>(P, 1, s);
-    if (pieces <= 1030 && P.rows >= 2 * sms) return fwd<XT, 128, 1>(P, 1, s);
+    if (P.k <= 8 && (pieces <= 260 || (pieces <= 520 && P.rows >= 16 * sms))) return fwd<XT, 32, kShortRows>(P, 1, s);
+    if (pieces <= 260 || (pieces <= 1030 && P.rows >= 2 * sms)) return fwd<XT, 128, 1>(P, 1, s);
     int parts = 1;
-    while (parts < kMaxParts && P.rows * parts <= 2 * sms && pieces > parts * 256) parts *= 2;
+    while (parts < kMaxParts && P.rows * parts <= 2 * sms && pieces > parts * 1024) parts *= 2;
     return fwd<XT, 256, 1>(P, parts, s);
 }
 template <int XT>
