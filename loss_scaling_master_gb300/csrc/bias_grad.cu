@@ -22,13 +22,13 @@ struct BiasBwd {
     int kb, otype;
 };
 
-template <int XT, int ACT, bool VEC>
-__global__ void __launch_bounds__(kSumThreads, kSumCtas) bias_bwd_kernel(BiasBwd P) {
-    using S = SumShape<VEC>;
+template <int XT, int ACT, class S>
+__global__ void __launch_bounds__(S::threads, S::ctas) bias_bwd_kernel(BiasBwd P) {
+    constexpr bool VEC = S::each == 8;
     constexpr int N = VEC ? 8 : 1, U = VEC ? 2 : 8;  // elements a thread and row, rows a step
     pdl_wait();
     pdl_trigger();
-    const SumShare at(P.rows);
+    const SumShare<S> at(P.rows);
     const int64_t c = at.col0 + int(threadIdx.x) % S::across * N;
     const bool in = c < P.cols;
     float a[N];
@@ -109,21 +109,88 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) bias_bwd_kernel(BiasBwd
             }
         }
     }
-    sum_join<VEC>(at, P.cols, a, P.db, P.otype);
+    sum_join<S>(at, P.cols, a, P.db, P.otype);
 }
 
 template <int XT, int ACT>
-cudaError_t go(const BiasBwd &P, bool vec, int sms, cudaStream_t s) {
-    return vec ? launch_sums(bias_bwd_kernel<XT, ACT, true>, P.rows, P.cols, SumShape<true>::groups, sms, s, P)
-               : launch_sums(bias_bwd_kernel<XT, ACT, false>, P.rows, P.cols, SumShape<false>::groups, sms, s, P);
+struct BiasFlat {
+    const BiasBwd &P;
+    int64_t all;
+    struct Raw {
+        RawGroup<XT> g;
+        uint2 q;
+    };
+    __device__ __forceinline__ Raw load(int64_t g, bool whole) const {
+        Raw r;
+        r.g.load(P.dy, g, whole, all);
+        r.q = make_uint2(0, 0);
+        if constexpr (ACT != kNoAct) {
+            if (whole) {
+                r.q = *reinterpret_cast<const uint2 *>(P.q + 8 * g);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t b = 8 * g + j < all ? P.q[8 * g + j] : 0u;
+                    if (j < 4) r.q.x |= b << (8 * j);
+                    else r.q.y |= b << (8 * (j - 4));
+                }
+            }
+        }
+        return r;
+    }
+    // c: column of element 0; elements before column 0 or behind the last one count for nothing
+    __device__ __forceinline__ void values(const Raw &raw, int64_t, int64_t r, int64_t c, float (&y)[8]) const {
+        raw8_to_f32<XT>(raw.g.u, y);
+        if constexpr (ACT != kNoAct) {
+            // 8 elements lie in at most two blocks
+            const int64_t c0 = max(c, int64_t(0)), b0 = c0 / kMxBlock, b1 = min(c + 7, P.cols - 1) / kMxBlock;
+            const float s0 = mx_scale(P.s[r * P.kb + b0]), s1 = mx_scale(P.s[r * P.kb + b1]);
+            float x[8];
+            e4m3x4_to_f32x4(raw.q.x, x);
+            e4m3x4_to_f32x4(raw.q.y, x + 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], c + j < (b0 + 1) * kMxBlock ? s0 : s1);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                float2 dz, unused;
+                act_grads<XT, ACT, false>(x[j], x[j + 1], 0.0f, 0.0f, y[j], y[j + 1], dz, unused);
+                y[j] = dz.x;
+                y[j + 1] = dz.y;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(int64_t g, int lo, int hi, const float (&y)[8]) const {
+        if constexpr (ACT != kNoAct) store_group<XT>(P.dz, g, lo, hi, y);
+    }
+};
+template <int XT, int ACT>
+__global__ void __launch_bounds__(SumFlat::threads, SumFlat::ctas) bias_bwd_flat_kernel(BiasBwd P) {
+    pdl_wait();
+    pdl_trigger();
+    const SumShare<SumFlat> at(P.rows);
+    BiasFlat<XT, ACT> op{P, P.rows * P.cols};
+    flat_sums(at, P.rows, P.cols, op, P.db, P.otype);
+}
+
+template <int XT, int ACT>
+cudaError_t go(const BiasBwd &P, bool aligned, int sms, cudaStream_t s) {
+    if (!aligned) return launch_sums<SumElem>(bias_bwd_kernel<XT, ACT, SumElem>, P.rows, P.cols, sms, s, P);
+    // the activations' longer way to a group's values needs CTAs enough to hide it (2047 x
+    // 1111 bf16 GELU 13.3 us, by single elements 10.4; 16383 x 5121 198 and 383)
+    if (P.cols % 8 && (ACT == kNoAct || !narrow_tiles(kBF16, P.cols, sms)))
+        return launch_sums<SumFlat>(bias_bwd_flat_kernel<XT, ACT>, P.rows, P.cols, sms, s, P);
+    if (P.cols % 8) return launch_sums<SumElem>(bias_bwd_kernel<XT, ACT, SumElem>, P.rows, P.cols, sms, s, P);
+    if (XT == kF32 || narrow_tiles(XT, P.cols, sms))
+        return launch_sums<SumVec<32>>(bias_bwd_kernel<XT, ACT, SumVec<32>>, P.rows, P.cols, sms, s, P);
+    return launch_sums<SumVec<64>>(bias_bwd_kernel<XT, ACT, SumVec<64>>, P.rows, P.cols, sms, s, P);
 }
 template <int XT>
-cudaError_t go_x(const BiasBwd &P, int act, bool vec, int sms, cudaStream_t s) {
+cudaError_t go_x(const BiasBwd &P, int act, bool aligned, int sms, cudaStream_t s) {
     switch (act) {
-    case AMP_ACT_GELU: return go<XT, AMP_ACT_GELU>(P, vec, sms, s);
-    case AMP_ACT_GELU_TANH: return go<XT, AMP_ACT_GELU_TANH>(P, vec, sms, s);
-    case AMP_ACT_SILU: return go<XT, AMP_ACT_SILU>(P, vec, sms, s);
-    default: return go<XT, kNoAct>(P, vec, sms, s);
+    case AMP_ACT_GELU: return go<XT, AMP_ACT_GELU>(P, aligned, sms, s);
+    case AMP_ACT_GELU_TANH: return go<XT, AMP_ACT_GELU_TANH>(P, aligned, sms, s);
+    case AMP_ACT_SILU: return go<XT, AMP_ACT_SILU>(P, aligned, sms, s);
+    default: return go<XT, kNoAct>(P, aligned, sms, s);
     }
 }
 
@@ -133,11 +200,11 @@ cudaError_t launch_bias_bwd(int act, const void *dy, int elem, int64_t rows, int
                             const uint8_t *sc, void *dz, void *db, int dbelem, int device, cudaStream_t s) {
     const BiasBwd P{dy, q, sc, dz, db, rows, cols, int((cols + kMxBlock - 1) / kMxBlock), dbelem};
     const auto off = [](const void *p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; };
-    const bool vec = cols % 8 == 0 && !off(dy, 15) && !off(dz, 15) && !off(q, 7);
+    const bool aligned = !off(dy, 15) && !off(dz, 15) && !off(q, 7);
     const int a = act < 0 ? int(kNoAct) : act, sms = sm_count(device);
-    const cudaError_t e = elem == kF32   ? go_x<kF32>(P, a, vec, sms, s)
-                          : elem == kF16 ? go_x<kF16>(P, a, vec, sms, s)
-                                         : go_x<kBF16>(P, a, vec, sms, s);
+    const cudaError_t e = elem == kF32   ? go_x<kF32>(P, a, aligned, sms, s)
+                          : elem == kF16 ? go_x<kF16>(P, a, aligned, sms, s)
+                                         : go_x<kBF16>(P, a, aligned, sms, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

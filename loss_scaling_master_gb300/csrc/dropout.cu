@@ -111,13 +111,12 @@ __global__ void __launch_bounds__(kThreads) dropout_elem_kernel(Dropout P) {
 }
 
 // The gradient with the bias's: by columns (column_sums.cuh).
-template <int XT, bool ALL>
-__global__ void __launch_bounds__(kSumThreads, kSumCtas) dropout_bias_vec_kernel(Dropout P) {
-    using S = SumShape<true>;
+template <int XT, bool ALL, class S>
+__global__ void __launch_bounds__(S::threads, S::ctas) dropout_bias_vec_kernel(Dropout P) {
     constexpr int U = XT == kF32 ? 2 : 4;
     pdl_wait();
     pdl_trigger();
-    const SumShare at(P.rows);
+    const SumShare<S> at(P.rows);
     const int32_t step = P.step ? *P.step : 0;
     const int64_t c = at.col0 + int(threadIdx.x) % S::across * 8;
     const bool in = c < P.cols;
@@ -144,20 +143,48 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) dropout_bias_vec_kernel
             stv<XT>(P.y, k, y);
         }
     }
-    sum_join<true>(at, P.cols, a, P.db, P.otype);
+    sum_join<S>(at, P.cols, a, P.db, P.otype);
+}
+// Rows of any length (flat_sums): a group of elements is one of the generator's.
+template <int XT, bool ALL>
+struct DropoutFlat {
+    const Dropout &P;
+    int64_t all;
+    int32_t step;
+    using Raw = RawGroup<XT>;
+    __device__ __forceinline__ Raw load(int64_t g, bool whole) const {
+        Raw r;
+        r.load(P.x, g, whole, all);
+        return r;
+    }
+    __device__ __forceinline__ void values(const Raw &raw, int64_t g, int64_t, int64_t, float (&y)[8]) const {
+        raw8_to_f32<XT>(raw.u, y);
+        drop8<ALL>(P, step, g, y);
+    }
+    __device__ __forceinline__ void store(int64_t g, int lo, int hi, const float (&y)[8]) const {
+        store_group<XT>(P.y, g, lo, hi, y);
+    }
+};
+template <int XT, bool ALL>
+__global__ void __launch_bounds__(SumFlat::threads, SumFlat::ctas) dropout_bias_flat_kernel(Dropout P) {
+    pdl_wait();
+    pdl_trigger();
+    const SumShare<SumFlat> at(P.rows);
+    DropoutFlat<XT, ALL> op{P, P.rows * P.cols, P.step ? *P.step : 0};
+    flat_sums(at, P.rows, P.cols, op, P.db, P.otype);
 }
 // Any size and address.  A warp's 32 columns of a row lie in at most 5 of the
 // generator's groups: 30 lanes make the masks of 6 rows.
 template <int XT, bool ALL>
-__global__ void __launch_bounds__(kSumThreads, kSumCtas) dropout_bias_elem_kernel(Dropout P) {
-    using S = SumShape<false>;
+__global__ void __launch_bounds__(SumElem::threads, SumElem::ctas) dropout_bias_elem_kernel(Dropout P) {
+    using S = SumElem;
     constexpr int U = 6;
     pdl_wait();
     pdl_trigger();
-    const SumShare at(P.rows);
+    const SumShare<S> at(P.rows);
     const int32_t step = P.step ? *P.step : 0;
     const int lane = threadIdx.x & 31;
-    const int64_t c0 = at.col0 + (int(threadIdx.x) % S::across & ~31), c = c0 + lane;
+    const int64_t c0 = at.col0, c = c0 + lane;  // a warp is a row of the tile
     const bool in = c < P.cols;
     float a[1] = {0.0f};
     for (int64_t r0 = at.row0 + int(threadIdx.x) / S::across; r0 < at.row1; r0 += U * S::groups) {
@@ -181,7 +208,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) dropout_bias_elem_kerne
             }
         }
     }
-    sum_join<false>(at, P.cols, a, P.db, P.otype);
+    sum_join<S>(at, P.cols, a, P.db, P.otype);
 }
 
 bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
@@ -190,9 +217,11 @@ template <int XT, bool ALL>
 cudaError_t go(const Dropout &P, int sms, cudaStream_t s) {
     const bool vec = !off16(P.x) && !off16(P.res) && !off16(P.y);
     if (P.db) {
-        return vec && P.cols % 8 == 0
-                   ? launch_sums(dropout_bias_vec_kernel<XT, ALL>, P.rows, P.cols, SumShape<true>::groups, sms, s, P)
-                   : launch_sums(dropout_bias_elem_kernel<XT, ALL>, P.rows, P.cols, SumShape<false>::groups, sms, s, P);
+        if (!vec) return launch_sums<SumElem>(dropout_bias_elem_kernel<XT, ALL>, P.rows, P.cols, sms, s, P);
+        if (P.cols % 8) return launch_sums<SumFlat>(dropout_bias_flat_kernel<XT, ALL>, P.rows, P.cols, sms, s, P);
+        if (XT == kF32 || narrow_tiles(XT, P.cols, sms))
+            return launch_sums<SumVec<32>>(dropout_bias_vec_kernel<XT, ALL, SumVec<32>>, P.rows, P.cols, sms, s, P);
+        return launch_sums<SumVec<64>>(dropout_bias_vec_kernel<XT, ALL, SumVec<64>>, P.rows, P.cols, sms, s, P);
     }
     Dropout F = P;
     F.cols = P.rows * P.cols;
