@@ -182,10 +182,15 @@ __device__ __forceinline__ void store_elem(void *x, int64_t k, float v) {
 }
 
 // fp32 bits of max |y| over 8 elements a lane and the 4 lanes of a block
+// (by three magnitudes an instruction, of which a NaN wins: 4 instead of 16)
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
+}
 __device__ __forceinline__ uint32_t block_max8(const float (&y)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+    const float a = absmax3(y[0], y[1], y[2]), b = absmax3(y[3], y[4], y[5]);
+    uint32_t m = __float_as_uint(absmax3(absmax3(y[6], y[7], a), b, 0.0f));
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
 }
