@@ -173,24 +173,24 @@ __global__ void __launch_bounds__(SumFlat::threads, SumFlat::ctas) bias_bwd_flat
 }
 
 template <int XT, int ACT>
-cudaError_t go(const BiasBwd &P, bool aligned, int sms, cudaStream_t s) {
-    if (!aligned) return launch_sums<SumElem>(bias_bwd_kernel<XT, ACT, SumElem>, P.rows, P.cols, sms, s, P);
+cudaError_t go(const BiasBwd &P, bool aligned, int dev, cudaStream_t s) {
+    if (!aligned) return launch_sums<SumElem, &bias_bwd_kernel<XT, ACT, SumElem>>(P.rows, P.cols, dev, s, P);
     // the activations' longer way to a group's values needs CTAs enough to hide it (2047 x
     // 1111 bf16 GELU 13.3 us, by single elements 10.4; 16383 x 5121 198 and 383)
-    if (P.cols % 8 && (ACT == kNoAct || !narrow_tiles(kBF16, P.cols, sms)))
-        return launch_sums<SumFlat>(bias_bwd_flat_kernel<XT, ACT>, P.rows, P.cols, sms, s, P);
-    if (P.cols % 8) return launch_sums<SumElem>(bias_bwd_kernel<XT, ACT, SumElem>, P.rows, P.cols, sms, s, P);
-    if (XT == kF32 || narrow_tiles(XT, P.cols, sms))
-        return launch_sums<SumVec<32>>(bias_bwd_kernel<XT, ACT, SumVec<32>>, P.rows, P.cols, sms, s, P);
-    return launch_sums<SumVec<64>>(bias_bwd_kernel<XT, ACT, SumVec<64>>, P.rows, P.cols, sms, s, P);
+    if (P.cols % 8 && (ACT == kNoAct || !narrow_tiles(kBF16, P.cols, dev)))
+        return launch_sums<SumFlat, &bias_bwd_flat_kernel<XT, ACT>>(P.rows, P.cols, dev, s, P);
+    if (P.cols % 8) return launch_sums<SumElem, &bias_bwd_kernel<XT, ACT, SumElem>>(P.rows, P.cols, dev, s, P);
+    if (XT == kF32 || narrow_tiles(XT, P.cols, dev))
+        return launch_sums<SumVec<32>, &bias_bwd_kernel<XT, ACT, SumVec<32>>>(P.rows, P.cols, dev, s, P);
+    return launch_sums<SumVec<64>, &bias_bwd_kernel<XT, ACT, SumVec<64>>>(P.rows, P.cols, dev, s, P);
 }
 template <int XT>
-cudaError_t go_x(const BiasBwd &P, int act, bool aligned, int sms, cudaStream_t s) {
+cudaError_t go_x(const BiasBwd &P, int act, bool aligned, int dev, cudaStream_t s) {
     switch (act) {
-    case AMP_ACT_GELU: return go<XT, AMP_ACT_GELU>(P, aligned, sms, s);
-    case AMP_ACT_GELU_TANH: return go<XT, AMP_ACT_GELU_TANH>(P, aligned, sms, s);
-    case AMP_ACT_SILU: return go<XT, AMP_ACT_SILU>(P, aligned, sms, s);
-    default: return go<XT, kNoAct>(P, aligned, sms, s);
+    case AMP_ACT_GELU: return go<XT, AMP_ACT_GELU>(P, aligned, dev, s);
+    case AMP_ACT_GELU_TANH: return go<XT, AMP_ACT_GELU_TANH>(P, aligned, dev, s);
+    case AMP_ACT_SILU: return go<XT, AMP_ACT_SILU>(P, aligned, dev, s);
+    default: return go<XT, kNoAct>(P, aligned, dev, s);
     }
 }
 
@@ -201,10 +201,10 @@ cudaError_t launch_bias_bwd(int act, const void *dy, int elem, int64_t rows, int
     const BiasBwd P{dy, q, sc, dz, db, rows, cols, int((cols + kMxBlock - 1) / kMxBlock), dbelem};
     const auto off = [](const void *p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; };
     const bool aligned = !off(dy, 15) && !off(dz, 15) && !off(q, 7);
-    const int a = act < 0 ? int(kNoAct) : act, sms = sm_count(device);
-    const cudaError_t e = elem == kF32   ? go_x<kF32>(P, a, aligned, sms, s)
-                          : elem == kF16 ? go_x<kF16>(P, a, aligned, sms, s)
-                                         : go_x<kBF16>(P, a, aligned, sms, s);
+    const int a = act < 0 ? int(kNoAct) : act;
+    const cudaError_t e = elem == kF32   ? go_x<kF32>(P, a, aligned, device, s)
+                          : elem == kF16 ? go_x<kF16>(P, a, aligned, device, s)
+                                         : go_x<kBF16>(P, a, aligned, device, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

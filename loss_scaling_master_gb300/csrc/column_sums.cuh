@@ -11,6 +11,7 @@
 
 #include <algorithm>
 
+#include "internal.h"
 #include "mx.cuh"
 #include "pdl.cuh"
 #include "tcgen05.cuh"
@@ -117,7 +118,7 @@ __device__ __forceinline__ void sum_join(const SumShare<S> &at, int64_t cols, co
 // groups of 8 elements, of which a tile's part of a row holds at most `across`, the first
 // and the last perhaps in part.  What the op makes of a warp's groups goes through shared
 // memory to a column or two a lane.  (By single elements 16383 x 5121 bf16 dropout 189 us,
-// so FLT1; with GELU 383 and FLT2.)
+// so 130; with GELU 383 and 198.)
 //
 // Op: Raw load(g, whole), void values(raw, g, r, c, y) (c: the column of element 0, may
 // lie before the tile), void store(g, lo, hi, y); g counts groups, whole: all 8 exist.
@@ -178,7 +179,7 @@ __device__ __forceinline__ void flat_sums(const SumShare<SumFlat> &at, int64_t r
 // Shares of the rows, of at least a row a group: as many as make the rounds of CTAs that
 // the GPU holds at once shortest.  CTAs of clusters start one after another, 5 ns each, so
 // beyond two an SM a share is at least four rows a group (1000 x 2304 dropout by 576 CTAs
-// 5.7 us, by 288 SHR1).
+// 5.7 us, by 288 4.8).
 template <class S>
 int sum_parts(int64_t rows, int64_t tiles, int sms) {
     const int64_t room = int64_t(sms) * S::ctas;
@@ -195,17 +196,17 @@ int sum_parts(int64_t rows, int64_t tiles, int sms) {
     }
     return parts;
 }
-template <class S, class A>
-cudaError_t launch_sums(void (*kernel)(A), int64_t rows, int64_t cols, int sms, cudaStream_t s, const A &args) {
+template <class S, auto Kernel, class A>
+cudaError_t launch_sums(int64_t rows, int64_t cols, int device, cudaStream_t s, const A &args) {
     const int64_t tiles = (cols + S::cols - 1) / S::cols;
-    const int parts = sum_parts<S>(rows, tiles, sms);
-    return launch_pdl_cluster(kernel, dim3(unsigned(tiles * parts)), dim3(S::threads), 0, parts, s, args);
+    const int parts = sum_parts<S>(rows, tiles, sm_count(device));
+    return launch_pdl_cluster<Kernel, kSmallShared>(device, dim3(unsigned(tiles * parts)), dim3(S::threads), parts, s, args);
 }
 // 16-bit rows in tiles of 32 columns where 64 would leave CTAs unused (1024 x 768 dropout
 // 3.7 us, by 64 4.1; 16384 x 768 16.8 and 25; but 4096 x 8192 37.5 and 32.5); fp32 ones always
 // (8192 x 2048 24.9 and 29.3).
-inline bool narrow_tiles(int elem, int64_t cols, int sms) {
-    return elem == kF32 || cols < int64_t(sms) * SumVec<64>::ctas * 64 / kSumParts;
+inline bool narrow_tiles(int elem, int64_t cols, int device) {
+    return elem == kF32 || cols < int64_t(sm_count(device)) * SumVec<64>::ctas * 64 / kSumParts;
 }
 
 // 8 elements of a group as raw words; a group that ends behind the tensor's last element

@@ -214,29 +214,29 @@ __global__ void __launch_bounds__(SumElem::threads, SumElem::ctas) dropout_bias_
 bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
 template <int XT, bool ALL>
-cudaError_t go(const Dropout &P, int sms, cudaStream_t s) {
+cudaError_t go(const Dropout &P, int dev, cudaStream_t s) {
     const bool vec = !off16(P.x) && !off16(P.res) && !off16(P.y);
     if (P.db) {
-        if (!vec) return launch_sums<SumElem>(dropout_bias_elem_kernel<XT, ALL>, P.rows, P.cols, sms, s, P);
-        if (P.cols % 8) return launch_sums<SumFlat>(dropout_bias_flat_kernel<XT, ALL>, P.rows, P.cols, sms, s, P);
-        if (XT == kF32 || narrow_tiles(XT, P.cols, sms))
-            return launch_sums<SumVec<32>>(dropout_bias_vec_kernel<XT, ALL, SumVec<32>>, P.rows, P.cols, sms, s, P);
-        return launch_sums<SumVec<64>>(dropout_bias_vec_kernel<XT, ALL, SumVec<64>>, P.rows, P.cols, sms, s, P);
+        if (!vec) return launch_sums<SumElem, &dropout_bias_elem_kernel<XT, ALL>>(P.rows, P.cols, dev, s, P);
+        if (P.cols % 8) return launch_sums<SumFlat, &dropout_bias_flat_kernel<XT, ALL>>(P.rows, P.cols, dev, s, P);
+        if (XT == kF32 || narrow_tiles(XT, P.cols, dev))
+            return launch_sums<SumVec<32>, &dropout_bias_vec_kernel<XT, ALL, SumVec<32>>>(P.rows, P.cols, dev, s, P);
+        return launch_sums<SumVec<64>, &dropout_bias_vec_kernel<XT, ALL, SumVec<64>>>(P.rows, P.cols, dev, s, P);
     }
     Dropout F = P;
     F.cols = P.rows * P.cols;
     F.rows = 1;
     const int64_t want = (F.cols + kThreads * 8 - 1) / (kThreads * 8);
-    const dim3 grid(unsigned(std::min<int64_t>(want, int64_t(sms) * 64))), block(kThreads);
+    const dim3 grid(unsigned(std::min<int64_t>(want, int64_t(sm_count(dev)) * 64))), block(kThreads);
     if (vec)
-        return F.res ? launch_pdl(dropout_vec_kernel<XT, true, ALL>, grid, block, 0, s, F)
-                     : launch_pdl(dropout_vec_kernel<XT, false, ALL>, grid, block, 0, s, F);
-    return F.res ? launch_pdl(dropout_elem_kernel<XT, true, ALL>, grid, block, 0, s, F)
-                 : launch_pdl(dropout_elem_kernel<XT, false, ALL>, grid, block, 0, s, F);
+        return F.res ? launch_pdl_cluster<&dropout_vec_kernel<XT, true, ALL>, kSmallShared>(dev, grid, block, 1, s, F)
+                     : launch_pdl_cluster<&dropout_vec_kernel<XT, false, ALL>, kSmallShared>(dev, grid, block, 1, s, F);
+    return F.res ? launch_pdl_cluster<&dropout_elem_kernel<XT, true, ALL>, kSmallShared>(dev, grid, block, 1, s, F)
+                 : launch_pdl_cluster<&dropout_elem_kernel<XT, false, ALL>, kSmallShared>(dev, grid, block, 1, s, F);
 }
 template <int XT>
-cudaError_t go_all(const Dropout &P, int sms, cudaStream_t s) {
-    return P.drop == 0 ? go<XT, true>(P, sms, s) : go<XT, false>(P, sms, s);
+cudaError_t go_all(const Dropout &P, int dev, cudaStream_t s) {
+    return P.drop == 0 ? go<XT, true>(P, dev, s) : go<XT, false>(P, dev, s);
 }
 
 }  // namespace
@@ -246,10 +246,9 @@ cudaError_t launch_dropout(const void *x, const void *res, int elem, int64_t row
                            int device, cudaStream_t s) {
     const float scale = drop < 65536u ? float(65536.0 / double(65536u - drop)) : 0.0f;
     const Dropout P{x, res, y, db, step, seed, rows, cols, scale, drop, (drop << 16) - 1, site, dbelem};
-    const int sms = sm_count(device);
-    const cudaError_t e = elem == kF32   ? go_all<kF32>(P, sms, s)
-                          : elem == kF16 ? go_all<kF16>(P, sms, s)
-                                         : go_all<kBF16>(P, sms, s);
+    const cudaError_t e = elem == kF32   ? go_all<kF32>(P, device, s)
+                          : elem == kF16 ? go_all<kF16>(P, device, s)
+                                         : go_all<kBF16>(P, device, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

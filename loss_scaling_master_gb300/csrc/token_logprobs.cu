@@ -15,7 +15,7 @@
 // these are hardly more than k.  What they read is read once more (a thread's share of
 // the row each, from L2), and what reaches the bound there is put in order.  (Lists kept
 // by warps along the row took 703 us for 5 of 4096 x 128256 bf16, 179 without; this
-// way TOPA.)
+// way 174.)
 //
 // Every row starts where its address lies: a first and a last piece of less than 16
 // bytes are taken by single elements, padded with -inf, which adds nothing.
@@ -664,34 +664,35 @@ __global__ void __launch_bounds__(THREADS *ROWS) logprobs_bwd_kernel(LogprobsBwd
 
 constexpr int kShortRows = 4;  // a CTA, a warp each
 template <int XT, int THREADS, int ROWS>
-cudaError_t fwd(const LogprobsFwd &P, int parts, cudaStream_t s) {
+cudaError_t fwd(const LogprobsFwd &P, int parts, int dev, cudaStream_t s) {
     const dim3 grid(unsigned((P.rows + ROWS - 1) / ROWS * parts)), block(THREADS, ROWS);
-    return P.k ? launch_pdl_cluster(logprobs_fwd_kernel<XT, THREADS, ROWS, true>, grid, block, 0, parts, s, P)
-               : launch_pdl_cluster(logprobs_fwd_kernel<XT, THREADS, ROWS, false>, grid, block, 0, parts, s, P);
+    return P.k ? launch_pdl_cluster<&logprobs_fwd_kernel<XT, THREADS, ROWS, true>, kAnyShared>(dev, grid, block, parts, s, P)
+               : launch_pdl_cluster<&logprobs_fwd_kernel<XT, THREADS, ROWS, false>, kAnyShared>(dev, grid, block, parts, s, P);
 }
 template <int XT>
 cudaError_t fwd_x(const LogprobsFwd &P, int device, cudaStream_t s) {
     const int pieces = P.cols / Pieces<XT>::VN + 1, sms = sm_count(device);
-    if (P.k <= 8 && (pieces <= 260 || (pieces <= 520 && P.rows >= 16 * sms))) return fwd<XT, 32, kShortRows>(P, 1, s);
-    if (pieces <= 260 || (pieces <= 1030 && P.rows >= 2 * sms)) return fwd<XT, 128, 1>(P, 1, s);
+    if (P.k <= 8 && (pieces <= 260 || (pieces <= 520 && P.rows >= 16 * sms))) return fwd<XT, 32, kShortRows>(P, 1, device, s);
+    if (pieces <= 260 || (pieces <= 1030 && P.rows >= 2 * sms)) return fwd<XT, 128, 1>(P, 1, device, s);
     int parts = 1;
     while (parts < kMaxParts && P.rows * parts <= 2 * sms && pieces > parts * 1024) parts *= 2;
-    return fwd<XT, 256, 1>(P, parts, s);
+    return fwd<XT, 256, 1>(P, parts, device, s);
 }
 template <int XT>
-cudaError_t bwd_x(LogprobsBwd P, int sms, cudaStream_t s) {
+cudaError_t bwd_x(LogprobsBwd P, int device, cudaStream_t s) {
+    const int sms = sm_count(device);
     const int64_t pieces = P.cols / Pieces<XT>::VN + 2;  // a row that starts inside a piece has one more
     P.chunks = 1;
     if (pieces <= 260)
-        return launch_pdl(logprobs_bwd_kernel<XT, 32, kShortRows>, dim3(unsigned((P.rows + kShortRows - 1) / kShortRows)),
-                          dim3(32, kShortRows), 0, s, P);
+        return launch_pdl_cluster<&logprobs_bwd_kernel<XT, 32, kShortRows>, kAnyShared>(
+            device, dim3(unsigned((P.rows + kShortRows - 1) / kShortRows)), dim3(32, kShortRows), 1, s, P);
     if (pieces <= 1030 && P.rows >= 2 * sms)
-        return launch_pdl(logprobs_bwd_kernel<XT, 128, 1>, dim3(unsigned(P.rows)), dim3(128), 0, s, P);
+        return launch_pdl_cluster<&logprobs_bwd_kernel<XT, 128, 1>, kAnyShared>(device, dim3(unsigned(P.rows)), dim3(128), 1, s, P);
     // shares of 8 loads a thread, smaller ones where rows are few
     int64_t chunks = (pieces + 8 * 256 - 1) / (8 * 256);
     while (chunks * P.rows < 4 * sms && chunks * 512 < pieces) chunks *= 2;
     P.chunks = int(chunks);
-    return launch_pdl(logprobs_bwd_kernel<XT, 256, 1>, dim3(unsigned(P.rows * P.chunks)), dim3(256), 0, s, P);
+    return launch_pdl_cluster<&logprobs_bwd_kernel<XT, 256, 1>, kAnyShared>(device, dim3(unsigned(P.rows * P.chunks)), dim3(256), 1, s, P);
 }
 
 }  // namespace
@@ -711,10 +712,9 @@ cudaError_t launch_logprobs_bwd(const void *z, int elem, int64_t rows, int64_t c
                                 const float *scale, void *dz, int64_t dld, int device, cudaStream_t s) {
     const LogprobsBwd P{z, t, reinterpret_cast<const float2 *>(stats), dlogp, ent, dent, scale, dz, rows, ld, dld,
                         int(cols), 1};
-    const int sms = sm_count(device);
-    const cudaError_t e = elem == kF32   ? bwd_x<kF32>(P, sms, s)
-                          : elem == kF16 ? bwd_x<kF16>(P, sms, s)
-                                         : bwd_x<kBF16>(P, sms, s);
+    const cudaError_t e = elem == kF32   ? bwd_x<kF32>(P, device, s)
+                          : elem == kF16 ? bwd_x<kF16>(P, device, s)
+                                         : bwd_x<kBF16>(P, device, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
