@@ -282,7 +282,8 @@ amp_status amp_dropout_backward(const void *dy, amp_dtype dtype, int64_t rows, i
  * A logit of -inf (a masked token) has probability 0 and log probability -inf.
  * A row with a NaN, with +inf, or with nothing but -inf gives NaN.
  * Errors: AMP_EINVAL (NULL z, logp without targets, top_n outside [0, 32], half
- * of the alternatives, ld < cols, negative or too large size), AMP_EDTYPE. */
+ * of the alternatives, ld < cols, negative or too large size, cols above 2^30),
+ * AMP_EDTYPE. */
 amp_status amp_token_logprobs_forward(const void *z, amp_dtype dtype, int64_t rows, int64_t cols,
                                       int64_t ld, const int64_t *targets, float *logp,
                                       float *entropy, float *stats, int64_t *top_ids,

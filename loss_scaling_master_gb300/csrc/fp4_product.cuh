@@ -390,28 +390,30 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
 // ------------------------------------------------------------------ one CTA a tile
 constexpr uint32_t kMaxParts = 4;  // CTAs that share one tile's reduction
-constexpr int kSoloThreads = 384;  // load, issue, allocate, (idle), 8 store warps
 
 template <int BN, bool SPLIT, class EP>
 struct Solo {
     static constexpr int staged = SPLIT ? 0 : EP::staged;
+    // load, issue, allocate, (idle), and the store warps: 16 for an epilogue on the widest
+    // tile (1000 x 2304 x 768 with bias, GELU and checkpoint 8.1 us by 8, SW16 by 16)
+    static constexpr int store_warps = staged && BN == 128 ? 16 : 8, threads = 128 + 32 * store_warps;
     static constexpr int w_bytes = kLanes * kStageBytes;
     static constexpr int t_bytes = BN * kStageBytes;
     static constexpr int stage = w_bytes + t_bytes + 2048;  // and 1 KB of scales of each operand
-    // an epilogue's shared memory takes the place of a stage where two CTAs share an SM
-    static constexpr int stages = BN == 128 ? 6 : (BN == 64 ? 4 : 5) - (staged ? 1 : 0);
+    // an epilogue's shared memory takes the place of a stage
+    static constexpr int stages = (BN == 128 ? 6 : BN == 64 ? 4 : 5) - (staged ? 1 : 0);
     static constexpr int ctas = BN == 128 ? 1 : 2;  // CTAs an SM holds
     static constexpr int sf_base = 2 * BN;          // two accumulators
     static constexpr int sf_cols = 16;
     static constexpr int tmem_cols = BN == 128 ? 512 : 256;
     static_assert(sf_base + stages * sf_cols <= tmem_cols, "tensor memory");
-    static constexpr int smem = stages * stage + 8 * staged + 1024;  // and the alignment to 1024
+    static constexpr int smem = stages * stage + store_warps * staged + 1024;  // and the alignment to 1024
     static_assert(BN * kLanes * 4 <= stages * stage, "the partial tile");
     static_assert(ctas * (smem + 1024 + 256) <= 228 * 1024, "shared memory");
 };
 
 template <int BN, bool SPLIT, class EP>
-__global__ void __launch_bounds__(kSoloThreads, Solo<BN, SPLIT, EP>::ctas)
+__global__ void __launch_bounds__(Solo<BN, SPLIT, EP>::threads, Solo<BN, SPLIT, EP>::ctas)
     fp4_product_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
                        typename EP::Args P) {
     using S = Solo<BN, SPLIT, EP>;
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN, SPLIT, EP>::ctas)
         }
         for (int i = 0; i < NA; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 256);
+            mbar_init(&acc_empty[i], 32 * S::store_warps);
         }
         mbar_init(&drain, 1);  // everything that was issued
         mbar_init(&ended, 2);  // loads and products: nothing is in flight
@@ -549,8 +551,8 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN, SPLIT, EP>::ctas)
         mbar_wait(&drain, 0);
         if (lane == 0) mbar_arrive(&ended);
     } else if (warp >= 4) {
-        // a quarter of the lanes and half of the columns a warp (all of 16)
-        constexpr int HALF = BN > 16 ? BN / 2 : BN;
+        // a quarter of the lanes and a share of the columns a warp (all of 16)
+        constexpr int HALF = BN > 16 ? BN / (S::store_warps / 4) : BN;
         constexpr int CH = HALF < 32 ? HALF : EP::none || SPLIT ? 32 : 16;  // columns at a time
         [[maybe_unused]] typename EP::State ep;
         const int quarter = warp & 3, c0 = (warp - 4) / 4 * HALF;
@@ -621,12 +623,12 @@ __global__ void __launch_bounds__(kSoloThreads, Solo<BN, SPLIT, EP>::ctas)
 #pragma unroll
         for (uint32_t r = 0; r < kMaxParts; ++r) part[r] = cluster_addr(smem, r < parts ? r : 0);
         if constexpr (!EP::none) {
-            EP::template join<kSoloThreads>(P, part, parts, rank, m0, int64_t(tn) * kLanes, cols);
+            EP::template join<S::threads>(P, part, parts, rank, m0, int64_t(tn) * kLanes, cols);
         } else {
             // groups of four neighbouring elements go round the CTAs' threads; the
             // loads of one group's parts are issued together
-            for (int i = int(rank) * kSoloThreads + int(threadIdx.x); i < cols * (kLanes / 4);
-                 i += int(parts) * kSoloThreads) {
+            for (int i = int(rank) * S::threads + int(threadIdx.x); i < cols * (kLanes / 4);
+                 i += int(parts) * S::threads) {
                 const int c = i / (kLanes / 4), l = 4 * (i % (kLanes / 4));
                 float4 v[kMaxParts];
 #pragma unroll
@@ -778,9 +780,9 @@ cudaError_t go(typename EP::Args P, const void *a, const void *b, int64_t row_by
     static std::atomic<uint64_t> ready[2];
     if (parts > 1)
         return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, true, EP>), ready[1], device, unsigned(tiles * parts),
-                      kSoloThreads, Solo<BN, true, EP>::smem, parts, s, args);
+                      Solo<BN, true, EP>::threads, Solo<BN, true, EP>::smem, parts, s, args);
     return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, false, EP>), ready[0], device,
-                  unsigned(std::min<int64_t>(tiles, room)), kSoloThreads, S::smem, 1, s, args);
+                  unsigned(std::min<int64_t>(tiles, room)), S::threads, S::smem, 1, s, args);
 }
 
 // What the kernels need of a product, the epilogue's aside.

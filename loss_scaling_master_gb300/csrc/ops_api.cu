@@ -428,9 +428,10 @@ amp_status amp_dropout_backward(const void *dy, amp_dtype dtype, int64_t rows, i
                   fn);
 }
 
-// A matrix whose rows lie ld elements apart.
+// A matrix whose rows lie ld elements apart; a row's 16-byte pieces are counted in 32 bits,
+// with a batch of loads behind the last one.
 static bool bad_rows(int64_t rows, int64_t cols, int64_t ld) {
-    return bad_shape(rows, cols) || ld < cols || bad_shape(rows, ld);
+    return bad_shape(rows, cols) || ld < cols || bad_shape(rows, ld) || cols > (int64_t(1) << 30);
 }
 
 amp_status amp_token_logprobs_forward(const void *z, amp_dtype dtype, int64_t rows, int64_t cols, int64_t ld,

@@ -109,7 +109,7 @@ def forward(z=D, dt=BF16, r=4, c=8, ld=8, t=D, logp=D, ent=D, stats=D, ids=N, lp
     (forward(z=ODD), EINVAL), (forward(z=HALF, dt=F32), EINVAL), (forward(t=ctypes.c_void_p(4100)), EINVAL),
     (forward(logp=HALF), EINVAL), (forward(ent=HALF), EINVAL), (forward(stats=ctypes.c_void_p(4100)), EINVAL),
     (forward(k=2, ids=ctypes.c_void_p(4100), lp=D), EINVAL), (forward(k=2, ids=D, lp=HALF), EINVAL),
-    (forward(r=0, z=N, logp=N), OK),
+    (forward(c=(1 << 30) + 1, ld=(1 << 30) + 1), EINVAL), (forward(r=0, z=N, logp=N), OK),
 ])
 def test_logprobs_forward_refusals(lib, args, want):
     assert lib.amp_token_logprobs_forward(*args, None) == want
