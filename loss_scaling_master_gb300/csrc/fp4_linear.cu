@@ -8,7 +8,7 @@ namespace {
 
 // z = bias for an empty reduction: a warp takes 32 columns of 16 tokens.
 __global__ void __launch_bounds__(kThreads) linear_empty_kernel(Fp4Linear P) {
-    __shared__ __align__(16) uint8_t s_stage[kThreads / 32][EpAny::staged];
+    __shared__ __align__(16) uint8_t s_stage[kThreads / 32][EpAny<false>::staged];
     pdl_wait();
     pdl_trigger();
     const int64_t items = (int64_t(P.m) + 15) / 16 * P.kb;
@@ -16,8 +16,8 @@ __global__ void __launch_bounds__(kThreads) linear_empty_kernel(Fp4Linear P) {
          i += int64_t(gridDim.x) * (kThreads / 32)) {
         const int64_t m0 = i / P.kb * 16;
         const uint32_t zero[16] = {};
-        EpAny::State ep;
-        EpAny::finish<16>(P, m0, int(min(int64_t(16), P.m - m0)), i % P.kb * kMxBlock + (threadIdx.x & 31), zero, ep,
+        EpAny<false>::State ep;
+        EpAny<false>::finish<16>(P, m0, int(min(int64_t(16), P.m - m0)), i % P.kb * kMxBlock + (threadIdx.x & 31), zero, ep,
                           s_stage[threadIdx.x / 32]);
     }
 }
@@ -45,7 +45,8 @@ cudaError_t launch_fp4_linear(const void *a, const uint8_t *sa, const void *b, c
         const int64_t want = ((m + 15) / 16 * P.kb * 32 + kThreads - 1) / kThreads;
         e = launch_pdl(linear_empty_kernel, dim3(unsigned(std::min<int64_t>(want, 4096))), dim3(kThreads), 0, s, P);
     } else if (!takes_pairs(m, n, device)) {
-        e = go_solo<EpAny>(P, a, b, row_bytes, device, s);
+        e = P.vec ? go_solo<EpAny<true>>(P, a, b, row_bytes, device, s)
+                  : go_solo<EpAny<false>>(P, a, b, row_bytes, device, s);
     } else {
         e = linear_pairs(P, a, b, row_bytes, device, s);
     }

@@ -3,12 +3,12 @@
 //
 //   z = A B^T + bias,  out = f(z) + residual (one rounding),  8-bit checkpoint of z
 //
-// A lane holds one column of C and consecutive tokens.  32 lanes are then one block of
-// the checkpoint for each token, whose maximum is one reduction over the warp.  The
-// residual comes in the layout in which store16 stores (two neighbouring elements of a
-// row a lane, even lanes the even tokens) and is turned over by one shuffle for two
-// elements; the words of the first 16 tokens are asked for before the accumulators are
-// waited for, the others 16 tokens ahead.
+// A lane holds one column of C and consecutive tokens.  A bias and a residual are added so
+// (EpOne): the residual comes in the layout in which store16 stores (two neighbouring
+// elements of a row a lane, even lanes the even tokens) and is turned over by one shuffle
+// for two elements; the words of the first 16 tokens are asked for before the accumulators
+// are waited for, the others 16 tokens ahead.  An activation and the checkpoint want
+// neighbouring columns in a lane (Stage).
 #pragma once
 
 #include "act.cuh"
@@ -48,9 +48,11 @@ __device__ __forceinline__ void scales_nan(const Fp4Linear &P, int64_t m0, int c
     for (int64_t m = m0; m < m0 + cnt && m < P.m; ++m) P.s[m * P.kb + nn / kMxBlock] = 255;
 }
 
-template <int OT, int ACT>
+// A bias and a residual alone, added a column a lane as the columns come.
+template <int OT>
 struct EpOne {
     using Args = Fp4Linear;
+    using Split = EpOne;
     static constexpr bool none = false;
     static constexpr int staged = 0;
     static constexpr int CH = OT == kF32 ? 8 : 16, WORDS = 8;
@@ -95,28 +97,10 @@ struct EpOne {
         if (P.res) residual(P, m0, rows, nn, ep.r);
     }
 
-    // The checkpoint of CH tokens' z (0 in columns behind the last one).
-    static __device__ __forceinline__ void save(const Args &P, int64_t m0, int rows, int64_t nn,
-                                                const float (&z)[CH]) {
-        const int lane = threadIdx.x & 31;
-        uint8_t *at = P.q + m0 * P.n + nn;
-        uint32_t mine = 0;  // lane i: token i's scale byte
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const uint32_t e = mx_scale_code<MxE4M3>(warp_max_u32(__float_as_uint(z[i]) & 0x7FFFFFFFu));
-            if (nn < P.n && i < rows)
-                *at = uint8_t(f32x2_to_fp8x2_raw<kE4M3>(__fmul_rn(z[i], mx_unscale(e)), 0.0f));
-            at += P.n;
-            if (lane == i) mine = e;
-        }
-        if (lane < CH && lane < rows && nn - lane < P.n) P.s[(m0 + lane) * P.kb + (nn - lane) / kMxBlock] = uint8_t(mine);
-    }
-
-    // f(z) + residual for two tokens, elements 2 i and 2 i + 1 of the residual's words
-    static __device__ __forceinline__ float2 value(const Args &P, float z0, float z1, int i,
-                                                   const uint32_t (&r)[WORDS]) {
+    // z + residual for two tokens, elements 2 i and 2 i + 1 of the residual's words
+    static __device__ __forceinline__ float2 add(const Args &P, float z0, float z1, int i,
+                                                 const uint32_t (&r)[WORDS]) {
         float2 y = make_float2(z0, z1);
-        if constexpr (ACT != kNoAct) y = act_apply<OT, ACT, false>(z0, z1, 0.0f, 0.0f);
         if (P.res) {
             if constexpr (OT == kF32) {
                 y.x += __uint_as_float(r[2 * i]);
@@ -133,6 +117,19 @@ struct EpOne {
         }
         return y;
     }
+    static __device__ __forceinline__ void pack(float2 y, int i, uint32_t (&o)[WORDS]) {
+        if constexpr (OT == kF32) {
+            o[2 * i] = __float_as_uint(y.x);
+            o[2 * i + 1] = __float_as_uint(y.y);
+        } else {
+            o[i] = f32x2_to_16x2<OT>(y.x, y.y);
+        }
+    }
+    static __device__ __forceinline__ void store(const Args &P, int64_t m0, int rows, int64_t nn,
+                                                 const uint32_t (&o)[WORDS]) {
+        if constexpr (OT == kF32) store32<CH>(P, m0, rows, nn, o);
+        else store16<CH>(P, m0, rows, nn, o);
+    }
 
     // ep: as begin() left it for the same place
     template <int CNT>
@@ -143,28 +140,13 @@ struct EpOne {
             if (c >= rows) break;
             State nxt;
             if (P.res && c + CH < CNT) residual(P, m0 + c + CH, rows - c - CH, nn, nxt.r);
-            float z[CH];
+            uint32_t o[WORDS];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) z[i] = __uint_as_float(v[c + i]) + ep.bias;
-            if (P.q) save(P, m0 + c, rows - c, nn, z);
-            if constexpr (OT == kF32) {
-                uint32_t o[CH];
-#pragma unroll
-                for (int i = 0; i < CH; i += 2) {
-                    const float2 y = value(P, z[i], z[i + 1], i / 2, ep.r);
-                    o[i] = __float_as_uint(y.x);
-                    o[i + 1] = __float_as_uint(y.y);
-                }
-                store32<CH>(P, m0 + c, rows - c, nn, o);
-            } else {
-                uint32_t o[CH / 2];
-#pragma unroll
-                for (int i = 0; i < CH / 2; ++i) {
-                    const float2 y = value(P, z[2 * i], z[2 * i + 1], i, ep.r);
-                    o[i] = f32x2_to_16x2<OT>(y.x, y.y);
-                }
-                store16<CH>(P, m0 + c, rows - c, nn, o);
-            }
+            for (int i = 0; i < CH / 2; ++i)
+                pack(add(P, __uint_as_float(v[c + 2 * i]) + ep.bias, __uint_as_float(v[c + 2 * i + 1]) + ep.bias, i,
+                         ep.r),
+                     i, o);
+            store(P, m0 + c, rows - c, nn, o);
             if (c + CH < CNT) {
 #pragma unroll
                 for (int i = 0; i < WORDS; ++i) ep.r[i] = nxt.r[i];
@@ -179,122 +161,181 @@ struct EpOne {
 // Eight neighbouring columns of one token, four lanes a block of the checkpoint.
 template <int OT>
 struct Eight {
-    uint4 r[kWords8<OT>];  // the residual's
-    // vec: the whole row is groups of eight, and aligned
-    __device__ __forceinline__ void load(const Fp4Linear &P, bool in, int64_t k, int left) {
+    uint4 r[kWords8<OT>];  // the residual's (rows of whole groups of eight)
+    __device__ __forceinline__ void load(const Fp4Linear &P, bool in, int64_t k) {
 #pragma unroll
-        for (int w = 0; w < kWords8<OT>; ++w) r[w] = make_uint4(0, 0, 0, 0);
-        if (!P.res || !in) return;
-        if (P.vec) {
-#pragma unroll
-            for (int w = 0; w < kWords8<OT>; ++w)
-                r[w] = ld16(static_cast<const char *>(P.res) + k * (OT == kF32 ? 4 : 2) + 16 * w);
-        } else {
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = j < left ? load_elem<OT>(P.res, k + j) : 0.0f;
-            f32_to_raw8<OT>(y, r);
+        for (int w = 0; w < kWords8<OT>; ++w) {
+            r[w] = make_uint4(0, 0, 0, 0);
+            if (P.res && in) r[w] = ld16(static_cast<const char *>(P.res) + k * (OT == kF32 ? 4 : 2) + 16 * w);
         }
     }
-    // z: with the bias, 0 where in is false or behind the last column (left: columns from here)
+    // The checkpoint's codes of z (0 where `in` is false and behind the last column), its
+    // scale stored; z becomes f(z).
     template <int ACT>
-    __device__ __forceinline__ void finish(const Fp4Linear &P, bool in, int64_t k, int left, int64_t scale_at,
-                                           float (&z)[8]) const {
+    static __device__ __forceinline__ uint2 apply(const Fp4Linear &P, bool in, int64_t scale_at, float (&z)[8]) {
+        uint2 c = make_uint2(0, 0);
         if (P.q) {
             const uint32_t e = mx_scale_code<MxE4M3>(block_max8(z));
-            const uint2 c = codes8(z, mx_unscale(e));
-            if (in) {
-                if (P.vec) {
-                    *reinterpret_cast<uint2 *>(P.q + k) = c;
-                } else {
+            c = codes8(z, mx_unscale(e));
+            if (in && (threadIdx.x & 3) == 0) P.s[scale_at] = uint8_t(e);
+        }
+        if constexpr (ACT != kNoAct) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < left) P.q[k + j] = uint8_t((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
-                }
-                if ((threadIdx.x & 3) == 0) P.s[scale_at] = uint8_t(e);
+            for (int j = 0; j < 8; j += 2) {
+                const float2 v = act_apply<OT, ACT, false>(z[j], z[j + 1], 0.0f, 0.0f);
+                z[j] = v.x;
+                z[j + 1] = v.y;
             }
         }
-        float y[8], b[8];
-        raw8_to_f32<OT>(r, b);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            float2 v = make_float2(z[j], z[j + 1]);
-            if constexpr (ACT != kNoAct) v = act_apply<OT, ACT, false>(v.x, v.y, 0.0f, 0.0f);
-            y[j] = v.x;
-            y[j + 1] = v.y;
-        }
+        return c;
+    }
+    // out = y + residual, and the codes
+    __device__ __forceinline__ void store(const Fp4Linear &P, bool in, int64_t k, float (&y)[8], uint2 c) const {
         if (P.res) {
+            float b[8];
+            raw8_to_f32<OT>(r, b);
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] += b[j];
         }
         if (!in) return;
-        if (P.vec) {
-            stv<OT>(P.out, k, y);
-        } else {
+        if (P.q) *reinterpret_cast<uint2 *>(P.q + k) = c;
+        stv<OT>(P.out, k, y);
+    }
+};
+
+// 16 tokens at a time through shared memory, so that a lane gets eight neighbouring columns:
+// scales serve eight elements, and accesses are 16 bytes (4096 x 8192 x 2048 bf16 with bias,
+// GELU and checkpoint 51 us, a column a lane 82).  Rows that are not whole groups of eight
+// come back the same way, values and codes, to a column a lane (1000 x 2303 x 768 8.8 us,
+// single elements eight a lane 24).  The rows of 36 floats keep the accesses free of bank
+// conflicts.
+struct Stage {
+    static constexpr int CH = 16, PITCH = 36, bytes = CH * PITCH * 4 + CH * 32;
+    float *z;
+    uint8_t *codes;
+    __device__ __forceinline__ explicit Stage(uint8_t *mem)
+        : z(reinterpret_cast<float *>(mem)), codes(mem + CH * PITCH * 4) {}
+
+    // the lane's two groups: tokens lane / 4 and 8 + lane / 4, columns from 8 (lane % 4)
+    static __device__ __forceinline__ int64_t column(int64_t nn) {
+        const int lane = threadIdx.x & 31;
+        return nn - lane + 8 * (lane & 3);
+    }
+    template <int OT>
+    static __device__ __forceinline__ void residual(const Fp4Linear &P, int64_t m0, int rows, int64_t nn,
+                                                    Eight<OT> (&e)[2]) {
+        const int64_t c = column(nn);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < left) store_elem<OT>(P.out, k + j, y[j]);
+        for (int h = 0; h < 2; ++h) {
+            const int t = 8 * h + (threadIdx.x & 31) / 4;
+            e[h].load(P, t < rows && c < P.n, int64_t(int(m0) + t) * int(P.n) + c);
+        }
+    }
+    __device__ __forceinline__ void put(const uint32_t (&v)[CH], float bias) const {
+        __syncwarp();  // the last tokens are read
+#pragma unroll
+        for (int i = 0; i < CH; ++i) z[i * PITCH + (threadIdx.x & 31)] = __uint_as_float(v[i]) + bias;
+        __syncwarp();
+    }
+    // VEC: rows of whole groups of eight.  PAIR: in the kernel of pairs of CTAs, whose
+    // unrolled steps the others have no registers for.
+    template <int OT, int ACT, bool VEC, bool PAIR>
+    __device__ __forceinline__ void finish(const Fp4Linear &P, int64_t m0, int rows, int64_t nn,
+                                           const Eight<OT> (&e)[2]) const {
+        const int lane = threadIdx.x & 31;
+        const int64_t c = column(nn);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = 8 * h + lane / 4, m = int(m0) + t;
+            const bool in = t < rows && c < P.n;
+            float4 *at = reinterpret_cast<float4 *>(z + t * PITCH + 8 * (lane & 3));
+            const float4 a = at[0], b = at[1];
+            float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            const uint2 code = Eight<OT>::template apply<ACT>(P, in, int64_t(m) * P.kb + int(c) / kMxBlock, y);
+            if constexpr (VEC) {
+                e[h].store(P, in, int64_t(m) * int(P.n) + c, y, code);
+            } else {
+                at[0] = make_float4(y[0], y[1], y[2], y[3]);
+                at[1] = make_float4(y[4], y[5], y[6], y[7]);
+                *reinterpret_cast<uint2 *>(codes + 32 * t + 8 * (lane & 3)) = code;
+            }
+        }
+        if constexpr (VEC) return;
+        __syncwarp();
+        if constexpr (!PAIR) {
+            const int64_t n = P.n;
+            int64_t k = m0 * n + nn;
+#pragma unroll 1
+            for (int i0 = 0; i0 < min(rows, CH) && nn < n; i0 += 8, k += 8 * n) {
+                float r[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    r[i] = P.res && i0 + i < rows ? load_elem<OT>(P.res, k + i * n) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (i0 + i >= rows) break;
+                    const float v = z[(i0 + i) * PITCH + lane];
+                    store_elem<OT>(P.out, k + i * n, P.res ? v + r[i] : v);
+                    if (P.q) P.q[k + i * n] = codes[32 * (i0 + i) + lane];
+                }
+            }
+            return;
+        }
+        using One = EpOne<OT>;
+#pragma unroll
+        for (int h = 0; h < CH; h += One::CH) {
+            uint32_t r[One::WORDS], o[One::WORDS];
+            if (P.res) One::residual(P, m0 + h, rows - h, nn, r);
+#pragma unroll
+            for (int i = 0; i < One::CH / 2; ++i)
+                One::pack(One::add(P, z[(h + 2 * i) * PITCH + lane], z[(h + 2 * i + 1) * PITCH + lane], i, r), i, o);
+            One::store(P, m0 + h, rows - h, nn, o);
+        }
+        if (P.q && nn < P.n) {
+            uint8_t *at = P.q + m0 * P.n + nn;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                if (i < rows) *at = codes[32 * i + lane];
+                at += P.n;
+            }
         }
     }
 };
 
-// For pairs of CTAs: 16 tokens at a time go through shared memory, so that a lane gets
-// eight neighbouring columns: scales serve eight elements, and accesses are 16 bytes.
-// (4096 x 8192 x 2048 bf16 with bias, GELU and checkpoint 51 us, a column a lane 82.)
-// The rows of 36 floats keep both accesses free of bank conflicts.
-template <int OT, int ACT>
+// For pairs of CTAs.
+template <int OT, int ACT, bool VEC>
 struct EpStaged {
     using Args = Fp4Linear;
+    using Split = EpStaged;
     static constexpr bool none = false;
-    static constexpr int CH = 16, PITCH = 36, staged = CH * PITCH * 4;
+    static constexpr int CH = Stage::CH, staged = Stage::bytes;
     struct State {
         Eight<OT> e[2];
         float bias;
     };
-    static __device__ __forceinline__ void residual(const Args &P, int64_t m0, int rows, int64_t nn, Eight<OT> (&e)[2]) {
-        const int lane = threadIdx.x & 31;
-        const int64_t c = nn - lane + 8 * (lane & 3);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int t = 8 * h + lane / 4;
-            e[h].load(P, t < rows && c < P.n, int64_t(int(m0) + t) * int(P.n) + c, 8);
-        }
-    }
     static __device__ __forceinline__ void begin(const Args &P, int64_t m0, int rows, int64_t nn, State &ep) {
         ep.bias = bias_at<OT>(P, nn);
-        residual(P, m0, rows, nn, ep.e);
+        if (VEC) Stage::residual(P, m0, rows, nn, ep.e);
     }
     template <int CNT>
     static __device__ __forceinline__ void finish(const Args &P, int64_t m0, int rows, int64_t nn,
                                                   const uint32_t (&v)[CNT], State &ep, uint8_t *mem) {
-        float *stage = reinterpret_cast<float *>(mem);
-        const int lane = threadIdx.x & 31;
-        const int64_t c = nn - lane + 8 * (lane & 3);
+        const Stage stage(mem);
 #pragma unroll
         for (int s = 0; s < CNT; s += CH) {
             if (s >= rows) break;
-            __syncwarp();  // the last tokens are read
+            uint32_t part[CH];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) stage[i * PITCH + lane] = __uint_as_float(v[s + i]) + ep.bias;
-            __syncwarp();
+            for (int i = 0; i < CH; ++i) part[i] = v[s + i];
+            stage.put(part, ep.bias);
             // 16-bit types: 16 tokens ahead (fp32 has no registers for that)
-            Eight<OT> nxt[OT == kF32 ? 1 : 2];
-            if constexpr (OT != kF32)
-                if (s + CH < CNT) residual(P, m0 + s + CH, rows - s - CH, nn, nxt);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = 8 * h + lane / 4;
-                const bool in = s + t < rows && c < P.n;
-                const int m = int(m0) + s + t;
-                const float4 *at = reinterpret_cast<const float4 *>(stage + t * PITCH + 8 * (lane & 3));
-                const float4 a = at[0], b = at[1];
-                float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                ep.e[h].template finish<ACT>(P, in, int64_t(m) * int(P.n) + c, 8,
-                                             int64_t(m) * P.kb + int(c) / kMxBlock, z);
-            }
-            if (s + CH < CNT) {
+            Eight<OT> nxt[2];
+            if constexpr (VEC && OT != kF32)
+                if (s + CH < CNT) Stage::residual(P, m0 + s + CH, rows - s - CH, nn, nxt);
+            stage.template finish<OT, ACT, VEC, true>(P, m0 + s, rows - s, nn, ep.e);
+            if (VEC && s + CH < CNT) {
                 if constexpr (OT == kF32) {
-                    residual(P, m0 + s + CH, rows - s - CH, nn, ep.e);
+                    Stage::residual(P, m0 + s + CH, rows - s - CH, nn, ep.e);
                 } else {
                     ep.e[0] = nxt[0];
                     ep.e[1] = nxt[1];
@@ -308,57 +349,34 @@ struct EpStaged {
 };
 
 // For one CTA a tile: as EpStaged, with the element type and the activation looked up for
-// every 16 tokens, and rows of any length.
+// every 16 tokens.
+template <bool VEC>
 struct EpAny {
     using Args = Fp4Linear;
+    using Split = EpAny<true>;  // joining a cut reduction's parts looks up VEC itself
     static constexpr bool none = false;
-    static constexpr int CH = 16, PITCH = 36, staged = CH * PITCH * 4;
+    static constexpr int CH = Stage::CH, staged = Stage::bytes;
     struct State {};
     static __device__ __forceinline__ void begin(const Args &, int64_t, int, int64_t, State &) {}
 
-    // 16 tokens from m0; stage: their z, a row of PITCH a token
-    template <int OT, int ACT>
-    static __device__ __forceinline__ void tokens(const Args &P, int64_t m0, int rows, int64_t c,
-                                                  const float *stage, const Eight<OT> (&e)[2]) {
-        const int lane = threadIdx.x & 31, left = int(min(int64_t(8), P.n - c));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int t = 8 * h + lane / 4;
-            const float4 *at = reinterpret_cast<const float4 *>(stage + t * PITCH + 8 * (lane & 3));
-            const float4 a = at[0], b = at[1];
-            float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            e[h].template finish<ACT>(P, t < rows && left > 0, (m0 + t) * P.n + c, left, (m0 + t) * P.kb + c / kMxBlock,
-                                      z);
-        }
-    }
     template <int OT>
     static __device__ __forceinline__ void run(const Args &P, int64_t m0, int rows, int64_t nn,
-                                               const uint32_t (&v)[CH], float *stage) {
-        const int lane = threadIdx.x & 31;
-        const int64_t c = nn - lane + 8 * (lane & 3);
+                                               const uint32_t (&v)[CH], const Stage &stage) {
         Eight<OT> e[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int t = 8 * h + lane / 4;
-            e[h].load(P, t < rows && c < P.n, (m0 + t) * P.n + c, int(min(int64_t(8), P.n - c)));
-        }
-        const float bias = bias_at<OT>(P, nn);
-        __syncwarp();  // the last tokens are read
-#pragma unroll
-        for (int i = 0; i < CH; ++i) stage[i * PITCH + lane] = __uint_as_float(v[i]) + bias;
-        __syncwarp();
+        if (VEC) Stage::residual(P, m0, rows, nn, e);
+        stage.put(v, bias_at<OT>(P, nn));
         switch (P.act) {
-        case AMP_ACT_GELU: return tokens<OT, AMP_ACT_GELU>(P, m0, rows, c, stage, e);
-        case AMP_ACT_GELU_TANH: return tokens<OT, AMP_ACT_GELU_TANH>(P, m0, rows, c, stage, e);
-        case AMP_ACT_SILU: return tokens<OT, AMP_ACT_SILU>(P, m0, rows, c, stage, e);
-        default: return tokens<OT, kNoAct>(P, m0, rows, c, stage, e);
+        case AMP_ACT_GELU: return stage.finish<OT, AMP_ACT_GELU, VEC, false>(P, m0, rows, nn, e);
+        case AMP_ACT_GELU_TANH: return stage.finish<OT, AMP_ACT_GELU_TANH, VEC, false>(P, m0, rows, nn, e);
+        case AMP_ACT_SILU: return stage.finish<OT, AMP_ACT_SILU, VEC, false>(P, m0, rows, nn, e);
+        default: return stage.finish<OT, kNoAct, VEC, false>(P, m0, rows, nn, e);
         }
     }
     template <int CNT>
     static __device__ __forceinline__ void finish(const Args &P, int64_t m0, int rows, int64_t nn,
                                                   const uint32_t (&v)[CNT], State &, uint8_t *mem) {
         static_assert(CNT == CH, "16 tokens");
-        float *stage = reinterpret_cast<float *>(mem);
+        const Stage stage(mem);
         if (P.ot == kF32) run<kF32>(P, m0, rows, nn, v, stage);
         else if (P.ot == kF16) run<kF16>(P, m0, rows, nn, v, stage);
         else run<kBF16>(P, m0, rows, nn, v, stage);

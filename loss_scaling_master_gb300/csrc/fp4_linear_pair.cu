@@ -5,15 +5,16 @@
 namespace amp {
 namespace {
 
-// Pairs of CTAs: staged where rows are whole groups of eight and there is something to
-// compute, or a residual and a short reduction to hide it behind (bf16 with a residual, a
-// column a lane and staged: 4096 x 8192 x 2048 44.8 and 40.3 us, 4096 x 4096 x 4096 32.0 and
-// 29.7, 8192 x 4096 x 8192 80.1 and 80.7); else a column a lane.
+// Pairs of CTAs: staged where there is something to compute, or a residual and a short
+// reduction to hide it behind (bf16 with a residual, a column a lane and staged: 4096 x 8192
+// x 2048 44.8 and 40.3 us, 4096 x 4096 x 4096 32.0 and 29.7, 8192 x 4096 x 8192 80.1 and
+// 80.7); else a column a lane.
 template <int OT, int ACT>
 cudaError_t pair_act(const Fp4Linear &P, const void *a, const void *b, int64_t row_bytes, int device, cudaStream_t s) {
-    if (P.vec && (ACT != kNoAct || P.q || (P.res && P.k64 <= 64)))
-        return go_pair<EpStaged<OT, ACT>>(P, a, b, row_bytes, device, s);
-    return go_pair<EpOne<OT, ACT>>(P, a, b, row_bytes, device, s);
+    if constexpr (ACT == kNoAct)
+        if (!P.q && !(P.vec && P.res && P.k64 <= 64)) return go_pair<EpOne<OT>>(P, a, b, row_bytes, device, s);
+    return P.vec ? go_pair<EpStaged<OT, ACT, true>>(P, a, b, row_bytes, device, s)
+                 : go_pair<EpStaged<OT, ACT, false>>(P, a, b, row_bytes, device, s);
 }
 template <int OT>
 cudaError_t pair_of(const Fp4Linear &P, const void *a, const void *b, int64_t row_bytes, int device, cudaStream_t s) {

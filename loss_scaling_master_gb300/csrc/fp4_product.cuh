@@ -76,6 +76,7 @@ constexpr int kStageBytes = 128;  // bytes of a row a stage: 256 elements
 
 struct EpNone {
     using Args = Fp4Product;
+    using Split = EpNone;  // for the kernels of a cut reduction
     static constexpr bool none = true;
     static constexpr int staged = 0;  // bytes of shared memory a store warp
     struct State {};
@@ -395,7 +396,7 @@ template <int BN, bool SPLIT, class EP>
 struct Solo {
     static constexpr int staged = SPLIT ? 0 : EP::staged;
     // load, issue, allocate, (idle), and the store warps: 16 for an epilogue on the widest
-    // tile (1000 x 2304 x 768 with bias, GELU and checkpoint 8.1 us by 8, SW16 by 16)
+    // tile (1000 x 2304 x 768 with bias, GELU and checkpoint 8.3 us by 8, 6.8 by 16)
     static constexpr int store_warps = staged && BN == 128 ? 16 : 8, threads = 128 + 32 * store_warps;
     static constexpr int w_bytes = kLanes * kStageBytes;
     static constexpr int t_bytes = BN * kStageBytes;
@@ -779,8 +780,9 @@ cudaError_t go(typename EP::Args P, const void *a, const void *b, int64_t row_by
     void *args[] = {&mt, &mw, &P};
     static std::atomic<uint64_t> ready[2];
     if (parts > 1)
-        return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, true, EP>), ready[1], device, unsigned(tiles * parts),
-                      Solo<BN, true, EP>::threads, Solo<BN, true, EP>::smem, parts, s, args);
+        return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, true, typename EP::Split>), ready[1], device, unsigned(tiles * parts),
+                      Solo<BN, true, typename EP::Split>::threads,
+                      Solo<BN, true, typename EP::Split>::smem, parts, s, args);
     return launch(reinterpret_cast<const void *>(&fp4_product_kernel<BN, false, EP>), ready[0], device,
                   unsigned(std::min<int64_t>(tiles, room)), S::threads, S::smem, 1, s, args);
 }
