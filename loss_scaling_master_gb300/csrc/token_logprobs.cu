@@ -674,8 +674,12 @@ cudaError_t fwd_x(const LogprobsFwd &P, int device, cudaStream_t s) {
     const int pieces = P.cols / Pieces<XT>::VN + 1, sms = sm_count(device);
     if (P.k <= 8 && (pieces <= 260 || (pieces <= 520 && P.rows >= 16 * sms))) return fwd<XT, 32, kShortRows>(P, 1, device, s);
     if (pieces <= 260 || (pieces <= 1030 && P.rows >= 2 * sms)) return fwd<XT, 128, 1>(P, 1, device, s);
+    // Until there is a CTA for each SM: a second one there costs the joined rows more than
+    // it gives (5 tokens, 1, 2, 4 and 8 CTAs a row: 1 x 128256 bf16 12.0, 9.1, 7.2, 6.3 us;
+    // 64 x 50257 fp32 8.8, 7.7, 7.2, 8.2; 150 x 128256 bf16 12.4, 11.6, 15.5, 19.9;
+    // 200 x 50257 fp16 9.6, 12.4 with two).
     int parts = 1;
-    while (parts < kMaxParts && P.rows * parts <= 2 * sms && pieces > parts * 1024) parts *= 2;
+    while (parts < kMaxParts && P.rows * parts <= sms && pieces > parts * 1024) parts *= 2;
     return fwd<XT, 256, 1>(P, parts, device, s);
 }
 template <int XT>
