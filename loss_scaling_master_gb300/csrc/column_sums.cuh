@@ -179,7 +179,7 @@ __device__ __forceinline__ void flat_sums(const SumShare<SumFlat> &at, int64_t r
 // Shares of the rows, of at least a row a group: as many as make the rounds of CTAs that
 // the GPU holds at once shortest.  CTAs of clusters start one after another, 5 ns each, so
 // beyond two an SM a share is at least four rows a group (1000 x 2304 dropout by 576 CTAs
-// 5.7 us, by 288 4.8).
+// 5.1 us, by 288 4.3).
 template <class S>
 int sum_parts(int64_t rows, int64_t tiles, int sms) {
     const int64_t room = int64_t(sms) * S::ctas;
@@ -203,8 +203,8 @@ cudaError_t launch_sums(int64_t rows, int64_t cols, int device, cudaStream_t s, 
     return launch_pdl_cluster<Kernel, kSmallShared>(device, dim3(unsigned(tiles * parts)), dim3(S::threads), parts, s, args);
 }
 // 16-bit rows in tiles of 32 columns where 64 would leave CTAs unused (1024 x 768 dropout
-// 3.7 us, by 64 4.1; 16384 x 768 16.8 and 25; but 4096 x 8192 37.5 and 32.5); fp32 ones always
-// (8192 x 2048 24.9 and 29.3).
+// 3.3 us, by 64 3.7; 16384 x 768 15.5 and 23; but 4096 x 8192 37.6 and 30.9); fp32 ones always
+// (8192 x 2048 25.0 and 29.3).
 inline bool narrow_tiles(int elem, int64_t cols, int device) {
     return elem == kF32 || cols < int64_t(sm_count(device)) * SumVec<64>::ctas * 64 / kSumParts;
 }
