@@ -673,7 +673,12 @@ template <int XT>
 cudaError_t fwd_x(const LogprobsFwd &P, int device, cudaStream_t s) {
     const int pieces = P.cols / Pieces<XT>::VN + 1, sms = sm_count(device);
     if (P.k <= 8 && (pieces <= 260 || (pieces <= 520 && P.rows >= 16 * sms))) return fwd<XT, 32, kShortRows>(P, 1, device, s);
-    if (pieces <= 260 || (pieces <= 1030 && P.rows >= 2 * sms)) return fwd<XT, 128, 1>(P, 1, device, s);
+    // 128 threads a row where those CTAs fill the SMs, 8 each (1216 x 50257 bf16 26.2 us with
+    // 256, 23.9 with 128, 5 tokens 30.3 and 27.5; 2048 x 20000 fp32 30.4 and 27.7; 4096 x 50257
+    // bf16 75.6 and 70.8, but 20 tokens 98.5 and 103, and 1023 x 50257 fp16 21.9 and 22.8,
+    // 4096 x 128256 158 and 160); shorter rows already when they are fewer
+    const int fits = P.rows >= 8 * sms ? (P.k <= 8 ? 6500 : 4200) : P.rows >= 2 * sms ? 1030 : 260;
+    if (pieces <= fits) return fwd<XT, 128, 1>(P, 1, device, s);
     // Until there is a CTA for each SM: a second one there costs the joined rows more than
     // it gives (5 tokens, 1, 2, 4 and 8 CTAs a row: 1 x 128256 bf16 12.0, 9.1, 7.2, 6.3 us;
     // 64 x 50257 fp32 8.8, 7.7, 7.2, 8.2; 150 x 128256 bf16 12.4, 11.6, 15.5, 19.9;

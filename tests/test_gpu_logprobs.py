@@ -130,7 +130,7 @@ def check_grad(G, dev, z, t, zd, td, got, dld, lead, scale):
 # rows, cols: one logit, less than a piece, whole pieces, odd; one row and few (cut over a
 # cluster), many short rows, a vocabulary
 SIZES = [(1, 1), (3, 2), (5, 7), (2, 8), (4, 33), (300, 65), (1, 4099), (7, 8192), (200, 1000), (1, 50257),
-         (40, 50257), (100, 20001), (170, 9001), (330, 5000), (1, 128256), (9, 128256), (3000, 17)]
+         (40, 50257), (100, 20001), (170, 9001), (330, 5000), (1300, 9001), (1, 128256), (9, 128256), (3000, 17)]
 
 
 @pytest.mark.parametrize("dt", TYPES)
