@@ -25,11 +25,10 @@ struct BiasBwd {
 template <int XT, int ACT, class S>
 __global__ void __launch_bounds__(S::threads, S::ctas) bias_bwd_kernel(BiasBwd P) {
     constexpr bool VEC = S::each == 8;
-    // Elements a thread and row, and rows a step, as many as 64 registers hold (of 16384 x
-    // 5120 bf16: the sums alone 2, 4, 8 rows 35.5, 31.5, 30.9 us; with GELU 2, 3, 4 rows
-    // 83.1, 79.4, 80.8; of 8192 x 2048 fp32: alone 2, 4, 8 rows 9.0, 7.8, 18, with GELU 2, 3 29.2, 33.8).
-    constexpr int N = VEC ? 8 : 1;
-    constexpr int U = !VEC ? 8 : ACT == kNoAct ? (XT == kF32 ? 4 : 8) : XT == kF32 ? 2 : 3;
+    static_assert(!VEC || XT == kF32, "16-bit ones by bias_bwd_ring_kernel");
+    // Elements a thread and row, and rows a step, as many as 64 registers hold (8192 x 2048
+    // fp32: the sums alone 2, 4, 8 rows 9.0, 7.8, 18 us, with GELU 2, 3 rows 29.2, 33.8).
+    constexpr int N = VEC ? 8 : 1, U = !VEC ? 8 : ACT == kNoAct ? 4 : 2;
     pdl_wait();
     pdl_trigger();
     const SumShare<S> at(P.rows);
@@ -116,6 +115,66 @@ __global__ void __launch_bounds__(S::threads, S::ctas) bias_bwd_kernel(BiasBwd P
     sum_join<S>(at, P.cols, a, P.db, P.otype);
 }
 
+// 16-bit rows of whole groups come ahead through shared memory; a block's scale, read by a
+// plain load, one row ahead.  (16384 x 5120 bf16 with GELU, 2, 3, 4, 6 rows: 76, 76, 81,
+// 124 us, the last by three CTAs an SM; by registers, three rows at once, 79.3.  The sums
+// alone, 16384 x 768, 3, 4, 6, 8 rows: 5.5, 5.2, 5.7, 5.6; eight by registers 5.9.)
+constexpr int kRingShared = 100;  // KB an SM: 4 CTAs of 17 or 21
+template <int XT, int ACT, class S>
+__global__ void __launch_bounds__(S::threads, S::ctas) bias_bwd_ring_kernel(BiasBwd P) {
+    static_assert(XT != kF32);
+    constexpr bool DO = ACT != kNoAct;
+    constexpr int AHEAD = DO ? 2 : 4;
+    __shared__ uint4 s_dy[AHEAD][S::threads];
+    __shared__ uint2 s_q[DO ? AHEAD : 1][DO ? S::threads : 1];
+    pdl_wait();
+    pdl_trigger();
+    const SumShare<S> at(P.rows);
+    const int64_t c = at.col0 + int(threadIdx.x) % S::across * 8, hop = S::groups * P.cols;
+    const int64_t r0 = at.row0 + int(threadIdx.x) / S::across, end = c < P.cols ? at.row1 * P.cols : 0;
+    int64_t k = r0 * P.cols + c;
+    const uint8_t *sc = P.s + r0 * P.kb + c / kMxBlock;
+    const int64_t sc_hop = int64_t(S::groups) * P.kb;
+    float a[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+    const auto ask = [&](int64_t at_k, int slot) {
+        if (at_k < end) {
+            copy_ahead<16>(&s_dy[slot][threadIdx.x], static_cast<const char *>(P.dy) + 2 * at_k);
+            if (DO) copy_ahead<8>(&s_q[DO ? slot : 0][DO ? threadIdx.x : 0], P.q + at_k);
+        }
+        copies_of_row();
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) ask(k + i * hop, i);
+    uint32_t e_next = DO && k < end ? *sc : 0;
+    for (int slot = 0; k < end; k += hop) {
+        const uint32_t e = e_next;
+        if (DO && k + hop < end) e_next = *(sc += sc_hop);
+        copies_wait<AHEAD - 1>();
+        const uint4 g[1] = {s_dy[slot][threadIdx.x]};
+        float y[8];
+        raw8_to_f32<XT>(g, y);
+        if constexpr (DO) {
+            float x[8];
+            values8(s_q[slot][threadIdx.x], mx_scale(e), x);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                float2 dz, unused;
+                act_grads<XT, ACT, false>(x[j], x[j + 1], 0.0f, 0.0f, y[j], y[j + 1], dz, unused);
+                y[j] = dz.x;
+                y[j + 1] = dz.y;
+            }
+            stv<XT>(P.dz, k, y);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] += y[j];
+        ask(k + AHEAD * hop, slot);
+        slot = slot + 1 == AHEAD ? 0 : slot + 1;
+    }
+    sum_join<S>(at, P.cols, a, P.db, P.otype);
+}
+
 template <int XT, int ACT>
 struct BiasFlat {
     const BiasBwd &P;
@@ -181,12 +240,15 @@ cudaError_t go(const BiasBwd &P, bool aligned, int dev, cudaStream_t s) {
     if (!aligned) return launch_sums<SumElem, &bias_bwd_kernel<XT, ACT, SumElem>>(P.rows, P.cols, dev, s, P);
     // the activations' longer way to a group's values needs CTAs enough to hide it (2047 x
     // 1111 bf16 GELU 13.3 us, by single elements 10.4; 16383 x 5121 198 and 383)
-    if (P.cols % 8 && (ACT == kNoAct || !narrow_tiles(kBF16, P.cols, dev)))
+    if (P.cols % 8 && (ACT == kNoAct || !narrow_tiles(P.cols, dev)))
         return launch_sums<SumFlat, &bias_bwd_flat_kernel<XT, ACT>>(P.rows, P.cols, dev, s, P);
     if (P.cols % 8) return launch_sums<SumElem, &bias_bwd_kernel<XT, ACT, SumElem>>(P.rows, P.cols, dev, s, P);
-    if (XT == kF32 || narrow_tiles(XT, P.cols, dev))
+    if constexpr (XT == kF32)
         return launch_sums<SumVec<32>, &bias_bwd_kernel<XT, ACT, SumVec<32>>>(P.rows, P.cols, dev, s, P);
-    return launch_sums<SumVec<64>, &bias_bwd_kernel<XT, ACT, SumVec<64>>>(P.rows, P.cols, dev, s, P);
+    else if (narrow_tiles(P.cols, dev))
+        return launch_sums<SumVec<32>, &bias_bwd_ring_kernel<XT, ACT, SumVec<32>>, kRingShared>(P.rows, P.cols, dev, s, P);
+    else
+        return launch_sums<SumVec<64>, &bias_bwd_ring_kernel<XT, ACT, SumVec<64>>, kRingShared>(P.rows, P.cols, dev, s, P);
 }
 template <int XT>
 cudaError_t go_x(const BiasBwd &P, int act, bool aligned, int dev, cudaStream_t s) {

@@ -114,6 +114,19 @@ __device__ __forceinline__ void sum_join(const SumShare<S> &at, int64_t cols, co
     }
 }
 
+// Rows on their way to shared memory, which takes no registers: N bytes a thread, for itself
+// alone, so that no barrier is needed.
+template <int N>
+__device__ __forceinline__ void copy_ahead(void *to, const void *from) {
+    const uint32_t at = uint32_t(__cvta_generic_to_shared(to));
+    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(N) : "memory");
+}
+// What was asked for since the last call belongs to one row.
+__device__ __forceinline__ void copies_of_row() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LATER>  // all rows but the last LATER are there
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory"); }
+
 // Rows of any length, tensors aligned to 16 bytes: the matrix is taken as a flat run of
 // groups of 8 elements, of which a tile's part of a row holds at most `across`, the first
 // and the last perhaps in part.  What the op makes of a warp's groups goes through shared
@@ -179,7 +192,7 @@ __device__ __forceinline__ void flat_sums(const SumShare<SumFlat> &at, int64_t r
 // Shares of the rows, of at least a row a group: as many as make the rounds of CTAs that
 // the GPU holds at once shortest.  CTAs of clusters start one after another, 5 ns each, so
 // beyond two an SM a share is at least four rows a group (1000 x 2304 dropout by 576 CTAs
-// 5.1 us, by 288 4.3).
+// 5.2 us, by 288 4.3).
 template <class S>
 int sum_parts(int64_t rows, int64_t tiles, int sms) {
     const int64_t room = int64_t(sms) * S::ctas;
@@ -196,17 +209,17 @@ int sum_parts(int64_t rows, int64_t tiles, int sms) {
     }
     return parts;
 }
-template <class S, auto Kernel, class A>
+template <class S, auto Kernel, int SharedKB = kSmallShared, class A>
 cudaError_t launch_sums(int64_t rows, int64_t cols, int device, cudaStream_t s, const A &args) {
     const int64_t tiles = (cols + S::cols - 1) / S::cols;
     const int parts = sum_parts<S>(rows, tiles, sm_count(device));
-    return launch_pdl_cluster<Kernel, kSmallShared>(device, dim3(unsigned(tiles * parts)), dim3(S::threads), parts, s, args);
+    return launch_pdl_cluster<Kernel, SharedKB>(device, dim3(unsigned(tiles * parts)), dim3(S::threads), parts, s, args);
 }
 // 16-bit rows in tiles of 32 columns where 64 would leave CTAs unused (1024 x 768 dropout
-// 3.3 us, by 64 3.7; 16384 x 768 15.5 and 23; but 4096 x 8192 37.6 and 30.9); fp32 ones always
-// (8192 x 2048 25.0 and 29.3).
-inline bool narrow_tiles(int elem, int64_t cols, int device) {
-    return elem == kF32 || cols < int64_t(sm_count(device)) * SumVec<64>::ctas * 64 / kSumParts;
+// 3.3 us, by 64 3.6; 16384 x 768 14.6 and 20.4; but 4096 x 8192 32.8 and 27.3); fp32 ones always
+// (8192 x 2048 22.8 and 27.2).
+inline bool narrow_tiles(int64_t cols, int device) {
+    return cols < int64_t(sm_count(device)) * SumVec<64>::ctas * 64 / kSumParts;
 }
 
 // 8 elements of a group as raw words; a group that ends behind the tensor's last element

@@ -110,12 +110,47 @@ __global__ void __launch_bounds__(kThreads) dropout_elem_kernel(Dropout P) {
     }
 }
 
-// The gradient with the bias's: by columns (column_sums.cuh).
-template <int XT, bool ALL, class S>
-__global__ void __launch_bounds__(S::threads, S::ctas) dropout_bias_vec_kernel(Dropout P) {
-    // rows a step: of 16384 x 5120 bf16 1, 2, 3, 4, 6 take 75.8, 68.1, 66.5, 69.1, 70.4 us,
-    // of 8192 x 2048 fp32 1, 2, 3 take 25.8, 25.3, 31.1
-    constexpr int U = XT == kF32 ? 2 : 3;
+// The gradient with the bias's: by columns (column_sums.cuh).  16-bit rows come kAhead
+// ahead through shared memory (16384 x 5120 bf16 59 us, after a forward pass 74; by
+// registers, three rows at once, 66.5 and 88; 4 rows ahead 59.2 and 77, 8 63 and 73).
+constexpr int kAhead = 6, kRingShared = 132;  // KB an SM: 4 CTAs of 29
+template <bool ALL, int XT, class S>
+__global__ void __launch_bounds__(S::threads, S::ctas) dropout_bias_ring_kernel(Dropout P) {
+    static_assert(XT != kF32);
+    __shared__ uint4 s_ring[kAhead][S::threads];
+    pdl_wait();
+    pdl_trigger();
+    const SumShare<S> at(P.rows);
+    const int32_t step = P.step ? *P.step : 0;
+    const int64_t c = at.col0 + int(threadIdx.x) % S::across * 8, hop = S::groups * P.cols;
+    const int64_t end = c < P.cols ? at.row1 * P.cols : 0;
+    int64_t k = (at.row0 + int(threadIdx.x) / S::across) * P.cols + c;
+    float a[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    const auto ask = [&](int64_t at_k, int slot) {
+        if (at_k < end) copy_ahead<16>(&s_ring[slot][threadIdx.x], static_cast<const char *>(P.x) + 2 * at_k);
+        copies_of_row();
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ask(k + i * hop, i);
+    for (int slot = 0; k < end; k += hop) {
+        copies_wait<kAhead - 1>();
+        const uint4 g[1] = {s_ring[slot][threadIdx.x]};
+        float y[8];
+        raw8_to_f32<XT>(g, y);
+        drop8<ALL>(P, step, k >> 3, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] += y[j];
+        stv<XT>(P.y, k, y);
+        ask(k + kAhead * hop, slot);
+        slot = slot + 1 == kAhead ? 0 : slot + 1;
+    }
+    sum_join<S>(at, P.cols, a, P.db, P.otype);
+}
+// fp32 rows go through registers, two a step (8192 x 2048 22.8 us; through shared memory,
+// where a thread's two copies each take half of every 32 bytes, 35).
+template <bool ALL, class S>
+__global__ void __launch_bounds__(S::threads, S::ctas) dropout_bias_f32_kernel(Dropout P) {
+    constexpr int U = 2;
     pdl_wait();
     pdl_trigger();
     const SumShare<S> at(P.rows);
@@ -124,25 +159,21 @@ __global__ void __launch_bounds__(S::threads, S::ctas) dropout_bias_vec_kernel(D
     const bool in = c < P.cols;
     float a[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     for (int64_t r0 = at.row0 + int(threadIdx.x) / S::across; in && r0 < at.row1; r0 += U * S::groups) {
-        uint4 g[U][kWords8<XT>];
+        float y[U][8];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + u * S::groups;
             if (r >= at.row1) break;
-#pragma unroll
-            for (int w = 0; w < kWords8<XT>; ++w)
-                g[u][w] = ld16(static_cast<const char *>(P.x) + (r * P.cols + c) * (XT == kF32 ? 4 : 2) + 16 * w);
+            ldv<kF32>(P.x, r * P.cols + c, y[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + u * S::groups, k = r * P.cols + c;
             if (r >= at.row1) break;
-            float y[8];
-            raw8_to_f32<XT>(g[u], y);
-            drop8<ALL>(P, step, k >> 3, y);
+            drop8<ALL>(P, step, k >> 3, y[u]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] += y[j];
-            stv<XT>(P.y, k, y);
+            for (int j = 0; j < 8; ++j) a[j] += y[u][j];
+            stv<kF32>(P.y, k, y[u]);
         }
     }
     sum_join<S>(at, P.cols, a, P.db, P.otype);
@@ -221,9 +252,12 @@ cudaError_t go(const Dropout &P, int dev, cudaStream_t s) {
     if (P.db) {
         if (!vec) return launch_sums<SumElem, &dropout_bias_elem_kernel<XT, ALL>>(P.rows, P.cols, dev, s, P);
         if (P.cols % 8) return launch_sums<SumFlat, &dropout_bias_flat_kernel<XT, ALL>>(P.rows, P.cols, dev, s, P);
-        if (XT == kF32 || narrow_tiles(XT, P.cols, dev))
-            return launch_sums<SumVec<32>, &dropout_bias_vec_kernel<XT, ALL, SumVec<32>>>(P.rows, P.cols, dev, s, P);
-        return launch_sums<SumVec<64>, &dropout_bias_vec_kernel<XT, ALL, SumVec<64>>>(P.rows, P.cols, dev, s, P);
+        if constexpr (XT == kF32)
+            return launch_sums<SumVec<32>, &dropout_bias_f32_kernel<ALL, SumVec<32>>>(P.rows, P.cols, dev, s, P);
+        else if (narrow_tiles(P.cols, dev))
+            return launch_sums<SumVec<32>, &dropout_bias_ring_kernel<ALL, XT, SumVec<32>>, kRingShared>(P.rows, P.cols, dev, s, P);
+        else
+            return launch_sums<SumVec<64>, &dropout_bias_ring_kernel<ALL, XT, SumVec<64>>, kRingShared>(P.rows, P.cols, dev, s, P);
     }
     Dropout F = P;
     F.cols = P.rows * P.cols;
