@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(S::threads, S::ctas) bias_bwd_ring_kernel(Bias
     const int64_t c = at.col0 + int(threadIdx.x) % S::across * 8, hop = S::groups * P.cols;
     const int64_t r0 = at.row0 + int(threadIdx.x) / S::across, end = c < P.cols ? at.row1 * P.cols : 0;
     int64_t k = r0 * P.cols + c;
-    const uint8_t *sc = P.s + r0 * P.kb + c / kMxBlock;
+    const uint8_t *sc = DO ? P.s + r0 * P.kb + c / kMxBlock : nullptr;
     const int64_t sc_hop = int64_t(S::groups) * P.kb;
     float a[8];
 #pragma unroll
