@@ -508,6 +508,12 @@ PyObject *logprobs_forward(PyObject *, Args a, Py_ssize_t n) {
             if (ids.dim() < 1) refuse("top_ids: needs at least one dimension");
             top = ids.size(-1);
             if (top < 1 || top > 32) refuse("top_ids: 1 to 32 alternatives a row");
+            if (a[6] != Py_None) {  // both are filled with rows of `top`
+                const at::Tensor &lp = tensor(a[6], "top_logp");
+                if (lp.dim() < 1 || lp.size(-1) != top)
+                    refuse("top_logp: rows of " + std::to_string(lp.dim() < 1 ? 0 : lp.size(-1)) +
+                           " alternatives, those of top_ids have " + std::to_string(top));
+            }
         }
         auto *ids = static_cast<int64_t *>(z.of(a[5], "top_ids", top, at::kLong));
         auto *lp = static_cast<float *>(z.of(a[6], "top_logp", top, at::kFloat));

@@ -225,7 +225,7 @@ def amp_token_logprobs_forward(logits, targets, logp, entropy=None, stats=None, 
                                top_logp=None, stream=None):
     """Log probabilities of the targets (int64, negative: row not used; or None) under softmax of
     each row of the logits, whose rows may lie apart; entropy, stats (fp32 [rows, 2], for the
-    backward pass) and the most probable tokens (int64 and fp32 [rows, n]) where given."""
+    backward pass) and the most probable tokens (int64 and fp32, both rows of n) where given."""
     st = (_native or _bound()).logprobs_forward(logits, targets, logp, entropy, stats, top_ids,
                                                 top_logp, stream)
     if st:
