@@ -22,8 +22,9 @@
  * synchronisation, negative status = nothing enqueued, message in
  * amp_last_error(), programmatic dependent launches, one NVTX range per call.
  * A tensor is aligned to its element type (else AMP_EINVAL); where a buffer has
- * to be aligned further its comment says so.  Empty shapes are accepted
- * everywhere.
+ * to be aligned further its comment says so.  An output shares no memory with
+ * another tensor of its call unless its comment allows it.  Empty shapes are
+ * accepted everywhere.
  *
  * Block formats (OCP Microscaling Formats specification 1.0: 32 consecutive
  * elements of a row share one E8M0 scale byte e, which stands for 2^(e-127)).
@@ -297,11 +298,13 @@ amp_status amp_token_logprobs_forward(const void *z, amp_dtype dtype, int64_t ro
  *             entropy is needed
  *   scale_dev the loss scale S, one fp32 on the device, or NULL (1)
  *   dz        [rows, cols] of dtype, rows dld >= cols elements apart (what lies
- *             between is left as it is); may be z itself with dld = ld
+ *             between is left as it is); may be z itself with dld = ld, and
+ *             otherwise shares no element with it (column slices of one buffer
+ *             do not; with two strides the ranges have to be apart)
  * Rows with a negative target get zeros, whatever their logits.
  * Errors: AMP_EINVAL (NULL z / stats / dz, dlogp without targets, dentropy
- * without entropy, ld or dld < cols, dz = z with another dld, negative or too
- * large size), AMP_EDTYPE. */
+ * without entropy, ld or dld < cols, dz = z with another dld, dz that overlaps z
+ * otherwise, negative or too large size), AMP_EDTYPE. */
 amp_status amp_token_logprobs_backward(const float *dlogp, const void *z, amp_dtype dtype,
                                        int64_t rows, int64_t cols, int64_t ld,
                                        const int64_t *targets, const float *stats,

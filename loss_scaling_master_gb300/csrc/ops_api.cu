@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <utility>
 
 #include "ampops.h"
 #include "internal.h"
@@ -460,6 +461,25 @@ amp_status amp_token_logprobs_forward(const void *z, amp_dtype dtype, int64_t ro
                   fn);
 }
 
+// Whether two matrices of this shape and element size share an element without being one
+// and the same.  Rows of one stride may lie between each other's (column slices of one
+// buffer); of two strides, the ranges they span have to be apart.
+static bool overlap_partly(const void *a, int64_t lda, const void *b, int64_t ldb, int64_t rows, int64_t cols,
+                           int64_t esz) {
+    if (a == b && (rows == 1 || lda == ldb)) return false;
+    const char *lo = static_cast<const char *>(a), *hi = static_cast<const char *>(b);
+    if (hi < lo) {
+        std::swap(lo, hi);
+        std::swap(lda, ldb);
+    }
+    const int64_t d = hi - lo;  // bytes; the lower one spans ((rows - 1) lda + cols) elements
+    if (d >= ((rows - 1) * lda + cols) * esz) return false;
+    if (rows == 1 || lda != ldb) return true;
+    // a row of the upper one starts `in` bytes behind the start of a row of the lower one
+    const int64_t in = d % (lda * esz), past = d / (lda * esz);
+    return in < cols * esz || (past + 1 < rows && in > (lda - cols) * esz);
+}
+
 amp_status amp_token_logprobs_backward(const float *dlogp, const void *z, amp_dtype dtype, int64_t rows, int64_t cols,
                                        int64_t ld, const int64_t *targets, const float *stats, const float *entropy,
                                        const float *dentropy, const float *scale_dev, void *dz, int64_t dld,
@@ -474,6 +494,8 @@ amp_status amp_token_logprobs_backward(const float *dlogp, const void *z, amp_dt
     if (dentropy && !entropy) return fail(AMP_EINVAL, "%s: dentropy needs the entropy", fn);
     if (!z || !stats || !dz) return fail(AMP_EINVAL, kNull, fn);
     if (dz == z && dld != ld) return fail(AMP_EINVAL, "%s: in place, the rows need one stride", fn);
+    if (overlap_partly(z, ld, dz, dld, rows, cols, ec == amp::kF32 ? 4 : 2))
+        return fail(AMP_EINVAL, "%s: dz overlaps z without being z", fn);
     if (off_type(ec, z, dz) || off_type(amp::kF32, dlogp, entropy, dentropy, scale_dev) || misaligned(targets, 8) ||
         misaligned(stats, 8))
         return fail(AMP_EINVAL, kOff, fn);
