@@ -89,6 +89,15 @@ __global__ void __launch_bounds__(kThreads, fwd_vec_ctas(XT, ACT, GATED))
     }
 }
 
+// block_max8 by integers, as large bits are large magnitudes.
+__device__ __forceinline__ uint32_t block_max8_ints(const float (&y)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+}
+
 // Any size, any address: a warp takes EB blocks of a row at a time, a lane one
 // element of each, so accesses stay side by side and a row's place is worked out
 // once for EB elements (with one block a step, 100 instructions an element bound
@@ -109,8 +118,8 @@ __device__ __forceinline__ float widen1(Elem<XT> v) {
 // consecutive ones a lane and their codes come back as bytes, so that scales and
 // conversions serve 8 elements (fp32: 16-byte pieces exchanged in every other
 // block, against bank conflicts).  n > 32 i: element i is in the row; kb: blocks
-// left in it.
-template <int XT, int EB>
+// left in it.  INTS: the blocks' maxima by integers.
+template <int XT, int EB, bool INTS>
 __device__ __forceinline__ void keep_elems(const Elem<XT> (&x)[EB], int n, int kb, uint8_t *q, uint8_t *sc,
                                            uint4 *s, uint2 *b) {
     const int lane = threadIdx.x & 31;
@@ -126,7 +135,7 @@ __device__ __forceinline__ void keep_elems(const Elem<XT> (&x)[EB], int n, int k
         for (int i = 0; i < W; ++i) u[i] = s[(W * lane + i) ^ (W == 2 ? (lane >> 2) & 1 : 0)];
         float y[8];
         raw8_to_f32<XT>(u, y);
-        const uint32_t e = mx_scale_code<MxE4M3>(block_max8(y));
+        const uint32_t e = mx_scale_code<MxE4M3>(INTS ? block_max8_ints(y) : block_max8(y));
         b[lane] = codes8(y, mx_unscale(e));
         if ((lane & 3) == 0 && lane / 4 < kb) sc[lane / 4] = uint8_t(e);
         __syncwarp();
@@ -165,8 +174,13 @@ __global__ void __launch_bounds__(kThreads) act_fwd_elem(ActFwd P) {
             u[i] = GATED && n > 32 * i ? up[32 * i] : Elem<XT>(0);
         }
         if constexpr (KEEP) {
-            keep_elems<XT, EB>(x, n, P.kb - b0, P.q + k, P.s + sb, s_x[warp], s_q[warp]);
-            if (GATED) keep_elems<XT, EB>(u, n, P.kb - b0, P.qu + k, P.su + sb, s_x[warp], s_q[warp]);
+            // Maxima by integers leave plain 16-bit activations 40 registers, by three magnitudes
+            // an instruction 42, and an SM 5 CTAs instead of 6 (4095 x 8191 bf16 GELU 42.6 and
+            // 44.0 us, tanh 45.9 and 46.6, SiLU 40.9 and 42.4).  Elsewhere they are slower:
+            // the checkpoint alone 25.9 and 25.1 us, gated SiLU 66.1 and 64.8, fp32 GELU 57.1 and 53.3.
+            constexpr bool INTS = ACT != kSave && !GATED && XT != kF32;
+            keep_elems<XT, EB, INTS>(x, n, P.kb - b0, P.q + k, P.s + sb, s_x[warp], s_q[warp]);
+            if (GATED) keep_elems<XT, EB, INTS>(u, n, P.kb - b0, P.qu + k, P.su + sb, s_x[warp], s_q[warp]);
         }
         if constexpr (ACT != kSave) {
             char *yp = static_cast<char *>(P.y) + k * int(sizeof(Elem<XT>));
