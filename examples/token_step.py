@@ -23,6 +23,7 @@ PAD = -100  # a position without a next token
 
 
 class TokenHead:
+    # one dropout, one micro-batch a step, one rank (others take sites and seeds of their own)
     EPS, SEED, SITE = 1e-5, 0x5EED, 0
 
     def __init__(self, tokens, d, hidden, vocab, p=0.1, entropy=0.0, seed=0, scale=2.0 ** 12, lr=1e-3):

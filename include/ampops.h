@@ -246,8 +246,14 @@ amp_status amp_bias_act_backward_mx8(int32_t act, const void *dy, amp_dtype dtyp
  * rounding under the same seed are others (their tensor words are below 2^30,
  * or 2^31 and more).
  *   step_dev  the step, one int32 on the device (so a captured graph draws
- *             another mask each time it is changed); NULL: 0
- *   site      which of a step's dropouts this is, in [0, 2^30)
+ *             another mask each time it is changed); NULL: 0, the same mask in
+ *             every call.  A step count that stays where a step was skipped
+ *             draws that step's masks again
+ *   site      which of a step's dropouts this is, in [0, 2^30).  Calls of one
+ *             seed, step and site draw one mask, so each dropout of a model has
+ *             its site, each micro-batch of an accumulated step sites of its own
+ *             (dropout * micro_batches + micro_batch), and each data-parallel
+ *             rank a seed of its own (seed + rank)
  *   residual  of the same type, or NULL (0); y may be x or residual
  * Errors: AMP_EINVAL (NULL x / y, p outside [0, 1] or NaN, site out of range,
  * negative or too large size), AMP_EDTYPE. */

@@ -207,7 +207,9 @@ def amp_bias_act_backward_mx8(dy, dbias, kind=None, saved=None, dx=None, stream=
 
 def amp_dropout_forward(x, p: float, seed: int, site: int, y, residual=None, step=None, stream=None):
     """y = residual + dropout(x), the mask a function of (seed, step, site, element); step: one
-    int32 on the device (AmpOptimizerStep.step_count, say; None: 0)."""
+    int32 on the device (AmpOptimizerStep.step_count, say; None: 0).  The count changes once an
+    optimizer step: micro-batches that share one need sites of their own (dropout * micro_batches +
+    micro_batch), data-parallel ranks seeds of their own (seed + rank)."""
     st = (_native or _bound()).dropout_forward(x, p, seed, site, y, residual, step, stream)
     if st:
         _check("amp_dropout_forward", st)
