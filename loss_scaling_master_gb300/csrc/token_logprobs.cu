@@ -205,14 +205,6 @@ struct Best {
         for (int j = 16; j > 0; j >>= 1) e = exchange(e, j, (lane & j) == 0);
         return e;
     }
-    static __device__ __forceinline__ Entry sorted(Entry e) {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int n = 2; n < 32; n *= 2)
-#pragma unroll
-            for (int j = n / 2; j > 0; j >>= 1) e = exchange(e, j, ((lane & j) == 0) == ((lane & n) == 0));
-        return settle(e);
-    }
     // with another sorted list
     __device__ __forceinline__ void merge(Entry e) {
         e = other(e, 31);
