@@ -39,8 +39,7 @@ cudaError_t launch_fp4_linear(const void *a, const uint8_t *sa, const void *b, c
     P.rpacked = P.packed && (reinterpret_cast<uintptr_t>(res) & 3) == 0;
     const auto off = [](const void *p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; };
     P.vec = n % 8 == 0 && !off(out, 15) && !off(res, 15) && !off(q, 7);
-    cudaError_t e = fp4_error_word(device, &P.error);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     const int64_t row_bytes = (k + kMxBlock - 1) / kMxBlock * 16;
     if (k == 0) {
         const int64_t want = ((m + 15) / 16 * P.kb * 32 + kThreads - 1) / kThreads;
@@ -52,6 +51,14 @@ cudaError_t launch_fp4_linear(const void *a, const uint8_t *sa, const void *b, c
         e = linear_pairs(P, a, b, row_bytes, device, s);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t fp4_linear_error_take(int32_t *v, cudaStream_t s) {
+    int32_t pairs = 0;
+    cudaError_t e = error_take(v, s);
+    if (e == cudaSuccess) e = linear_pairs_error_take(&pairs, s);
+    *v |= pairs;
+    return e;
 }
 
 }  // namespace amp

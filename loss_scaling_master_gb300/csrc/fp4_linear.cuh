@@ -19,7 +19,6 @@ namespace amp {
 struct Fp4Linear : Fp4Product {
     const void *bias, *res;
     uint8_t *q, *s;
-    int32_t *error;  // the product's error word
     int kb;          // blocks of 32 columns
     uint8_t bt;      // ElemType of bias
     uint8_t act;     // amp_act or kNoAct
@@ -27,9 +26,10 @@ struct Fp4Linear : Fp4Product {
     uint8_t vec;     // rows are whole groups of 8 elements, and every address is aligned for one
 };
 
-// The kernels of pairs of CTAs (fp4_linear_pair.cu).
+// The kernels of pairs of CTAs (fp4_linear_pair.cu), and that file's error word.
 cudaError_t linear_pairs(const Fp4Linear &P, const void *a, const void *b, int64_t row_bytes, int device,
                          cudaStream_t s);
+cudaError_t linear_pairs_error_take(int32_t *v, cudaStream_t s);
 
 namespace {
 
@@ -41,13 +41,6 @@ __device__ __forceinline__ float bias_at(const Fp4Linear &P, int64_t nn) {
     return P.bt == kF32 ? static_cast<const float *>(P.bias)[nn] : load_elem<OT>(P.bias, nn);
 }
 
-// What all of these epilogues are.
-struct EpLinear {
-    using Args = Fp4Linear;
-    static constexpr bool none = false;
-    static __device__ __forceinline__ void gave_up(const Args &P) { *P.error = 1; }
-};
-
 // The checkpoint's scales of cnt tokens from m0 for the 32 columns that hold nn: NaN.
 __device__ __forceinline__ void scales_nan(const Fp4Linear &P, int64_t m0, int cnt, int64_t nn) {
     if (!P.q || (threadIdx.x & 31) != 0) return;
@@ -57,8 +50,10 @@ __device__ __forceinline__ void scales_nan(const Fp4Linear &P, int64_t m0, int c
 
 // A bias and a residual alone, added a column a lane as the columns come.
 template <int OT>
-struct EpOne : EpLinear {
+struct EpOne {
+    using Args = Fp4Linear;
     using Split = EpOne;
+    static constexpr bool none = false;
     static constexpr int staged = 0;
     static constexpr int CH = OT == kF32 ? 8 : 16, WORDS = 8;
     struct State {
@@ -309,8 +304,10 @@ struct Stage {
 
 // For pairs of CTAs.
 template <int OT, int ACT, bool VEC>
-struct EpStaged : EpLinear {
+struct EpStaged {
+    using Args = Fp4Linear;
     using Split = EpStaged;
+    static constexpr bool none = false;
     static constexpr int CH = Stage::CH, staged = Stage::bytes;
     struct State {
         Eight<OT> e[2];
@@ -354,8 +351,10 @@ struct EpStaged : EpLinear {
 // For one CTA a tile: as EpStaged, with the element type and the activation looked up for
 // every 16 tokens.
 template <bool VEC>
-struct EpAny : EpLinear {
+struct EpAny {
+    using Args = Fp4Linear;
     using Split = EpAny<true>;  // joining a cut reduction's parts looks up VEC itself
+    static constexpr bool none = false;
     static constexpr int CH = Stage::CH, staged = Stage::bytes;
     struct State {};
     static __device__ __forceinline__ void begin(const Args &, int64_t, int, int64_t, State &) {}

@@ -35,4 +35,6 @@ cudaError_t linear_pairs(const Fp4Linear &P, const void *a, const void *b, int64
                           : pair_of<kBF16>(P, a, b, row_bytes, device, s);
 }
 
+cudaError_t linear_pairs_error_take(int32_t *v, cudaStream_t s) { return error_take(v, s); }
+
 }  // namespace amp

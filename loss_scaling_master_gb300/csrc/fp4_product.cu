@@ -1,21 +1,9 @@
 // fp4_product.cu - C = A B^T of two 4-bit block-scaled matrices: the kernels of
-// fp4_product.cuh with the accumulators stored as they are; and the error word of all
-// kernels there.
+// fp4_product.cuh with the accumulators stored as they are.
 #include "fp4_product.cuh"
 
 namespace amp {
 namespace {
-
-__device__ int32_t g_fp4_error;
-
-struct EpNone {
-    using Args = Fp4Product;
-    using Split = EpNone;  // for the kernels of a cut reduction
-    static constexpr bool none = true;
-    static constexpr int staged = 0;  // bytes of shared memory a store warp
-    struct State {};
-    static __device__ __forceinline__ void gave_up(const Args &) { g_fp4_error = 1; }
-};
 
 // C = 0 for an empty reduction.
 __global__ void __launch_bounds__(kThreads) fp4_zero_kernel(uint8_t *out, int64_t bytes) {
@@ -47,21 +35,10 @@ cudaError_t launch_fp4_product(const void *a, const uint8_t *sa, const void *b, 
 }
 
 cudaError_t fp4_error_take(int32_t *v, cudaStream_t s) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(v, g_fp4_error, sizeof *v, 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess || *v == 0) return e;
-    const int32_t zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_fp4_error, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
-    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
-}
-
-cudaError_t fp4_error_word(int device, int32_t **at) {
-    static std::atomic<int32_t *> known[64];
-    if (device < 64 && (*at = known[device].load(std::memory_order_relaxed)) != nullptr) return cudaSuccess;
-    void *p = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&p, g_fp4_error);
-    *at = static_cast<int32_t *>(p);
-    if (e == cudaSuccess && device < 64) known[device].store(*at, std::memory_order_relaxed);
+    int32_t linear = 0;
+    cudaError_t e = error_take(v, s);
+    if (e == cudaSuccess) e = fp4_linear_error_take(&linear, s);
+    *v |= linear;
     return e;
 }
 

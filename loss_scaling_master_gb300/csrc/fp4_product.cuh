@@ -69,9 +69,18 @@ struct Fp4Product {
 
 namespace {
 
+__device__ int32_t g_fp4_error;
+
 constexpr int kLanes = 128;       // rows of B a CTA
 constexpr int kStageBytes = 128;  // bytes of a row a stage: 256 elements
 
+struct EpNone {
+    using Args = Fp4Product;
+    using Split = EpNone;  // for the kernels of a cut reduction
+    static constexpr bool none = true;
+    static constexpr int staged = 0;  // bytes of shared memory a store warp
+    struct State {};
+};
 // One line of the constant cache: a second one is missed at every start (0.15 us a
 // call of a few tokens).
 static_assert(sizeof(Fp4Product) == 64, "one line of constants");
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int tiles = P.tiles_m * P.tiles_n;
     const int first = int(blockIdx.x >> 1), stride = int(gridDim.x >> 1);
     const int ks_all = (P.kt + 1) / 2;
-    auto give_up = [&]() { EP::gave_up(P); };
+    auto give_up = [&]() { g_fp4_error = 1; };
 
     if (warp == 0) {
         const int stop = stop_after(P, rank);
@@ -448,7 +457,7 @@ __global__ void __launch_bounds__(Solo<BN, SPLIT, EP>::threads, Solo<BN, SPLIT, 
     const int first = SPLIT ? int(blockIdx.x / parts) : int(blockIdx.x);
     const int ks_all = (P.kt + 1) / 2;
     const int ks0 = int(int64_t(ks_all) * rank / parts), ks1 = int(int64_t(ks_all) * (rank + 1) / parts);
-    auto give_up = [&]() { EP::gave_up(P); };
+    auto give_up = [&]() { g_fp4_error = 1; };
 
     if (warp == 0) {
         const int stop = stop_after(P, 0);
@@ -804,6 +813,16 @@ cudaError_t go_solo(const typename EP::Args &P, const void *a, const void *b, in
     if (P.m <= 32) return go<32, EP>(P, a, b, row_bytes, device, s);
     if (P.m <= 64) return go<64, EP>(P, a, b, row_bytes, device, s);
     return go<128, EP>(P, a, b, row_bytes, device, s);
+}
+
+// Reads and clears this file's error word.
+inline cudaError_t error_take(int32_t *v, cudaStream_t s) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(v, g_fp4_error, sizeof *v, 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess || *v == 0) return e;
+    const int32_t zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_fp4_error, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
+    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
 }
 
 }  // namespace

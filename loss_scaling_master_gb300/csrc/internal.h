@@ -163,11 +163,10 @@ struct Fp4Limits {
 cudaError_t launch_fp4_product(const void *a, const uint8_t *sa, const void *b, const uint8_t *sb,
                                int64_t m, int64_t n, int64_t k, void *out, int oelem, int device,
                                cudaStream_t s, Fp4Limits limits = {30, 3, 0});
-// Reads and clears the sticky error word of the product and of the linear layer (waits for
-// the stream).
+// Reads and clears the sticky error words of the product and of the linear layer (waits for
+// the stream); the second one the linear layer's alone.
 cudaError_t fp4_error_take(int32_t *v, cudaStream_t s);
-// Its address on the current device, which is `device`.
-cudaError_t fp4_error_word(int device, int32_t **at);
+cudaError_t fp4_linear_error_take(int32_t *v, cudaStream_t s);
 
 cudaError_t launch_fp4_linear(const void *a, const uint8_t *sa, const void *b, const uint8_t *sb,
                               int64_t m, int64_t n, int64_t k, const void *bias, int belem, int act,
