@@ -6,6 +6,8 @@
 namespace amp {
 namespace {
 
+Launched g_launched;
+
 // z = bias for an empty reduction: a warp takes 32 columns of 16 tokens.
 __global__ void __launch_bounds__(kThreads) linear_empty_kernel(Fp4Linear P) {
     __shared__ __align__(16) uint8_t s_stage[kThreads / 32][EpAny<false>::staged];
@@ -45,6 +47,7 @@ cudaError_t launch_fp4_linear(const void *a, const uint8_t *sa, const void *b, c
         const int64_t want = ((m + 15) / 16 * P.kb * 32 + kThreads - 1) / kThreads;
         e = launch_pdl(linear_empty_kernel, dim3(unsigned(std::min<int64_t>(want, 4096))), dim3(kThreads), 0, s, P);
     } else if (!takes_pairs(m, n, device)) {
+        g_launched.mark(device);
         e = P.vec ? go_solo<EpAny<true>>(P, a, b, row_bytes, device, s)
                   : go_solo<EpAny<false>>(P, a, b, row_bytes, device, s);
     } else {
@@ -54,9 +57,12 @@ cudaError_t launch_fp4_linear(const void *a, const uint8_t *sa, const void *b, c
 }
 
 cudaError_t fp4_linear_error_take(int32_t *v, cudaStream_t s) {
+    *v = 0;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess && g_launched.any(device)) e = error_take(v, s);
     int32_t pairs = 0;
-    cudaError_t e = error_take(v, s);
-    if (e == cudaSuccess) e = linear_pairs_error_take(&pairs, s);
+    if (e == cudaSuccess) e = linear_pairs_error_take(&pairs, device, s);
     *v |= pairs;
     return e;
 }

@@ -29,7 +29,7 @@ struct Fp4Linear : Fp4Product {
 // The kernels of pairs of CTAs (fp4_linear_pair.cu), and that file's error word.
 cudaError_t linear_pairs(const Fp4Linear &P, const void *a, const void *b, int64_t row_bytes, int device,
                          cudaStream_t s);
-cudaError_t linear_pairs_error_take(int32_t *v, cudaStream_t s);
+cudaError_t linear_pairs_error_take(int32_t *v, int device, cudaStream_t s);
 
 namespace {
 

@@ -5,6 +5,8 @@
 namespace amp {
 namespace {
 
+Launched g_launched;
+
 // Pairs of CTAs: staged where there is something to compute, or a residual and a short
 // reduction to hide it behind (bf16 with a residual, a column a lane and staged: 4096 x 8192
 // x 2048 44.8 and 40.3 us, 4096 x 4096 x 4096 32.0 and 29.7, 8192 x 4096 x 8192 80.1 and
@@ -30,11 +32,14 @@ cudaError_t pair_of(const Fp4Linear &P, const void *a, const void *b, int64_t ro
 
 cudaError_t linear_pairs(const Fp4Linear &P, const void *a, const void *b, int64_t row_bytes, int device,
                          cudaStream_t s) {
+    g_launched.mark(device);
     return P.ot == kF32   ? pair_of<kF32>(P, a, b, row_bytes, device, s)
            : P.ot == kF16 ? pair_of<kF16>(P, a, b, row_bytes, device, s)
                           : pair_of<kBF16>(P, a, b, row_bytes, device, s);
 }
 
-cudaError_t linear_pairs_error_take(int32_t *v, cudaStream_t s) { return error_take(v, s); }
+cudaError_t linear_pairs_error_take(int32_t *v, int device, cudaStream_t s) {
+    return g_launched.any(device) ? error_take(v, s) : cudaSuccess;
+}
 
 }  // namespace amp

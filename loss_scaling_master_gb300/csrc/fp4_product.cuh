@@ -815,7 +815,20 @@ cudaError_t go_solo(const typename EP::Args &P, const void *a, const void *b, in
     return go<128, EP>(P, a, b, row_bytes, device, s);
 }
 
-// Reads and clears this file's error word.
+// Devices on which a file's kernels were launched or captured, a bit each; it stays, since a
+// captured launch may run at any time.
+class Launched {
+    std::atomic<uint64_t> on{0};
+
+public:
+    void mark(int device) {
+        const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+        if ((on.load(std::memory_order_relaxed) & bit) == 0) on.fetch_or(bit, std::memory_order_relaxed);
+    }
+    bool any(int device) const { return device >= 64 || (on.load(std::memory_order_relaxed) >> device & 1) != 0; }
+};
+
+// Reads and clears this file's error word (10 us).
 inline cudaError_t error_take(int32_t *v, cudaStream_t s) {
     cudaError_t e = cudaMemcpyFromSymbolAsync(v, g_fp4_error, sizeof *v, 0, cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
