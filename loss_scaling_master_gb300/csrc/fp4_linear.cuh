@@ -279,24 +279,24 @@ struct Stage {
                     if (P.q) P.q[k + i * n] = codes[32 * (i0 + i) + lane];
                 }
             }
-            return;
-        }
-        using One = EpOne<OT>;
+        } else {
+            using One = EpOne<OT>;
 #pragma unroll
-        for (int h = 0; h < CH; h += One::CH) {
-            uint32_t r[One::WORDS], o[One::WORDS];
-            if (P.res) One::residual(P, m0 + h, rows - h, nn, r);
+            for (int h = 0; h < CH; h += One::CH) {
+                uint32_t r[One::WORDS], o[One::WORDS];
+                if (P.res) One::residual(P, m0 + h, rows - h, nn, r);
 #pragma unroll
-            for (int i = 0; i < One::CH / 2; ++i)
-                One::pack(One::add(P, z[(h + 2 * i) * PITCH + lane], z[(h + 2 * i + 1) * PITCH + lane], i, r), i, o);
-            One::store(P, m0 + h, rows - h, nn, o);
-        }
-        if (P.q && nn < P.n) {
-            uint8_t *at = P.q + m0 * P.n + nn;
+                for (int i = 0; i < One::CH / 2; ++i)
+                    One::pack(One::add(P, z[(h + 2 * i) * PITCH + lane], z[(h + 2 * i + 1) * PITCH + lane], i, r), i, o);
+                One::store(P, m0 + h, rows - h, nn, o);
+            }
+            if (P.q && nn < P.n) {
+                uint8_t *at = P.q + m0 * P.n + nn;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                if (i < rows) *at = codes[32 * i + lane];
-                at += P.n;
+                for (int i = 0; i < CH; ++i) {
+                    if (i < rows) *at = codes[32 * i + lane];
+                    at += P.n;
+                }
             }
         }
     }
@@ -333,7 +333,8 @@ struct EpStaged {
             if constexpr (VEC && OT != kF32)
                 if (s + CH < CNT) Stage::residual(P, m0 + s + CH, rows - s - CH, nn, nxt);
             stage.template finish<OT, ACT, VEC, true>(P, m0 + s, rows - s, nn, ep.e);
-            if (VEC && s + CH < CNT) {
+            if constexpr (VEC) {
+                if (s + CH == CNT) break;
                 if constexpr (OT == kF32) {
                     Stage::residual(P, m0 + s + CH, rows - s - CH, nn, ep.e);
                 } else {
