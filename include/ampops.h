@@ -223,8 +223,8 @@ amp_status fp4_linear_mx_selftest(const void *a, const void *a_scales, const voi
  * fp4_linear_mx made (values zh):
  *     dz = dy * f'(zh),   dbias = sum over rows of dz
  * in fp32; dbias sums dz before its rounding, in an order that depends on the
- * shape, the tensors' alignment and the device alone.  With AMP_ACT_NONE dz = dy: q, scales and dz are
- * NULL and only dbias is written.
+ * shape, the tensors' alignment and the device alone.  With AMP_ACT_NONE
+ * dz = dy: q, scales and dz are NULL and only dbias is written.
  *   dy, dz  [rows, cols] of dtype; dz may be dy
  *   dbias   [cols] of bias_dtype (f32, or dtype); zeros for no rows
  * Errors: AMP_EINVAL (NULL, an activation without q, scales and dz or one of
@@ -286,6 +286,7 @@ amp_status amp_dropout_backward(const void *dy, amp_dtype dtype, int64_t rows, i
  *            most probable tokens (at most 32), larger logits first, equal ones
  *            by index; -1 and -inf where there are no more.  Logits of -inf and
  *            NaN are not listed
+ * An exponential is within (3 |z_j - m| + 4) 2^-24 of its value, relatively.
  * A logit of -inf (a masked token) has probability 0 and log probability -inf.
  * A row with a NaN, with +inf, or with nothing but -inf gives NaN.
  * Errors: AMP_EINVAL (NULL z, logp without targets, top_n outside [0, 32], half

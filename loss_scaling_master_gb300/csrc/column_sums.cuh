@@ -59,8 +59,8 @@ struct SumShare {
 };
 
 // Adds up all threads' a[] (8 columns from 8 x, or column x, x the thread's place on
-// the row; SumFlat: the lane's column and the 32nd after it) and stores the columns' sums.  Every thread of every CTA of the cluster
-// calls it once.
+// the row; SumFlat: the lane's column and the 32nd after it) and stores the columns' sums.
+// Every thread of every CTA of the cluster calls it once.
 template <class S>
 __device__ __forceinline__ void sum_join(const SumShare<S> &at, int64_t cols, const float (&a)[S::each], void *out,
                                          int otype) {
@@ -190,8 +190,8 @@ __device__ __forceinline__ void flat_sums(const SumShare<SumFlat> &at, int64_t r
     sum_join<S>(at, cols, a, out, otype);
 }
 
-// Shares of the rows, of at least a row a group: as many as make the rounds of CTAs that
-// the GPU holds at once shortest.  CTAs of clusters start one after another, 5 ns each, so
+// Shares of the rows: as many as make the rounds of CTAs that the GPU holds at once
+// shortest, while all but one of them would have more than a row a group.  CTAs of clusters start one after another, 5 ns each, so
 // beyond two an SM a share is at least four rows a group (1000 x 2304 dropout by 576 CTAs
 // 5.2 us, by 288 4.3).
 template <class S>

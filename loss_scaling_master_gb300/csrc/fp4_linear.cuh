@@ -6,8 +6,8 @@
 // A lane holds one column of C and consecutive tokens.  A bias and a residual are added so
 // (EpOne): the residual comes in the layout in which store16 stores (two neighbouring
 // elements of a row a lane, even lanes the even tokens) and is turned over by one shuffle
-// for two elements; the words of the first 16 tokens are asked for before the accumulators
-// are waited for, the others 16 tokens ahead.  An activation and the checkpoint want
+// for two elements; the words of the first 16 tokens (fp32: 8) are asked for before the
+// accumulators are waited for, the others as many tokens ahead.  An activation and the checkpoint want
 // neighbouring columns in a lane (Stage).
 #pragma once
 

@@ -49,6 +49,10 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
 // All of it would leave too little for loads on the way (16384 x 5120 dropout 84 instead of
 // 75 us), and for kernels with most on the way this is too much already (kAnyShared, as the
 // driver chooses: token log probabilities 4096 x 128256 forward 158 us, with 64 KB 179).
+// Column sums whose rows come ahead through shared memory need more for four CTAs an SM,
+// and ask for it (bias_grad.cu, dropout.cu): 16384 x 5120 dropout's gradient 57.8 us, with
+// 64 KB 74.4; the change between the two divisions is 1.6 us of dropout of 1024 x 768 with
+// its gradients (6.8 us).
 constexpr int kSmallShared = 64, kAnyShared = -1;
 
 // The same in clusters of `cluster` CTAs along x.

@@ -7,15 +7,14 @@
 //
 // Forward.  The logits are read once: each thread keeps a running maximum and the
 // two sums relative to it, which are rescaled when the maximum grows, at most once
-// for four 16-byte loads.  Few rows are cut over the CTAs of a cluster, whose results
+// for eight 16-byte loads.  Few rows are cut over the CTAs of a cluster, whose results
 // the first of them joins from shared memory.
 //
 // The k most probable tokens.  The k-th largest of the threads' maxima is reached by at
 // least k elements, so only threads whose maximum reaches it hold any of the k, and
 // these are hardly more than k.  What they read is read once more (a thread's share of
-// the row each, from L2), and what reaches the bound there is put in order.  (Lists kept
-// by warps along the row took 703 us for 5 of 4096 x 128256 bf16, 179 without; this
-// way 174.)
+// the row each, from L2), and what reaches the bound there is put in order.  (5 of 4096 x
+// 128256 bf16 take 174 us so, none 158; lists kept by warps along the row took 703.)
 //
 // Every row starts where its address lies: a first and a last piece of less than 16
 // bytes are taken by single elements, padded with -inf, which adds nothing.
@@ -30,7 +29,7 @@
 namespace amp {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e+38f;
 constexpr int kMaxParts = 8;  // CTAs of a cluster that share a row
 constexpr int kLoads = 8, kBwdLoads = 2;  // 16-byte loads a thread has in flight
@@ -402,7 +401,7 @@ __device__ __forceinline__ void top_of(const Pieces<XT> &row, int first_piece, i
 template <int XT, int THREADS, int ROWS, bool TOP>
 __global__ void __launch_bounds__(THREADS *ROWS, 1024 / (THREADS * ROWS))
     logprobs_fwd_kernel(LogprobsFwd P) {
-    constexpr int WARPS = THREADS / 32, VN = Pieces<XT>::VN;
+    constexpr int WARPS = THREADS / 32;
     __shared__ float s_m[WARPS], s_s[WARPS], s_w[WARPS];
     __shared__ Entry s_tops[TOP ? ROWS : 1][32], s_all[TOP && WARPS > 1 ? kMaxParts * 32 : 1];
     __shared__ float3 s_cta;
@@ -664,11 +663,27 @@ cudaError_t fwd(const LogprobsFwd &P, int parts, int dev, cudaStream_t s) {
 template <int XT>
 cudaError_t fwd_x(const LogprobsFwd &P, int device, cudaStream_t s) {
     const int pieces = P.cols / Pieces<XT>::VN + 1, sms = sm_count(device);
+    // A warp a short row, up to 8 alternatives.  Beyond that a lane's maximum bounds little,
+    // and one warp orders what reaches the bound: no gain in few rows, up to 20 alternatives
+    // one in many, then its queue overflows.  us by a warp and by 128 threads, bf16:
+    //     alternatives    0            5            8            20           32
+    //     64 x 1000       2.3   2.4    5.7   4.4    6.7   4.7    12.5  6.1    46    7.4
+    //     300 x 2000      2.7   2.7    5.8   4.8    7.4   5.1    13.1  6.7    54    8.2
+    //     3000 x 4000     7.9   9.3    13.2  15.3   15.0  16.2   23.4  21.3   106   27.0
+    //     8192 x 1000     6.7   17.3   14.2  31.9   17.3  34.1   31.6  45.3   130   57.7
     if (P.k <= 8 && (pieces <= 260 || (pieces <= 520 && P.rows >= 16 * sms))) return fwd<XT, 32, kShortRows>(P, 1, device, s);
-    // 128 threads a row where those CTAs fill the SMs, 8 each (1216 x 50257 bf16 26.2 us with
-    // 256, 23.9 with 128, 5 tokens 30.3 and 27.5; 2048 x 20000 fp32 30.4 and 27.7; 4096 x 50257
-    // bf16 75.6 and 70.8, but 20 tokens 98.5 and 103, and 1023 x 50257 fp16 21.9 and 22.8,
-    // 4096 x 128256 158 and 160); shorter rows already when they are fewer
+    // 128 threads a row where those CTAs fill the SMs, 8 each (1023 x 50257 fp16 22.8 us with
+    // 128, 21.9 with 256), and rows are not too long; shorter rows already when they are fewer.
+    // us with 128 and with 256, bf16:
+    //     tokens               32000         50257         64000         80000         128256
+    //     1216, alone          13.6  14.8    23.9  26.4    27.5  29.2    33.3  34.6    50.8  52.3
+    //     4096, alone          45.5  50.2    71.4  76.4    83.6  86.2    102   105     161   159
+    //     1216, 5 alternatives 17.1  19.3    27.4  30.3    32.1  33.8    39.8  40.3    63.0  59.1
+    //     4096, 5 alternatives 53.4  64.3    83.6  89.8    98.9  99.3    124   119     202   177
+    //     2048, 20             34.6  40.3    56.3  54.5    68.7  59.4    89.2  74.2    143   113
+    //     4096, 20             62.9  73.3    104   99.2    129   109     168   134     277   210
+    // So the two cross beyond 100000 tokens alone, next to 64000 with 5 alternatives (8000
+    // pieces) and between 32000 and 50257 with 20; the limits in pieces are below each.
     const int fits = P.rows >= 8 * sms ? (P.k <= 8 ? 6500 : 4200) : P.rows >= 2 * sms ? 1030 : 260;
     if (pieces <= fits) return fwd<XT, 128, 1>(P, 1, device, s);
     // Until there is a CTA for each SM: a second one there costs the joined rows more than
