@@ -286,7 +286,8 @@ amp_status amp_dropout_backward(const void *dy, amp_dtype dtype, int64_t rows, i
  *            most probable tokens (at most 32), larger logits first, equal ones
  *            by index; -1 and -inf where there are no more.  Logits of -inf and
  *            NaN are not listed
- * An exponential is within (3 |z_j - m| + 4) 2^-24 of its value, relatively.
+ * An exponential is within (3 |z_j - m| + 4) 2^-24 of its value, relatively, and
+ * 0 below 2^-126.
  * A logit of -inf (a masked token) has probability 0 and log probability -inf.
  * A row with a NaN, with +inf, or with nothing but -inf gives NaN.
  * Errors: AMP_EINVAL (NULL z, logp without targets, top_n outside [0, 32], half

@@ -828,7 +828,7 @@ public:
     bool any(int device) const { return device >= 64 || (on.load(std::memory_order_relaxed) >> device & 1) != 0; }
 };
 
-// Reads and clears this file's error word (10 us).
+// Reads and clears this file's error word (9 us of the host).
 inline cudaError_t error_take(int32_t *v, cudaStream_t s) {
     cudaError_t e = cudaMemcpyFromSymbolAsync(v, g_fp4_error, sizeof *v, 0, cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);

@@ -165,7 +165,7 @@ cudaError_t launch_fp4_product(const void *a, const uint8_t *sa, const void *b, 
                                cudaStream_t s, Fp4Limits limits = {30, 3, 0});
 // Reads and clears the current device's sticky error words of the product and of the linear
 // layer (waits for the stream); the second one the linear layer's alone, where its kernels
-// were launched: a word is 10 us of the host (one for them all, by an address among the
+// were launched: a word is 9 us of the host (one for them all, by an address among the
 // arguments, cost the widest epilogue of odd rows 3 % of its time by the registers it moved).
 cudaError_t fp4_error_take(int32_t *v, cudaStream_t s);
 cudaError_t fp4_linear_error_take(int32_t *v, cudaStream_t s);
